@@ -71,6 +71,8 @@ typedef struct CUstream_st *hpa_stream_t;
 #define HPA_STATUS_BAD_MAP 32   /* a malformed map: a partition's segment range, a segment row
                                    (request, owner, tile range) or a request's segment range
                                    out of bounds; the row was skipped, never followed */
+#define HPA_STATUS_BAD_BUDGET 64 /* hpa_evict_select: a budget below 1, below sinks + recent of a
+                                    longer request, or beyond kept_stride */
 
 /* ---- KV element types ---- */
 #define HPA_KV_BF16 0 /* bfloat16 */
@@ -81,7 +83,8 @@ typedef struct CUstream_st *hpa_stream_t;
  * hpa_plan_static and read by hpa_decode_attn and hpa_combine.  One map
  * serves every layer of a decode step ([HPC-Ops §二.1]).  Layout (int32 words):
  *   [0,16)  header: T, base, rem, C, B, S (segments), status, tile, kind
- *           (0 dynamic / 1 static / 2 token-weighted), splits, S_cap, 0...
+ *           (0 dynamic / 1 static / 2 token-weighted / 3 window), splits, S_cap,
+ *           then window, sinks, q_len of a window map, 0...
  *   lens[B]            copy of the sequence lengths
  *   cu_tiles[B+1]      exclusive running sum of tiles per request
  *   cta_begin[C+1]     first stream tile of each partition
@@ -90,6 +93,7 @@ typedef struct CUstream_st *hpa_stream_t;
  *   (padding to a multiple of 4 words)
  *   seg[S_cap][4]      {request, tile_lo, tile_hi, partition}; tiles are
  *                      request-local, [tile_lo, tile_hi); unused rows are -1.
+ *                      In a window map tiles count the pages the window reaches.
  * A segment is the part of one request that one partition owns.
  */
 
@@ -157,6 +161,24 @@ int hpa_plan_weighted(const int32_t *seq_lens_dev, int32_t B, int32_t tile, int3
  */
 int hpa_plan_static(const int32_t *seq_lens_dev, int32_t B, int32_t tile, int32_t splits,
                     void *taskmap_dev, size_t taskmap_bytes, hpa_stream_t stream);
+
+/*
+ * hpa_plan_window -- the dynamic plan for attention with a sliding window and sink
+ * tokens (the pages have no counterpart to it).  With W = window >= 1 and
+ * S = sinks >= 0, token j of request r, at position a = L_r - q_len + j, sees key
+ * i <= a when i > a - W or i < S.  The map (kind 3) cuts into tiles only the pages
+ * that hold such a key: those of the sinks and those from position
+ * max(0, L_r - q_len + 1 - W) on, joined without the pages between them; so the
+ * budget of a partition is what it reads, whatever the length.  window, sinks and
+ * q_len are kept in the map, and the calls that read it follow them:
+ * hpa_decode_attn_window, hpa_combine and hpa_key_weights.  The other attention
+ * calls report such a map as HPA_STATUS_BAD_MAP.  L_r < q_len sets
+ * HPA_STATUS_BAD_SEQLEN.  Sizes as hpa_plan; a tile of 64 (one page) balances
+ * short windows best.
+ */
+int hpa_plan_window(const int32_t *seq_lens_dev, int32_t B, int32_t q_len, int32_t window,
+                    int32_t sinks, int32_t tile, int32_t num_ctas, void *taskmap_dev,
+                    size_t taskmap_bytes, hpa_stream_t stream);
 
 /*
  * hpa_decode_attn -- the split-KV attention kernel ([Notes §3.1] steps 4-5).
@@ -243,6 +265,26 @@ int hpa_decode_attn_tc(const void *q_dev, const void *k_pool_dev, const void *v_
 /* Partitions per KV head that fill the current device once with
  * hpa_decode_attn_tc CTAs (SMs x resident CTAs per SM / Hkv), or -1. */
 int32_t hpa_default_num_ctas_tc(int32_t Hq, int32_t Hkv, int32_t q_len, int32_t kv_dtype);
+
+/*
+ * hpa_decode_attn_window -- hpa_decode_attn over a map of hpa_plan_window: the same
+ * step for the keys the window and the sinks show to each token (see there), reading
+ * only their pages.  Arguments, layouts, supported shapes, partials and errors are
+ * those of hpa_decode_attn; q_len is the one the map was planned with
+ * (HPA_STATUS_MISMATCH).  What lies in hidden places of a page, NaN included, does
+ * not enter the result.  hpa_combine merges the partials.
+ */
+int hpa_decode_attn_window(const void *q_dev, const void *k_pool_dev, const void *v_pool_dev,
+                           int32_t kv_dtype, const float *k_scale_dev, const float *v_scale_dev,
+                           int64_t num_pages, const int32_t *page_indptr_dev,
+                           const int32_t *page_indices_dev, int32_t page_size, int32_t B,
+                           int32_t q_len, int32_t Hq, int32_t Hkv, int32_t d, float sm_scale,
+                           void *taskmap_dev, int32_t num_ctas, float *partial_o_dev,
+                           float *partial_lse_dev, hpa_stream_t stream);
+
+/* Partitions per KV head that fill the current device once with
+ * hpa_decode_attn_window, or <= 0 as hpa_default_num_ctas. */
+int32_t hpa_default_num_ctas_window(int32_t Hq, int32_t Hkv, int32_t q_len, int32_t kv_dtype);
 
 /*
  * hpa_decode_attn_traced -- hpa_decode_attn (the same kernel choice) that
@@ -355,6 +397,94 @@ int hpa_store_kv(const void *k_new_dev, const void *v_new_dev, const int32_t *se
                  const float *k_scale_dev, const float *v_scale_dev, void *k_pool_dev,
                  void *v_pool_dev, int32_t B, int32_t q_len, int32_t Hkv, int32_t d,
                  int32_t *status_dev, hpa_stream_t stream);
+
+/*
+ * hpa_store_kv_at -- hpa_store_kv for a cache that evicts (below): the slot of token j
+ * is still position L_r - q_len + j of the cache, and its rotation is that of position
+ * text_pos_dev[r] + j of the text, which the evictions have left ahead of it.
+ * text_pos_dev: int32 [B], the text position of each request's first new token.  A
+ * text position outside [0, max_pos) sets HPA_STATUS_BAD_SEQLEN.
+ */
+int hpa_store_kv_at(const void *k_new_dev, const void *v_new_dev, const int32_t *seq_lens_dev,
+                    const int32_t *text_pos_dev, const int32_t *page_indptr_dev,
+                    const int32_t *page_indices_dev, int64_t num_pages, int32_t page_size,
+                    const float *cos_sin_dev, int32_t max_pos, const float *norm_w_dev, float eps,
+                    int32_t use_hadamard, int32_t kv_dtype, const float *k_scale_dev,
+                    const float *v_scale_dev, void *k_pool_dev, void *v_pool_dev, int32_t B,
+                    int32_t q_len, int32_t Hkv, int32_t d, int32_t *status_dev,
+                    hpa_stream_t stream);
+
+/*
+ * The three calls below keep a cache bounded by the attention its keys receive (the
+ * pages have no counterpart to them).  Accumulated weights live in pools of their own,
+ * fp32 [num_pages][Hkv][page_size], paged by the same table as K and V.  Each call
+ * writes what it names for the pages of a request, so a page that is listed twice (a
+ * prefix shared by two requests) is not for these calls: its results are unspecified.
+ * Copy such a prefix first (hpa_evict_compact to pages of the request's own).
+ *
+ * hpa_key_weights -- adds one attention step's weights to the accumulators.  With
+ * lse_dev the step's out_lse (fp32 [B][q_len][Hq], natural log), for every key
+ * i < L_r that some token sees:
+ *   acc_out[i] = (i < L_r - q_len ? decay * acc_in[i] : 0)
+ *              + sum over the rows (j, g) of the KV head that see i of
+ *                exp(sm_scale * q . k_i - lse[j][g]),
+ * in fp32, the same order on every run.  The q_len new keys start from zero, whatever
+ * their slots held.  Other slots are not written (with a window map: keys no token
+ * sees; they keep their weight and do not decay).  acc_in_dev may equal acc_out_dev
+ * (the usual, in place), be another pool (draft tokens that may yet be rejected) or be
+ * NULL for zero; decay 0 does not read it.  A row whose lse is -inf adds nothing.
+ * taskmap_dev: the map of the attention step, of any plan; num_ctas as planned.  Both
+ * pools 16-byte aligned.  q, K, shapes and errors as hpa_decode_attn; the pages of a
+ * bad page id and the keys of a request shorter than q_len are not written.
+ */
+int hpa_key_weights(const void *q_dev, const float *lse_dev, const void *k_pool_dev,
+                    int32_t kv_dtype, const float *k_scale_dev, int64_t num_pages,
+                    const int32_t *page_indptr_dev, const int32_t *page_indices_dev,
+                    int32_t page_size, int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv,
+                    int32_t d, float sm_scale, float decay, void *taskmap_dev, int32_t num_ctas,
+                    const float *acc_in_dev, float *acc_out_dev, hpa_stream_t stream);
+
+/*
+ * hpa_evict_select -- which keys each KV head keeps.  For request r with budget
+ * budgets_dev[r] and every KV head: if L_r is within the budget, all of them; else the
+ * first `sinks` keys, the last `recent` keys and, of the others, the
+ * budget - sinks - recent with the largest weight in acc_dev, ties to the lower index
+ * (-0 equals 0; NaN ranks above every number).  Writes their indices in ascending
+ * order to kept_dev[(r * Hkv + h) * kept_stride + t], t < new_lens_dev[r] =
+ * min(L_r, budget); entries past that are left as they were.  A request that cannot
+ * be served gets new_lens -1, which hpa_evict_compact passes over, and sets bits in
+ * status_dev (optional int32, 4-byte aligned): L_r < 1 HPA_STATUS_BAD_SEQLEN; a budget
+ * below 1, min(L_r, budget) > kept_stride, or sinks + recent > budget < L_r
+ * HPA_STATUS_BAD_BUDGET; a missing or out-of-range page HPA_STATUS_BAD_PAGE.
+ * kept_dev: int32, B * Hkv * kept_stride.  new_lens_dev: int32 [B], neither
+ * seq_lens_dev nor budgets_dev.  acc_dev 16-byte aligned.
+ */
+int hpa_evict_select(const float *acc_dev, const int32_t *seq_lens_dev,
+                     const int32_t *page_indptr_dev, const int32_t *page_indices_dev,
+                     int64_t num_pages, int32_t page_size, const int32_t *budgets_dev,
+                     int32_t sinks, int32_t recent, int32_t B, int32_t Hkv, int32_t *kept_dev,
+                     int64_t kept_stride, int32_t *new_lens_dev, int32_t *status_dev,
+                     hpa_stream_t stream);
+
+/*
+ * hpa_evict_compact -- moves the kept rows of K, V and (unless NULL) the accumulated
+ * weights together: position t of the request's new cache gets the row of position
+ * kept[t], for t < new_lens[r] and every KV head.  With dst_indptr_dev and
+ * dst_indices_dev NULL the new cache is the front of the request's own pages; the pages
+ * past ceil(new_len / page_size) are then free.  Otherwise it is the pages that this
+ * second table lists, none of them among the pages being read: the old cache stays as
+ * it was (a shared prefix, say).  Order is kept, so windows, sinks and causal masks mean
+ * the same as before.  kept must ascend, as hpa_evict_select writes it.  new_lens[r]
+ * below 1 or beyond kept_stride: the request is passed over.  A position without a
+ * valid page sets HPA_STATUS_BAD_PAGE in status_dev (optional), and that row is not
+ * moved.  k_pool_dev, v_pool_dev 16-byte aligned.
+ */
+int hpa_evict_compact(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, float *acc_dev,
+                      int64_t num_pages, const int32_t *page_indptr_dev,
+                      const int32_t *page_indices_dev, const int32_t *dst_indptr_dev,
+                      const int32_t *dst_indices_dev, int32_t page_size, const int32_t *kept_dev,
+                      int64_t kept_stride, const int32_t *new_lens_dev, int32_t B, int32_t Hkv,
+                      int32_t d, int32_t *status_dev, hpa_stream_t stream);
 
 /*
  * hpa_selftest_wait_timeout -- diagnostic for the failure path of the

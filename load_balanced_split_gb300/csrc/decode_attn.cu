@@ -101,9 +101,10 @@ struct SegInfo {
 };
 
 // Segment s of partition c, checked (a malformed row reads as an empty segment).
+template <bool WIN>
 __device__ __forceinline__ SegInfo seg_info(const AttnParams &p, int s, int tile, int c,
                                             bool report) {
-  const SegRow sr = read_seg_row(p.tm, p.lay, p.B, s, c, tile, report);
+  const SegRow sr = read_seg_row<WIN>(p.tm, p.lay, p.B, s, c, tile, report);
   SegInfo f;
   f.r = sr.r;
   f.L = sr.L;
@@ -115,7 +116,7 @@ __device__ __forceinline__ SegInfo seg_info(const AttnParams &p, int s, int tile
 }
 
 // ----------------------------------------------------------------------------- producer
-template <int KV, bool FUSED, bool ALLH>
+template <int KV, bool FUSED, bool ALLH, bool WIN>
 __device__ void producer(const AttnParams &p, const CUtensorMap *tmk, const CUtensorMap *tmv,
                          uint8_t *smem, int s_begin, int s_end, int tile, int h0) {
   using S = Smem<KV>;
@@ -130,6 +131,7 @@ __device__ void producer(const AttnParams &p, const CUtensorMap *tmk, const CUte
     prefetch_tmap(tmv);
   }
   const uint32_t qfull0 = empty0 + 8 * S::kStages, qempty0 = qfull0 + 16;
+  const int window = WIN ? p.tm[TM_WINDOW] : 0, sinks = WIN ? p.tm[TM_SINKS] : 0;
   int stage = 0;
   uint32_t phase = 0, issued = 0, parity_bits = 0;
   bool ok = true;
@@ -138,7 +140,9 @@ __device__ void producer(const AttnParams &p, const CUtensorMap *tmk, const CUte
   const int hpc = ALLH ? p.heads_per_cta : 1, n_items = (s_end - s_begin) * hpc;
   for (int k = 0; k < n_items && ok; ++k) {
     const int s = s_begin + k / hpc, h = h0 + k % hpc;
-    const SegInfo f = seg_info(p, s, tile, blockIdx.x, lane == 0 && h == h0);
+    const SegInfo f = seg_info<WIN>(p, s, tile, blockIdx.x, lane == 0 && h == h0);
+    WinSpan win = {};
+    if (WIN && f.pg0 < f.pg1) win = WinSpan::make(f.L, p.q_len, window, sinks);
     // stage the item's segment info and query rows for the consumers
     {
       const int slot = k & 1;
@@ -176,7 +180,8 @@ __device__ void producer(const AttnParams &p, const CUtensorMap *tmk, const CUte
       const int cnt = min(32, f.pg1 - pb);
       int id = 0;
       if (lane < cnt) {
-        id = pb + lane < pcount ? pidx[pb + lane] : -1;
+        const int pg = WIN ? win.real_page(pb + lane) : pb + lane;
+        id = pg < pcount ? pidx[pg] : -1;
         if (id < 0 || id >= p.num_pages) {  // bad id or too short a page list
           status_or(p.tm, HPA_STATUS_BAD_PAGE);
           id = 0;
@@ -234,32 +239,96 @@ __device__ __forceinline__ float absmax4_bf16(const __nv_bfloat16 *x) {
   return fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y)));
 }
 
-// e such that amax * 2^e lies in [2^14, 2^15) (0 for a zero row), clamped so that
-// both 2^e and 2^-e are fp32 normals.
-__device__ __forceinline__ int f16_row_exponent(float amax) {
-  if (!(amax > 0.f)) return 0;
-  const int ea = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127;  // floor(log2)
-  return 14 - min(max(ea, -112), 126);
-}
-
-// Zero the V rows (keys >= L) this warp reads from a page that ends past L.
-template <int KV>
-__device__ __forceinline__ void zero_tail_rows(uint8_t *vtile, int w, int wk, int L, int lane) {
+// Zero the V rows this warp reads that no token sees: keys >= L and, with a window, keys
+// from the sinks up to the first token's window.
+template <int KV, bool WIN>
+__device__ __forceinline__ void zero_hidden_rows(uint8_t *vtile, int w, int wk, int L, int sinks,
+                                                 int low, int lane) {
   const int4 z = make_int4(0, 0, 0, 0);
+  auto hidden = [&](int key) { return key >= L || (WIN && key >= sinks && key < low); };
   if (KV == HPA_KV_BF16) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int id = lane + 32 * i, rr = id >> 4, hf = (id >> 3) & 1, ch = id & 7;
-      if (wk + rr >= L)
+      if (hidden(wk + rr))
         *reinterpret_cast<int4 *>(vtile + hf * 8192 + (16 * w + rr) * 128 + ch * 16) = z;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int id = lane + 32 * i, rr = id >> 3, ch = id & 7;
-      if (wk + rr >= L) *reinterpret_cast<int4 *>(vtile + (16 * w + rr) * 128 + ch * 16) = z;
+      if (hidden(wk + rr)) *reinterpret_cast<int4 *>(vtile + (16 * w + rr) * 128 + ch * 16) = z;
     }
   }
+}
+
+// A key that some query rows see and others do not (the ends of the windows of a request
+// with several new tokens) has probability 0 for the others, and 0 times an infinite or
+// NaN value element would be NaN in rows that must not see it.  Of the warp's 16 keys,
+// every `partial` one whose V row holds such an element is added here in fp32, for the
+// rows that see it alone (`sees(key, 0 / 1)` for the thread's two rows), and its V row is
+// zeroed before the MMA.  Rare, so one key at a time; true if a row was zeroed.
+template <int KV, typename Sees, typename Partial>
+__device__ __forceinline__ bool take_out_nonfinite(float (&o)[16][4], const float (&sc)[2][4],
+                                                   uint8_t *vt, int w, int lane, Sees sees,
+                                                   Partial partial, int wk) {
+  const int r8 = lane >> 2, qd = lane & 3;
+  bool any = false;
+#pragma unroll 1
+  for (int kk = 0; kk < 16; ++kk) {
+    if (!partial(wk + kk)) continue;
+    const int row = 16 * w + kk;
+    uint8_t *mine;  // the bytes of this lane's four dims [4 lane, 4 lane + 4)
+    bool bad;
+    if (KV == HPA_KV_BF16) {
+      mine = vt + (lane >> 4) * 8192 + row * 128 + ((((lane & 15) >> 1) ^ (row & 7)) << 4) +
+             (lane & 1) * 8;
+      const uint2 x = *reinterpret_cast<const uint2 *>(mine);
+      auto inf2 = [](uint32_t v) {
+        return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
+      };
+      bad = inf2(x.x) || inf2(x.y);
+    } else {
+      mine = vt + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4;
+      const uint32_t x = *reinterpret_cast<const uint32_t *>(mine);
+      bad = false;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) bad |= ((x >> (8 * b)) & 0x7fu) == 0x7fu;
+    }
+    if (!__any_sync(kFull, bad)) continue;
+    any = true;
+    const int src = (r8 << 2) | ((kk & 7) >> 1);
+    const bool hi = kk & 8, odd = kk & 1;
+    const float x0 = odd ? (hi ? sc[1][1] : sc[0][1]) : (hi ? sc[1][0] : sc[0][0]);
+    const float x1 = odd ? (hi ? sc[1][3] : sc[0][3]) : (hi ? sc[1][2] : sc[0][2]);
+    const float p0 = __shfl_sync(kFull, x0, src);
+    const float p1 = __shfl_sync(kFull, x1, src);
+    const bool s0 = sees(wk + kk, 0), s1 = sees(wk + kk, 1);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float v;
+        if (KV == HPA_KV_BF16) {
+          const int dim = 8 * i + 2 * qd + c;
+          v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(
+              vt + (dim >> 6) * 8192 + row * 128 + ((((dim & 63) >> 3) ^ (row & 7)) << 4) +
+              (dim & 7) * 2));
+        } else {
+          const int dim = 16 * (2 * qd + c) + i;
+          const uint32_t h2 =
+              e4m3x2_to_f16x2(vt[row * 128 + (((dim >> 4) ^ (row & 7)) << 4) + (dim & 15)]);
+          v = __half2float(__ushort_as_half(static_cast<unsigned short>(h2 & 0xffffu)));
+        }
+        if (s0) o[i][c] += p0 * v;
+        if (s1) o[i][2 + c] += p1 * v;
+      }
+    __syncwarp();
+    if (KV == HPA_KV_BF16) *reinterpret_cast<uint2 *>(mine) = make_uint2(0u, 0u);
+    else *reinterpret_cast<uint32_t *>(mine) = 0u;
+    __syncwarp();
+  }
+  return any;
 }
 
 // S[16 rows x 16 keys] = Q K^T for the warp's keys of the page in `kt`.
@@ -403,7 +472,7 @@ __device__ void merge_request(const AttnParams &p, int r, int h, int seg_first, 
 }
 
 // ----------------------------------------------------------------------------- consumer
-template <int KV, bool FUSED, bool ALLH>
+template <int KV, bool FUSED, bool ALLH, bool WIN>
 __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_end, int tile,
                          int h0) {
   using S = Smem<KV>;
@@ -425,6 +494,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
   const uint32_t qfull0 = empty0 + 8 * S::kStages, qempty0 = qfull0 + 16;
   int stage = 0;
   uint32_t phase = 0;
+  const int window = WIN ? p.tm[TM_WINDOW] : 0, sinks = WIN ? p.tm[TM_SINKS] : 0;
   // score and output scales of the KV head (loaded once on the per-head grid)
   float sl2_h = p.scale_log2, vsc_h = 1.f;
   if (!ALLH && KV == HPA_KV_E4M3) {
@@ -462,6 +532,9 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
     const int lim_min = f.L - q_len + 1;  // first key hidden from some row
     const int lim0 = v0 ? f.L - q_len + 1 + j0 : f.L;
     const int lim1 = v1 ? f.L - q_len + 1 + j1 : f.L;
+    // sliding window: row j sees key i < lim when i < sinks or i >= start + j
+    WinSpan win = {};
+    if (WIN && f.pg0 < f.pg1) win = WinSpan::make(f.L, q_len, window, sinks);
 
     // query fragments (A operand, 16 rows x 128) from the staged rows
     uint32_t qa[8][4];
@@ -534,10 +607,14 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
       }
       uint8_t *kt = smem + stage * S::kStageBytes;
       uint8_t *vt = kt + Cfg<KV>::kKBytes;
-      const int key0 = pg * PAGE, wk = key0 + 16 * w;
-      const bool tail = wk + 16 > f.L;
+      const int key0 = (WIN ? win.real_page(pg) : pg) * PAGE, wk = key0 + 16 * w;
+      // the warp's 16 keys reach past the request's end, or some key among them lies
+      // between the sinks and the first token's window: V rows that no token sees are
+      // zeroed, so what they hold (NaN among it) stays out of the sums
+      bool tail = wk + 16 > f.L;
+      if (WIN) tail |= wk < win.low && wk + 16 > sinks;
       if (tail) {
-        zero_tail_rows<KV>(vt, w, wk, f.L, lane);
+        zero_hidden_rows<KV, WIN>(vt, w, wk, f.L, sinks, win.low, lane);
         __syncwarp();
       }
 
@@ -554,6 +631,15 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
           for (int e = 0; e < 4; ++e) {
             const int key = wk + 8 * nt + 2 * qd + (e & 1);
             if (key >= (e < 2 ? lim0 : lim1)) sc[nt][e] = -CUDART_INF_F;
+          }
+      }
+      if (WIN && wk < win.start + q_len - 1 && wk + 16 > sinks) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = wk + 8 * nt + 2 * qd + (e & 1);
+            if (key >= sinks && key < win.start + (e < 2 ? j0 : j1)) sc[nt][e] = -CUDART_INF_F;
           }
       }
       // online softmax, rows row0 (e = 0,1) and row1 (e = 2,3)
@@ -592,6 +678,15 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
           o[i][2] *= a1;
           o[i][3] *= a1;
         }
+      }
+      if (WIN && q_len > 1) {
+        const int pl = max(win.low, sinks);  // keys some tokens see: [pl, ph), [lim_min, L)
+        const int ph = win.start + q_len - 1;
+        if ((wk < ph && wk + 16 > pl) || (wk < f.L && wk + 16 > lim_min))
+          tail |= take_out_nonfinite<KV>(o, sc, vt, w, lane, [&](int key, int row) {
+            const int j = row ? j1 : j0;
+            return key < (row ? lim1 : lim0) && (key < sinks || key >= win.start + j);
+          }, [&](int key) { return (key >= pl && key < ph) || (key >= lim_min && key < f.L); }, wk);
       }
       uint32_t pa[4];
       if (KV == HPA_KV_BF16) {
@@ -754,7 +849,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
 }
 
 // ----------------------------------------------------------------------------- kernel
-template <int KV, bool FUSED, bool ALLH>
+template <int KV, bool FUSED, bool ALLH, bool WIN>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_attn_kernel(const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, const AttnParams p) {
@@ -780,7 +875,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (c == 0 && h0 == 0) status_or(p.tm, HPA_STATUS_MISMATCH);
       go = 0;
     }
-    if (go && !map_ranges_ok(tm, p.lay, p.B, p.C, c)) {
+    if (go && WIN && tm[TM_KIND] == KIND_WINDOW && tm[TM_QLEN] != p.q_len) {
+      if (c == 0 && h0 == 0) status_or(p.tm, HPA_STATUS_MISMATCH);
+      go = 0;
+    }
+    if (go && !map_ranges_ok<WIN>(tm, p.lay, p.B, p.C, c)) {
       status_or(p.tm, HPA_STATUS_BAD_MAP);
       go = 0;
     }
@@ -829,14 +928,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int tile = hdr[1], s_begin = hdr[2], s_end = hdr[3];
 
   if (threadIdx.x >= kConsumerWarps * 32) {
-    producer<KV, FUSED, ALLH>(p, &tmk, &tmv, smem, s_begin, s_end, tile, h0);
+    producer<KV, FUSED, ALLH, WIN>(p, &tmk, &tmv, smem, s_begin, s_end, tile, h0);
   } else {
-    consumer<KV, FUSED, ALLH>(p, smem, s_begin, s_end, tile, h0);
+    consumer<KV, FUSED, ALLH, WIN>(p, smem, s_begin, s_end, tile, h0);
     if (trace && threadIdx.x == 0) trace[2] = globaltimer_ns();  // after the last epilogue
   }
 }
 
-template <int KV, bool FUSED, bool ALLH>
+template <int KV, bool FUSED, bool ALLH, bool WIN = false>
 cudaError_t launch(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv,
                    cudaStream_t s) {
   static int configured[64] = {0};
@@ -844,7 +943,7 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMa
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && !configured[dev]) {
-    e = cudaFuncSetAttribute(decode_attn_kernel<KV, FUSED, ALLH>,
+    e = cudaFuncSetAttribute(decode_attn_kernel<KV, FUSED, ALLH, WIN>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<KV>::kAlloc);
     if (e != cudaSuccess) return e;
     configured[dev] = 1;
@@ -859,16 +958,16 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMa
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_attn_kernel<KV, FUSED, ALLH>, tmk, tmv, p);
+  return cudaLaunchKernelEx(&cfg, decode_attn_kernel<KV, FUSED, ALLH, WIN>, tmk, tmv, p);
 }
 
 template <int KV>
 int occupancy(int *ctas) {
-  cudaError_t e = cudaFuncSetAttribute(decode_attn_kernel<KV, false, false>,
+  cudaError_t e = cudaFuncSetAttribute(decode_attn_kernel<KV, false, false, false>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Smem<KV>::kAlloc);
   if (e != cudaSuccess) return -1;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, decode_attn_kernel<KV, false, false>,
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, decode_attn_kernel<KV, false, false, false>,
                                                     kThreads, Smem<KV>::kAlloc);
   return e == cudaSuccess ? 0 : -1;
 }
@@ -880,6 +979,11 @@ cudaError_t launch_decode_attn(const AttnParams &p, const CUtensorMap &tmk,
   const bool fused = p.out != nullptr;  // the fused combine is its own instantiation
   const bool all_heads = p.heads_per_cta > 1;  // every KV head in the CTA (unfused only)
   if (fused && all_heads) return cudaErrorInvalidValue;
+  if (p.window) {  // windows run on the per-head grid and write partials
+    if (fused || all_heads) return cudaErrorInvalidValue;
+    return kv_dtype == HPA_KV_BF16 ? launch<HPA_KV_BF16, false, false, true>(p, tmk, tmv, s)
+                                   : launch<HPA_KV_E4M3, false, false, true>(p, tmk, tmv, s);
+  }
   if (kv_dtype == HPA_KV_BF16)
     return fused       ? launch<HPA_KV_BF16, true, false>(p, tmk, tmv, s)
            : all_heads ? launch<HPA_KV_BF16, false, true>(p, tmk, tmv, s)

@@ -193,6 +193,20 @@ int hpa_plan_static(const int32_t *seq_lens_dev, int32_t B, int32_t tile, int32_
   return e == cudaSuccess ? HPA_OK : cuda_fail(e);
 }
 
+int hpa_plan_window(const int32_t *seq_lens_dev, int32_t B, int32_t q_len, int32_t window,
+                    int32_t sinks, int32_t tile, int32_t num_ctas, void *taskmap_dev,
+                    size_t taskmap_bytes, hpa_stream_t stream) {
+  const int64_t s_cap = int64_t(B) + num_ctas - 1;
+  if (q_len < 1 || window < 1 || sinks < 0) return HPA_ERR_INVALID;
+  int rc = check_plan_args(seq_lens_dev, B, tile, num_ctas, taskmap_dev, taskmap_bytes, s_cap);
+  if (rc != HPA_OK) return rc;
+  cudaError_t e = hpa::launch_plan(seq_lens_dev, B, tile, num_ctas, hpa::KIND_WINDOW, 0,
+                                   static_cast<int32_t *>(taskmap_dev), s_cap,
+                                   reinterpret_cast<cudaStream_t>(stream),
+                                   hpa::PlanWindow{window, sinks, q_len});
+  return e == cudaSuccess ? HPA_OK : cuda_fail(e);
+}
+
 static int decode_attn_impl(const void *q_dev, const void *k_pool_dev, const void *v_pool_dev,
                             int32_t kv_dtype, const float *k_scale_dev,
                             const float *v_scale_dev, int64_t num_pages,
@@ -201,7 +215,8 @@ static int decode_attn_impl(const void *q_dev, const void *k_pool_dev, const voi
                             int32_t d, float sm_scale, void *taskmap_dev, int32_t num_ctas,
                             float *partial_o_dev, float *partial_lse_dev, uint64_t *trace_dev,
                             void *out_dev, float *out_lse_dev, int32_t *arrivals_dev,
-                            hpa_stream_t stream, bool tc = false, bool all_heads = false) {
+                            hpa_stream_t stream, bool tc = false, bool all_heads = false,
+                            bool window = false) {
   if (!q_dev || !k_pool_dev || !v_pool_dev || !page_indptr_dev || !page_indices_dev ||
       !taskmap_dev || !partial_o_dev || !partial_lse_dev)
     return HPA_ERR_INVALID;
@@ -244,6 +259,7 @@ static int decode_attn_impl(const void *q_dev, const void *k_pool_dev, const voi
   p.G = Hq / Hkv;
   p.rows = p.G * q_len;
   p.heads_per_cta = all_heads ? Hkv : 1;
+  p.window = window;
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   cudaError_t e =
       tc ? hpa::launch_decode_attn_tc(p, tmk, tmv, kv_dtype, reinterpret_cast<cudaStream_t>(stream))
@@ -293,6 +309,24 @@ int hpa_decode_attn_mma(const void *q_dev, const void *k_pool_dev, const void *v
                           num_pages, page_indptr_dev, page_indices_dev, page_size, B, q_len, Hq,
                           Hkv, d, sm_scale, taskmap_dev, num_ctas, partial_o_dev,
                           partial_lse_dev, nullptr, nullptr, nullptr, nullptr, stream);
+}
+
+int hpa_decode_attn_window(const void *q_dev, const void *k_pool_dev, const void *v_pool_dev,
+                           int32_t kv_dtype, const float *k_scale_dev, const float *v_scale_dev,
+                           int64_t num_pages, const int32_t *page_indptr_dev,
+                           const int32_t *page_indices_dev, int32_t page_size, int32_t B,
+                           int32_t q_len, int32_t Hq, int32_t Hkv, int32_t d, float sm_scale,
+                           void *taskmap_dev, int32_t num_ctas, float *partial_o_dev,
+                           float *partial_lse_dev, hpa_stream_t stream) {
+  return decode_attn_impl(q_dev, k_pool_dev, v_pool_dev, kv_dtype, k_scale_dev, v_scale_dev,
+                          num_pages, page_indptr_dev, page_indices_dev, page_size, B, q_len, Hq,
+                          Hkv, d, sm_scale, taskmap_dev, num_ctas, partial_o_dev,
+                          partial_lse_dev, nullptr, nullptr, nullptr, nullptr, stream, false,
+                          false, true);
+}
+
+int32_t hpa_default_num_ctas_window(int32_t Hq, int32_t Hkv, int32_t q_len, int32_t kv_dtype) {
+  return hpa_default_num_ctas_mma(Hq, Hkv, q_len, kv_dtype);
 }
 
 // More than 16 query rows per KV head (MTP with several draft tokens) go to the
@@ -418,13 +452,15 @@ int hpa_selftest_wait_timeout(int32_t *status_dev, int64_t limit_ns, hpa_stream_
   return e == cudaSuccess ? HPA_OK : cuda_fail(e);
 }
 
-int hpa_store_kv(const void *k_new_dev, const void *v_new_dev, const int32_t *seq_lens_dev,
-                 const int32_t *page_indptr_dev, const int32_t *page_indices_dev,
-                 int64_t num_pages, int32_t page_size, const float *cos_sin_dev, int32_t max_pos,
-                 const float *norm_w_dev, float eps, int32_t use_hadamard, int32_t kv_dtype,
-                 const float *k_scale_dev, const float *v_scale_dev, void *k_pool_dev,
-                 void *v_pool_dev, int32_t B, int32_t q_len, int32_t Hkv, int32_t d,
-                 int32_t *status_dev, hpa_stream_t stream) {
+static int store_kv_impl(const void *k_new_dev, const void *v_new_dev,
+                         const int32_t *seq_lens_dev, const int32_t *page_indptr_dev,
+                         const int32_t *page_indices_dev, int64_t num_pages, int32_t page_size,
+                         const float *cos_sin_dev, int32_t max_pos, const float *norm_w_dev,
+                         float eps, int32_t use_hadamard, int32_t kv_dtype,
+                         const float *k_scale_dev, const float *v_scale_dev, void *k_pool_dev,
+                         void *v_pool_dev, int32_t B, int32_t q_len, int32_t Hkv, int32_t d,
+                         int32_t *status_dev, const int32_t *text_pos_dev,
+                         hpa_stream_t stream) {
   if (!k_new_dev || !v_new_dev || !seq_lens_dev || !page_indptr_dev || !page_indices_dev ||
       !cos_sin_dev || !norm_w_dev || !k_pool_dev || !v_pool_dev)
     return HPA_ERR_INVALID;
@@ -460,7 +496,162 @@ int hpa_store_kv(const void *k_new_dev, const void *v_new_dev, const int32_t *se
   p.q_len = q_len;
   p.Hkv = Hkv;
   p.status = status_dev;
+  p.text_pos = text_pos_dev;
   cudaError_t e = hpa::launch_store_kv(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HPA_OK : cuda_fail(e);
+}
+
+int hpa_store_kv(const void *k_new_dev, const void *v_new_dev, const int32_t *seq_lens_dev,
+                 const int32_t *page_indptr_dev, const int32_t *page_indices_dev,
+                 int64_t num_pages, int32_t page_size, const float *cos_sin_dev, int32_t max_pos,
+                 const float *norm_w_dev, float eps, int32_t use_hadamard, int32_t kv_dtype,
+                 const float *k_scale_dev, const float *v_scale_dev, void *k_pool_dev,
+                 void *v_pool_dev, int32_t B, int32_t q_len, int32_t Hkv, int32_t d,
+                 int32_t *status_dev, hpa_stream_t stream) {
+  return store_kv_impl(k_new_dev, v_new_dev, seq_lens_dev, page_indptr_dev, page_indices_dev,
+                       num_pages, page_size, cos_sin_dev, max_pos, norm_w_dev, eps, use_hadamard,
+                       kv_dtype, k_scale_dev, v_scale_dev, k_pool_dev, v_pool_dev, B, q_len, Hkv, d,
+                       status_dev, nullptr, stream);
+}
+
+int hpa_store_kv_at(const void *k_new_dev, const void *v_new_dev, const int32_t *seq_lens_dev,
+                    const int32_t *text_pos_dev, const int32_t *page_indptr_dev,
+                    const int32_t *page_indices_dev, int64_t num_pages, int32_t page_size,
+                    const float *cos_sin_dev, int32_t max_pos, const float *norm_w_dev, float eps,
+                    int32_t use_hadamard, int32_t kv_dtype, const float *k_scale_dev,
+                    const float *v_scale_dev, void *k_pool_dev, void *v_pool_dev, int32_t B,
+                    int32_t q_len, int32_t Hkv, int32_t d, int32_t *status_dev,
+                    hpa_stream_t stream) {
+  if (!text_pos_dev) return HPA_ERR_INVALID;
+  return store_kv_impl(k_new_dev, v_new_dev, seq_lens_dev, page_indptr_dev, page_indices_dev,
+                       num_pages, page_size, cos_sin_dev, max_pos, norm_w_dev, eps, use_hadamard,
+                       kv_dtype, k_scale_dev, v_scale_dev, k_pool_dev, v_pool_dev, B, q_len, Hkv, d,
+                       status_dev, text_pos_dev, stream);
+}
+
+int hpa_key_weights(const void *q_dev, const float *lse_dev, const void *k_pool_dev,
+                    int32_t kv_dtype, const float *k_scale_dev, int64_t num_pages,
+                    const int32_t *page_indptr_dev, const int32_t *page_indices_dev,
+                    int32_t page_size, int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv,
+                    int32_t d, float sm_scale, float decay, void *taskmap_dev, int32_t num_ctas,
+                    const float *acc_in_dev, float *acc_out_dev, hpa_stream_t stream) {
+  if (!q_dev || !lse_dev || !k_pool_dev || !page_indptr_dev || !page_indices_dev ||
+      !taskmap_dev || !acc_out_dev)
+    return HPA_ERR_INVALID;
+  if (kv_dtype != HPA_KV_BF16 && kv_dtype != HPA_KV_E4M3) return HPA_ERR_INVALID;
+  if (kv_dtype == HPA_KV_E4M3 && !k_scale_dev) return HPA_ERR_INVALID;
+  if (B < 1 || B > kMaxB || num_ctas < 1 || num_ctas > kMaxC || q_len < 1 || Hq < 1 ||
+      Hkv < 1 || Hkv > 65535 || num_pages < 1 || !std::isfinite(sm_scale) ||
+      !std::isfinite(decay) || decay < 0.f)
+    return HPA_ERR_INVALID;
+  if (d != hpa::HEAD_DIM || page_size != hpa::PAGE || Hq % Hkv != 0 ||
+      int64_t(Hq / Hkv) * q_len > hpa::MAX_ROWS_TOTAL)
+    return HPA_ERR_UNSUPPORTED;
+  if (num_pages * Hkv > INT_MAX) return HPA_ERR_UNSUPPORTED;
+  if (!aligned(q_dev, 16) || !aligned(k_pool_dev, 16) || !aligned(taskmap_dev, 16) ||
+      !aligned(acc_in_dev, 16) || !aligned(acc_out_dev, 16) || !aligned(lse_dev, 4))
+    return HPA_ERR_ALIGN;
+  CUtensorMap tmk;
+  const int rc = pool_map(k_pool_dev, num_pages, Hkv, kv_dtype, &tmk);
+  if (rc != HPA_OK) return rc;
+  hpa::KeyWeightsParams p;
+  p.q = static_cast<const __nv_bfloat16 *>(q_dev);
+  p.lse = lse_dev;
+  p.tm = static_cast<int32_t *>(taskmap_dev);
+  p.page_indptr = page_indptr_dev;
+  p.page_indices = page_indices_dev;
+  p.k_scale = k_scale_dev;
+  p.acc_in = decay == 0.f ? nullptr : acc_in_dev;  // nothing of it would be left
+  p.acc_out = acc_out_dev;
+  p.num_pages = num_pages;
+  p.lay = hpa::TaskMapLayout::make(B, num_ctas);
+  p.B = B;
+  p.C = num_ctas;
+  p.q_len = q_len;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.rows = p.G * q_len;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.decay = decay;
+  cudaError_t e =
+      hpa::launch_key_weights(p, tmk, kv_dtype, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HPA_OK : cuda_fail(e);
+}
+
+int hpa_evict_select(const float *acc_dev, const int32_t *seq_lens_dev,
+                     const int32_t *page_indptr_dev, const int32_t *page_indices_dev,
+                     int64_t num_pages, int32_t page_size, const int32_t *budgets_dev,
+                     int32_t sinks, int32_t recent, int32_t B, int32_t Hkv, int32_t *kept_dev,
+                     int64_t kept_stride, int32_t *new_lens_dev, int32_t *status_dev,
+                     hpa_stream_t stream) {
+  if (!acc_dev || !seq_lens_dev || !page_indptr_dev || !page_indices_dev || !budgets_dev ||
+      !kept_dev || !new_lens_dev)
+    return HPA_ERR_INVALID;
+  if (B < 1 || B > kMaxB || Hkv < 1 || Hkv > 65535 || num_pages < 1 || sinks < 0 ||
+      recent < 0 || kept_stride < 1)
+    return HPA_ERR_INVALID;
+  // the blocks of a request's other heads may still read what the first one writes
+  if (new_lens_dev == seq_lens_dev || new_lens_dev == budgets_dev) return HPA_ERR_INVALID;
+  if (page_size != hpa::PAGE || int64_t(B) * Hkv > INT_MAX) return HPA_ERR_UNSUPPORTED;
+  if (!aligned(acc_dev, 16) || !aligned(kept_dev, 4) || !aligned(new_lens_dev, 4) ||
+      (status_dev && !aligned(status_dev, 4)))
+    return HPA_ERR_ALIGN;
+  hpa::EvictParams p;
+  p.acc = acc_dev;
+  p.seq_lens = seq_lens_dev;
+  p.page_indptr = page_indptr_dev;
+  p.page_indices = page_indices_dev;
+  p.budgets = budgets_dev;
+  p.num_pages = num_pages;
+  p.sinks = sinks;
+  p.recent = recent;
+  p.B = B;
+  p.Hkv = Hkv;
+  p.kept = kept_dev;
+  p.kept_stride = kept_stride;
+  p.new_lens = new_lens_dev;
+  p.status = status_dev;
+  cudaError_t e = hpa::launch_evict_select(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HPA_OK : cuda_fail(e);
+}
+
+int hpa_evict_compact(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, float *acc_dev,
+                      int64_t num_pages, const int32_t *page_indptr_dev,
+                      const int32_t *page_indices_dev, const int32_t *dst_indptr_dev,
+                      const int32_t *dst_indices_dev, int32_t page_size, const int32_t *kept_dev,
+                      int64_t kept_stride, const int32_t *new_lens_dev, int32_t B, int32_t Hkv,
+                      int32_t d, int32_t *status_dev, hpa_stream_t stream) {
+  if (!k_pool_dev || !v_pool_dev || !page_indptr_dev || !page_indices_dev || !kept_dev ||
+      !new_lens_dev || !dst_indptr_dev != !dst_indices_dev || k_pool_dev == v_pool_dev)
+    return HPA_ERR_INVALID;
+  if (kv_dtype != HPA_KV_BF16 && kv_dtype != HPA_KV_E4M3) return HPA_ERR_INVALID;
+  if (B < 1 || B > kMaxB || Hkv < 1 || Hkv > 65535 || num_pages < 1 || kept_stride < 1)
+    return HPA_ERR_INVALID;
+  if (d != hpa::HEAD_DIM || page_size != hpa::PAGE || int64_t(B) * Hkv > INT_MAX)
+    return HPA_ERR_UNSUPPORTED;
+  if (!aligned(k_pool_dev, 16) || !aligned(v_pool_dev, 16) || !aligned(acc_dev, 4) ||
+      (status_dev && !aligned(status_dev, 4)))
+    return HPA_ERR_ALIGN;
+  if (dst_indptr_dev == page_indptr_dev && dst_indices_dev == page_indices_dev)
+    dst_indptr_dev = dst_indices_dev = nullptr;  // the request's own pages: in place
+  hpa::CompactParams p;
+  p.k_pool = k_pool_dev;
+  p.v_pool = v_pool_dev;
+  p.acc = acc_dev;
+  p.page_indptr = page_indptr_dev;
+  p.page_indices = page_indices_dev;
+  p.dst_indptr = dst_indptr_dev;
+  p.dst_indices = dst_indices_dev;
+  p.num_pages = num_pages;
+  p.kept = kept_dev;
+  p.new_lens = new_lens_dev;
+  p.kept_stride = kept_stride;
+  p.B = B;
+  p.Hkv = Hkv;
+  p.row_bytes = d * (kv_dtype == HPA_KV_BF16 ? 2 : 1);
+  p.status = status_dev;
+  cudaError_t e = hpa::launch_evict_compact(p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? HPA_OK : cuda_fail(e);
 }
 

@@ -17,8 +17,9 @@ namespace hpa {
 // ----------------------------------------------------------------------------- task map
 enum : int {
   TM_T = 0, TM_BASE, TM_REM, TM_C, TM_B, TM_S, TM_STATUS, TM_TILE, TM_KIND, TM_SPLITS,
-  TM_SCAP, TM_HEADER_WORDS = 16
+  TM_SCAP, TM_WINDOW, TM_SINKS, TM_QLEN, TM_HEADER_WORDS = 16
 };
+constexpr int KIND_WINDOW = 3;  // the map kind of hpa_plan_window
 
 struct TaskMapLayout {
   int64_t lens, cu_tiles, cta_begin, cta_seg, seg_off, segs;  // word offsets
@@ -40,6 +41,31 @@ constexpr int HEAD_DIM = 128;  // d
 constexpr int MAX_ROWS = 16;   // query rows per CTA (one m16 MMA tile)
 constexpr int MAX_ROWS_TOTAL = 64;  // G * q_len rows per KV head, in groups of 16
 
+// The pages of one request that a sliding window of `window` keys with `sinks` first
+// keys reaches, as a shorter "compact" sequence of pages: the pages holding sinks, then
+// the pages from the first key of token 0's window on; the `hidden` pages between them
+// are left out.  Compact page v is real page v (v < sink_pages) or v + hidden.  Requires
+// L >= q_len >= 1, window >= 1, sinks >= 0 (then nothing here overflows).
+struct WinSpan {
+  int start;       // token j's window starts at start + j (negative: before the first key)
+  int low;         // first key of token 0's window: start, or 0
+  int sink_pages;  // pages before the gap
+  int hidden;      // pages in the gap
+  int L;           // compact length in keys: the real one less the gap
+  __host__ __device__ static WinSpan make(int L, int q_len, int window, int sinks) {
+    WinSpan w;
+    w.start = L - q_len + 1 - window;
+    w.low = w.start > 0 ? w.start : 0;
+    const int ns = sinks < w.low ? sinks : w.low;
+    w.sink_pages = ns / PAGE + (ns % PAGE != 0);
+    const int gap = w.low / PAGE - w.sink_pages;
+    w.hidden = gap > 0 ? gap : 0;
+    w.L = L - PAGE * w.hidden;
+    return w;
+  }
+  __host__ __device__ int real_page(int v) const { return v < sink_pages ? v : v + hidden; }
+};
+
 // ----------------------------------------------------------------------------- launch blocks
 struct AttnParams {
   const __nv_bfloat16 *q;
@@ -55,6 +81,7 @@ struct AttnParams {
   TaskMapLayout lay;
   int B, C, q_len, Hq, Hkv, G, rows;
   int heads_per_cta;  // KV heads one CTA walks per segment: 1 (grid over heads) or Hkv
+  bool window;        // the map is one of hpa_plan_window
   float scale_log2;   // sm_scale * log2(e)
 };
 
@@ -65,8 +92,11 @@ int last_cuda_error();
 
 constexpr size_t kPlanStageLimit = 40 * 1024;  // shared memory the plan kernel may stage in
 size_t plan_stage_bytes(int B, int C, int kind);
+struct PlanWindow {
+  int window, sinks, q_len;  // hpa_plan_window (kind 3); zeros otherwise
+};
 cudaError_t launch_plan(const int32_t *seq_lens, int B, int tile, int C, int kind, int splits,
-                        int32_t *tm, int64_t s_cap, cudaStream_t s);
+                        int32_t *tm, int64_t s_cap, cudaStream_t s, PlanWindow win = {0, 0, 0});
 cudaError_t launch_combine(const float *po, const float *plse, int32_t *tm, int B, int C,
                            int q_len, int Hq, __nv_bfloat16 *out, float *out_lse,
                            cudaStream_t s);
@@ -77,6 +107,46 @@ cudaError_t launch_decode_attn_tc(const AttnParams &p, const CUtensorMap &tmk,
                                   const CUtensorMap &tmv, int kv_dtype, cudaStream_t s);
 int attn_tc_ctas_per_sm(int kv_dtype, int rows, int *ctas);  // occupancy query (host)
 cudaError_t launch_selftest_wait(int32_t *status, long long limit_ns, cudaStream_t s);
+
+struct KeyWeightsParams {
+  const __nv_bfloat16 *q;
+  const float *lse;
+  int32_t *tm;
+  const int32_t *page_indptr, *page_indices;
+  const float *k_scale;
+  const float *acc_in;  // nullptr: the sums start from zero
+  float *acc_out;
+  int64_t num_pages;
+  TaskMapLayout lay;
+  int B, C, q_len, Hq, Hkv, G, rows;
+  float scale_log2, decay;
+};
+cudaError_t launch_key_weights(const KeyWeightsParams &p, const CUtensorMap &tmk, int kv_dtype,
+                               cudaStream_t s);
+
+struct EvictParams {
+  const float *acc;
+  const int32_t *seq_lens, *page_indptr, *page_indices, *budgets;
+  int64_t num_pages;
+  int sinks, recent, B, Hkv;
+  int32_t *kept;
+  int64_t kept_stride;
+  int32_t *new_lens;
+  int32_t *status;
+};
+cudaError_t launch_evict_select(const EvictParams &p, cudaStream_t s);
+
+struct CompactParams {
+  void *k_pool, *v_pool;
+  float *acc;  // optional
+  const int32_t *page_indptr, *page_indices, *dst_indptr, *dst_indices;
+  int64_t num_pages;
+  const int32_t *kept, *new_lens;
+  int64_t kept_stride;
+  int B, Hkv, row_bytes;  // bytes of one K (or V) row
+  int32_t *status;
+};
+cudaError_t launch_evict_compact(const CompactParams &p, cudaStream_t s);
 
 struct StoreKvParams {
   const __nv_bfloat16 *k_new, *v_new;
@@ -91,6 +161,7 @@ struct StoreKvParams {
   void *k_pool, *v_pool;
   int B, q_len, Hkv;
   int32_t *status;
+  const int32_t *text_pos;  // hpa_store_kv_at: text position of each request's first new token
 };
 cudaError_t launch_store_kv(const StoreKvParams &p, cudaStream_t s);
 
@@ -189,6 +260,17 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, 
       : "memory");
 }
 
+// Untiled bulk copy global -> shared, counted on `bar`; both ends 16-byte aligned, bytes a
+// multiple of 16.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -214,6 +296,10 @@ __device__ __forceinline__ void lds128(uint32_t addr, uint32_t &a, uint32_t &b, 
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
                : "r"(addr));
+}
+
+__device__ __forceinline__ void lds64(uint32_t addr, uint32_t &a, uint32_t &b) {
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
 }
 
 // D += A(16x16, row) * B(16x8, col); bf16 inputs, fp32 accumulate.
@@ -295,6 +381,14 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return d;
 }
 
+// e such that amax * 2^e lies in [2^14, 2^15) (0 for a zero row), clamped so that
+// both 2^e and 2^-e are fp32 normals.
+__device__ __forceinline__ int f16_row_exponent(float amax) {
+  if (!(amax > 0.f)) return 0;
+  const int ea = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127;  // floor(log2)
+  return 14 - min(max(ea, -112), 126);
+}
+
 // 2^k for an integer k in [-126, 127], built from the exponent bits (exact).
 __device__ __forceinline__ float exp2i(int k) {
   return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
@@ -323,17 +417,24 @@ __device__ __forceinline__ void status_or(int32_t *tm, int bits) {
 // `report` is set and read as an empty segment of request 0, so no kernel follows
 // an index out of the buffers the map was sized for.  Every reader of a row gets
 // the same answer, so the roles of one CTA stay in step.
+// With WIN (a map of hpa_plan_window, whose header holds q_len, the window and the sinks)
+// the range is in keys of the request's compact pages (WinSpan).
 struct SegRow {
   int r, L, klo, khi;  // request, its length, key range [klo, khi)
 };
+template <bool WIN = false>
 __device__ __forceinline__ SegRow read_seg_row(int32_t *tm, const TaskMapLayout &lay, int B,
                                                int s, int c, int tile, bool report) {
   const int4 sg = reinterpret_cast<const int4 *>(tm + lay.segs)[s];
   if (sg.x >= 0 && sg.x < B && sg.w == c && sg.y >= 0 && sg.y < sg.z) {
     const int L = tm[lay.lens + sg.x];
-    if (L >= 1 && sg.z <= (L - 1) / tile + 1) {
-      const long long hi = static_cast<long long>(sg.z) * tile;
-      return SegRow{sg.x, L, sg.y * tile, hi < L ? static_cast<int>(hi) : L};
+    if (L >= (WIN ? tm[TM_QLEN] : 1)) {
+      const int span =
+          WIN ? WinSpan::make(L, tm[TM_QLEN], tm[TM_WINDOW], tm[TM_SINKS]).L : L;
+      if (sg.z <= (span - 1) / tile + 1) {
+        const long long hi = static_cast<long long>(sg.z) * tile;
+        return SegRow{sg.x, L, sg.y * tile, hi < span ? static_cast<int>(hi) : span};
+      }
     }
   }
   if (report) status_or(tm, HPA_STATUS_BAD_MAP);
@@ -342,14 +443,18 @@ __device__ __forceinline__ SegRow read_seg_row(int32_t *tm, const TaskMapLayout 
 
 // Header checks an attention kernel makes before it walks partition c: the map's
 // kind and segment capacity match what hpa_plan / hpa_plan_static build for (B, C),
-// and c's segment range lies inside the map's S segments.
+// and c's segment range lies inside the map's S segments.  WIN asks for a map of
+// hpa_plan_window instead, with its window, sinks and q_len in range.
+template <bool WIN = false>
 __device__ __forceinline__ bool map_ranges_ok(const int32_t *tm, const TaskMapLayout &lay, int B,
                                               int C, int c) {
   const int kind = tm[TM_KIND], S = tm[TM_S];
   const int cap = kind == 1 ? C : B + C - 1;
   const int sb = tm[lay.cta_seg + c], se = tm[lay.cta_seg + c + 1];
-  return kind >= 0 && kind <= 2 && tm[TM_SCAP] == cap && S >= 0 && S <= cap && sb >= 0 &&
-         sb <= se && se <= S;
+  const bool kind_ok = WIN ? kind == KIND_WINDOW && tm[TM_WINDOW] >= 1 && tm[TM_SINKS] >= 0 &&
+                                 tm[TM_QLEN] >= 1
+                           : kind >= 0 && kind <= 2;
+  return kind_ok && tm[TM_SCAP] == cap && S >= 0 && S <= cap && sb >= 0 && sb <= se && se <= S;
 }
 
 }  // namespace hpa

@@ -14,6 +14,9 @@
 //   stream, with budgets in keys: tile t (keys P_t before it, w_t in it) goes
 //   to partition floor(C (2 P_t + w_t) / (2 K)), K the total key count, so a
 //   partial last tile weighs its fill.
+// Window map (kind 3): the dynamic map over each request's compact pages, those that
+//   a sliding window with sink tokens reaches (WinSpan), so the budget counts the keys
+//   that are read and not the length; the header keeps window, sinks and q_len.
 #include <climits>
 
 #include "hpa_internal.cuh"
@@ -67,7 +70,8 @@ template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *__restrict__ lens_in,
                                                             int B, int tile, int C, int kind,
                                                             int splits, int32_t *tm,
-                                                            long long s_cap, int staged) {
+                                                            long long s_cap, int staged,
+                                                            PlanWindow win) {
   // Let the attention kernel that follows start its prologue now; it waits for
   // this grid's completion before it reads the map.
   pdl_launch_dependents();
@@ -100,8 +104,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *__res
     if (i < B) {
       const int L = lens_in[i];
       lens[i] = L;
-      if (L < 1) atomicOr(&s_bad, HPA_STATUS_BAD_SEQLEN);
-      else n = (L - 1) / tile + 1, keys = L;
+      const int need = kind == KIND_WINDOW ? win.q_len : 1;
+      if (L < need) {
+        atomicOr(&s_bad, HPA_STATUS_BAD_SEQLEN);
+      } else {
+        keys = kind == KIND_WINDOW ? WinSpan::make(L, win.q_len, win.window, win.sinks).L : L;
+        n = (keys - 1) / tile + 1;
+      }
     }
     const long long incl = block_scan<kPlanThreads>(n, wbuf, total);
     if (i < B) cu[i + 1] = cu_g[i + 1] = static_cast<int32_t>(carry + incl);
@@ -131,6 +140,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *__res
       tm[TM_SPLITS] = splits;
       tm[TM_SCAP] = static_cast<int32_t>(s_cap);
       tm[TM_STATUS] = bad;
+      if (kind == KIND_WINDOW) {
+        tm[TM_WINDOW] = win.window;
+        tm[TM_SINKS] = win.sinks;
+        tm[TM_QLEN] = win.q_len;
+      }
     }
     return;
   }
@@ -139,7 +153,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *__res
   const long long tbase = T / C, trem = T % C;
   for (int c = tid; c < C; c += kPlanThreads) {
     long long begin;
-    if (kind == 0) {
+    if (kind == 0 || kind == KIND_WINDOW) {
       begin = c * tbase + (c < trem ? c : trem);
     } else if (kind == 2) {
       // first tile whose doubled middle key 2 P_t + w_t reaches X = ceil(2 K c / C)
@@ -230,8 +244,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *__res
       tm[TM_BASE] = static_cast<int32_t>(kb > INT_MAX ? INT_MAX : kb);
       tm[TM_REM] = static_cast<int32_t>(kcarry % C);
     } else {
-      tm[TM_BASE] = kind == 0 ? static_cast<int32_t>(tbase) : -1;
-      tm[TM_REM] = kind == 0 ? static_cast<int32_t>(trem) : -1;
+      tm[TM_BASE] = kind != 1 ? static_cast<int32_t>(tbase) : -1;
+      tm[TM_REM] = kind != 1 ? static_cast<int32_t>(trem) : -1;
+    }
+    if (kind == KIND_WINDOW) {
+      tm[TM_WINDOW] = win.window;
+      tm[TM_SINKS] = win.sinks;
+      tm[TM_QLEN] = win.q_len;
     }
     tm[TM_C] = C;
     tm[TM_B] = B;
@@ -253,7 +272,7 @@ size_t plan_stage_bytes(int B, int C, int kind) {
 }
 
 cudaError_t launch_plan(const int32_t *seq_lens, int B, int tile, int C, int kind, int splits,
-                        int32_t *tm, int64_t s_cap, cudaStream_t s) {
+                        int32_t *tm, int64_t s_cap, cudaStream_t s, PlanWindow win) {
   // cu_tiles and cta_begin (and the key prefix) are staged in shared memory when
   // they fit in 40 KB; the token-weighted map requires it (checked by the caller)
   const size_t stage_bytes = plan_stage_bytes(B, C, kind);
@@ -275,21 +294,21 @@ cudaError_t launch_plan(const int32_t *seq_lens, int B, int tile, int C, int kin
   if (need <= 32) {
     cfg.blockDim = dim3(32);
     return cudaLaunchKernelEx(&cfg, plan_kernel<32>, lens, B, tile, C, kind, splits, tm,
-                              static_cast<long long>(s_cap), staged);
+                              static_cast<long long>(s_cap), staged, win);
   }
   if (need <= 128) {
     cfg.blockDim = dim3(128);
     return cudaLaunchKernelEx(&cfg, plan_kernel<128>, lens, B, tile, C, kind, splits, tm,
-                              static_cast<long long>(s_cap), staged);
+                              static_cast<long long>(s_cap), staged, win);
   }
   if (need <= 256) {
     cfg.blockDim = dim3(256);
     return cudaLaunchKernelEx(&cfg, plan_kernel<256>, lens, B, tile, C, kind, splits, tm,
-                              static_cast<long long>(s_cap), staged);
+                              static_cast<long long>(s_cap), staged, win);
   }
   cfg.blockDim = dim3(1024);
   return cudaLaunchKernelEx(&cfg, plan_kernel<1024>, lens, B, tile, C, kind, splits, tm,
-                            static_cast<long long>(s_cap), staged);
+                            static_cast<long long>(s_cap), staged, win);
 }
 
 }  // namespace hpa

@@ -222,24 +222,33 @@ __device__ __forceinline__ void fetch_item(const Item &x, const __nv_bfloat16 *k
 
 // Where an item's token goes: its position, its page (or -1) and whether both are
 // valid; looked up one item ahead, when the item's rows are fetched.
+// With AT (hpa_store_kv_at) the row of the cos/sin table goes by the token's position in
+// the text, which an eviction leaves ahead of its position in the cache.
 struct Place {
-  int pos, page;
+  int pos, page, text;
   bool good;
 };
 
+template <bool AT>
 __device__ __forceinline__ Place look_up(const Item &x, const int32_t *seq_lens,
                                          const int32_t *page_indptr,
                                          const int32_t *page_indices, int64_t num_pages,
-                                         int max_pos, int q_len) {
+                                         int max_pos, int q_len, const int32_t *text_pos) {
   Place pl;
   const int r = x.r, j = x.j;
   pl.pos = seq_lens[r] - q_len + j;
+  pl.text = pl.pos;
+  if (AT) {  // a sum past INT_MAX is out of the table as well
+    const int t0 = text_pos[r];
+    pl.text = t0 < max_pos - j ? t0 + j : max_pos;
+  }
   pl.page = -1;
-  if (pl.pos >= 0 && pl.pos < max_pos) {
+  const bool in_range = pl.pos >= 0 && pl.text >= 0 && pl.text < max_pos;
+  if (in_range) {
     const int pi = page_indptr[r] + pl.pos / PAGE;
     pl.page = pi < page_indptr[r + 1] ? page_indices[pi] : -1;
   }
-  pl.good = pl.pos >= 0 && pl.pos < max_pos && pl.page >= 0 && pl.page < num_pages;
+  pl.good = in_range && pl.page >= 0 && pl.page < num_pages;
   return pl;
 }
 
@@ -248,11 +257,12 @@ __device__ __forceinline__ void fetch_cos_sin(const Place &pl, const float *cos_
                                               uint32_t slot, int lane) {
   if (pl.good)
     cp_async16(slot + kCosOff + 16 * lane,
-               cos_sin + static_cast<int64_t>(pl.pos) * HEAD_DIM + 4 * lane);
+               cos_sin + static_cast<int64_t>(pl.text) * HEAD_DIM + 4 * lane);
 }
 
 // Warps walk the items grid-stride; each holds its next item's rows in flight
 // (one cp.async group) while it works on the current one.
+template <bool AT>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     store_kv_kernel(const __nv_bfloat16 *__restrict__ k_new,
                     const __nv_bfloat16 *__restrict__ v_new, const int32_t *__restrict__ seq_lens,
@@ -262,7 +272,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
                     const float *__restrict__ norm_w, float eps, int use_hadamard, int kv_dtype,
                     const float *__restrict__ k_scale, const float *__restrict__ v_scale,
                     void *k_pool, void *v_pool, int B, int q_len, int Hkv,
-                    int32_t *__restrict__ status) {
+                    int32_t *__restrict__ status, const int32_t *__restrict__ text_pos) {
   extern __shared__ __align__(16) uint8_t kv_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int k = lane % kLanesPerHead, hp = lane / kLanesPerHead;
@@ -301,7 +311,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   walk.d_r = walk.d_rj / q_len;
   walk.d_j = static_cast<int>(walk.d_rj - walk.d_r * q_len);
   Item cur = walk.first(it);
-  Place here = look_up(cur, seq_lens, page_indptr, page_indices, num_pages, max_pos, q_len);
+  Place here =
+      look_up<AT>(cur, seq_lens, page_indptr, page_indices, num_pages, max_pos, q_len, text_pos);
   fetch_item(cur, k_new, v_new, Hkv, slots, lane);
   fetch_cos_sin(here, cos_sin, slots, lane);
   cp_async_commit();
@@ -315,7 +326,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       nxt = walk.next(cur);
       const uint32_t other = slots + (buf ^ 1) * kSlotBytes;
       fetch_item(nxt, k_new, v_new, Hkv, other, lane);
-      there = look_up(nxt, seq_lens, page_indptr, page_indices, num_pages, max_pos, q_len);
+      there = look_up<AT>(nxt, seq_lens, page_indptr, page_indices, num_pages, max_pos, q_len,
+                          text_pos);
       fetch_cos_sin(there, cos_sin, other, lane);
     }
     cp_async_commit();
@@ -324,8 +336,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     const int pos = here.pos, page = here.page;
     const bool good = here.good;
     if (lane == 0 && status && cur.hc == 0 && !good)
-      atomicOr(reinterpret_cast<int *>(status), pos < 0 || pos >= max_pos ? HPA_STATUS_BAD_SEQLEN
-                                                                         : HPA_STATUS_BAD_PAGE);
+      atomicOr(reinterpret_cast<int *>(status), pos < 0 || here.text < 0 || here.text >= max_pos
+                                                    ? HPA_STATUS_BAD_SEQLEN
+                                                    : HPA_STATUS_BAD_PAGE);
     cp_async_wait_1();  // this item's group has landed (the next one may still fly)
     __syncwarp();
     const uint32_t slot = slots + buf * kSlotBytes;
@@ -387,21 +400,24 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 
 }  // namespace
 
-cudaError_t launch_store_kv(const StoreKvParams &p, cudaStream_t s) {
+namespace {
+
+template <bool AT>
+cudaError_t launch_store(const StoreKvParams &p, cudaStream_t s) {
   static int configured[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   constexpr int kSmem = kWarps * kWarpSmem;  // 72 KB: two 4.5 KB slots per warp
   if (dev < 64 && !configured[dev]) {
-    e = cudaFuncSetAttribute(store_kv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(store_kv_kernel<AT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     configured[dev] = 1;
   }
   int sms = 0, per_sm = 0;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess)
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, store_kv_kernel, kWarps * 32, kSmem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, store_kv_kernel<AT>, kWarps * 32, kSmem);
   if (e != cudaSuccess) return e;
   // one resident wave of warps that walk the items grid-stride
   const int64_t n_items = static_cast<int64_t>(p.B) * p.q_len *
@@ -409,11 +425,17 @@ cudaError_t launch_store_kv(const StoreKvParams &p, cudaStream_t s) {
   const int64_t want = (n_items + kWarps - 1) / kWarps;
   const int64_t wave = static_cast<int64_t>(sms) * (per_sm > 0 ? per_sm : 1);
   const unsigned blocks = static_cast<unsigned>(want < wave ? want : wave);
-  store_kv_kernel<<<blocks, kWarps * 32, kSmem, s>>>(
+  store_kv_kernel<AT><<<blocks, kWarps * 32, kSmem, s>>>(
       p.k_new, p.v_new, p.seq_lens, p.page_indptr, p.page_indices, p.num_pages, p.cos_sin,
       p.max_pos, p.norm_w, p.eps, p.use_hadamard, p.kv_dtype, p.k_scale, p.v_scale, p.k_pool,
-      p.v_pool, p.B, p.q_len, p.Hkv, p.status);
+      p.v_pool, p.B, p.q_len, p.Hkv, p.status, p.text_pos);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_store_kv(const StoreKvParams &p, cudaStream_t s) {
+  return p.text_pos ? launch_store<true>(p, s) : launch_store<false>(p, s);
 }
 
 }  // namespace hpa

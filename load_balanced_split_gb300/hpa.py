@@ -19,7 +19,7 @@ from . import build as _build
 
 KV_BF16, KV_E4M3 = 0, 1
 STATUS_BITS = {1: "BAD_SEQLEN", 2: "MISMATCH", 4: "BAD_PAGE", 8: "TIMEOUT", 16: "OVERFLOW",
-               32: "BAD_MAP"}
+               32: "BAD_MAP", 64: "BAD_BUDGET"}
 HEADER_WORDS = 16
 
 _lock = threading.Lock()
@@ -77,6 +77,18 @@ def lib():
                                                     ctypes.c_int),
                 "hpa_store_kv": ([P, P, P, P, P, I64, I32, P, I32, P, F, I32, I32, P, P, P, P,
                                   I32, I32, I32, I32, P, P], ctypes.c_int),
+                "hpa_plan_window": ([P, I32, I32, I32, I32, I32, I32, P, SZ, P], ctypes.c_int),
+                "hpa_decode_attn_window": ([P, P, P, I32, P, P, I64, P, P, I32, I32, I32, I32,
+                                            I32, I32, F, P, I32, P, P, P], ctypes.c_int),
+                "hpa_default_num_ctas_window": ([I32, I32, I32, I32], I32),
+                "hpa_store_kv_at": ([P, P, P, P, P, P, I64, I32, P, I32, P, F, I32, I32, P, P, P,
+                                     P, I32, I32, I32, I32, P, P], ctypes.c_int),
+                "hpa_key_weights": ([P, P, P, I32, P, I64, P, P, I32, I32, I32, I32, I32, I32, F,
+                                     F, P, I32, P, P, P], ctypes.c_int),
+                "hpa_evict_select": ([P, P, P, P, I64, I32, P, I32, I32, I32, I32, P, I64, P, P,
+                                      P], ctypes.c_int),
+                "hpa_evict_compact": ([P, P, I32, P, I64, P, P, P, P, I32, P, I64, P, I32, I32,
+                                       I32, P, P], ctypes.c_int),
                 "hpa_error_string": ([ctypes.c_int], ctypes.c_char_p),
                 "hpa_last_cuda_error": ([], ctypes.c_int),
             }
@@ -163,6 +175,14 @@ def hpa_default_num_ctas_allheads(Hkv: int, q_len: int, kv_dtype: int, Hq: int =
     return c
 
 
+def hpa_default_num_ctas_window(Hkv: int, q_len: int, kv_dtype: int, Hq: int = 64) -> int:
+    c = int(lib().hpa_default_num_ctas_window(Hq, Hkv, q_len, kv_dtype))
+    if c <= 0:
+        raise HpaError("hpa_default_num_ctas_window failed (cudaError %d)" %
+                       lib().hpa_last_cuda_error())
+    return c
+
+
 # ----------------------------------------------------------------------------- the three calls
 def hpa_plan(seq_lens, tile: int, num_ctas: int, taskmap, stream=None):
     _dev(seq_lens, "seq_lens", torch.int32)
@@ -185,6 +205,18 @@ def hpa_plan_static(seq_lens, tile: int, splits: int, taskmap, stream=None):
     _check(lib().hpa_plan_static(_ptr(seq_lens), seq_lens.numel(), tile, splits, _ptr(taskmap),
                                  taskmap.numel() * taskmap.element_size(), _stream(stream)),
            "hpa_plan_static")
+
+
+def hpa_plan_window(seq_lens, q_len: int, window: int, sinks: int, tile: int, num_ctas: int,
+                    taskmap, stream=None):
+    """The plan for hpa_decode_attn_window: token at position a sees key i <= a when
+    i > a - window or i < sinks."""
+    _dev(seq_lens, "seq_lens", torch.int32)
+    _dev(taskmap, "taskmap")
+    _check(lib().hpa_plan_window(_ptr(seq_lens), seq_lens.numel(), q_len, window, sinks, tile,
+                                 num_ctas, _ptr(taskmap),
+                                 taskmap.numel() * taskmap.element_size(), _stream(stream)),
+           "hpa_plan_window")
 
 
 def _attn_args(q, k_pool, v_pool, page_indptr, page_indices, taskmap, k_scale, v_scale):
@@ -238,18 +270,19 @@ def _outputs(out, out_lse, B, q_len, Hq, d):
 def hpa_decode_attn(q, k_pool, v_pool, page_indptr, page_indices, taskmap, num_ctas: int,
                     partial_o, partial_lse, k_scale=None, v_scale=None,
                     sm_scale: float | None = None, stream=None, tc: bool = False,
-                    mma: bool = False):
+                    mma: bool = False, window: bool = False):
     """q bf16 [B][q_len][Hq][d]; k/v pools bf16 or uint8 (E4M3) [P][Hkv][page][d].
 
     hpa_decode_attn picks the kernel by query rows per KV head (mma.sync up to 16,
-    tcgen05 above); tc=True calls hpa_decode_attn_tc and mma=True hpa_decode_attn_mma
-    with the same arguments."""
+    tcgen05 above); tc=True calls hpa_decode_attn_tc, mma=True hpa_decode_attn_mma and
+    window=True hpa_decode_attn_window with the same arguments."""
     kv, B, q_len, Hq, d, P, Hkv, page = _attn_args(q, k_pool, v_pool, page_indptr,
                                                    page_indices, taskmap, k_scale, v_scale)
     _partials(partial_o, partial_lse, B, num_ctas, q_len, Hq, d)
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(d)
-    name = "hpa_decode_attn_tc" if tc else "hpa_decode_attn_mma" if mma else "hpa_decode_attn"
+    name = ("hpa_decode_attn_tc" if tc else "hpa_decode_attn_mma" if mma else
+            "hpa_decode_attn_window" if window else "hpa_decode_attn")
     _check(getattr(lib(), name)(
         _ptr(q), _ptr(k_pool), _ptr(v_pool), kv, _ptr(k_scale), _ptr(v_scale), P,
         _ptr(page_indptr), _ptr(page_indices), page, B, q_len, Hq, Hkv, d, float(sm_scale),
@@ -270,6 +303,14 @@ def hpa_decode_attn_tc(q, k_pool, v_pool, page_indptr, page_indices, taskmap, nu
     """hpa_decode_attn computed on the tcgen05 tensor cores (one pass for up to 64 rows)."""
     hpa_decode_attn(q, k_pool, v_pool, page_indptr, page_indices, taskmap, num_ctas, partial_o,
                     partial_lse, k_scale, v_scale, sm_scale, stream, tc=True)
+
+
+def hpa_decode_attn_window(q, k_pool, v_pool, page_indptr, page_indices, taskmap, num_ctas: int,
+                           partial_o, partial_lse, k_scale=None, v_scale=None,
+                           sm_scale: float | None = None, stream=None):
+    """hpa_decode_attn over a map of hpa_plan_window (sliding window and sink tokens)."""
+    hpa_decode_attn(q, k_pool, v_pool, page_indptr, page_indices, taskmap, num_ctas, partial_o,
+                    partial_lse, k_scale, v_scale, sm_scale, stream, window=True)
 
 
 def hpa_decode_attn_allheads(q, k_pool, v_pool, page_indptr, page_indices, taskmap,
@@ -416,13 +457,8 @@ def hpa_decode_attn_combine_noalloc(q, k_pool, v_pool, page_indptr, page_indices
         "hpa_decode_attn_combine_noalloc")
 
 
-def hpa_store_kv(k_new, v_new, seq_lens, page_indptr, page_indices, cos_sin, norm_w, k_pool,
-                 v_pool, eps: float = 1e-6, use_hadamard: bool = True, k_scale=None,
-                 v_scale=None, status=None, stream=None):
-    """Fused RoPE + RMSNorm + Hadamard + quantise + paged store of the new tokens' K/V.
-
-    k_new, v_new: bf16 [B][q_len][Hkv][d]; cos_sin: fp32 [max_pos][d]; norm_w: fp32 [d];
-    pools: bf16 or uint8 (E4M3) [P][Hkv][page][d] (E4M3 needs k_scale / v_scale)."""
+def _store_kv(name, k_new, v_new, seq_lens, text_pos, page_indptr, page_indices, cos_sin, norm_w,
+              k_pool, v_pool, eps, use_hadamard, k_scale, v_scale, status, stream):
     for t, n in ((k_new, "k_new"), (v_new, "v_new")):
         _dev(t, n, torch.bfloat16)
     _dev(cos_sin, "cos_sin", torch.float32)
@@ -437,11 +473,183 @@ def hpa_store_kv(k_new, v_new, seq_lens, page_indptr, page_indices, cos_sin, nor
     P, Hkv2, page, _ = k_pool.shape
     if Hkv2 != Hkv:
         raise HpaError("KV head count mismatch")
-    _check(lib().hpa_store_kv(
-        _ptr(k_new), _ptr(v_new), _ptr(seq_lens), _ptr(page_indptr), _ptr(page_indices), P,
+    at = ()
+    if name == "hpa_store_kv_at":
+        _dev(text_pos, "text_pos", torch.int32)
+        if text_pos.numel() != B or seq_lens.numel() != B:
+            raise HpaError("text_pos and seq_lens need one value per request")
+        at = (_ptr(text_pos),)
+    _check(getattr(lib(), name)(
+        _ptr(k_new), _ptr(v_new), _ptr(seq_lens), *at, _ptr(page_indptr), _ptr(page_indices), P,
         page, _ptr(cos_sin), cos_sin.shape[0], _ptr(norm_w), float(eps), int(use_hadamard), kv,
         _ptr(k_scale), _ptr(v_scale), _ptr(k_pool), _ptr(v_pool), B, q_len, Hkv, d,
-        _ptr(status), _stream(stream)), "hpa_store_kv")
+        _ptr(status), _stream(stream)), name)
+
+
+def hpa_store_kv(k_new, v_new, seq_lens, page_indptr, page_indices, cos_sin, norm_w, k_pool,
+                 v_pool, eps: float = 1e-6, use_hadamard: bool = True, k_scale=None,
+                 v_scale=None, status=None, stream=None):
+    """Fused RoPE + RMSNorm + Hadamard + quantise + paged store of the new tokens' K/V.
+
+    k_new, v_new: bf16 [B][q_len][Hkv][d]; cos_sin: fp32 [max_pos][d]; norm_w: fp32 [d];
+    pools: bf16 or uint8 (E4M3) [P][Hkv][page][d] (E4M3 needs k_scale / v_scale)."""
+    _store_kv("hpa_store_kv", k_new, v_new, seq_lens, None, page_indptr, page_indices, cos_sin,
+              norm_w, k_pool, v_pool, eps, use_hadamard, k_scale, v_scale, status, stream)
+
+
+def hpa_store_kv_at(k_new, v_new, seq_lens, text_pos, page_indptr, page_indices, cos_sin, norm_w,
+                    k_pool, v_pool, eps: float = 1e-6, use_hadamard: bool = True, k_scale=None,
+                    v_scale=None, status=None, stream=None):
+    """hpa_store_kv for a cache that evicts: seq_lens place the new tokens in the cache, and
+    text_pos (int32 [B], the text position of each request's first new token) rotates them."""
+    _store_kv("hpa_store_kv_at", k_new, v_new, seq_lens, text_pos, page_indptr, page_indices,
+              cos_sin, norm_w, k_pool, v_pool, eps, use_hadamard, k_scale, v_scale, status, stream)
+
+
+# ----------------------------------------------------------------------------- bounded cache
+def _one_device(*tensors):
+    """The library launches on the current device: every tensor has to live there."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != here:
+            raise HpaError("tensors must be on the current device (cuda:%d), got %s" %
+                           (here, t.device))
+
+
+def _acc_pool(t, name, k_pool):
+    _dev(t, name, torch.float32)
+    if tuple(t.shape) != tuple(k_pool.shape[:3]):
+        raise HpaError("%s must have shape %s, one weight per cached key, got %s" %
+                       (name, tuple(k_pool.shape[:3]), tuple(t.shape)))
+
+
+def _page_table(indptr, indices, B, what="page"):
+    _dev(indptr, what + "_indptr", torch.int32)
+    _dev(indices, what + "_indices", torch.int32)
+    if indptr.numel() != B + 1:
+        raise HpaError("%s_indptr must have B + 1 = %d entries" % (what, B + 1))
+
+
+def hpa_key_weights(q, lse, k_pool, page_indptr, page_indices, taskmap, num_ctas: int, acc,
+                    out=None, k_scale=None, decay: float = 1.0, sm_scale: float | None = None,
+                    stream=None):
+    """Adds one attention step's weights to the accumulators of the cached keys.
+
+    lse: the step's out_lse, fp32 [B][q_len][Hq]; acc: fp32 [P][Hkv][page], updated in
+    place, or read only when `out` (same shape) is given, or None for zero (then `out` is
+    required); taskmap: the map of the attention step (any plan, window maps included)."""
+    _dev(q, "q", torch.bfloat16)
+    if q.dim() != 4 or k_pool.dim() != 4:
+        raise HpaError("q must be [B][q_len][Hq][d] and the pool [P][Hkv][page][d]")
+    _dev(k_pool, "k_pool")
+    B, q_len, Hq, d = q.shape
+    P, Hkv, page, d2 = k_pool.shape
+    if d2 != d:
+        raise HpaError("head dim mismatch")
+    if k_pool.dtype == torch.bfloat16:
+        kv = KV_BF16
+    elif k_pool.dtype in (torch.uint8, torch.float8_e4m3fn):
+        kv = KV_E4M3
+        _dev(k_scale, "k_scale", torch.float32)
+        if k_scale.numel() < Hkv:
+            raise HpaError("k_scale needs one fp32 value per KV head")
+    else:
+        raise HpaError("unsupported KV dtype %s" % k_pool.dtype)
+    _dev(lse, "lse", torch.float32)
+    if tuple(lse.shape) != (B, q_len, Hq):
+        raise HpaError("lse must have shape %s" % ((B, q_len, Hq),))
+    out = acc if out is None else out
+    for t, n in ((acc, "acc"), (out, "out")):
+        if t is not None or n == "out":
+            _acc_pool(t, n, k_pool)
+    _page_table(page_indptr, page_indices, B)
+    _dev(taskmap, "taskmap")
+    # a static map holds num_ctas segment rows of 16 bytes, the others B + num_ctas - 1
+    if taskmap.numel() * taskmap.element_size() < hpa_taskmap_bytes(B, num_ctas) - 16 * (B - 1):
+        raise HpaError("taskmap is too small for %d requests over %d partitions" % (B, num_ctas))
+    _one_device(q, lse, k_pool, k_scale, acc, out, page_indptr, page_indices, taskmap)
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(d)
+    _check(lib().hpa_key_weights(
+        _ptr(q), _ptr(lse), _ptr(k_pool), kv, _ptr(k_scale), P, _ptr(page_indptr),
+        _ptr(page_indices), page, B, q_len, Hq, Hkv, d, float(sm_scale), float(decay),
+        _ptr(taskmap), num_ctas, _ptr(acc), _ptr(out), _stream(stream)), "hpa_key_weights")
+
+
+def _kept(kept, new_lens, B, Hkv):
+    _dev(kept, "kept", torch.int32)
+    _dev(new_lens, "new_lens", torch.int32)
+    if kept.dim() != 3 or tuple(kept.shape[:2]) != (B, Hkv) or kept.shape[2] < 1:
+        raise HpaError("kept must be int32 [B][Hkv][at least the largest budget]")
+    if new_lens.numel() != B:
+        raise HpaError("new_lens needs one value per request")
+
+
+def hpa_evict_select(acc, seq_lens, page_indptr, page_indices, budgets, sinks: int, recent: int,
+                     kept, new_lens, status=None, stream=None):
+    """The keys every KV head keeps, ascending, in kept [B][Hkv][stride] (int32), and how many
+    in new_lens [B]: the first `sinks`, the last `recent` and the heaviest of the rest up to
+    budgets[r], or all of a request within its budget."""
+    _dev(acc, "acc", torch.float32)
+    if acc.dim() != 3:
+        raise HpaError("acc must be [P][Hkv][page]")
+    P, Hkv, page = acc.shape
+    _dev(seq_lens, "seq_lens", torch.int32)
+    _dev(budgets, "budgets", torch.int32)
+    B = seq_lens.numel()
+    if budgets.numel() != B:
+        raise HpaError("budgets needs one value per request")
+    _page_table(page_indptr, page_indices, B)
+    _kept(kept, new_lens, B, Hkv)
+    if status is not None:
+        _dev(status, "status", torch.int32)
+    _one_device(acc, seq_lens, budgets, page_indptr, page_indices, kept, new_lens, status)
+    _check(lib().hpa_evict_select(
+        _ptr(acc), _ptr(seq_lens), _ptr(page_indptr), _ptr(page_indices), P, page, _ptr(budgets),
+        sinks, recent, B, Hkv, _ptr(kept), kept.shape[2], _ptr(new_lens), _ptr(status),
+        _stream(stream)), "hpa_evict_select")
+
+
+def hpa_evict_compact(k_pool, v_pool, page_indptr, page_indices, kept, new_lens, acc=None,
+                      dst_indptr=None, dst_indices=None, status=None, stream=None):
+    """Moves the kept rows of K, V and acc to the front of each request's own pages, or to the
+    pages that dst_indptr / dst_indices list (the old cache then stays as it was)."""
+    _dev(k_pool, "k_pool")
+    _dev(v_pool, "v_pool")
+    if k_pool.dim() != 4 or v_pool.dtype != k_pool.dtype or v_pool.shape != k_pool.shape:
+        raise HpaError("k_pool and v_pool must match, [P][Hkv][page][d]")
+    if k_pool.dtype not in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn):
+        raise HpaError("unsupported KV dtype %s" % k_pool.dtype)
+    kv = KV_BF16 if k_pool.dtype == torch.bfloat16 else KV_E4M3
+    P, Hkv, page, d = k_pool.shape
+    B = page_indptr.numel() - 1
+    _page_table(page_indptr, page_indices, B)
+    _kept(kept, new_lens, B, Hkv)
+    if acc is not None:
+        _acc_pool(acc, "acc", k_pool)
+    if (dst_indptr is None) != (dst_indices is None):
+        raise HpaError("dst_indptr and dst_indices go together")
+    if dst_indptr is not None:
+        _page_table(dst_indptr, dst_indices, B, "dst")
+    if status is not None:
+        _dev(status, "status", torch.int32)
+    _one_device(k_pool, v_pool, page_indptr, page_indices, kept, new_lens, acc, dst_indptr,
+                dst_indices, status)
+    _check(lib().hpa_evict_compact(
+        _ptr(k_pool), _ptr(v_pool), kv, _ptr(acc), P, _ptr(page_indptr), _ptr(page_indices),
+        _ptr(dst_indptr), _ptr(dst_indices), page, _ptr(kept), kept.shape[2], _ptr(new_lens), B,
+        Hkv, d, _ptr(status), _stream(stream)), "hpa_evict_compact")
+
+
+def evict_step(acc, k_pool, v_pool, seq_lens, page_indptr, page_indices, budgets, sinks: int,
+               recent: int, kept, new_lens, dst_indptr=None, dst_indices=None, status=None,
+               stream=None):
+    """hpa_evict_select -> hpa_evict_compact of K, V and acc, enqueued on one stream; the cache
+    then has new_lens[r] keys per request (-1: a request that `status` reports, untouched)."""
+    hpa_evict_select(acc, seq_lens, page_indptr, page_indices, budgets, sinks, recent, kept,
+                     new_lens, status, stream)
+    hpa_evict_compact(k_pool, v_pool, page_indptr, page_indices, kept, new_lens, acc, dst_indptr,
+                      dst_indices, status, stream)
 
 
 # ----------------------------------------------------------------------------- workspace helper
@@ -454,11 +662,17 @@ class Workspace:
     normally hpa_default_num_ctas(...), which follows hpa_decode_attn's kernel
     choice (mma.sync up to 16 query rows per KV head, tcgen05 above);
     hpa_default_num_ctas_mma / _tc size for a forced kernel.  Either kernel
-    accepts any partition count.
+    accepts any partition count.  With `window` (keys) and `sinks` the steps run
+    sliding-window attention: hpa_plan_window and hpa_decode_attn_window, sized by
+    hpa_default_num_ctas_window.
     """
 
     def __init__(self, B, q_len, Hq, d, num_ctas=None, splits=None, device="cuda", Hkv=8,
-                 weighted=False):
+                 weighted=False, window=None, sinks=0):
+        if window is not None and (splits is not None or weighted):
+            raise HpaError("a window has the dynamic plan alone")
+        if window is None and sinks:
+            raise HpaError("sinks come with a window")
         if splits is not None:
             self.num_ctas = hpa_static_num_ctas(B, splits)
             nbytes = hpa_static_taskmap_bytes(B, splits)
@@ -470,6 +684,7 @@ class Workspace:
             raise HpaError("workspace size query failed")
         self.splits = splits
         self.weighted = weighted
+        self.window, self.sinks, self.q_len = window, sinks, q_len
         self.capacity = cap
         self.taskmap = torch.zeros((nbytes + 3) // 4, dtype=torch.int32, device=device)
         self.partial_o = torch.empty(cap * q_len * Hq * d, dtype=torch.float32, device=device)
@@ -477,8 +692,14 @@ class Workspace:
         self.arrivals = torch.zeros(hpa_arrivals_elems(B, Hq, Hkv, q_len), dtype=torch.int32,
                                     device=device)  # fused combine
 
-    def plan(self, seq_lens, tile=512, stream=None):
-        if self.splits is not None:
+    def plan(self, seq_lens, tile=None, stream=None):
+        """tile: keys per tile, by default 512, or one page of 64 with a window."""
+        if tile is None:
+            tile = 512 if self.window is None else 64
+        if self.window is not None:
+            hpa_plan_window(seq_lens, self.q_len, self.window, self.sinks, tile, self.num_ctas,
+                            self.taskmap, stream)
+        elif self.splits is not None:
             hpa_plan_static(seq_lens, tile, self.splits, self.taskmap, stream)
         elif self.weighted:
             hpa_plan_weighted(seq_lens, tile, self.num_ctas, self.taskmap, stream)
@@ -491,9 +712,9 @@ class Workspace:
 
 
 def decode_step(ws: Workspace, q, k_pool, v_pool, seq_lens, page_indptr, page_indices, out,
-                out_lse=None, k_scale=None, v_scale=None, tile=512, plan=True, stream=None,
+                out_lse=None, k_scale=None, v_scale=None, tile=None, plan=True, stream=None,
                 fused=False, tc=False, sm_scale: float | None = None, allheads=False,
-                mma=False):
+                mma=False, acc=None, decay: float = 1.0):
     """plan (optional) -> split-KV attention -> combine, all enqueued on one stream.
 
     fused=True runs the attention kernel with the combine folded in (one launch);
@@ -501,24 +722,36 @@ def decode_step(ws: Workspace, q, k_pool, v_pool, seq_lens, page_indptr, page_in
     head (size the workspace with hpa_default_num_ctas); tc=True forces the tcgen05
     kernel (hpa_default_num_ctas_tc), mma=True the mma.sync kernel
     (hpa_default_num_ctas_mma), allheads=True the mma.sync variant with every KV head
-    inside the CTA (hpa_default_num_ctas_allheads); sm_scale defaults to 1/sqrt(d)."""
+    inside the CTA (hpa_default_num_ctas_allheads); sm_scale defaults to 1/sqrt(d).  A
+    workspace with a window runs hpa_decode_attn_window (and none of the variants above).
+    acc: accumulators of the cached keys ([P][Hkv][page] fp32), which the step's weights
+    are added to in place after a decay (hpa_key_weights); needs out_lse."""
     if fused and tc:
         raise HpaError("the tcgen05 kernel has no fused-combine variant")
     if allheads and (fused or tc):
         raise HpaError("the all-heads variant has no fused or tcgen05 form")
+    if ws.window is not None and (fused or tc or allheads or mma):
+        raise HpaError("a window has one attention kernel")
+    if acc is not None and out_lse is None:
+        raise HpaError("accumulating key weights needs out_lse")
+    if acc is not None and allheads:
+        raise HpaError("hpa_key_weights needs a map per KV head, which the all-heads one is not")
     if plan:
         ws.plan(seq_lens, tile, stream)
     if fused:
         hpa_decode_attn_fused(q, k_pool, v_pool, page_indptr, page_indices, ws.taskmap,
                               ws.num_ctas, ws.partial_o, ws.partial_lse, out, ws.arrivals,
                               out_lse, k_scale, v_scale, sm_scale=sm_scale, stream=stream)
-        return
-    if allheads:
+    elif allheads:
         hpa_decode_attn_allheads(q, k_pool, v_pool, page_indptr, page_indices, ws.taskmap,
                                  ws.num_ctas, ws.partial_o, ws.partial_lse, k_scale, v_scale,
                                  sm_scale=sm_scale, stream=stream)
     else:
         hpa_decode_attn(q, k_pool, v_pool, page_indptr, page_indices, ws.taskmap, ws.num_ctas,
                         ws.partial_o, ws.partial_lse, k_scale, v_scale, sm_scale=sm_scale,
-                        stream=stream, tc=tc, mma=mma)
-    hpa_combine(ws.partial_o, ws.partial_lse, ws.taskmap, ws.num_ctas, out, out_lse, stream)
+                        stream=stream, tc=tc, mma=mma, window=ws.window is not None)
+    if not fused:
+        hpa_combine(ws.partial_o, ws.partial_lse, ws.taskmap, ws.num_ctas, out, out_lse, stream)
+    if acc is not None:
+        hpa_key_weights(q, out_lse, k_pool, page_indptr, page_indices, ws.taskmap, ws.num_ctas,
+                        acc, k_scale=k_scale, decay=decay, sm_scale=sm_scale, stream=stream)
