@@ -33,6 +33,8 @@ class HpaError(RuntimeError):
 def lib():
     """Load libhpa.so (building it first if it is missing or older than its sources)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB
@@ -110,13 +112,15 @@ def _check(rc: int, what: str):
 
 
 def _stream(stream):
+    """The stream's handle; a torch stream, a handle, or None for torch's current stream (read
+    without the Stream object of torch.cuda.current_stream(), which takes longer than a launch)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return getattr(stream, "cuda_stream", stream)
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _dev(t, name, dtype=None):
@@ -251,7 +255,7 @@ def _attn_args(q, k_pool, v_pool, page_indptr, page_indices, taskmap, k_scale, v
 def _partials(partial_o, partial_lse, B, num_ctas, q_len, Hq, d):
     _dev(partial_o, "partial_o", torch.float32)
     _dev(partial_lse, "partial_lse", torch.float32)
-    need = hpa_max_segments(B, num_ctas) * q_len * Hq
+    need = (B + num_ctas - 1) * q_len * Hq
     if partial_lse.numel() < need or partial_o.numel() < need * d:
         raise HpaError("partial buffers too small: need (B + num_ctas - 1) segments")
 
@@ -646,6 +650,7 @@ def evict_step(acc, k_pool, v_pool, seq_lens, page_indptr, page_indices, budgets
                stream=None):
     """hpa_evict_select -> hpa_evict_compact of K, V and acc, enqueued on one stream; the cache
     then has new_lens[r] keys per request (-1: a request that `status` reports, untouched)."""
+    stream = _stream(stream)
     hpa_evict_select(acc, seq_lens, page_indptr, page_indices, budgets, sinks, recent, kept,
                      new_lens, status, stream)
     hpa_evict_compact(k_pool, v_pool, page_indptr, page_indices, kept, new_lens, acc, dst_indptr,
@@ -736,6 +741,7 @@ def decode_step(ws: Workspace, q, k_pool, v_pool, seq_lens, page_indptr, page_in
         raise HpaError("accumulating key weights needs out_lse")
     if acc is not None and allheads:
         raise HpaError("hpa_key_weights needs a map per KV head, which the all-heads one is not")
+    stream = _stream(stream)
     if plan:
         ws.plan(seq_lens, tile, stream)
     if fused:
