@@ -3,285 +3,453 @@
 //
 // Selection.  A request longer than its budget keeps its first `sinks` keys, its last
 // `recent` keys and, of the others, the budget - sinks - recent with the largest weight,
-// ties to the lower index.  One block per (request, KV head): a radix select over an
-// order-preserving integer image of the weights (digits of 11, 11 and 10 bits: three
-// histograms instead of a sort) finds the last weight that stays, T, and how many keys of
-// weight T stay; a pass with ballots and one scan over the block then writes the kept
-// indices in ascending order.  The weights are read from memory once and kept in shared
-// memory (up to kKeyCap of them; a longer request's rest is read again in each pass).
+// ties to the lower index.  One cluster of 1 to 8 blocks per (request, KV head): a radix
+// select over an order-preserving integer image of the weights (digits of 11, 11 and 10
+// bits: three histograms instead of a sort) finds the last weight that stays, T, and how
+// many keys of weight T stay; the blocks add up one another's histograms through
+// distributed shared memory.  A pass with ballots and a scan over the warps and blocks
+// then writes the kept indices in ascending order.  The weights are read from memory once,
+// eight pages in flight per warp, and stay in the shared memory of the cluster (22 K keys
+// a block; a longer request's rest is read again in each pass, from L2).  The second digit's
+// pass also counts what lies above and lists the few keys that share the first digit, so
+// the third digit and the final counts go over that list.
 //
 // Compaction.  Row t of the new cache is row kept[t] of the old one, and kept is
 // ascending, so kept[t] >= t: a block that takes the rows of one (request, head) in order,
-// a chunk at a time, and writes a chunk after all of its rows are read never overwrites a
+// a batch at a time, and writes a batch after all of its rows are read never overwrites a
 // row that is still needed.  Columns of a row are independent, so with few (request, head)
 // pairs a row is split over several blocks; a move to other pages also splits the rows.
+#include <cooperative_groups.h>
+
+#include <climits>
+#include <type_traits>
+
 #include "hpa_internal.cuh"
 
 namespace hpa {
 namespace {
 
-constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kKeyCap = 48 * 1024;  // weights held in shared memory
-constexpr int kBins = 2048;
-constexpr int kSelSmem = kKeyCap * 4 + kBins * 4;
+namespace cg = cooperative_groups;
 
-// Integers in the order of the weights: NaN above every number, -0 equal to +0.
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kWarpPages = 22;                               // pages a warp holds in shared memory
+constexpr int kBlockPages = kSelWarps * kWarpPages;
+constexpr int kBins = 2048;
+constexpr int kBinsPerThread = kBins / kSelThreads;
+constexpr int kList = 1024;                                  // keys that share the first digit
+constexpr int kMaxCluster = 8;
+constexpr int64_t kMinKeys = 4096;                           // per block before a cluster grows
+constexpr int kSelSmem = kBlockPages * PAGE * 4 + 2 * kBins * 4 + kList * 8;
+constexpr int kSelBlocks = 2;                                // per SM: 112 KB of shared memory each
+constexpr int kFlight = 4;                                   // page pairs in flight per warp
+// Keys that are no candidates: beyond the request, and those that stay in any case
+constexpr uint32_t kAbsent = 0u, kFixed = 0xffffffffu;
+
+// Integers in the order of the weights, between kAbsent and kFixed: NaN above every
+// number, -0 equal to +0.
 __device__ __forceinline__ uint32_t weight_key(uint32_t u) {
-  if ((u & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
+  if ((u & 0x7fffffffu) > 0x7f800000u) return kFixed - 1;
   if (u == 0x80000000u) u = 0u;
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// The bin that holds the k-th largest entry (k >= 1, k <= the entries counted), and the
-// number of entries in higher bins.  All threads of the block call it.
-__device__ void find_bin(const int *hist, int k, int *wsum, int &bin, int &above) {
-  __shared__ int s_bin, s_above;
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  // thread t owns bins kBins - 1 - 2 t and the one below: a scan from the top
-  const int b0 = kBins - 1 - 2 * tid, h0 = hist[b0], h1 = hist[b0 - 1];
-  int v = h0 + h1;
+// Over the whole cluster: the bin of the k-th largest entry (1 <= k <= the entries
+// counted) and the number of entries in higher bins.  The caller has synchronised the
+// cluster after the last count into `hist`.
+__device__ void find_bin(cg::cluster_group &cl, int *hist, int k, int &bin, int &above) {
+  __shared__ int wsum[kSelWarps], s_bin, s_above;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, n = cl.num_blocks();
+  // thread t owns bins [low, low + 4), low = kBins - 4 (t + 1): a scan from the highest bin
+  static_assert(kBinsPerThread == 4, "one 16-byte load per block");
+  const int low = kBins - kBinsPerThread * (tid + 1);
+  int4 c = *reinterpret_cast<const int4 *>(hist + low);
+  if (n > 1) {
+    const int me = cl.block_rank();
+#pragma unroll
+    for (int x = 1; x < kMaxCluster; ++x)  // all the others' loads in flight
+      if (x < n) {
+        const int4 o =
+            *reinterpret_cast<const int4 *>(cl.map_shared_rank(hist, (me + x) & (n - 1)) + low);
+        c.x += o.x, c.y += o.y, c.z += o.z, c.w += o.w;
+      }
+  }
+  const int mine = c.x + c.y + c.z + c.w;
+  int v = mine;
+#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(kFull, v, o);
-    if (lane >= o) v += n;
+    const int u = __shfl_up_sync(kFull, v, o);
+    if (lane >= o) v += u;
   }
   if (lane == 31) wsum[wid] = v;
   __syncthreads();
-  if (wid == 0) {
-    int s = wsum[lane];
-    for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(kFull, s, o);
-      if (lane >= o) s += n;
+  int before = v - mine;
+#pragma unroll
+  for (int x = 0; x < kSelWarps; ++x) before += x < wid ? wsum[x] : 0;
+  if (before < k && before + mine >= k) {
+    const int h[4] = {c.w, c.z, c.y, c.x};
+    for (int x = 0; x < 4; ++x) {
+      if (before + h[x] >= k) {
+        s_bin = low + 3 - x;
+        s_above = before;
+        break;
+      }
+      before += h[x];
     }
-    wsum[lane] = s;
-  }
-  __syncthreads();
-  const int before = v - h0 - h1 + (wid ? wsum[wid - 1] : 0);
-  if (before < k && before + h0 >= k) {
-    s_bin = b0;
-    s_above = before;
-  } else if (before + h0 < k && before + h0 + h1 >= k) {
-    s_bin = b0 - 1;
-    s_above = before + h0;
   }
   __syncthreads();
   bin = s_bin;
   above = s_above;
-  __syncthreads();
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kSelThreads, kSelBlocks)
+    evict_select_kernel(const EvictParams p) {
   extern __shared__ __align__(16) uint32_t sel_smem[];
-  uint32_t *keys = sel_smem;
-  int *hist = reinterpret_cast<int *>(sel_smem + kKeyCap);
-  __shared__ int wsum[kSelWarps], s_bad;
+  __shared__ int s_bad, s_listed, s_total[2], s_gt[kSelWarps], s_eq[kSelWarps];
+  cg::cluster_group cl = cg::this_cluster();
+  const int ranks = cl.num_blocks(), rank = cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int r = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
-  if (tid == 0) s_bad = 0;
-  for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-  __syncthreads();
+  int *hist0 = reinterpret_cast<int *>(sel_smem + kBlockPages * PAGE), *hist1 = hist0 + kBins;
+  uint2 *list = reinterpret_cast<uint2 *>(hist1 + kBins);  // (key, warp)
+  uint32_t *keys = sel_smem + wid * (kWarpPages * PAGE);   // this warp's first pages
+  const int pair = blockIdx.x / ranks, r = pair / p.Hkv, h = pair % p.Hkv;
+  if (tid == 0) s_bad = s_listed = 0;
+  if (tid < kSelWarps) s_gt[tid] = s_eq[tid] = 0;
+  for (int i = tid; i < kBins / 2; i += kSelThreads)  // both histograms
+    reinterpret_cast<int4 *>(hist0)[i] = make_int4(0, 0, 0, 0);
+  // No early launch of the kernel after this one: compaction blocks that wait on the SMs
+  // settle unevenly around these (174 -> 251 us of compaction on 64 requests cut to 4096).
+  pdl_wait();
   const int L = p.seq_lens[r], budget = p.budgets[r];
   const int pstart = p.page_indptr[r], pcount = p.page_indptr[r + 1] - pstart;
   const int n = min(L, budget);
-  int bad = 0;
+  int bad = 0;  // the same in every block of the cluster
   if (L < 1) bad = HPA_STATUS_BAD_SEQLEN;
   else if (budget < 1 || n > p.kept_stride ||
            (L > budget && static_cast<int64_t>(p.sinks) + p.recent > budget))
     bad = HPA_STATUS_BAD_BUDGET;
   else if ((L - 1) / PAGE + 1 > pcount)
     bad = HPA_STATUS_BAD_PAGE;
-  int32_t *kept = p.kept + static_cast<int64_t>(blockIdx.x) * p.kept_stride;
-  const bool cut = !bad && L > budget;
-  const int lo = p.sinks, hi = L - p.recent;  // candidates [lo, hi) when the request is cut
-  const int npages = bad ? 0 : (L - 1) / PAGE + 1;
-
-  // page pg's two weights of this lane, as order-preserving integers
-  auto load_page = [&](int pg) {
-    const int id = p.page_indices[pstart + pg];
-    uint2 x = make_uint2(0u, 0u);
-    if (id < 0 || id >= p.num_pages) s_bad = HPA_STATUS_BAD_PAGE;
-    else
-      x = reinterpret_cast<const uint2 *>(p.acc + (static_cast<int64_t>(id) * p.Hkv + h) * PAGE)[lane];
-    return make_uint2(weight_key(x.x), weight_key(x.y));
-  };
-  // every candidate's key in turn, a page per warp and turn
-  auto each = [&](bool first, auto f) {
-    for (int pg = wid; pg < npages; pg += kSelWarps) {
-      const int i = pg * PAGE + 2 * lane;
-      uint2 k;
-      if (!first && pg < kKeyCap / PAGE) {
-        k = *reinterpret_cast<const uint2 *>(keys + i);
-      } else {
-        k = load_page(pg);
-        if (pg < kKeyCap / PAGE) *reinterpret_cast<uint2 *>(keys + i) = k;
-      }
-      if (i >= lo && i < hi) f(k.x);
-      if (i + 1 >= lo && i + 1 < hi) f(k.y);
-    }
-  };
-
-  if (!cut && !bad) {  // nothing leaves: the pages are checked, as below
-    for (int pg = tid; pg < npages; pg += kSelThreads) {
-      const int id = p.page_indices[pstart + pg];
-      if (id < 0 || id >= p.num_pages) s_bad = HPA_STATUS_BAD_PAGE;
-    }
-  }
-  uint32_t T = 0xffffffffu;
-  int need = 0, take = cut ? budget - p.sinks - p.recent : 0;
-  if (cut) {
-    each(true, [&](uint32_t k) { atomicAdd(&hist[k >> 21], 1); });
-    __syncthreads();
-    if (take > 0) {  // uniform over the block
-      int b1, b2, b3, above;
-      find_bin(hist, take, wsum, b1, above);
-      need = take - above;
-      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      each(false, [&](uint32_t k) { if (k >> 21 == b1) atomicAdd(&hist[(k >> 10) & 2047], 1); });
-      __syncthreads();
-      find_bin(hist, need, wsum, b2, above);
-      need -= above;
-      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      const uint32_t top = (static_cast<uint32_t>(b1) << 11) | b2;
-      each(false, [&](uint32_t k) { if (k >> 10 == top) atomicAdd(&hist[k & 1023], 1); });
-      __syncthreads();
-      find_bin(hist, need, wsum, b3, above);
-      need -= above;  // keys equal to T that stay
-      T = (top << 10) | b3;
-    }
-  }
-  __syncthreads();
-  if (!bad) bad = s_bad;
-  if (bad) {
-    if (tid == 0) {
-      if (p.status) atomicOr(reinterpret_cast<int *>(p.status), bad);
+  const bool lead = rank == 0 && tid == 0;
+  auto refuse = [&](int why) {
+    if (lead) {
+      if (p.status) atomicOr(reinterpret_cast<int *>(p.status), why);
       if (h == 0) p.new_lens[r] = -1;
     }
-    return;
-  }
-  if (tid == 0 && h == 0) p.new_lens[r] = n;
-  if (!cut) {
-    for (int i = tid; i < n; i += kSelThreads) kept[i] = i;
-    return;
-  }
-  // a contiguous range of pages per warp: keys above T (and the fixed ones) and equal to T
-  __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
-  const int per = (npages + kSelWarps - 1) / kSelWarps;
-  const int p0 = min(npages, wid * per), p1 = min(npages, p0 + per);
-  auto classify = [&](int pg, int half, bool &gt, bool &eq) {
-    const int i = pg * PAGE + 32 * half + lane;
-    gt = eq = false;
-    if (i >= L) return;
-    if (i < lo || i >= hi) {
-      gt = true;
-      return;
-    }
-    uint32_t k;
-    if (pg < kKeyCap / PAGE) {
-      k = keys[i];
-    } else {
-      const int id = p.page_indices[pstart + pg];  // in range: checked when it was first read
-      k = weight_key(__float_as_uint(p.acc[(static_cast<int64_t>(id) * p.Hkv + h) * PAGE + i % PAGE]));
-    }
-    gt = take > 0 && k > T;
-    eq = take > 0 && k == T;
   };
-  int gt_n = 0, eq_n = 0;
-  for (int pg = p0; pg < p1; ++pg)
-    for (int half = 0; half < 2; ++half) {
-      bool gt, eq;
-      classify(pg, half, gt, eq);
-      gt_n += __popc(__ballot_sync(kFull, gt));
-      eq_n += __popc(__ballot_sync(kFull, eq));
-    }
-  if (lane == 0) s_gt[wid] = gt_n, s_eq[wid] = eq_n;
+  if (bad) {
+    refuse(bad);
+    return;
+  }
   __syncthreads();
-  int gt_at = 0, eq_at = 0;
-  for (int x = 0; x < wid; ++x) gt_at += s_gt[x], eq_at += s_eq[x];
-  const uint32_t below = (1u << lane) - 1u;
-  for (int pg = p0; pg < p1; ++pg)
-    for (int half = 0; half < 2; ++half) {
-      bool gt, eq;
-      classify(pg, half, gt, eq);
-      const uint32_t mg = __ballot_sync(kFull, gt), me = __ballot_sync(kFull, eq);
-      const int eq_rank = eq_at + __popc(me & below);
-      if (gt || (eq && eq_rank < need))
-        kept[gt_at + __popc(mg & below) + min(eq_rank, need)] = pg * PAGE + 32 * half + lane;
-      gt_at += __popc(mg);
-      eq_at += __popc(me);
-    }
-}
+  int32_t *kept = p.kept + static_cast<int64_t>(pair) * p.kept_stride;
+  const int32_t *pidx = p.page_indices + pstart;
+  const bool cut = L > budget;
+  const int npages = (L - 1) / PAGE + 1;
+  // contiguous pages: per block, and within it per warp
+  const int per_block = (npages + ranks - 1) / ranks;
+  const int b0 = min(npages, rank * per_block), b1 = min(npages, b0 + per_block);
+  const int per_warp = (b1 - b0 + kSelWarps - 1) / kSelWarps;
+  const int w0 = min(b1, b0 + wid * per_warp), w1 = min(b1, w0 + per_warp);
+  const int held = min(w1, w0 + kWarpPages);  // pages [w0, held) stay in shared memory
+  const int lo = p.sinks, hi = L - p.recent;  // candidates [lo, hi) of a request that is cut
+  const int take = cut ? budget - p.sinks - p.recent : 0;
 
-// ----------------------------------------------------------------------------- compaction
-constexpr int kCmpThreads = 256;
-constexpr int kCmpRows = 4;  // rows in flight per thread
-
-// Moves the T-wide column `col` of rows [t0, t1) of one (request, head); `lanes` threads
-// share a row.  base: the pool as T; row_ts: Ts per row.
-template <typename T>
-__device__ void move_rows(const CompactParams &p, T *base, int row_ts, int col, int lanes, int r,
-                          int h, int t0, int t1) {
-  const int32_t *kept = p.kept + (static_cast<int64_t>(r) * p.Hkv + h) * p.kept_stride;
-  const bool in_place = p.dst_indptr == nullptr;
-  const int ps = p.page_indptr[r], pn = p.page_indptr[r + 1] - ps;
-  const int ds = in_place ? ps : p.dst_indptr[r];
-  const int dn = in_place ? pn : p.dst_indptr[r + 1] - ds;
-  const int32_t *didx = in_place ? p.page_indices : p.dst_indices;
-  const int per = kCmpThreads / lanes, row = threadIdx.x / lanes;
-  const int c = col + threadIdx.x % lanes;
-  auto place = [&](const int32_t *idx, int start, int count, int t) -> int64_t {
-    const int id = t >= 0 && t / PAGE < count ? idx[start + t / PAGE] : -1;
-    if (id < 0 || id >= p.num_pages) {
-      if (p.status) atomicOr(reinterpret_cast<int *>(p.status), HPA_STATUS_BAD_PAGE);
-      return -1;
-    }
-    return ((static_cast<int64_t>(id) * p.Hkv + h) * PAGE + t % PAGE) * row_ts + c;
-  };
-  for (int b = t0; b < t1; b += kCmpRows * per) {
-    T x[kCmpRows];
-    int64_t to[kCmpRows];
+  // Reads pages [from, to), two per turn (lane: 4 consecutive keys), and gives f each
+  // turn's keys in order; KEEP stores them as well.
+  auto read_pages = [&](int from, int to, auto keep, auto f) {
+    constexpr bool KEEP = decltype(keep)::value;
+    for (int g = from; g < to; g += 32) {
+      const int cnt = min(32, to - g);
+      int id = 0;
+      if (lane < cnt) {
+        id = pidx[g + lane];
+        if (id < 0 || id >= p.num_pages) {
+          s_bad = 1;
+          id = 0;
+        }
+      }
+      for (int u0 = 0; u0 < cnt; u0 += 2 * kFlight) {
+        uint4 k[kFlight];
 #pragma unroll
-    for (int u = 0; u < kCmpRows; ++u) {
-      const int t = b + u * per + row;
-      to[u] = -1;
-      if (t < t1) {
-        const int src = kept[t];
-        if (!(in_place && src == t)) {
-          const int64_t from = place(p.page_indices, ps, pn, src);
-          if (from >= 0) {
-            to[u] = place(didx, ds, dn, t);
-            x[u] = base[from];
+        for (int u = 0; u < kFlight; ++u) {
+          const int at = u0 + 2 * u + (lane >> 4);
+          const int pid = __shfl_sync(kFull, id, at & 31);
+          k[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (at < cnt)
+            k[u] = reinterpret_cast<const uint4 *>(
+                p.acc + (static_cast<int64_t>(pid) * p.Hkv + h) * PAGE)[lane & 15];
+        }
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+          const int at = u0 + 2 * u, i = (g + at) * PAGE + 4 * lane;
+          if (at >= cnt) break;
+          auto key = [&](uint32_t x, int j) {
+            return j >= hi || j < lo ? (j < L ? kFixed : kAbsent) : weight_key(x);
+          };
+          const bool there = at + (lane >> 4) < cnt;  // an odd last page
+          uint4 x = make_uint4(kAbsent, kAbsent, kAbsent, kAbsent);
+          if (there) {
+            x = make_uint4(key(k[u].x, i), key(k[u].y, i + 1), key(k[u].z, i + 2),
+                           key(k[u].w, i + 3));
+            if (KEEP) *reinterpret_cast<uint4 *>(keys + (g + at - w0) * PAGE + 4 * lane) = x;
           }
+          f(i, x);
         }
       }
     }
-    if (in_place) __syncthreads();  // the chunk is read before any of it is written
-#pragma unroll
-    for (int u = 0; u < kCmpRows; ++u)
-      if (to[u] >= 0) base[to[u]] = x[u];
+  };
+  // All keys of the warp again, in order: those held, then the rest from memory.
+  auto each = [&](auto f) {
+    for (int pg = w0; pg < held; pg += 2) {
+      uint4 x = make_uint4(kAbsent, kAbsent, kAbsent, kAbsent);
+      if (pg + (lane >> 4) < held)
+        x = *reinterpret_cast<const uint4 *>(keys + (pg - w0) * PAGE + 4 * lane);
+      f(pg * PAGE + 4 * lane, x);
+    }
+    read_pages(held, w1, std::false_type(), f);
+  };
+
+  if (cut) {
+    auto first = [&](int, uint4 x) {
+      auto add = [&](uint32_t k) {
+        if (k - 1u < kFixed - 1u) atomicAdd(&hist0[k >> 21], 1);
+      };
+      add(x.x), add(x.y), add(x.z), add(x.w);
+    };
+    read_pages(w0, held, std::true_type(), first);
+    read_pages(held, w1, std::false_type(), first);
+    __syncwarp();
+  } else {  // nothing leaves, but the pages are checked in the same way
+    for (int g = w0 + lane; g < w1; g += 32)
+      if (pidx[g] < 0 || pidx[g] >= p.num_pages) s_bad = 1;
   }
+  auto cluster_sync = [&]() {
+    if (ranks > 1) cl.sync();
+    else __syncthreads();
+  };
+  cluster_sync();
+  if (ranks > 1) {
+#pragma unroll
+    for (int x = 0; x < kMaxCluster; ++x)
+      if (x < ranks) bad |= *cl.map_shared_rank(&s_bad, x);
+  } else {
+    bad = s_bad;
+  }
+  if (bad || !cut) {
+    if (bad) refuse(HPA_STATUS_BAD_PAGE);
+    else {
+      if (lead && h == 0) p.new_lens[r] = n;
+      for (int i = rank * kSelThreads + tid; i < n; i += ranks * kSelThreads) kept[i] = i;
+    }
+    cluster_sync();  // no block leaves while another reads its shared memory
+    return;
+  }
+  uint32_t T = kFixed - 1;  // with nothing to take, only the fixed keys are above
+  int need = 0, gt_n = 0, eq_n = 0;
+  if (take > 0) {
+    int d1, d2, d3, above;
+    find_bin(cl, hist0, take, d1, above);
+    need = take - above;
+    const uint32_t top1 = d1;
+    // keys above the digit are counted; those that share it go on the list
+    each([&](int, uint4 x) {
+      auto see = [&](uint32_t k) {
+        gt_n += k >> 21 > top1 || k == kFixed;
+        if (k >> 21 == top1 && k != kFixed) {
+          atomicAdd(&hist1[(k >> 10) & 2047], 1);
+          const int at = atomicAdd(&s_listed, 1);
+          if (at < kList) list[at] = make_uint2(k, wid);
+        }
+      };
+      see(x.x), see(x.y), see(x.z), see(x.w);
+    });
+    cluster_sync();
+    const int listed = s_listed;  // of this block: beyond kList its keys are walked again
+    find_bin(cl, hist1, need, d2, above);
+    need -= above;
+    // every block has read hist0 (before the barrier above): it takes the last digit
+    for (int i = tid; i < kBins / 4; i += kSelThreads)
+      reinterpret_cast<int4 *>(hist0)[i] = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    const uint32_t top2 = top1 << 11 | static_cast<uint32_t>(d2);
+    auto third = [&](uint32_t k) {
+      if (k >> 10 == top2 && k != kFixed) atomicAdd(&hist0[k & 1023], 1);
+    };
+    if (listed <= kList) {
+      for (int i = tid; i < listed; i += kSelThreads) third(list[i].x);
+    } else {
+      each([&](int, uint4 x) { third(x.x), third(x.y), third(x.z), third(x.w); });
+    }
+    cluster_sync();
+    find_bin(cl, hist0, need, d3, above);
+    need -= above;  // keys equal to T that stay
+    T = top2 << 10 | static_cast<uint32_t>(d3);
+    if (listed <= kList) {
+      for (int i = tid; i < listed; i += kSelThreads) {
+        const uint2 e = list[i];
+        if (e.x > T) atomicAdd(&s_gt[e.y], 1);
+        else if (e.x == T) atomicAdd(&s_eq[e.y], 1);
+      }
+    } else {
+      each([&](int, uint4 x) {
+        auto see = [&](uint32_t k) {
+          gt_n += k >> 21 == top1 && k != kFixed && k > T;
+          eq_n += k == T;
+        };
+        see(x.x), see(x.y), see(x.z), see(x.w);
+      });
+    }
+  } else {
+    each([&](int, uint4 x) {
+      gt_n += (x.x == kFixed) + (x.y == kFixed) + (x.z == kFixed) + (x.w == kFixed);
+    });
+  }
+  gt_n = __reduce_add_sync(kFull, gt_n);
+  eq_n = __reduce_add_sync(kFull, eq_n);
+  if (lane == 0) atomicAdd(&s_gt[wid], gt_n), atomicAdd(&s_eq[wid], eq_n);
+  __syncthreads();
+  int gt_at = 0, eq_at = 0, gt_all = 0, eq_all = 0;  // before this warp, and in the block
+#pragma unroll
+  for (int x = 0; x < kSelWarps; ++x) {
+    gt_at += x < wid ? s_gt[x] : 0, eq_at += x < wid ? s_eq[x] : 0;
+    gt_all += s_gt[x], eq_all += s_eq[x];
+  }
+  if (ranks > 1) {
+    if (tid == 0) s_total[0] = gt_all, s_total[1] = eq_all;
+    cl.sync();
+#pragma unroll
+    for (int x = 0; x < kMaxCluster - 1; ++x)
+      if (x < rank) {
+        const int *o = cl.map_shared_rank(s_total, x);
+        gt_at += o[0], eq_at += o[1];
+      }
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  each([&](int i, uint4 x) {
+    const uint32_t k[4] = {x.x, x.y, x.z, x.w};
+    int mine = 0, gts = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t m = __ballot_sync(kFull, k[e] > T);
+      gts += __popc(m & below);
+      mine += __popc(m);
+    }
+    int gr = gt_at + gts;
+    if (__any_sync(kFull, k[0] == T || k[1] == T || k[2] == T || k[3] == T)) {
+      int eqs = 0, all = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t m = __ballot_sync(kFull, k[e] == T);
+        eqs += __popc(m & below);
+        all += __popc(m);
+      }
+      int er = eq_at + eqs;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (k[e] > T || (k[e] == T && er < need)) kept[gr + min(er, need)] = i + e;
+        gr += k[e] > T, er += k[e] == T;
+      }
+      eq_at += all;
+    } else {
+      gr += min(eq_at, need);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (k[e] > T) kept[gr++] = i + e;
+    }
+    gt_at += mine;
+  });
+  if (lead && h == 0) p.new_lens[r] = n;
+  if (ranks > 1) cl.sync();  // no block leaves while another reads its shared memory
 }
 
+// ----------------------------------------------------------------------------- compaction
+constexpr int kCmpThreads = 256;  // also the rows of a tile
+constexpr int kCmpFlight = 8;     // 16-byte pieces in flight per thread
+
+// Where row t of a cache lives: (page, slot) as page * PAGE + slot, or -1 without a valid page.
+__device__ __forceinline__ int64_t row_place(const CompactParams &p, const int32_t *idx, int start,
+                                             int count, int t) {
+  const int id = t >= 0 && t / PAGE < count ? idx[start + t / PAGE] : -1;
+  if (id < 0 || id >= p.num_pages) {
+    if (p.status) atomicOr(reinterpret_cast<int *>(p.status), HPA_STATUS_BAD_PAGE);
+    return -1;
+  }
+  return static_cast<int64_t>(id) * p.Hkv * PAGE + t % PAGE;
+}
+
+// Block (pair, slice, z): tiles z, z + gridDim.z, ... of 256 rows of one (request, head),
+// columns [slice * lanes, (slice + 1) * lanes) of 16 bytes of K and V.  A thread finds one
+// row's source and destination (the next tile's while this one moves: an index, a page id
+// and the row are three dependent reads), then the block moves the tile in batches of
+// 8 pieces per thread.  In place there is one block per column and its batches go in
+// order, each read whole before it is written.
+template <bool IN_PLACE>
 __global__ void __launch_bounds__(kCmpThreads)
-    evict_compact_kernel(const CompactParams p, int slices, int t_split) {
-  const int r = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
+    evict_compact_kernel(const CompactParams p, int lanes) {
+  __shared__ int64_t s_src[kCmpThreads], s_dst[kCmpThreads];
+  const int r = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv, tid = threadIdx.x;
+  pdl_wait();  // the selection is usually the kernel just before
   const int n = p.new_lens[r];
   if (n <= 0 || n > p.kept_stride) return;  // left as it is (new_lens -1: a bad request)
-  int t0 = 0, t1 = n;
-  if (t_split > 1) {
-    const int64_t z = blockIdx.z;
-    t0 = static_cast<int>(n * z / t_split);
-    t1 = static_cast<int>(n * (z + 1) / t_split);
-  }
-  const int part = blockIdx.y, row_ts = p.row_bytes / 16;
-  if (part < 2 * slices) {
-    uint4 *base = static_cast<uint4 *>(part & 1 ? p.v_pool : p.k_pool);
-    const int lanes = row_ts / slices;
-    move_rows<uint4>(p, base, row_ts, (part >> 1) * lanes, lanes, r, h, t0, t1);
-  } else {
-    move_rows<float>(p, p.acc, 1, 0, 1, r, h, t0, t1);
+  const int32_t *kept = p.kept + static_cast<int64_t>(blockIdx.x) * p.kept_stride;
+  const int ps = p.page_indptr[r], pn = p.page_indptr[r + 1] - ps;
+  const int ds = IN_PLACE ? ps : p.dst_indptr[r];
+  const int dn = IN_PLACE ? pn : p.dst_indptr[r + 1] - ds;
+  const int32_t *didx = IN_PLACE ? p.page_indices : p.dst_indices;
+  const int row_ts = p.row_bytes / 16, col = blockIdx.y * lanes;
+  const int sh = 31 - __clz(lanes);  // lanes is a power of two
+  const int64_t head = static_cast<int64_t>(h) * PAGE;
+  const int64_t step = static_cast<int64_t>(gridDim.z) * kCmpThreads;
+
+  int64_t src = -1, dst = -1;
+  auto resolve = [&](int64_t at) {  // rows that stay where they are, and none, have src -1
+    src = dst = -1;
+    if (at < n) {
+      const int t = static_cast<int>(at);
+      const int k = kept[t];
+      if (!(IN_PLACE && k == t)) {
+        src = row_place(p, p.page_indices, ps, pn, k);
+        dst = row_place(p, didx, ds, dn, t);
+        if (dst < 0) src = -1;
+      }
+    }
+  };
+  int64_t t0 = static_cast<int64_t>(blockIdx.z) * kCmpThreads;
+  if (t0 < n) resolve(t0 + tid);
+  for (; t0 < n; t0 += step) {
+    __syncthreads();  // the previous tile's places are no longer needed
+    s_src[tid] = src < 0 ? -1 : src + head;
+    s_dst[tid] = dst + head;
+    float a = 0.f;
+    const int64_t as = src + head, ad = dst + head;
+    const bool weigh = p.acc && blockIdx.y == 0 && src >= 0;
+    if (weigh) a = p.acc[as];
+    __syncthreads();
+    if (weigh) p.acc[ad] = a;  // in place: read by every thread of the tile before this
+    if (t0 + step < n) resolve(t0 + step + tid);
+    const int pieces = static_cast<int>(n - t0 < kCmpThreads ? n - t0 : kCmpThreads) << sh;
+#pragma unroll 1
+    for (int kv = 0; kv < 2; ++kv) {
+      uint4 *pool = static_cast<uint4 *>(kv ? p.v_pool : p.k_pool);
+      for (int b = 0; b < pieces; b += kCmpFlight * kCmpThreads) {
+        uint4 x[kCmpFlight];
+#pragma unroll
+        for (int u = 0; u < kCmpFlight; ++u) {
+          const int e = b + u * kCmpThreads + tid;
+          const int64_t from = e < pieces ? s_src[e >> sh] : -1;
+          if (from >= 0) x[u] = pool[from * row_ts + col + (e & (lanes - 1))];
+        }
+        if (IN_PLACE) __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kCmpFlight; ++u) {
+          const int e = b + u * kCmpThreads + tid;
+          if (e < pieces && s_src[e >> sh] >= 0)
+            pool[s_dst[e >> sh] * row_ts + col + (e & (lanes - 1))] = x[u];
+        }
+      }
+    }
   }
 }
 
@@ -289,8 +457,9 @@ __global__ void __launch_bounds__(kCmpThreads)
 
 cudaError_t launch_evict_select(const EvictParams &p, cudaStream_t s) {
   static int configured[64] = {0};
-  int dev = 0;
+  int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !configured[dev]) {
     e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -298,8 +467,32 @@ cudaError_t launch_evict_select(const EvictParams &p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 64) configured[dev] = 1;
   }
-  evict_select_kernel<<<static_cast<unsigned>(p.B * p.Hkv), kSelThreads, kSelSmem, s>>>(p);
-  return cudaGetLastError();
+  // Blocks per (request, head), by a request of the pool's average length (the lengths
+  // themselves are on the device): enough to hold its weights, and up to filling the GPU
+  // once as long as a block has kMinKeys of them (a request of 1024 keys: 6 us in one
+  // block, 18 in eight, each of whose barriers costs a microsecond).
+  const int64_t pairs = static_cast<int64_t>(p.B) * p.Hkv;
+  const int64_t mean = p.num_pages * PAGE / p.B;
+  int ranks = 1;
+  while (ranks < kMaxCluster &&
+         ((pairs * ranks * 2 <= kSelBlocks * sms && ranks * kMinKeys < mean) ||
+          static_cast<int64_t>(ranks) * kBlockPages * PAGE < mean) &&
+         pairs * ranks * 2 <= INT_MAX)
+    ranks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs * ranks));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = kSelSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
 }
 
 cudaError_t launch_evict_compact(const CompactParams &p, cudaStream_t s) {
@@ -308,14 +501,28 @@ cudaError_t launch_evict_compact(const CompactParams &p, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int64_t pairs = static_cast<int64_t>(p.B) * p.Hkv;
-  int slices = 1;  // at least 32 bytes of a row
-  while (slices < p.row_bytes / 32 && pairs * 2 * slices < 4 * sms) slices *= 2;
-  int t_split = 1;
-  if (p.dst_indptr != nullptr)
-    while (t_split < 64 && pairs * 2 * slices * t_split < 8 * sms) t_split *= 2;
-  const dim3 grid(static_cast<unsigned>(pairs), 2 * slices + (p.acc ? 1 : 0), t_split);
-  evict_compact_kernel<<<grid, kCmpThreads, 0, s>>>(p, slices, t_split);
-  return cudaGetLastError();
+  const bool in_place = p.dst_indptr == nullptr;
+  int slices = 1, split = 1;
+  if (in_place) {  // columns of 32 bytes or more per block, until four blocks per SM
+    while (slices < p.row_bytes / 32 && pairs * slices < 4 * sms) slices *= 2;
+  } else {  // rows: as many tiles as the kept lists can hold, up to 32 blocks per SM
+    const int64_t tiles = (p.kept_stride + kCmpThreads - 1) / kCmpThreads;
+    const int64_t most = 1 + 32 * static_cast<int64_t>(sms) / pairs;
+    split = static_cast<int>(tiles < most ? tiles : most);
+    while (slices < p.row_bytes / 64 && pairs * split * slices < 2 * sms) slices *= 2;
+  }
+  const int lanes = p.row_bytes / 16 / slices;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs), slices, split);
+  cfg.blockDim = dim3(kCmpThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return in_place ? cudaLaunchKernelEx(&cfg, evict_compact_kernel<true>, p, lanes)
+                  : cudaLaunchKernelEx(&cfg, evict_compact_kernel<false>, p, lanes);
 }
 
 }  // namespace hpa

@@ -205,6 +205,18 @@ def test_select_many_requests():
     _check_select(weights, lens, [100] * 500, 1, 10, Hkv=1)
 
 
+def test_select_one_long_among_many():
+    """A length far beyond the mean that the blocks per (request, head) are chosen by."""
+    g = np.random.default_rng(10)
+    lens = [70] * 200 + [60001] + [70] * 100
+    weights = [g.random((1, L)).astype(np.float32) for L in lens]
+    kept, new, st = _select(weights, lens, [64] * 200 + [2000] + [64] * 100, 2, 30, Hkv=1)
+    assert st == 0
+    for r in (0, 199, 200, 300):
+        n = int(new[r])
+        assert list(kept[r, 0, :n]) == bounded.kept_keys(weights[r][0], n, 2, 30)
+
+
 def test_select_refusals():
     g = np.random.default_rng(9)
     lens = [100, 100, 100, 100, 0]
