@@ -8,361 +8,409 @@
 // independent: the task map of the attention step only serves as a balanced work list.
 //
 // GB300 design:
-//  * one CTA per (partition, KV head): a TMA producer warp and groups of four consumer
-//    warps; a page of K (16 KB bf16 / 8 KB E4M3) and the page's 256 bytes of acc_in are
-//    one pipeline stage, so the read of the accumulators needs no latency of its own;
-//  * keys are the M dimension of the m16n8k16 MMAs and query rows the N dimension: the 8
-//    rows of a usual GQA group fill N exactly, where rows as M would pad them to 16;
-//  * a warp owns 16 keys and all rows, so it sums its exponentials in registers and two
-//    lane exchanges, and writes 16 accumulators: no exchange between warps, no atomics,
-//    the same sums in the same order on every run;
-//  * up to 16 rows the query fragments stay in registers; above, they are read from
-//    shared memory for every 16 keys, in fragment order (8-byte conflict-free loads);
-//  * the producer warp stages each segment's query rows ahead: fragment order, for E4M3
-//    pages converted to f16 after a power-of-two scale per row (exact, as in
-//    decode_attn.cu), with each row's score factor and log-sum-exp in base 2.
+//  * a step is two pages (128 keys) of one KV head: S[128 keys][rows] = K . Q^T runs as
+//    tcgen05.mma with the accumulators in tensor memory.  Keys sit on the TMEM lanes, so
+//    a compute thread owns one key: it sums its rows' exponentials alone, without an
+//    exchange between lanes, and neighbouring threads read and write neighbouring
+//    accumulators.  The sums are in the same order on every run;
+//  * E4M3 pages enter the MMA as they are, the query rows as two E4M3 terms side by side
+//    in N (as in decode_attn_tc.cu), so nothing is widened;
+//  * roles: a TMA producer warp, one thread issuing MMAs, eight compute warps in two groups
+//    that take every other step, and one to four warps that stage each segment's query rows
+//    ahead.  With the staging in the producer warp, 64 rows took 17 us before the first page
+//    was asked for (16 E4M3 rows 8, 8 rows 3), at every segment.  A stage is free as soon
+//    as its MMAs are done; the accumulators of a step's pages (256 bytes each) come with it
+//    into a ring of their own;
+//  * up to 16 rows two CTAs share an SM, above one with a deeper ring: the partition
+//    counts of hpa_default_num_ctas for these row counts.
+// Every wait is bounded in time, as in the attention kernels.
 #include <math_constants.h>
 
-#include "hpa_internal.cuh"
+#include "tcgen05.cuh"
 
 namespace hpa {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kGroupWarps = 4;      // consumer warps that share a page: 16 keys each
-constexpr int kQStride = 288;       // bytes per staged query row: 64-bit loads hit all banks
+constexpr int kGroupWarps = 4;  // compute warps that share a step: one key per thread
+constexpr int kGroups = 2;
+constexpr int kCompute = kGroups * kGroupWarps;
+constexpr int kStepPages = 2;
 constexpr int kAccBytes = PAGE * 4;
 
-// RT: n-tiles of 8 query rows kept in registers (1 or 2); 0: 3 to 8 tiles, from shared memory.
-template <int KV, int RT>
+// RP: query rows, padded to 8, 16, 32, 48 or 64.
+template <int KV, int RP>
 struct KwCfg {
-  static constexpr int kGroups = RT ? 1 : 2;
-  static constexpr int kConsumers = kGroups * kGroupWarps;
-  static constexpr int kThreads = (kConsumers + 1) * 32;
-  static constexpr int kRows = RT ? 8 * RT : MAX_ROWS_TOTAL;
-  static constexpr int kKBytes = KV == HPA_KV_BF16 ? 16384 : 8192;
-  static constexpr int kStages = KV == HPA_KV_BF16 ? 5 : 10;
-  static constexpr int kAcc = kStages * kKBytes;            // float[kStages][64]
-  static constexpr int kQ = kAcc + kStages * kAccBytes;     // two slots of query rows
-  static constexpr int kQSlot = kRows * kQStride;
-  static constexpr int kRow = kQ + 2 * kQSlot;              // float2[2][kRows]: factor, lse
-  static constexpr int kInfo = kRow + 2 * kRows * 8;        // int4[2]
-  static constexpr int kPid = kInfo + 32;                   // int[kStages]
-  static constexpr int kBars = (kPid + kStages * 4 + 15) & ~15;
-  static constexpr int kFlag = kBars + (2 * kStages + 4) * 8;
-  static constexpr int kAlloc = kFlag + 16 + 1024;          // room to align the base
+  static constexpr bool kSmall = RP <= 16;
+  static constexpr int kStagers = RP <= 8 ? 1 : RP <= 16 ? 2 : 4;  // warps, 8 rows at a time each
+  static constexpr int kThreads = (kCompute + 2 + kStagers) * 32;
+  static constexpr int kPageBytes = KV == HPA_KV_BF16 ? 16384 : 8192;
+  static constexpr int kStageBytes = kStepPages * kPageBytes;
+  static constexpr int kN = KV == HPA_KV_E4M3 ? 2 * RP : RP < 16 ? 16 : RP;  // MMA columns
+  static constexpr int kStages = (kSmall ? 96 : 160) * 1024 / kStageBytes;
+  static constexpr int kBufs = KV == HPA_KV_E4M3 && kSmall ? 2 : 4;  // S buffers in TMEM
+  // Slots of the accumulator ring.  The copy for step n is issued once the MMAs of step
+  // n - kStages are done, these once step n - kStages - kBufs has been read: with as many
+  // slots, none is overwritten early.
+  static constexpr int kAccs = kSmall ? 8 : 16;
+  static_assert(kStages + kBufs <= kAccs && kAccs % kGroups == 0, "accumulator ring");
+  static constexpr int kTmem = kBufs * kN <= 32    ? 32
+                               : kBufs * kN <= 64  ? 64
+                               : kBufs * kN <= 128 ? 128
+                               : kBufs * kN <= 256 ? 256
+                                                   : 512;
+  static_assert(kBufs * kN <= 512, "TMEM");
+  static constexpr int kQSlot = kN * (KV == HPA_KV_BF16 ? 256 : 128);
+  static constexpr int kQ = kStages * kStageBytes;              // two slots
+  static constexpr int kAcc = kQ + 2 * kQSlot;                  // float[kAccs][2][64]
+  static constexpr int kRow = kAcc + kAccs * kStepPages * kAccBytes;  // float2[2][RP]
+  static constexpr int kJRow = kRow + 2 * RP * 8;               // int[RP]: token j of a row
+  static constexpr int kInfo = (kJRow + RP * 4 + 15) & ~15;     // int4[2]
+  static constexpr int kPid = kInfo + 32;                       // int2[kAccs]
+  // kv_full[kStages] kv_empty[kStages] s_full[kBufs] s_free[kBufs] acc_full[kAccs]
+  // q_full[2] q_empty[2] drain
+  static constexpr int kBars = kPid + kAccs * 8;
+  static constexpr int kKvFull = kBars, kKvEmpty = kKvFull + 8 * kStages,
+                       kSFull = kKvEmpty + 8 * kStages, kSFree = kSFull + 8 * kBufs,
+                       kAccFull = kSFree + 8 * kBufs, kQFull = kAccFull + 8 * kAccs,
+                       kQEmpty = kQFull + 16, kDrain = kQEmpty + 16;
+  static constexpr int kTmemAt = kDrain + 8;
+  static constexpr int kAbort = kTmemAt + 4;
+  static constexpr int kAlloc = kAbort + 4 + 1024;              // room to align the base
 };
 
-// A segment's walk: real pages of request r over the compact (or plain) key range.
+// Segment s of this partition: request, length, compact pages [pg0, pg1).  The keys of a
+// request shorter than q_len are not followed.
 struct KwSeg {
   int r, L, pg0, pg1;
-  WinSpan win;
 };
-
-__device__ __forceinline__ KwSeg kw_seg(const KeyWeightsParams &p, bool windowed, int window,
-                                        int sinks, int s, int tile, bool report) {
-  const int c = blockIdx.x;
-  const SegRow sr = windowed ? read_seg_row<true>(p.tm, p.lay, p.B, s, c, tile, report)
-                             : read_seg_row<false>(p.tm, p.lay, p.B, s, c, tile, report);
-  KwSeg f;
-  f.r = sr.r;
-  f.L = sr.L;
-  f.pg0 = sr.klo / PAGE;
-  f.pg1 = (sr.khi + PAGE - 1) / PAGE;
-  f.win = WinSpan{};
+__device__ __forceinline__ KwSeg kw_seg(const KeyWeightsParams &p, bool windowed, int s, int tile,
+                                        bool report) {
+  const SegRow sr = windowed
+                        ? read_seg_row<true>(p.tm, p.lay, p.B, s, blockIdx.x, tile, report)
+                        : read_seg_row<false>(p.tm, p.lay, p.B, s, blockIdx.x, tile, report);
+  KwSeg f = {sr.r, sr.L, sr.klo / PAGE, (sr.khi + PAGE - 1) / PAGE};
   if (sr.L < p.q_len) {
     if (report) status_or(p.tm, HPA_STATUS_BAD_SEQLEN);
     f.pg1 = f.pg0;
-  } else if (windowed && f.pg0 < f.pg1) {
-    f.win = WinSpan::make(sr.L, p.q_len, window, sinks);
   }
   return f;
 }
 
-// (score factor, lse in base 2) of a row; a row that sees no key (lse -inf) weighs nothing.
-__device__ __forceinline__ float2 row_consts(float factor, float lse) {
-  const float l2 = lse * 1.4426950408889634f;
-  return make_float2(factor, l2 == -CUDART_INF_F ? CUDART_INF_F : l2);
+// ----------------------------------------------------------------------------- stagers
+// Each segment's query rows as the MMA's B operand (K-major, 128-byte swizzle), and each
+// row's score factor and log-sum-exp in base 2: a weight is 2^(factor * S - lse).
+template <int KV, int RP>
+__device__ void kw_stager(const KeyWeightsParams &p, uint8_t *smem, int s_begin, int n_seg,
+                          int tile, bool windowed, int ws) {
+  using S = KwCfg<KV, RP>;
+  const int lane = threadIdx.x & 31, G = p.G, h = blockIdx.y;
+  const uint32_t base = smem_u32(smem);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kAbort);
+  const int *jrow = reinterpret_cast<const int *>(smem + S::kJRow);
+  float factor = p.scale_log2;
+  if (KV == HPA_KV_E4M3) factor *= p.k_scale[h];
+  for (int k = 0; k < n_seg; ++k) {
+    const int slot = k & 1;
+    const KwSeg f = kw_seg(p, windowed, s_begin + k, tile, false);
+    int good = 1;
+    if (lane == 0)
+      good = !*abort_flag &&
+             mbar_wait_bounded_rolled(base + S::kQEmpty + 8 * slot, ((k >> 1) & 1) ^ 1);
+    if (!__shfl_sync(kFull, good, 0)) {
+      if (lane == 0) {
+        status_or(p.tm, HPA_STATUS_TIMEOUT);
+        *abort_flag = 1;
+      }
+      return;
+    }
+    uint8_t *qs = smem + S::kQ + slot * S::kQSlot;
+    float2 *rc = reinterpret_cast<float2 *>(smem + S::kRow) + slot * RP;
+    const int64_t row_at = static_cast<int64_t>(f.r) * p.q_len * p.Hq + h * G;
+#pragma unroll 1
+    for (int row0 = 8 * ws; row0 < (KV == HPA_KV_BF16 ? S::kN : RP); row0 += 8 * S::kStagers) {
+      uint2 x[8];
+      float lse = 0.f;  // lane i < 8: of row row0 + i
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // eight rows' loads in flight; lane: dims [4 lane, 4 lane + 4)
+        const int row = row0 + i;
+        x[i] = make_uint2(0u, 0u);
+        if (row < p.rows) {
+          const int j = jrow[row];
+          const int64_t at = row_at + static_cast<int64_t>(j) * p.Hq + (row - j * G);
+          x[i] = reinterpret_cast<const uint2 *>(p.q + at * HEAD_DIM)[lane];
+          if (lane == i) lse = p.lse[at];
+        }
+      }
+      float mine = factor;  // lane i: row i's score factor
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = row0 + i;
+        if (KV == HPA_KV_BF16) {
+          *reinterpret_cast<uint2 *>(qs + kmaj(row, 8 * lane, S::kN * 128)) = x[i];
+        } else {
+          const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x[i].x));
+          const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x[i].y));
+          const float v[4] = {a.x, a.y, b.x, b.y};
+          const float sq = pow2_to_128(
+              warp_max(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y)))));
+          uint32_t hi, lo;
+          e4m3_two_terms(v, sq, hi, lo);
+          *reinterpret_cast<uint32_t *>(qs + kmaj(row, 4 * lane, 0)) = hi;
+          *reinterpret_cast<uint32_t *>(qs + RP * 128 + kmaj(row, 4 * lane, 0)) = lo;
+          if (lane == i) mine = factor / sq;
+        }
+      }
+      if (lane < 8 && row0 + lane < RP) {
+        const float l2 = lse * 1.4426950408889634f;
+        // rows that pad the tile, and rows that see no key (lse -inf), weigh nothing
+        const bool none = row0 + lane >= p.rows || l2 == -CUDART_INF_F;
+        rc[row0 + lane] = none ? make_float2(0.f, CUDART_INF_F) : make_float2(mine, l2);
+      }
+    }
+    if (ws == 0 && lane == 0)
+      reinterpret_cast<int4 *>(smem + S::kInfo)[slot] = make_int4(f.r, f.L, f.pg0, f.pg1);
+    fence_proxy_async_smem();  // the MMA reads the slot through the async proxy
+    mbar_arrive(base + S::kQFull + 8 * slot);  // every lane publishes its own stores
+  }
 }
 
 // ----------------------------------------------------------------------------- producer
-template <int KV, int RT>
-__device__ void kw_stage_rows(const KeyWeightsParams &p, uint8_t *smem, int slot, int r, int h) {
-  using S = KwCfg<KV, RT>;
-  const int lane = threadIdx.x & 31, G = p.G;
-  uint8_t *qs = smem + S::kQ + slot * S::kQSlot;
-  float2 *rc = reinterpret_cast<float2 *>(smem + S::kRow) + slot * S::kRows;
-  const int padded = RT ? S::kRows : (p.rows + 7) & ~7;
-  float factor = p.scale_log2;
-  if (KV == HPA_KV_E4M3) factor *= p.k_scale[h];
-  for (int row0 = 0; row0 < padded; row0 += 8) {
-    uint2 x[8];
-    float lse = 0.f;  // lane i < 8: of row row0 + i
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {  // eight rows' loads in flight; lane: dims [4 lane, 4 lane + 4)
-      const int row = row0 + i;
-      x[i] = make_uint2(0u, 0u);
-      if (row < p.rows) {
-        const int64_t at = (static_cast<int64_t>(r) * p.q_len + row / G) * p.Hq + h * G + row % G;
-        x[i] = reinterpret_cast<const uint2 *>(p.q + at * HEAD_DIM)[lane];
-        if (lane == i) lse = p.lse[at];
-      }
-    }
-    float mine = 0.f;  // lane i: row i's score factor
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint8_t *dst = qs + (row0 + i) * kQStride;
-      if (KV == HPA_KV_BF16) {
-        // k-step lane / 4; its thread qd holds dims 2 qd, 2 qd + 1, 2 qd + 8, 2 qd + 9
-        const int in = 4 * (lane & 3), at = (lane >> 2) * 32 + (in & 4) * 4 + (in >> 3) * 4;
-        *reinterpret_cast<uint32_t *>(dst + at) = x[i].x;
-        *reinterpret_cast<uint32_t *>(dst + at + 8) = x[i].y;
-        if (lane == i) mine = factor;
-      } else {
-        const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x[i].x));
-        const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x[i].y));
-        float m = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y)));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-        const int e = f16_row_exponent(m);
-        const float sc = exp2i(e);
-        // k-step ks of thread qd is dims 32 qd + 4 ks + [0, 4): lane = 8 qd + ks
-        uint2 v;
-        v.x = pack_f16(a.x * sc, a.y * sc);
-        v.y = pack_f16(b.x * sc, b.y * sc);
-        *reinterpret_cast<uint2 *>(dst + (lane & 7) * 32 + (lane >> 3) * 8) = v;
-        if (lane == i) mine = factor * exp2i(-e);
-      }
-    }
-    if (lane < 8)
-      rc[row0 + lane] = row0 + lane < p.rows ? row_consts(mine, lse)
-                                             : make_float2(0.f, CUDART_INF_F);
-  }
-}
-
-template <int KV, int RT>
+template <int KV, int RP>
 __device__ void kw_producer(const KeyWeightsParams &p, const CUtensorMap *tmk, uint8_t *smem,
                             int s_begin, int s_end, int tile, bool windowed) {
-  using S = KwCfg<KV, RT>;
+  using S = KwCfg<KV, RP>;
   const int lane = threadIdx.x & 31, h = blockIdx.y;
   const uint32_t base = smem_u32(smem);
-  const uint32_t full0 = base + S::kBars, empty0 = full0 + 8 * S::kStages;
-  const uint32_t qfull0 = empty0 + 8 * S::kStages, qempty0 = qfull0 + 16;
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kFlag);
-  volatile int *pids = reinterpret_cast<volatile int *>(smem + S::kPid);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kAbort);
+  volatile int2 *pids = reinterpret_cast<volatile int2 *>(smem + S::kPid);
   const int window = windowed ? p.tm[TM_WINDOW] : 0, sinks = windowed ? p.tm[TM_SINKS] : 0;
   uint64_t pol = 0;
-  if (lane == 0) {
-    pol = l2_policy_evict_first();
-    prefetch_tmap(tmk);
-  }
-  int stage = 0;
-  uint32_t phase = 0, issued = 0, parity_bits = 0;
+  if (lane == 0) pol = l2_policy_evict_first();
+  int st = 0, slot_a = 0;
+  uint32_t phase = 0, issued = 0, parity_bits = 0, acc_issued = 0, acc_parity = 0, acc_phase = 0;
   bool ok = true;
-  for (int k = 0; k < s_end - s_begin && ok; ++k) {
-    const KwSeg f = kw_seg(p, windowed, window, sinks, s_begin + k, tile, lane == 0);
-    const int slot = k & 1;
-    int good = 1;
-    if (lane == 0) good = !*abort_flag && mbar_wait_bounded(qempty0 + 8 * slot, ((k >> 1) & 1) ^ 1);
-    if (!__shfl_sync(kFull, good, 0)) {
-      ok = false;
-      break;
-    }
-    kw_stage_rows<KV, RT>(p, smem, slot, f.r, h);
-    if (lane == 0)
-      reinterpret_cast<int4 *>(smem + S::kInfo)[slot] = make_int4(f.r, f.L, f.pg0, f.pg1);
-    mbar_arrive(qfull0 + 8 * slot);  // every lane publishes its own stores
+  for (int s = s_begin; s < s_end && ok; ++s) {
+    const KwSeg f = kw_seg(p, windowed, s, tile, lane == 0);
+    WinSpan win = {};
+    if (windowed && f.pg0 < f.pg1) win = WinSpan::make(f.L, p.q_len, window, sinks);
     const int pstart = p.page_indptr[f.r];
     const int pcount = p.page_indptr[f.r + 1] - pstart;
-    for (int pb = f.pg0; pb < f.pg1 && ok; pb += 32) {
-      const int cnt = min(32, f.pg1 - pb);
-      int id = 0;
-      if (lane < cnt) {
-        const int pg = windowed ? f.win.real_page(pb + lane) : pb + lane;
-        id = pg < pcount ? p.page_indices[pstart + pg] : -1;
-        if (id < 0 || id >= p.num_pages) {
-          status_or(p.tm, HPA_STATUS_BAD_PAGE);
-          id = -1;  // page 0 is read in its place and nothing is written
+    for (int pb = f.pg0; pb < f.pg1 && ok; pb += 32 * kStepPages) {
+      int id[kStepPages];
+#pragma unroll
+      for (int u = 0; u < kStepPages; ++u) {
+        const int v = pb + kStepPages * lane + u;
+        id[u] = 0;
+        if (v < f.pg1) {
+          const int pg = windowed ? win.real_page(v) : v;
+          id[u] = pg < pcount ? p.page_indices[pstart + pg] : -1;
+          if (id[u] < 0 || id[u] >= p.num_pages) {
+            status_or(p.tm, HPA_STATUS_BAD_PAGE);
+            id[u] = -1;  // page 0 is read in its place and nothing is written
+          }
         }
       }
-      for (int i = 0; i < cnt; ++i) {
-        const int pid = __shfl_sync(kFull, id, i);
-        good = 1;
+      const int steps = min(32, (f.pg1 - pb + kStepPages - 1) / kStepPages);
+      for (int i = 0; i < steps; ++i) {
+        const int n = min(kStepPages, f.pg1 - (pb + kStepPages * i));
+        const int i0 = __shfl_sync(kFull, id[0], i), i1 = __shfl_sync(kFull, id[1], i);
+        int good = 1;
         if (lane == 0) {
-          if (*abort_flag || !mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1)) {
+          if (*abort_flag || !mbar_wait_bounded_rolled(base + S::kKvEmpty + 8 * st, phase ^ 1)) {
             good = 0;
           } else {
-            const uint32_t fb = full0 + 8 * stage, dst = base + stage * S::kKBytes;
-            const int z = max(pid, 0) * p.Hkv + h;
-            pids[stage] = pid;
-            mbar_arrive_expect_tx(fb, S::kKBytes + (p.acc_in ? kAccBytes : 0));
-            tma_load_3d(dst, tmk, fb, 0, 0, z, pol);
-            if (KV == HPA_KV_BF16) tma_load_3d(dst + 8192, tmk, fb, 64, 0, z, pol);
-            if (p.acc_in)
-              bulk_load(base + S::kAcc + stage * kAccBytes,
-                        p.acc_in + static_cast<int64_t>(z) * PAGE, kAccBytes, fb);
-            issued |= 1u << stage;
-            parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
+            const uint32_t fb = base + S::kKvFull + 8 * st, dst = base + st * S::kStageBytes;
+            const uint32_t ab = base + S::kAccFull + 8 * slot_a;
+            pids[slot_a].x = i0;
+            pids[slot_a].y = n > 1 ? i1 : -1;
+            mbar_arrive_expect_tx(fb, n * S::kPageBytes);
+            if (p.acc_in) mbar_arrive_expect_tx(ab, n * kAccBytes);
+            else mbar_arrive(ab);
+#pragma unroll
+            for (int u = 0; u < kStepPages; ++u) {
+              if (u >= n) break;
+              const int z = max(u ? i1 : i0, 0) * p.Hkv + h;
+              tma_load_3d(dst + u * 8192, tmk, fb, 0, 0, z, pol);
+              if (KV == HPA_KV_BF16)  // [dim block][128 keys][128 B]
+                tma_load_3d(dst + kStepPages * 8192 + u * 8192, tmk, fb, 64, 0, z, pol);
+              if (p.acc_in)
+                bulk_load(base + S::kAcc + (slot_a * kStepPages + u) * kAccBytes,
+                          p.acc_in + static_cast<int64_t>(z) * PAGE, kAccBytes, ab);
+            }
+            issued |= 1u << st;
+            parity_bits = (parity_bits & ~(1u << st)) | (phase << st);
+            acc_issued |= 1u << slot_a;
+            acc_parity = (acc_parity & ~(1u << slot_a)) | (acc_phase << slot_a);
           }
         }
         ok = __shfl_sync(kFull, good, 0) != 0;
         if (!ok) break;
-        if (++stage == S::kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
+        if (++st == S::kStages) st = 0, phase ^= 1;
+        if (++slot_a == S::kAccs) slot_a = 0, acc_phase ^= 1;
       }
     }
   }
   if (!ok && lane == 0) {
     status_or(p.tm, HPA_STATUS_TIMEOUT);
     *abort_flag = 1;
-    for (int st = 0; st < S::kStages; ++st)  // no copy may land after the CTA has left
-      if (issued & (1u << st))
-        mbar_wait_bounded(full0 + 8 * st, (parity_bits >> st) & 1u, 1000000000ull);
+    // no copy may land after the CTA has left
+    for (int i = 0; i < S::kStages; ++i)
+      if (issued >> i & 1u)
+        mbar_wait_bounded_rolled(base + S::kKvFull + 8 * i, parity_bits >> i & 1u, 1000000000ull);
+    for (int i = 0; i < S::kAccs; ++i)
+      if (acc_issued >> i & 1u)
+        mbar_wait_bounded_rolled(base + S::kAccFull + 8 * i, acc_parity >> i & 1u, 1000000000ull);
   }
 }
 
-// ----------------------------------------------------------------------------- consumer
-// A fragments (16 keys x 128 dims) of the warp's keys of the page at kt.
-template <int KV>
-__device__ __forceinline__ void kw_load_keys(uint32_t (&a)[8][4], uint32_t kt, int w, int lane) {
-  if (KV == HPA_KV_BF16) {
-    const int mi = lane >> 3, key = 16 * w + (mi & 1) * 8 + (lane & 7);
-    const uint32_t row = kt + key * 128;
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-      const int chunk = (ks & 3) * 2 + (mi >> 1);
-      ldsm_x4(row + (ks >> 2) * 8192 + ((chunk ^ (lane & 7)) << 4), a[ks][0], a[ks][1], a[ks][2],
-              a[ks][3]);
-    }
-  } else {
-    // thread (r8, qd) widens dims [32 qd, 32 qd + 32) of keys r8 and r8 + 8; k-step ks
-    // is dims 32 qd + 4 ks + [0, 4), as the query rows are staged
-    const int r8 = lane >> 2, qd = lane & 3;
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const uint32_t row = kt + (16 * w + 8 * hf + r8) * 128;
-      uint32_t u[8];
-      lds128(row + (((2 * qd) ^ r8) << 4), u[0], u[1], u[2], u[3]);
-      lds128(row + (((2 * qd + 1) ^ r8) << 4), u[4], u[5], u[6], u[7]);
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        a[ks][hf] = e4m3x2_to_f16x2(static_cast<uint16_t>(u[ks] & 0xffffu));
-        a[ks][2 + hf] = e4m3x2_to_f16x2(static_cast<uint16_t>(u[ks] >> 16));
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ void kw_load_rows(uint32_t (&b)[8][2], uint32_t qrow, int lane) {
-#pragma unroll
-  for (int ks = 0; ks < 8; ++ks)
-    lds64(qrow + (lane >> 2) * kQStride + ks * 32 + (lane & 3) * 8, b[ks][0], b[ks][1]);
-}
-
-template <int KV, int RT>
-__device__ void kw_consumer(const KeyWeightsParams &p, uint8_t *smem, int s_begin, int s_end,
-                            bool windowed) {
-  using S = KwCfg<KV, RT>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int w = warp % kGroupWarps, group = warp / kGroupWarps;
-  const int r8 = lane >> 2, qd = lane & 3, h = blockIdx.y;
+// ----------------------------------------------------------------------------- MMA issuer
+template <int KV, int RP>
+__device__ void kw_issuer(const KeyWeightsParams &p, uint8_t *smem, int n_seg, uint32_t tmem) {
+  using S = KwCfg<KV, RP>;
   const uint32_t base = smem_u32(smem);
-  const uint32_t full0 = base + S::kBars, empty0 = full0 + 8 * S::kStages;
-  const uint32_t qfull0 = empty0 + 8 * S::kStages, qempty0 = qfull0 + 16;
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kFlag);
-  volatile int *pids = reinterpret_cast<volatile int *>(smem + S::kPid);
-  const int window = windowed ? p.tm[TM_WINDOW] : 0, sinks = windowed ? p.tm[TM_SINKS] : 0;
-  const int q_len = p.q_len, n_tiles = RT ? RT : (p.rows + 7) / 8;
-  int stage = 0, turn = 0;
-  uint32_t phase = 0;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kAbort);
+  const uint32_t idesc = tc_idesc(KV == HPA_KV_BF16 ? 1 : 0, S::kN, 0, 0);
+  int st = 0, buf = 0;
+  uint32_t phase = 0, sphase = 0;
   bool ok = true;
-  for (int k = 0; k < s_end - s_begin && ok; ++k) {
+  for (int k = 0; k < n_seg && ok; ++k) {
     const int slot = k & 1;
-    ok = __all_sync(kFull, !*abort_flag && mbar_wait_bounded(qfull0 + 8 * slot, (k >> 1) & 1));
+    if (*abort_flag || !mbar_wait_bounded_rolled(base + S::kQFull + 8 * slot, (k >> 1) & 1)) {
+      ok = false;
+      break;
+    }
+    const int4 info = reinterpret_cast<const int4 *>(smem + S::kInfo)[slot];
+    const int steps = (info.w - info.z + kStepPages - 1) / kStepPages;
+    const uint32_t q = base + S::kQ + slot * S::kQSlot;
+    for (int i = 0; i < steps; ++i) {
+      if (*abort_flag || !mbar_wait_bounded_rolled(base + S::kKvFull + 8 * st, phase) ||
+          !mbar_wait_bounded_rolled(base + S::kSFree + 8 * buf, sphase ^ 1)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t kb = base + st * S::kStageBytes, d = tmem + buf * S::kN;
+      if (KV == HPA_KV_BF16) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)  // 16 dims per MMA
+          tc_mma<KV>(d, tc_desc(kb + (kk >> 2) * (kStepPages * 8192) + (kk & 3) * 32, 16, 1024),
+                     tc_desc(q + (kk >> 2) * (S::kN * 128) + (kk & 3) * 32, 16, 1024), idesc,
+                     kk > 0);
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)  // 32 dims per MMA
+          tc_mma<KV>(d, tc_desc(kb + kk * 32, 16, 1024), tc_desc(q + kk * 32, 16, 1024), idesc,
+                     kk > 0);
+      }
+      tc_commit(base + S::kSFull + 8 * buf);
+      tc_commit(base + S::kKvEmpty + 8 * st);
+      if (i == steps - 1) tc_commit(base + S::kQEmpty + 8 * slot);
+      if (++st == S::kStages) st = 0, phase ^= 1;
+      if (++buf == S::kBufs) buf = 0, sphase ^= 1;
+    }
+    if (steps == 0) mbar_arrive(base + S::kQEmpty + 8 * slot);
+  }
+  if (!ok) {
+    status_or(p.tm, HPA_STATUS_TIMEOUT);
+    *abort_flag = 1;
+  }
+  tc_commit(base + S::kDrain);  // every MMA completes before the CTA frees its TMEM
+}
+
+// ----------------------------------------------------------------------------- compute
+template <int KV, int RP>
+__device__ void kw_compute(const KeyWeightsParams &p, uint8_t *smem, int n_seg, uint32_t tmem,
+                           bool windowed) {
+  using S = KwCfg<KV, RP>;
+  constexpr int kPart = RP < 16 ? RP : 16;  // rows read from TMEM at a time
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
+  const int w = warp % kGroupWarps, group = warp / kGroupWarps, t = 32 * w + lane;
+  const uint32_t base = smem_u32(smem);
+  const uint32_t lane_t = tmem + (static_cast<uint32_t>(32 * w) << 16);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kAbort);
+  const int *jrow = reinterpret_cast<const int *>(smem + S::kJRow);
+  const int window = windowed ? p.tm[TM_WINDOW] : 0, sinks = windowed ? p.tm[TM_SINKS] : 0;
+  const int q_len = p.q_len;
+  int n = 0;  // step of the CTA
+  bool ok = true;
+  for (int k = 0; k < n_seg && ok; ++k) {
+    const int slot = k & 1;
+    ok = __all_sync(kFull, !*abort_flag && mbar_wait_bounded_rolled(base + S::kQFull + 8 * slot,
+                                                                    (k >> 1) & 1));
     if (!ok) break;
     const int4 info = reinterpret_cast<const int4 *>(smem + S::kInfo)[slot];
     const int L = info.y, pg0 = info.z, pg1 = info.w;
+    const int steps = (pg1 - pg0 + kStepPages - 1) / kStepPages;
     WinSpan win = {};
-    if (windowed && pg0 < pg1) win = WinSpan::make(L, q_len, window, sinks);
+    if (windowed && steps > 0) win = WinSpan::make(L, q_len, window, sinks);
     const int lim_min = L - q_len + 1;  // first key hidden from some row
-    const uint32_t qs = base + S::kQ + slot * S::kQSlot;
-    const float4 *rc = reinterpret_cast<const float4 *>(smem + S::kRow) + slot * (S::kRows / 2);
-    uint32_t qb[RT ? RT : 1][8][2];
-    float4 qc[RT ? RT : 1];
-    if (RT) {
+    const uint32_t rows = base + S::kRow + slot * RP * 8;
+    for (int i = (group + kGroups - n % kGroups) % kGroups; i < steps; i += kGroups) {
+      const int m = n + i, buf = m % S::kBufs, sa = m % S::kAccs;
+      ok = __all_sync(kFull,
+                      !*abort_flag &&
+                          mbar_wait_bounded_rolled(base + S::kAccFull + 8 * sa, m / S::kAccs & 1) &&
+                          mbar_wait_bounded_rolled(base + S::kSFull + 8 * buf, m / S::kBufs & 1));
+      if (!ok) break;
+      tc_fence_after();
+      const int v = pg0 + kStepPages * i + t / PAGE;  // compact page of this thread's key
+      const int key = (windowed ? win.real_page(v) : v) * PAGE + t % PAGE;
+      const int2 pid2 = const_cast<const int2 *>(reinterpret_cast<int2 *>(smem + S::kPid))[sa];
+      const int pid = t < PAGE ? pid2.x : pid2.y;
+      // some rows do not see this key: the causal end, a window's start
+      const bool part =
+          key >= lim_min || (windowed && key >= sinks && key < win.start + q_len - 1);
+      const bool any_part = __any_sync(kFull, part);
+      f32x2 sum = pk(0.f, 0.f);
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        kw_load_rows(qb[t], qs + t * 8 * kQStride, lane);
-        qc[t] = rc[4 * t + qd];
+      for (int r0 = 0; r0 < RP; r0 += kPart) {
+        float s[kPart], u[KV == HPA_KV_E4M3 ? kPart : 8];
+#pragma unroll
+        for (int c = 0; c < kPart; c += 8) {
+          const uint32_t col = lane_t + buf * S::kN + r0 + c;
+          tc_ld8(col, *reinterpret_cast<float(*)[8]>(s + c));
+          if (KV == HPA_KV_E4M3) tc_ld8(col + RP, *reinterpret_cast<float(*)[8]>(u + c));
+        }
+        tc_wait_ld();
+        if (r0 + kPart >= RP) {  // every score of the step is in registers
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(base + S::kSFree + 8 * buf);
+        }
+#pragma unroll
+        for (int e = 0; e < kPart; e += 2) {
+          uint32_t c0, l0, c1, l1;  // two rows' score factor and lse
+          lds128(rows + (r0 + e) * 8, c0, l0, c1, l1);
+          f32x2 x = pk(s[e], s[e + 1]);
+          if (KV == HPA_KV_E4M3) x = fma2(pk(u[e], u[e + 1]), pk(0.0625f, 0.0625f), x);
+          float a, b;
+          upk(fma2(x, pk(__uint_as_float(c0), __uint_as_float(c1)),
+                   pk(-__uint_as_float(l0), -__uint_as_float(l1))),
+              a, b);
+          a = exp2f(a), b = exp2f(b);
+          if (any_part) {
+            auto hidden = [&](int j) {
+              return key >= lim_min + j || (windowed && key >= sinks && key < win.start + j);
+            };
+            if (hidden(jrow[r0 + e])) a = 0.f;
+            if (hidden(jrow[r0 + e + 1])) b = 0.f;
+          }
+          sum = add2(sum, pk(a, b));
+        }
+      }
+      float wt, w1;
+      upk(sum, wt, w1);
+      wt += w1;
+      if (pid >= 0 && key < L && !(windowed && key >= sinks && key < win.low)) {
+        if (p.acc_in && key < L - q_len)
+          wt += p.decay * reinterpret_cast<const float *>(smem + S::kAcc)[sa * 128 + t];
+        p.acc_out[(static_cast<int64_t>(pid) * p.Hkv + h) * PAGE + t % PAGE] = wt;
       }
     }
-    for (int pg = pg0; pg < pg1; ++pg) {
-      const bool mine = S::kGroups == 1 || turn == group;
-      if (S::kGroups > 1 && ++turn == S::kGroups) turn = 0;
-      if (mine) {
-        ok = __all_sync(kFull, !*abort_flag && mbar_wait_bounded(full0 + 8 * stage, phase));
-        if (!ok) break;
-        const int key0 = (windowed ? win.real_page(pg) : pg) * PAGE, wk = key0 + 16 * w;
-        uint32_t a[8][4];
-        kw_load_keys<KV>(a, base + stage * S::kKBytes, w, lane);
-        // some rows do not see some of the warp's keys: the causal end, a window's start
-        const bool part = wk + 16 > lim_min ||
-                          (windowed && wk < win.start + q_len - 1 && wk + 16 > sinks);
-        float w0 = 0.f, w1 = 0.f;  // keys wk + r8 and wk + r8 + 8, rows 8 t + 2 qd + {0, 1}
-        auto tile = [&](const uint32_t(&b)[8][2], float4 c, int t) {
-          float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            if (KV == HPA_KV_BF16) mma_bf16(s, a[ks], b[ks][0], b[ks][1]);
-            else mma_f16(s, a[ks], b[ks][0], b[ks][1]);
-          }
-          float e[4];
-          e[0] = exp2f(fmaf(s[0], c.x, -c.y));
-          e[1] = exp2f(fmaf(s[1], c.z, -c.w));
-          e[2] = exp2f(fmaf(s[2], c.x, -c.y));
-          e[3] = exp2f(fmaf(s[3], c.z, -c.w));
-          if (part) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int j = (8 * t + 2 * qd + (x & 1)) / p.G, key = wk + r8 + 8 * (x >> 1);
-              if (key >= lim_min + j || (windowed && key >= sinks && key < win.start + j)) e[x] = 0.f;
-            }
-          }
-          w0 += e[0] + e[1];
-          w1 += e[2] + e[3];
-        };
-        if (RT) {
-#pragma unroll
-          for (int t = 0; t < RT; ++t) tile(qb[t], qc[t], t);
-        } else {
-          for (int t = 0; t < n_tiles; ++t) {
-            kw_load_rows(qb[0], qs + t * 8 * kQStride, lane);
-            tile(qb[0], rc[4 * t + qd], t);
-          }
-        }
-        w0 += __shfl_xor_sync(kFull, w0, 1);
-        w0 += __shfl_xor_sync(kFull, w0, 2);
-        w1 += __shfl_xor_sync(kFull, w1, 1);
-        w1 += __shfl_xor_sync(kFull, w1, 2);
-        const int pid = pids[stage], at = 16 * w + r8 + 8 * qd, key = key0 + at;
-        if (qd < 2 && pid >= 0 && key < L && !(windowed && key >= sinks && key < win.low)) {
-          float v = qd ? w1 : w0;
-          if (p.acc_in && key < L - q_len)
-            v += p.decay * reinterpret_cast<const float *>(smem + S::kAcc + stage * kAccBytes)[at];
-          p.acc_out[(static_cast<int64_t>(pid) * p.Hkv + h) * PAGE + at] = v;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty0 + 8 * stage);
-      }
-      if (++stage == S::kStages) {
-        stage = 0;
-        phase ^= 1;
-      }
-    }
+    n += steps;
     __syncwarp();
-    if (lane == 0) mbar_arrive(qempty0 + 8 * slot);
+    if (lane == 0) mbar_arrive(base + S::kQEmpty + 8 * slot);
   }
   if (!ok && lane == 0) {
     status_or(p.tm, HPA_STATUS_TIMEOUT);
@@ -371,16 +419,17 @@ __device__ void kw_consumer(const KeyWeightsParams &p, uint8_t *smem, int s_begi
 }
 
 // ----------------------------------------------------------------------------- kernel
-template <int KV, int RT>
-__global__ void __launch_bounds__(KwCfg<KV, RT>::kThreads, RT ? 2 : 1)
+template <int KV, int RP>
+__global__ void __launch_bounds__(KwCfg<KV, RP>::kThreads, RP <= 16 ? 2 : 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap tmk, const KeyWeightsParams p) {
-  using S = KwCfg<KV, RT>;
+  using S = KwCfg<KV, RP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int c = blockIdx.x;
+  const int c = blockIdx.x, warp = threadIdx.x >> 5;
   __shared__ int hdr[5];  // go, tile, s_begin, s_end, windowed
   const uint32_t base = smem_u32(smem);
+  if (threadIdx.x == 32) prefetch_tmap(&tmk);
   pdl_wait();  // nothing above reads what an earlier kernel writes
   if (threadIdx.x == 0) {
     const int32_t *tm = p.tm;
@@ -402,35 +451,65 @@ __global__ void __launch_bounds__(KwCfg<KV, RT>::kThreads, RT ? 2 : 1)
     hdr[3] = go ? tm[p.lay.cta_seg + c + 1] : 0;
     hdr[0] = go && hdr[2] < hdr[3];
     hdr[4] = windowed;
-    for (int st = 0; st < S::kStages; ++st) {
-      mbar_init(base + S::kBars + 8 * st, 1);
-      mbar_init(base + S::kBars + 8 * (S::kStages + st), kGroupWarps);
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(base + S::kKvFull + 8 * i, 1);   // TMA bytes
+      mbar_init(base + S::kKvEmpty + 8 * i, 1);  // MMA commit
     }
-    for (int sl = 0; sl < 2; ++sl) {
-      mbar_init(base + S::kBars + 8 * (2 * S::kStages + sl), 32);                     // qfull
-      mbar_init(base + S::kBars + 8 * (2 * S::kStages + 2 + sl), S::kConsumers);      // qempty
+    for (int i = 0; i < S::kBufs; ++i) {
+      mbar_init(base + S::kSFull + 8 * i, 1);            // MMA commit
+      mbar_init(base + S::kSFree + 8 * i, kGroupWarps);  // the step's compute warps
     }
-    *reinterpret_cast<int *>(smem + S::kFlag) = 0;
+    for (int i = 0; i < S::kAccs; ++i) mbar_init(base + S::kAccFull + 8 * i, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(base + S::kQFull + 8 * i, 32 * S::kStagers);
+      mbar_init(base + S::kQEmpty + 8 * i, 1 + kCompute);
+    }
+    mbar_init(base + S::kDrain, 1);
+    *reinterpret_cast<int *>(smem + S::kAbort) = 0;
     fence_barrier_init();
   }
+  if (threadIdx.x < RP) reinterpret_cast<int *>(smem + S::kJRow)[threadIdx.x] = threadIdx.x / p.G;
   __syncthreads();
   pdl_launch_dependents();
   if (!hdr[0]) return;
-  if (threadIdx.x >= S::kConsumers * 32)
-    kw_producer<KV, RT>(p, &tmk, smem, hdr[2], hdr[3], hdr[1], hdr[4]);
-  else
-    kw_consumer<KV, RT>(p, smem, hdr[2], hdr[3], hdr[4]);
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     base + S::kTmemAt),
+                 "r"(S::kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + S::kTmemAt);
+  if (warp < kCompute)
+    kw_compute<KV, RP>(p, smem, hdr[3] - hdr[2], tmem, hdr[4]);
+  else if (warp == kCompute)
+    kw_producer<KV, RP>(p, &tmk, smem, hdr[2], hdr[3], hdr[1], hdr[4]);
+  else if (warp >= kCompute + 2)
+    kw_stager<KV, RP>(p, smem, hdr[2], hdr[3] - hdr[2], hdr[1], hdr[4], warp - kCompute - 2);
+  else if ((threadIdx.x & 31) == 0)
+    kw_issuer<KV, RP>(p, smem, hdr[3] - hdr[2], tmem);
+  tc_fence_before();
+  __syncthreads();
+  mbar_wait_bounded_rolled(base + S::kDrain, 0, 1000000000ull);
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kTmem)
+                 : "memory");
+  }
 }
 
-template <int KV, int RT>
+template <int KV, int RP>
 cudaError_t launch(const KeyWeightsParams &p, const CUtensorMap &tmk, cudaStream_t s) {
-  using S = KwCfg<KV, RT>;
+  using S = KwCfg<KV, RP>;
   static int configured[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !configured[dev]) {
-    e = cudaFuncSetAttribute(key_weights_kernel<KV, RT>,
+    e = cudaFuncSetAttribute(key_weights_kernel<KV, RP>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, S::kAlloc);
     if (e != cudaSuccess) return e;
     if (dev < 64) configured[dev] = 1;
@@ -445,20 +524,24 @@ cudaError_t launch(const KeyWeightsParams &p, const CUtensorMap &tmk, cudaStream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, key_weights_kernel<KV, RT>, tmk, p);
+  return cudaLaunchKernelEx(&cfg, key_weights_kernel<KV, RP>, tmk, p);
+}
+
+template <int KV>
+cudaError_t launch_kv(const KeyWeightsParams &p, const CUtensorMap &tmk, cudaStream_t s) {
+  return p.rows <= 8    ? launch<KV, 8>(p, tmk, s)
+         : p.rows <= 16 ? launch<KV, 16>(p, tmk, s)
+         : p.rows <= 32 ? launch<KV, 32>(p, tmk, s)
+         : p.rows <= 48 ? launch<KV, 48>(p, tmk, s)
+                        : launch<KV, 64>(p, tmk, s);
 }
 
 }  // namespace
 
 cudaError_t launch_key_weights(const KeyWeightsParams &p, const CUtensorMap &tmk, int kv_dtype,
                                cudaStream_t s) {
-  if (kv_dtype == HPA_KV_BF16)
-    return p.rows <= 8    ? launch<HPA_KV_BF16, 1>(p, tmk, s)
-           : p.rows <= 16 ? launch<HPA_KV_BF16, 2>(p, tmk, s)
-                          : launch<HPA_KV_BF16, 0>(p, tmk, s);
-  return p.rows <= 8    ? launch<HPA_KV_E4M3, 1>(p, tmk, s)
-         : p.rows <= 16 ? launch<HPA_KV_E4M3, 2>(p, tmk, s)
-                        : launch<HPA_KV_E4M3, 0>(p, tmk, s);
+  return kv_dtype == HPA_KV_BF16 ? launch_kv<HPA_KV_BF16>(p, tmk, s)
+                                 : launch_kv<HPA_KV_E4M3>(p, tmk, s);
 }
 
 }  // namespace hpa
