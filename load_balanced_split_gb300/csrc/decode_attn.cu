@@ -49,6 +49,7 @@ __host__ __device__ constexpr int merge_phys(int dd) { return dd + 4 * (dd >> 5)
 // accumulators are rescaled: P values stay <= 256, well inside bf16/f16 range.
 constexpr float kRescaleSlack = 8.f;
 constexpr int kThreads = (kConsumerWarps + 1) * 32;
+constexpr int kWinThreads = kThreads + 32;  // a staging warp beside the producer
 constexpr uint32_t kFull = 0xffffffffu;
 
 template <int KV>
@@ -116,7 +117,7 @@ __device__ __forceinline__ SegInfo seg_info(const AttnParams &p, int s, int tile
 }
 
 // ----------------------------------------------------------------------------- producer
-template <int KV, bool FUSED, bool ALLH, bool WIN>
+template <int KV, bool FUSED, bool ALLH>
 __device__ void producer(const AttnParams &p, const CUtensorMap *tmk, const CUtensorMap *tmv,
                          uint8_t *smem, int s_begin, int s_end, int tile, int h0) {
   using S = Smem<KV>;
@@ -131,7 +132,6 @@ __device__ void producer(const AttnParams &p, const CUtensorMap *tmk, const CUte
     prefetch_tmap(tmv);
   }
   const uint32_t qfull0 = empty0 + 8 * S::kStages, qempty0 = qfull0 + 16;
-  const int window = WIN ? p.tm[TM_WINDOW] : 0, sinks = WIN ? p.tm[TM_SINKS] : 0;
   int stage = 0;
   uint32_t phase = 0, issued = 0, parity_bits = 0;
   bool ok = true;
@@ -140,9 +140,7 @@ __device__ void producer(const AttnParams &p, const CUtensorMap *tmk, const CUte
   const int hpc = ALLH ? p.heads_per_cta : 1, n_items = (s_end - s_begin) * hpc;
   for (int k = 0; k < n_items && ok; ++k) {
     const int s = s_begin + k / hpc, h = h0 + k % hpc;
-    const SegInfo f = seg_info<WIN>(p, s, tile, blockIdx.x, lane == 0 && h == h0);
-    WinSpan win = {};
-    if (WIN && f.pg0 < f.pg1) win = WinSpan::make(f.L, p.q_len, window, sinks);
+    const SegInfo f = seg_info<false>(p, s, tile, blockIdx.x, lane == 0 && h == h0);
     // stage the item's segment info and query rows for the consumers
     {
       const int slot = k & 1;
@@ -180,8 +178,7 @@ __device__ void producer(const AttnParams &p, const CUtensorMap *tmk, const CUte
       const int cnt = min(32, f.pg1 - pb);
       int id = 0;
       if (lane < cnt) {
-        const int pg = WIN ? win.real_page(pb + lane) : pb + lane;
-        id = pg < pcount ? pidx[pg] : -1;
+        id = pb + lane < pcount ? pidx[pb + lane] : -1;
         if (id < 0 || id >= p.num_pages) {  // bad id or too short a page list
           status_or(p.tm, HPA_STATUS_BAD_PAGE);
           id = 0;
@@ -218,6 +215,167 @@ __device__ void producer(const AttnParams &p, const CUtensorMap *tmk, const CUte
           phase ^= 1;
         }
       }
+    }
+  }
+  if (!ok && lane == 0) {
+    status_or(p.tm, HPA_STATUS_TIMEOUT);
+    *abort_flag = 1;
+    // never leave the CTA with copies still landing in its shared memory
+    for (int st = 0; st < S::kStages; ++st)
+      if (issued & (1u << st))
+        mbar_wait_bounded(full0 + 8 * st, (parity_bits >> st) & 1u, 1000000000ull);
+  }
+}
+
+// ----------------------------------------------------------------------------- window roles
+// Windows make short segments (a window of 4096 keys is 64 pages, where a long request has
+// thousands), and the reads that lead to a segment's first page -- its row, its length,
+// its page range, the page ids -- each wait for the one before, behind the page traffic.
+// So the window kernel gives the staging to a warp of its own that runs up to two segments
+// ahead, and the producer warp asks for the next 32 page ids, of the next segment where
+// this one ends, before it issues the pages it has.
+template <int KV>
+__device__ void win_stager(const AttnParams &p, uint8_t *smem, int s_begin, int s_end, int tile,
+                           int h, int window, int sinks) {
+  using S = Smem<KV>;
+  const int lane = threadIdx.x & 31, G = p.G, rb = row_base(), rows = group_rows(p);
+  const uint32_t base = smem_u32(smem);
+  const uint32_t qfull0 = base + S::kBars + 16 * S::kStages, qempty0 = qfull0 + 16;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kFlag);
+  // this lane's 16-byte chunks of the group's rows (256 bytes each): chunk lane + 32 u
+  constexpr int kChunks = MAX_ROWS * 16 / 32;
+  int64_t off[kChunks];
+#pragma unroll
+  for (int u = 0; u < kChunks; ++u) {
+    const int row = (lane + 32 * u) >> 4, j = (rb + row) / G, g = (rb + row) - j * G;
+    off[u] = row < rows ? (static_cast<int64_t>(j) * p.Hq + h * G + g) * HEAD_DIM +
+                              ((lane + 32 * u) & 15) * 8
+                        : -1;
+  }
+  for (int s = s_begin; s < s_end; ++s) {
+    const int k = s - s_begin, slot = k & 1;
+    const SegInfo f = seg_info<true>(p, s, tile, blockIdx.x, lane == 0);
+    const int pstart = p.page_indptr[f.r], pcount = p.page_indptr[f.r + 1] - pstart;
+    WinSpan win = {};
+    if (f.pg0 < f.pg1) win = WinSpan::make(f.L, p.q_len, window, sinks);
+    const __nv_bfloat16 *q = p.q + static_cast<int64_t>(f.r) * p.q_len * p.Hq * HEAD_DIM;
+    int4 v[kChunks];
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u)
+      if (off[u] >= 0) v[u] = *reinterpret_cast<const int4 *>(q + off[u]);
+    int good = 1;
+    if (lane == 0) good = !*abort_flag && mbar_wait_bounded(qempty0 + 8 * slot, ((k >> 1) & 1) ^ 1);
+    if (!__shfl_sync(kFull, good, 0)) {
+      if (lane == 0) {
+        status_or(p.tm, HPA_STATUS_TIMEOUT);
+        *abort_flag = 1;
+      }
+      return;
+    }
+    uint8_t *qs = smem + S::kQ + slot * kQSlotBytes;
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u)
+      if (off[u] >= 0)
+        *reinterpret_cast<int4 *>(qs + ((lane + 32 * u) >> 4) * kQRowBytes +
+                                  ((lane + 32 * u) & 15) * 16) = v[u];
+    if (lane == 0) {
+      int4 *info = reinterpret_cast<int4 *>(smem + S::kInfo) + 2 * slot;
+      info[0] = make_int4(f.r, f.L, f.klo, f.khi);
+      info[1] = make_int4(pstart, pcount, win.sink_pages, win.hidden);
+    }
+    mbar_arrive(qfull0 + 8 * slot);  // every lane publishes its own stores
+  }
+}
+
+template <int KV>
+__device__ void win_producer(const AttnParams &p, const CUtensorMap *tmk, const CUtensorMap *tmv,
+                             uint8_t *smem, int n_seg, int h) {
+  using S = Smem<KV>;
+  const int lane = threadIdx.x & 31;
+  const uint32_t base = smem_u32(smem);
+  const uint32_t full0 = base + S::kBars, empty0 = full0 + 8 * S::kStages;
+  const uint32_t qfull0 = empty0 + 8 * S::kStages, qempty0 = qfull0 + 16;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kFlag);
+  uint64_t pol = 0;
+  if (lane == 0) pol = l2_policy_evict_first();
+  int stage = 0;
+  uint32_t phase = 0, issued = 0, parity_bits = 0;
+  // The next 32 compact pages [pb, pb + 32) of the segment at hand, which ends at pg1; `id`:
+  // this lane's page id.  where: first page index, page count, sink pages, hidden pages.
+  int k = 0, pb = 0, pg1 = 0, id = 0;
+  int4 where = make_int4(0, 0, 0, 0);
+  bool ok = true, more = true;
+  // Takes the next staged segment where the one at hand is through, and asks for the ids.
+  // False if it is not staged yet (not with `wait`, unless the wait gave up: ok); `more`
+  // is cleared after the last segment.
+  auto ask = [&](bool wait) {
+    while (pb >= pg1) {  // again where a malformed segment has no pages
+      if (k == n_seg) {
+        more = false;
+        return true;
+      }
+      const uint32_t bar = qfull0 + 8 * (k & 1), parity = (k >> 1) & 1;
+      const bool staged = wait ? !*abort_flag && mbar_wait_bounded(bar, parity)
+                               : mbar_try_wait(bar, parity);
+      if (!__all_sync(kFull, staged)) {
+        ok = !wait;
+        return false;
+      }
+      const int4 *info = reinterpret_cast<const int4 *>(smem + S::kInfo) + 2 * (k & 1);
+      pb = info[0].z / PAGE;
+      pg1 = (info[0].w + PAGE - 1) / PAGE;
+      where = info[1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qempty0 + 8 * (k & 1));
+      ++k;
+    }
+    id = 0;
+    if (pb + lane < pg1) {
+      const int pg = pb + lane < where.z ? pb + lane : pb + lane + where.w;
+      id = pg < where.y ? p.page_indices[where.x + pg] : -1;
+    }
+    return true;
+  };
+  bool asked = ask(true);
+  while (ok && more) {
+    const int cnt = min(32, pg1 - pb);
+    int ids = id;
+    pb += 32;
+    asked = ask(false);
+    if (lane < cnt && (ids < 0 || ids >= p.num_pages)) {  // bad id or too short a page list
+      status_or(p.tm, HPA_STATUS_BAD_PAGE);
+      ids = 0;
+    }
+    for (int i = 0; i < cnt; ++i) {
+      const int pid = __shfl_sync(kFull, ids, i);
+      int good = 1;
+      if (lane == 0) {
+        if (*abort_flag || !mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1)) {
+          good = 0;
+        } else {
+          const uint32_t fb = full0 + 8 * stage, dst = base + stage * S::kStageBytes;
+          const int z = pid * p.Hkv + h;
+          mbar_arrive_expect_tx(fb, S::kStageBytes);
+          if (KV == HPA_KV_BF16) {
+            tma_load_3d(dst, tmk, fb, 0, 0, z, pol);
+            tma_load_3d(dst + 8192, tmk, fb, 64, 0, z, pol);
+            tma_load_3d(dst + 16384, tmv, fb, 0, 0, z, pol);
+            tma_load_3d(dst + 24576, tmv, fb, 64, 0, z, pol);
+          } else {
+            tma_load_3d(dst, tmk, fb, 0, 0, z, pol);
+            tma_load_3d(dst + 8192, tmv, fb, 0, 0, z, pol);
+          }
+          issued |= 1u << stage;
+          parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
+        }
+      }
+      ok = __shfl_sync(kFull, good, 0) != 0;
+      if (!ok) break;
+      if (++stage == S::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+      if (!asked) asked = ask(i + 1 == cnt);  // until the next segment is staged
     }
   }
   if (!ok && lane == 0) {
@@ -474,7 +632,7 @@ __device__ void merge_request(const AttnParams &p, int r, int h, int seg_first, 
 // ----------------------------------------------------------------------------- consumer
 template <int KV, bool FUSED, bool ALLH, bool WIN>
 __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_end, int tile,
-                         int h0) {
+                         int h0, int window, int sinks) {
   using S = Smem<KV>;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r8 = lane >> 2, qd = lane & 3;
@@ -494,7 +652,6 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
   const uint32_t qfull0 = empty0 + 8 * S::kStages, qempty0 = qfull0 + 16;
   int stage = 0;
   uint32_t phase = 0;
-  const int window = WIN ? p.tm[TM_WINDOW] : 0, sinks = WIN ? p.tm[TM_SINKS] : 0;
   // score and output scales of the KV head (loaded once on the per-head grid)
   float sl2_h = p.scale_log2, vsc_h = 1.f;
   if (!ALLH && KV == HPA_KV_E4M3) {
@@ -532,9 +689,15 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
     const int lim_min = f.L - q_len + 1;  // first key hidden from some row
     const int lim0 = v0 ? f.L - q_len + 1 + j0 : f.L;
     const int lim1 = v1 ? f.L - q_len + 1 + j1 : f.L;
-    // sliding window: row j sees key i < lim when i < sinks or i >= start + j
-    WinSpan win = {};
-    if (WIN && f.pg0 < f.pg1) win = WinSpan::make(f.L, q_len, window, sinks);
+    // Sliding window: row j sees key i < lim when i < sinks or i >= start + j.  Compact pages
+    // [clear0, clear1) hold no key that some row does not see; the others look closer.
+    int clear0 = 0, clear1 = 0;
+    if (WIN && f.pg0 < f.pg1) {
+      const WinSpan win = WinSpan::make(f.L, q_len, window, sinks);
+      const int first = win.start + q_len - 1;  // where the last row's window starts
+      clear0 = first > 0 ? (first - 1) / PAGE + 1 - win.hidden : 0;
+      clear1 = lim_min / PAGE - win.hidden;
+    }
 
     // query fragments (A operand, 16 rows x 128) from the staged rows
     uint32_t qa[8][4];
@@ -599,20 +762,24 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
-    for (int pg = f.pg0; pg < f.pg1; ++pg) {
+    // One page; EDGE looks for keys that some row does not see.  False when a wait gave up.
+    auto page = [&](int pg, auto edge_tag) {
+      constexpr bool EDGE = decltype(edge_tag)::value;
       const bool got = !(*abort_flag) && mbar_wait_bounded(full0 + 8 * stage, phase);
       if (!__all_sync(kFull, got)) {
         ok = false;  // the rest of this CTA's work is abandoned (see below)
-        break;
+        return false;
       }
       uint8_t *kt = smem + stage * S::kStageBytes;
       uint8_t *vt = kt + Cfg<KV>::kKBytes;
+      WinSpan win = {};
+      if (WIN && EDGE) win = WinSpan::make(f.L, q_len, window, sinks);
       const int key0 = (WIN ? win.real_page(pg) : pg) * PAGE, wk = key0 + 16 * w;
       // the warp's 16 keys reach past the request's end, or some key among them lies
       // between the sinks and the first token's window: V rows that no token sees are
       // zeroed, so what they hold (NaN among it) stays out of the sums
-      bool tail = wk + 16 > f.L;
-      if (WIN) tail |= wk < win.low && wk + 16 > sinks;
+      bool tail = EDGE && wk + 16 > f.L;
+      if (WIN && EDGE) tail |= wk < win.low && wk + 16 > sinks;
       if (tail) {
         zero_hidden_rows<KV, WIN>(vt, w, wk, f.L, sinks, win.low, lane);
         __syncwarp();
@@ -624,7 +791,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[nt][e] *= e < 2 ? sl2_0 : sl2_1;
-      if (wk + 16 > lim_min) {
+      if (EDGE && wk + 16 > lim_min) {
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -633,7 +800,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
             if (key >= (e < 2 ? lim0 : lim1)) sc[nt][e] = -CUDART_INF_F;
           }
       }
-      if (WIN && wk < win.start + q_len - 1 && wk + 16 > sinks) {
+      if (WIN && EDGE && wk < win.start + q_len - 1 && wk + 16 > sinks) {
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -679,7 +846,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
           o[i][3] *= a1;
         }
       }
-      if (WIN && q_len > 1) {
+      if (WIN && EDGE && q_len > 1) {
         const int pl = max(win.low, sinks);  // keys some tokens see: [pl, ph), [lim_min, L)
         const int ph = win.start + q_len - 1;
         if ((wk < ph && wk + 16 > pl) || (wk < f.L && wk + 16 > lim_min))
@@ -707,6 +874,18 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
       if (++stage == S::kStages) {
         stage = 0;
         phase ^= 1;
+      }
+      return true;
+    };
+    if constexpr (!WIN) {
+      for (int pg = f.pg0; pg < f.pg1; ++pg)
+        if (!page(pg, std::true_type())) break;
+    } else {
+      // the clear pages' loop is a copy without the masks (191 -> 163 us of a 1.08 GB batch
+      // against one loop that tests each page)
+      for (int pg = f.pg0; pg < f.pg1; ++pg) {
+        const bool clear = pg >= clear0 && pg < clear1;
+        if (clear ? !page(pg, std::false_type()) : !page(pg, std::true_type())) break;
       }
     }
     // A timed-out warp flags the map and raises the CTA's abort flag; it still
@@ -850,7 +1029,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
 
 // ----------------------------------------------------------------------------- kernel
 template <int KV, bool FUSED, bool ALLH, bool WIN>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(WIN ? kWinThreads : kThreads, 2)
     decode_attn_kernel(const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, const AttnParams p) {
   using S = Smem<KV>;
@@ -858,43 +1037,55 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int c = blockIdx.x, h0 = ALLH ? 0 : blockIdx.y;  // first KV head of the CTA
-  __shared__ int hdr[5];  // go, tile, s_begin, s_end, bad map -- read once, used by all threads
+  // go, tile, s_begin, s_end, then bad map (or window and sinks) -- read once, for all threads
+  __shared__ int hdr[WIN ? 6 : 5];
   const uint32_t base = smem_u32(smem);
   unsigned long long *trace =
       p.trace ? p.trace + 4 * ((static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y) * p.C + c)
               : nullptr;
   if (trace && threadIdx.x == 0) trace[0] = globaltimer_ns();
+  if (WIN && threadIdx.x == 32) {
+    prefetch_tmap(&tmk);
+    prefetch_tmap(&tmv);
+  }
   // Nothing above this line reads memory that an earlier kernel writes: with
   // programmatic dependent launch the prologue overlaps the previous kernel.
   pdl_wait();
   if (threadIdx.x == 0) {
-    const int32_t *tm = p.tm;
-    const int tile = tm[TM_TILE];
-    int go = tm[TM_STATUS] == 0;
-    if (go && (tm[TM_B] != p.B || tm[TM_C] != p.C || tile <= 0 || tile % PAGE != 0)) {
-      if (c == 0 && h0 == 0) status_or(p.tm, HPA_STATUS_MISMATCH);
-      go = 0;
+    if constexpr (WIN) {
+      const MapHead m = read_map_head(p.tm, p.lay, p.B, p.C, c, p.q_len, true, c == 0 && h0 == 0);
+      hdr[0] = m.go;
+      hdr[1] = m.tile;
+      hdr[2] = m.s_begin;
+      hdr[3] = m.s_end;
+      hdr[4] = m.window;
+      hdr[5] = m.sinks;
+    } else {
+      const int32_t *tm = p.tm;
+      const int tile = tm[TM_TILE];
+      int go = tm[TM_STATUS] == 0;
+      if (go && (tm[TM_B] != p.B || tm[TM_C] != p.C || tile <= 0 || tile % PAGE != 0)) {
+        if (c == 0 && h0 == 0) status_or(p.tm, HPA_STATUS_MISMATCH);
+        go = 0;
+      }
+      if (go && !map_ranges_ok(tm, p.lay, p.B, p.C, c)) {
+        status_or(p.tm, HPA_STATUS_BAD_MAP);
+        go = 0;
+      }
+      hdr[4] = !go;
+      hdr[1] = tile;
+      hdr[2] = go ? tm[p.lay.cta_seg + c] : 0;
+      hdr[3] = go ? tm[p.lay.cta_seg + c + 1] : 0;
+      hdr[0] = go && hdr[2] < hdr[3];
     }
-    if (go && WIN && tm[TM_KIND] == KIND_WINDOW && tm[TM_QLEN] != p.q_len) {
-      if (c == 0 && h0 == 0) status_or(p.tm, HPA_STATUS_MISMATCH);
-      go = 0;
-    }
-    if (go && !map_ranges_ok<WIN>(tm, p.lay, p.B, p.C, c)) {
-      status_or(p.tm, HPA_STATUS_BAD_MAP);
-      go = 0;
-    }
-    hdr[4] = !go;
-    hdr[1] = tile;
-    hdr[2] = go ? tm[p.lay.cta_seg + c] : 0;
-    hdr[3] = go ? tm[p.lay.cta_seg + c + 1] : 0;
-    hdr[0] = go && hdr[2] < hdr[3];
     for (int st = 0; st < S::kStages; ++st) {
       mbar_init(base + S::kBars + 8 * st, 1);
       mbar_init(base + S::kBars + 8 * (S::kStages + st), kConsumerWarps);
     }
     for (int sl = 0; sl < 2; ++sl) {
       mbar_init(base + S::kBars + 8 * (2 * S::kStages + sl), 32);                 // qfull
-      mbar_init(base + S::kBars + 8 * (2 * S::kStages + 2 + sl), kConsumerWarps);  // qempty
+      mbar_init(base + S::kBars + 8 * (2 * S::kStages + 2 + sl),
+                kConsumerWarps + (WIN ? 1 : 0));  // qempty (the window producer reads slots too)
     }
     *reinterpret_cast<int *>(smem + S::kFlag) = 0;
     fence_barrier_init();
@@ -928,9 +1119,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int tile = hdr[1], s_begin = hdr[2], s_end = hdr[3];
 
   if (threadIdx.x >= kConsumerWarps * 32) {
-    producer<KV, FUSED, ALLH, WIN>(p, &tmk, &tmv, smem, s_begin, s_end, tile, h0);
+    if constexpr (!WIN)
+      producer<KV, FUSED, ALLH>(p, &tmk, &tmv, smem, s_begin, s_end, tile, h0);
+    else if (threadIdx.x < kThreads)
+      win_producer<KV>(p, &tmk, &tmv, smem, s_end - s_begin, h0);
+    else
+      win_stager<KV>(p, smem, s_begin, s_end, tile, h0, hdr[4], hdr[5]);
   } else {
-    consumer<KV, FUSED, ALLH, WIN>(p, smem, s_begin, s_end, tile, h0);
+    consumer<KV, FUSED, ALLH, WIN>(p, smem, s_begin, s_end, tile, h0, WIN ? hdr[4] : 0,
+                                    WIN ? hdr[WIN ? 5 : 0] : 0);
     if (trace && threadIdx.x == 0) trace[2] = globaltimer_ns();  // after the last epilogue
   }
 }
@@ -950,7 +1147,7 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMa
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.C, ALLH ? 1 : p.Hkv, (p.rows + MAX_ROWS - 1) / MAX_ROWS);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(WIN ? kWinThreads : kThreads);
   cfg.dynamicSmemBytes = Smem<KV>::kAlloc;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

@@ -443,18 +443,53 @@ __device__ __forceinline__ SegRow read_seg_row(int32_t *tm, const TaskMapLayout 
 
 // Header checks an attention kernel makes before it walks partition c: the map's
 // kind and segment capacity match what hpa_plan / hpa_plan_static build for (B, C),
-// and c's segment range lies inside the map's S segments.  WIN asks for a map of
-// hpa_plan_window instead, with its window, sinks and q_len in range.
-template <bool WIN = false>
+// and c's segment range lies inside the map's S segments.
 __device__ __forceinline__ bool map_ranges_ok(const int32_t *tm, const TaskMapLayout &lay, int B,
                                               int C, int c) {
   const int kind = tm[TM_KIND], S = tm[TM_S];
   const int cap = kind == 1 ? C : B + C - 1;
   const int sb = tm[lay.cta_seg + c], se = tm[lay.cta_seg + c + 1];
-  const bool kind_ok = WIN ? kind == KIND_WINDOW && tm[TM_WINDOW] >= 1 && tm[TM_SINKS] >= 0 &&
-                                 tm[TM_QLEN] >= 1
-                           : kind >= 0 && kind <= 2;
-  return kind_ok && tm[TM_SCAP] == cap && S >= 0 && S <= cap && sb >= 0 && sb <= se && se <= S;
+  return kind >= 0 && kind <= 2 && tm[TM_SCAP] == cap && S >= 0 && S <= cap && sb >= 0 &&
+         sb <= se && se <= S;
+}
+
+// The same checks for kernels that read window maps, from one round of loads of the whole
+// header (the words lie behind the plan's kernel in L2, and a check at a time costs a round
+// trip each) and one of the partition's segment range.  With need_window a map of another
+// kind is malformed; without, all kinds are read.  A map for another shape or q_len is
+// reported by the CTA with `report`, a malformed one by every CTA that finds it.
+struct MapHead {
+  int go, tile, s_begin, s_end, windowed, window, sinks;
+};
+__device__ __forceinline__ MapHead read_map_head(int32_t *tm, const TaskMapLayout &lay, int B,
+                                                 int C, int c, int q_len, bool need_window,
+                                                 bool report) {
+  const int4 *h = reinterpret_cast<const int4 *>(tm);
+  const int4 a = h[0], b = h[1], d = h[2], e = h[3];
+  static_assert(TM_C == 3 && TM_B == 4 && TM_S == 5 && TM_STATUS == 6 && TM_TILE == 7 &&
+                    TM_KIND == 8 && TM_SCAP == 10 && TM_WINDOW == 11 && TM_SINKS == 12 &&
+                    TM_QLEN == 13,
+                "header words");
+  MapHead m = {0, b.w, 0, 0, d.x == KIND_WINDOW, d.w, e.x};
+  if (b.z != 0) return m;
+  if (a.w != C || b.x != B || m.tile <= 0 || m.tile % PAGE != 0 ||
+      (m.windowed && e.y != q_len)) {
+    if (report) status_or(tm, HPA_STATUS_MISMATCH);
+    return m;
+  }
+  const int S = b.y, cap = d.x == 1 ? C : B + C - 1;
+  m.s_begin = tm[lay.cta_seg + c];
+  m.s_end = tm[lay.cta_seg + c + 1];
+  const bool kind_ok = m.windowed ? m.window >= 1 && m.sinks >= 0
+                                  : !need_window && d.x >= 0 && d.x <= 2;
+  if (!kind_ok || d.z != cap || S < 0 || S > cap || m.s_begin < 0 || m.s_begin > m.s_end ||
+      m.s_end > S) {
+    status_or(tm, HPA_STATUS_BAD_MAP);
+    m.s_begin = m.s_end = 0;
+    return m;
+  }
+  m.go = m.s_begin < m.s_end;
+  return m;
 }
 
 }  // namespace hpa

@@ -84,11 +84,11 @@ struct KwCfg {
 struct KwSeg {
   int r, L, pg0, pg1;
 };
-__device__ __forceinline__ KwSeg kw_seg(const KeyWeightsParams &p, bool windowed, int s, int tile,
+__device__ __forceinline__ KwSeg kw_seg(const KeyWeightsParams &p, const MapHead &m, int s,
                                         bool report) {
-  const SegRow sr = windowed
-                        ? read_seg_row<true>(p.tm, p.lay, p.B, s, blockIdx.x, tile, report)
-                        : read_seg_row<false>(p.tm, p.lay, p.B, s, blockIdx.x, tile, report);
+  const SegRow sr = m.windowed
+                        ? read_seg_row<true>(p.tm, p.lay, p.B, s, blockIdx.x, m.tile, report)
+                        : read_seg_row<false>(p.tm, p.lay, p.B, s, blockIdx.x, m.tile, report);
   KwSeg f = {sr.r, sr.L, sr.klo / PAGE, (sr.khi + PAGE - 1) / PAGE};
   if (sr.L < p.q_len) {
     if (report) status_or(p.tm, HPA_STATUS_BAD_SEQLEN);
@@ -101,8 +101,7 @@ __device__ __forceinline__ KwSeg kw_seg(const KeyWeightsParams &p, bool windowed
 // Each segment's query rows as the MMA's B operand (K-major, 128-byte swizzle), and each
 // row's score factor and log-sum-exp in base 2: a weight is 2^(factor * S - lse).
 template <int KV, int RP>
-__device__ void kw_stager(const KeyWeightsParams &p, uint8_t *smem, int s_begin, int n_seg,
-                          int tile, bool windowed, int ws) {
+__device__ void kw_stager(const KeyWeightsParams &p, uint8_t *smem, const MapHead &m, int ws) {
   using S = KwCfg<KV, RP>;
   const int lane = threadIdx.x & 31, G = p.G, h = blockIdx.y;
   const uint32_t base = smem_u32(smem);
@@ -110,9 +109,9 @@ __device__ void kw_stager(const KeyWeightsParams &p, uint8_t *smem, int s_begin,
   const int *jrow = reinterpret_cast<const int *>(smem + S::kJRow);
   float factor = p.scale_log2;
   if (KV == HPA_KV_E4M3) factor *= p.k_scale[h];
-  for (int k = 0; k < n_seg; ++k) {
+  for (int k = 0; k < m.s_end - m.s_begin; ++k) {
     const int slot = k & 1;
-    const KwSeg f = kw_seg(p, windowed, s_begin + k, tile, false);
+    const KwSeg f = kw_seg(p, m, m.s_begin + k, false);
     int good = 1;
     if (lane == 0)
       good = !*abort_flag &&
@@ -178,22 +177,22 @@ __device__ void kw_stager(const KeyWeightsParams &p, uint8_t *smem, int s_begin,
 // ----------------------------------------------------------------------------- producer
 template <int KV, int RP>
 __device__ void kw_producer(const KeyWeightsParams &p, const CUtensorMap *tmk, uint8_t *smem,
-                            int s_begin, int s_end, int tile, bool windowed) {
+                            const MapHead &m) {
   using S = KwCfg<KV, RP>;
   const int lane = threadIdx.x & 31, h = blockIdx.y;
   const uint32_t base = smem_u32(smem);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kAbort);
   volatile int2 *pids = reinterpret_cast<volatile int2 *>(smem + S::kPid);
-  const int window = windowed ? p.tm[TM_WINDOW] : 0, sinks = windowed ? p.tm[TM_SINKS] : 0;
+  const bool windowed = m.windowed;
   uint64_t pol = 0;
   if (lane == 0) pol = l2_policy_evict_first();
   int st = 0, slot_a = 0;
   uint32_t phase = 0, issued = 0, parity_bits = 0, acc_issued = 0, acc_parity = 0, acc_phase = 0;
   bool ok = true;
-  for (int s = s_begin; s < s_end && ok; ++s) {
-    const KwSeg f = kw_seg(p, windowed, s, tile, lane == 0);
+  for (int s = m.s_begin; s < m.s_end && ok; ++s) {
+    const KwSeg f = kw_seg(p, m, s, lane == 0);
     WinSpan win = {};
-    if (windowed && f.pg0 < f.pg1) win = WinSpan::make(f.L, p.q_len, window, sinks);
+    if (windowed && f.pg0 < f.pg1) win = WinSpan::make(f.L, p.q_len, m.window, m.sinks);
     const int pstart = p.page_indptr[f.r];
     const int pcount = p.page_indptr[f.r + 1] - pstart;
     for (int pb = f.pg0; pb < f.pg1 && ok; pb += 32 * kStepPages) {
@@ -320,8 +319,8 @@ __device__ void kw_issuer(const KeyWeightsParams &p, uint8_t *smem, int n_seg, u
 
 // ----------------------------------------------------------------------------- compute
 template <int KV, int RP>
-__device__ void kw_compute(const KeyWeightsParams &p, uint8_t *smem, int n_seg, uint32_t tmem,
-                           bool windowed) {
+__device__ void kw_compute(const KeyWeightsParams &p, uint8_t *smem, const MapHead &head,
+                           uint32_t tmem) {
   using S = KwCfg<KV, RP>;
   constexpr int kPart = RP < 16 ? RP : 16;  // rows read from TMEM at a time
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
@@ -330,8 +329,8 @@ __device__ void kw_compute(const KeyWeightsParams &p, uint8_t *smem, int n_seg, 
   const uint32_t lane_t = tmem + (static_cast<uint32_t>(32 * w) << 16);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kAbort);
   const int *jrow = reinterpret_cast<const int *>(smem + S::kJRow);
-  const int window = windowed ? p.tm[TM_WINDOW] : 0, sinks = windowed ? p.tm[TM_SINKS] : 0;
-  const int q_len = p.q_len;
+  const bool windowed = head.windowed;
+  const int sinks = head.sinks, q_len = p.q_len, n_seg = head.s_end - head.s_begin;
   int n = 0;  // step of the CTA
   bool ok = true;
   for (int k = 0; k < n_seg && ok; ++k) {
@@ -343,7 +342,7 @@ __device__ void kw_compute(const KeyWeightsParams &p, uint8_t *smem, int n_seg, 
     const int L = info.y, pg0 = info.z, pg1 = info.w;
     const int steps = (pg1 - pg0 + kStepPages - 1) / kStepPages;
     WinSpan win = {};
-    if (windowed && steps > 0) win = WinSpan::make(L, q_len, window, sinks);
+    if (windowed && steps > 0) win = WinSpan::make(L, q_len, head.window, sinks);
     const int lim_min = L - q_len + 1;  // first key hidden from some row
     const uint32_t rows = base + S::kRow + slot * RP * 8;
     for (int i = (group + kGroups - n % kGroups) % kGroups; i < steps; i += kGroups) {
@@ -427,30 +426,12 @@ __global__ void __launch_bounds__(KwCfg<KV, RP>::kThreads, RP <= 16 ? 2 : 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int c = blockIdx.x, warp = threadIdx.x >> 5;
-  __shared__ int hdr[5];  // go, tile, s_begin, s_end, windowed
+  __shared__ MapHead head;  // read once, for all threads
   const uint32_t base = smem_u32(smem);
   if (threadIdx.x == 32) prefetch_tmap(&tmk);
   pdl_wait();  // nothing above reads what an earlier kernel writes
   if (threadIdx.x == 0) {
-    const int32_t *tm = p.tm;
-    const int tile = tm[TM_TILE];
-    const bool windowed = tm[TM_KIND] == KIND_WINDOW;
-    int go = tm[TM_STATUS] == 0;
-    if (go && (tm[TM_B] != p.B || tm[TM_C] != p.C || tile <= 0 || tile % PAGE != 0 ||
-               (windowed && tm[TM_QLEN] != p.q_len))) {
-      if (c == 0 && blockIdx.y == 0) status_or(p.tm, HPA_STATUS_MISMATCH);
-      go = 0;
-    }
-    if (go && !(windowed ? map_ranges_ok<true>(tm, p.lay, p.B, p.C, c)
-                         : map_ranges_ok<false>(tm, p.lay, p.B, p.C, c))) {
-      status_or(p.tm, HPA_STATUS_BAD_MAP);
-      go = 0;
-    }
-    hdr[1] = tile;
-    hdr[2] = go ? tm[p.lay.cta_seg + c] : 0;
-    hdr[3] = go ? tm[p.lay.cta_seg + c + 1] : 0;
-    hdr[0] = go && hdr[2] < hdr[3];
-    hdr[4] = windowed;
+    head = read_map_head(p.tm, p.lay, p.B, p.C, c, p.q_len, false, c == 0 && blockIdx.y == 0);
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(base + S::kKvFull + 8 * i, 1);   // TMA bytes
       mbar_init(base + S::kKvEmpty + 8 * i, 1);  // MMA commit
@@ -471,7 +452,7 @@ __global__ void __launch_bounds__(KwCfg<KV, RP>::kThreads, RP <= 16 ? 2 : 1)
   if (threadIdx.x < RP) reinterpret_cast<int *>(smem + S::kJRow)[threadIdx.x] = threadIdx.x / p.G;
   __syncthreads();
   pdl_launch_dependents();
-  if (!hdr[0]) return;
+  if (!head.go) return;
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      base + S::kTmemAt),
@@ -483,14 +464,15 @@ __global__ void __launch_bounds__(KwCfg<KV, RP>::kThreads, RP <= 16 ? 2 : 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + S::kTmemAt);
+  const MapHead m = head;
   if (warp < kCompute)
-    kw_compute<KV, RP>(p, smem, hdr[3] - hdr[2], tmem, hdr[4]);
+    kw_compute<KV, RP>(p, smem, m, tmem);
   else if (warp == kCompute)
-    kw_producer<KV, RP>(p, &tmk, smem, hdr[2], hdr[3], hdr[1], hdr[4]);
+    kw_producer<KV, RP>(p, &tmk, smem, m);
   else if (warp >= kCompute + 2)
-    kw_stager<KV, RP>(p, smem, hdr[2], hdr[3] - hdr[2], hdr[1], hdr[4], warp - kCompute - 2);
+    kw_stager<KV, RP>(p, smem, m, warp - kCompute - 2);
   else if ((threadIdx.x & 31) == 0)
-    kw_issuer<KV, RP>(p, smem, hdr[3] - hdr[2], tmem);
+    kw_issuer<KV, RP>(p, smem, m.s_end - m.s_begin, tmem);
   tc_fence_before();
   __syncthreads();
   mbar_wait_bounded_rolled(base + S::kDrain, 0, 1000000000ull);
