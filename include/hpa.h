@@ -415,7 +415,7 @@ int hpa_store_kv_at(const void *k_new_dev, const void *v_new_dev, const int32_t 
                     hpa_stream_t stream);
 
 /*
- * The three calls below keep a cache bounded by the attention its keys receive (the
+ * The calls below keep a cache bounded by the attention its keys receive (the
  * pages have no counterpart to them).  Accumulated weights live in pools of their own,
  * fp32 [num_pages][Hkv][page_size], paged by the same table as K and V.  Each call
  * writes what it names for the pages of a request, so a page that is listed twice (a
@@ -485,6 +485,19 @@ int hpa_evict_compact(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, floa
                       const int32_t *dst_indices_dev, int32_t page_size, const int32_t *kept_dev,
                       int64_t kept_stride, const int32_t *new_lens_dev, int32_t B, int32_t Hkv,
                       int32_t d, int32_t *status_dev, hpa_stream_t stream);
+
+/*
+ * hpa_evict -- hpa_evict_select followed by hpa_evict_compact of K, V and the weights
+ * (acc_dev, not NULL) in one call, with their arguments, results and checks (all made
+ * before the first launch).
+ */
+int hpa_evict(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, float *acc_dev,
+              int64_t num_pages, const int32_t *seq_lens_dev, const int32_t *page_indptr_dev,
+              const int32_t *page_indices_dev, const int32_t *dst_indptr_dev,
+              const int32_t *dst_indices_dev, int32_t page_size, const int32_t *budgets_dev,
+              int32_t sinks, int32_t recent, int32_t B, int32_t Hkv, int32_t d, int32_t *kept_dev,
+              int64_t kept_stride, int32_t *new_lens_dev, int32_t *status_dev,
+              hpa_stream_t stream);
 
 /*
  * hpa_selftest_wait_timeout -- diagnostic for the failure path of the

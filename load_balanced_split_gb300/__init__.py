@@ -4,7 +4,7 @@ The compute path is the C-ABI library libhpa (include/hpa.h, sources in
 csrc/); `hpa` is its ctypes binding.  Nothing here computes on the CPU.
 """
 from .hpa import (KV_BF16, KV_E4M3, HpaError, Workspace, decode_step, evict_step,  # noqa: F401
-                  hpa_decode_attn_window, hpa_default_num_ctas_window, hpa_evict_compact,
+                  hpa_decode_attn_window, hpa_default_num_ctas_window, hpa_evict, hpa_evict_compact,
                   hpa_evict_select, hpa_key_weights, hpa_plan_window, hpa_store_kv_at,
                   hpa_arrivals_elems, hpa_combine, hpa_decode_attn, hpa_decode_attn_allheads,
                   hpa_decode_attn_combine_noalloc, hpa_default_num_ctas_allheads,

@@ -4,13 +4,13 @@
 // Selection.  A request longer than its budget keeps its first `sinks` keys, its last
 // `recent` keys and, of the others, the budget - sinks - recent with the largest weight,
 // ties to the lower index.  One cluster of 1 to 8 blocks per (request, KV head): a radix
-// select over an order-preserving integer image of the weights (digits of 11, 11 and 10
+// select over an order-preserving integer image of the weights (digits of 11, 10 and 11
 // bits: three histograms instead of a sort) finds the last weight that stays, T, and how
 // many keys of weight T stay; the blocks add up one another's histograms through
 // distributed shared memory.  A pass with ballots and a scan over the warps and blocks
 // then writes the kept indices in ascending order.  The weights are read from memory once,
-// eight pages in flight per warp, and stay in the shared memory of the cluster (22 K keys
-// a block; a longer request's rest is read again in each pass, from L2).  The second digit's
+// eight pages in flight per warp, and stay in the shared memory of the cluster (24 K keys
+// a block, 192 K a cluster; a longer request's rest is read again in each pass, from L2).  The second digit's
 // pass also counts what lies above and lists the few keys that share the first digit, so
 // the third digit and the final counts go over that list.
 //
@@ -34,14 +34,13 @@ namespace cg = cooperative_groups;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kWarpPages = 22;                               // pages a warp holds in shared memory
+constexpr int kWarpPages = 24;                               // pages a warp holds in shared memory
 constexpr int kBlockPages = kSelWarps * kWarpPages;
-constexpr int kBins = 2048;
-constexpr int kBinsPerThread = kBins / kSelThreads;
+constexpr int kBins = 2048, kBins2 = 1024;                    // first and third digit; second
 constexpr int kList = 1024;                                  // keys that share the first digit
 constexpr int kMaxCluster = 8;
 constexpr int64_t kMinKeys = 4096;                           // per block before a cluster grows
-constexpr int kSelSmem = kBlockPages * PAGE * 4 + 2 * kBins * 4 + kList * 8;
+constexpr int kSelSmem = kBlockPages * PAGE * 4 + (kBins + kBins2 + kList) * 4;
 constexpr int kSelBlocks = 2;                                // per SM: 112 KB of shared memory each
 constexpr int kFlight = 4;                                   // page pairs in flight per warp
 // Keys that are no candidates: beyond the request, and those that stay in any case
@@ -58,24 +57,32 @@ __device__ __forceinline__ uint32_t weight_key(uint32_t u) {
 // Over the whole cluster: the bin of the k-th largest entry (1 <= k <= the entries
 // counted) and the number of entries in higher bins.  The caller has synchronised the
 // cluster after the last count into `hist`.
+template <int BINS>
 __device__ void find_bin(cg::cluster_group &cl, int *hist, int k, int &bin, int &above) {
+  constexpr int N = BINS / kSelThreads;  // bins per thread: 4 or 2
+  typedef typename std::conditional<N == 4, int4, int2>::type Bins;
+  static_assert(sizeof(Bins) == 4 * N, "one load per block");
   __shared__ int wsum[kSelWarps], s_bin, s_above;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, n = cl.num_blocks();
-  // thread t owns bins [low, low + 4), low = kBins - 4 (t + 1): a scan from the highest bin
-  static_assert(kBinsPerThread == 4, "one 16-byte load per block");
-  const int low = kBins - kBinsPerThread * (tid + 1);
-  int4 c = *reinterpret_cast<const int4 *>(hist + low);
+  // thread t owns bins [low, low + N), low = BINS - N (t + 1): a scan from the highest bin
+  const int low = BINS - N * (tid + 1);
+  int c[N];
+  auto add = [&](const int *from, bool first) {
+    const Bins o = *reinterpret_cast<const Bins *>(from + low);
+    const int *x = reinterpret_cast<const int *>(&o);
+#pragma unroll
+    for (int i = 0; i < N; ++i) c[i] = (first ? 0 : c[i]) + x[i];
+  };
+  add(hist, true);
   if (n > 1) {
     const int me = cl.block_rank();
 #pragma unroll
     for (int x = 1; x < kMaxCluster; ++x)  // all the others' loads in flight
-      if (x < n) {
-        const int4 o =
-            *reinterpret_cast<const int4 *>(cl.map_shared_rank(hist, (me + x) & (n - 1)) + low);
-        c.x += o.x, c.y += o.y, c.z += o.z, c.w += o.w;
-      }
+      if (x < n) add(cl.map_shared_rank(hist, (me + x) & (n - 1)), false);
   }
-  const int mine = c.x + c.y + c.z + c.w;
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) mine += c[i];
   int v = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -88,14 +95,15 @@ __device__ void find_bin(cg::cluster_group &cl, int *hist, int k, int &bin, int 
 #pragma unroll
   for (int x = 0; x < kSelWarps; ++x) before += x < wid ? wsum[x] : 0;
   if (before < k && before + mine >= k) {
-    const int h[4] = {c.w, c.z, c.y, c.x};
-    for (int x = 0; x < 4; ++x) {
-      if (before + h[x] >= k) {
-        s_bin = low + 3 - x;
+    bool found = false;
+#pragma unroll
+    for (int x = N - 1; x >= 0; --x) {
+      if (!found && before + c[x] >= k) {
+        s_bin = low + x;
         s_above = before;
-        break;
+        found = true;
       }
-      before += h[x];
+      before += c[x];
     }
   }
   __syncthreads();
@@ -111,12 +119,13 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
   const int ranks = cl.num_blocks(), rank = cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   int *hist0 = reinterpret_cast<int *>(sel_smem + kBlockPages * PAGE), *hist1 = hist0 + kBins;
-  uint2 *list = reinterpret_cast<uint2 *>(hist1 + kBins);  // (key, warp)
+  // keys that share the first digit: their other 21 bits, and the warp above them
+  uint32_t *list = reinterpret_cast<uint32_t *>(hist1 + kBins2);
   uint32_t *keys = sel_smem + wid * (kWarpPages * PAGE);   // this warp's first pages
   const int pair = blockIdx.x / ranks, r = pair / p.Hkv, h = pair % p.Hkv;
   if (tid == 0) s_bad = s_listed = 0;
   if (tid < kSelWarps) s_gt[tid] = s_eq[tid] = 0;
-  for (int i = tid; i < kBins / 2; i += kSelThreads)  // both histograms
+  for (int i = tid; i < (kBins + kBins2) / 4; i += kSelThreads)  // both histograms
     reinterpret_cast<int4 *>(hist0)[i] = make_int4(0, 0, 0, 0);
   // No early launch of the kernel after this one: compaction blocks that wait on the SMs
   // settle unevenly around these (174 -> 251 us of compaction on 64 requests cut to 4096).
@@ -250,7 +259,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
   int need = 0, gt_n = 0, eq_n = 0;
   if (take > 0) {
     int d1, d2, d3, above;
-    find_bin(cl, hist0, take, d1, above);
+    find_bin<kBins>(cl, hist0, take, d1, above);
     need = take - above;
     const uint32_t top1 = d1;
     // keys above the digit are counted; those that share it go on the list
@@ -258,39 +267,39 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
       auto see = [&](uint32_t k) {
         gt_n += k >> 21 > top1 || k == kFixed;
         if (k >> 21 == top1 && k != kFixed) {
-          atomicAdd(&hist1[(k >> 10) & 2047], 1);
+          atomicAdd(&hist1[(k >> 11) & 1023], 1);
           const int at = atomicAdd(&s_listed, 1);
-          if (at < kList) list[at] = make_uint2(k, wid);
+          if (at < kList) list[at] = (k & 0x1fffffu) | static_cast<uint32_t>(wid) << 21;
         }
       };
       see(x.x), see(x.y), see(x.z), see(x.w);
     });
     cluster_sync();
     const int listed = s_listed;  // of this block: beyond kList its keys are walked again
-    find_bin(cl, hist1, need, d2, above);
+    find_bin<kBins2>(cl, hist1, need, d2, above);
     need -= above;
     // every block has read hist0 (before the barrier above): it takes the last digit
     for (int i = tid; i < kBins / 4; i += kSelThreads)
       reinterpret_cast<int4 *>(hist0)[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    const uint32_t top2 = top1 << 11 | static_cast<uint32_t>(d2);
+    const uint32_t top2 = top1 << 10 | static_cast<uint32_t>(d2);
     auto third = [&](uint32_t k) {
-      if (k >> 10 == top2 && k != kFixed) atomicAdd(&hist0[k & 1023], 1);
+      if (k >> 11 == top2 && k != kFixed) atomicAdd(&hist0[k & 2047], 1);
     };
     if (listed <= kList) {
-      for (int i = tid; i < listed; i += kSelThreads) third(list[i].x);
+      for (int i = tid; i < listed; i += kSelThreads) third(top1 << 21 | (list[i] & 0x1fffffu));
     } else {
       each([&](int, uint4 x) { third(x.x), third(x.y), third(x.z), third(x.w); });
     }
     cluster_sync();
-    find_bin(cl, hist0, need, d3, above);
+    find_bin<kBins>(cl, hist0, need, d3, above);
     need -= above;  // keys equal to T that stay
-    T = top2 << 10 | static_cast<uint32_t>(d3);
+    T = top2 << 11 | static_cast<uint32_t>(d3);
     if (listed <= kList) {
       for (int i = tid; i < listed; i += kSelThreads) {
-        const uint2 e = list[i];
-        if (e.x > T) atomicAdd(&s_gt[e.y], 1);
-        else if (e.x == T) atomicAdd(&s_eq[e.y], 1);
+        const uint32_t k = top1 << 21 | (list[i] & 0x1fffffu), w = list[i] >> 21;
+        if (k > T) atomicAdd(&s_gt[w], 1);
+        else if (k == T) atomicAdd(&s_eq[w], 1);
       }
     } else {
       each([&](int, uint4 x) {
@@ -385,6 +394,9 @@ __device__ __forceinline__ int64_t row_place(const CompactParams &p, const int32
 // and the row are three dependent reads), then the block moves the tile in batches of
 // 8 pieces per thread.  In place there is one block per column and its batches go in
 // order, each read whole before it is written.
+// Moving the rows in the selection's own blocks, to overlap one request's selection with
+// another's move, was slower: 108 -> 121 and 263 -> 302 us (32 x 8192 cut to 2048, 64 x
+// 24000 to 4096), the blocks that a selection wants being too few and too large to move.
 template <bool IN_PLACE>
 __global__ void __launch_bounds__(kCmpThreads)
     evict_compact_kernel(const CompactParams p, int lanes) {

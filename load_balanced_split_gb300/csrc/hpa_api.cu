@@ -579,12 +579,12 @@ int hpa_key_weights(const void *q_dev, const float *lse_dev, const void *k_pool_
   return e == cudaSuccess ? HPA_OK : cuda_fail(e);
 }
 
-int hpa_evict_select(const float *acc_dev, const int32_t *seq_lens_dev,
-                     const int32_t *page_indptr_dev, const int32_t *page_indices_dev,
-                     int64_t num_pages, int32_t page_size, const int32_t *budgets_dev,
-                     int32_t sinks, int32_t recent, int32_t B, int32_t Hkv, int32_t *kept_dev,
-                     int64_t kept_stride, int32_t *new_lens_dev, int32_t *status_dev,
-                     hpa_stream_t stream) {
+static int evict_params(const float *acc_dev, const int32_t *seq_lens_dev,
+                        const int32_t *page_indptr_dev, const int32_t *page_indices_dev,
+                        int64_t num_pages, int32_t page_size, const int32_t *budgets_dev,
+                        int32_t sinks, int32_t recent, int32_t B, int32_t Hkv, int32_t *kept_dev,
+                        int64_t kept_stride, int32_t *new_lens_dev, int32_t *status_dev,
+                        hpa::EvictParams *p) {
   if (!acc_dev || !seq_lens_dev || !page_indptr_dev || !page_indices_dev || !budgets_dev ||
       !kept_dev || !new_lens_dev)
     return HPA_ERR_INVALID;
@@ -597,31 +597,20 @@ int hpa_evict_select(const float *acc_dev, const int32_t *seq_lens_dev,
   if (!aligned(acc_dev, 16) || !aligned(kept_dev, 4) || !aligned(new_lens_dev, 4) ||
       (status_dev && !aligned(status_dev, 4)))
     return HPA_ERR_ALIGN;
-  hpa::EvictParams p;
-  p.acc = acc_dev;
-  p.seq_lens = seq_lens_dev;
-  p.page_indptr = page_indptr_dev;
-  p.page_indices = page_indices_dev;
-  p.budgets = budgets_dev;
-  p.num_pages = num_pages;
-  p.sinks = sinks;
-  p.recent = recent;
-  p.B = B;
-  p.Hkv = Hkv;
-  p.kept = kept_dev;
-  p.kept_stride = kept_stride;
-  p.new_lens = new_lens_dev;
-  p.status = status_dev;
-  cudaError_t e = hpa::launch_evict_select(p, reinterpret_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? HPA_OK : cuda_fail(e);
+  *p = hpa::EvictParams{acc_dev,   seq_lens_dev, page_indptr_dev, page_indices_dev,
+                        budgets_dev, num_pages,  sinks,           recent,
+                        B,         Hkv,          kept_dev,        kept_stride,
+                        new_lens_dev, status_dev};
+  return HPA_OK;
 }
 
-int hpa_evict_compact(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, float *acc_dev,
-                      int64_t num_pages, const int32_t *page_indptr_dev,
-                      const int32_t *page_indices_dev, const int32_t *dst_indptr_dev,
-                      const int32_t *dst_indices_dev, int32_t page_size, const int32_t *kept_dev,
-                      int64_t kept_stride, const int32_t *new_lens_dev, int32_t B, int32_t Hkv,
-                      int32_t d, int32_t *status_dev, hpa_stream_t stream) {
+static int compact_params(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, float *acc_dev,
+                          int64_t num_pages, const int32_t *page_indptr_dev,
+                          const int32_t *page_indices_dev, const int32_t *dst_indptr_dev,
+                          const int32_t *dst_indices_dev, int32_t page_size,
+                          const int32_t *kept_dev, int64_t kept_stride,
+                          const int32_t *new_lens_dev, int32_t B, int32_t Hkv, int32_t d,
+                          int32_t *status_dev, hpa::CompactParams *p) {
   if (!k_pool_dev || !v_pool_dev || !page_indptr_dev || !page_indices_dev || !kept_dev ||
       !new_lens_dev || !dst_indptr_dev != !dst_indices_dev || k_pool_dev == v_pool_dev)
     return HPA_ERR_INVALID;
@@ -635,23 +624,64 @@ int hpa_evict_compact(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, floa
     return HPA_ERR_ALIGN;
   if (dst_indptr_dev == page_indptr_dev && dst_indices_dev == page_indices_dev)
     dst_indptr_dev = dst_indices_dev = nullptr;  // the request's own pages: in place
+  *p = hpa::CompactParams{k_pool_dev,     v_pool_dev,      acc_dev,   page_indptr_dev,
+                          page_indices_dev, dst_indptr_dev, dst_indices_dev, num_pages,
+                          kept_dev,       new_lens_dev,    kept_stride, B,
+                          Hkv,            d * (kv_dtype == HPA_KV_BF16 ? 2 : 1), status_dev};
+  return HPA_OK;
+}
+
+int hpa_evict_select(const float *acc_dev, const int32_t *seq_lens_dev,
+                     const int32_t *page_indptr_dev, const int32_t *page_indices_dev,
+                     int64_t num_pages, int32_t page_size, const int32_t *budgets_dev,
+                     int32_t sinks, int32_t recent, int32_t B, int32_t Hkv, int32_t *kept_dev,
+                     int64_t kept_stride, int32_t *new_lens_dev, int32_t *status_dev,
+                     hpa_stream_t stream) {
+  hpa::EvictParams p;
+  const int rc = evict_params(acc_dev, seq_lens_dev, page_indptr_dev, page_indices_dev, num_pages,
+                              page_size, budgets_dev, sinks, recent, B, Hkv, kept_dev, kept_stride,
+                              new_lens_dev, status_dev, &p);
+  if (rc != HPA_OK) return rc;
+  cudaError_t e = hpa::launch_evict_select(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HPA_OK : cuda_fail(e);
+}
+
+int hpa_evict_compact(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, float *acc_dev,
+                      int64_t num_pages, const int32_t *page_indptr_dev,
+                      const int32_t *page_indices_dev, const int32_t *dst_indptr_dev,
+                      const int32_t *dst_indices_dev, int32_t page_size, const int32_t *kept_dev,
+                      int64_t kept_stride, const int32_t *new_lens_dev, int32_t B, int32_t Hkv,
+                      int32_t d, int32_t *status_dev, hpa_stream_t stream) {
   hpa::CompactParams p;
-  p.k_pool = k_pool_dev;
-  p.v_pool = v_pool_dev;
-  p.acc = acc_dev;
-  p.page_indptr = page_indptr_dev;
-  p.page_indices = page_indices_dev;
-  p.dst_indptr = dst_indptr_dev;
-  p.dst_indices = dst_indices_dev;
-  p.num_pages = num_pages;
-  p.kept = kept_dev;
-  p.new_lens = new_lens_dev;
-  p.kept_stride = kept_stride;
-  p.B = B;
-  p.Hkv = Hkv;
-  p.row_bytes = d * (kv_dtype == HPA_KV_BF16 ? 2 : 1);
-  p.status = status_dev;
+  const int rc = compact_params(k_pool_dev, v_pool_dev, kv_dtype, acc_dev, num_pages,
+                                page_indptr_dev, page_indices_dev, dst_indptr_dev,
+                                dst_indices_dev, page_size, kept_dev, kept_stride, new_lens_dev, B,
+                                Hkv, d, status_dev, &p);
+  if (rc != HPA_OK) return rc;
   cudaError_t e = hpa::launch_evict_compact(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HPA_OK : cuda_fail(e);
+}
+
+int hpa_evict(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, float *acc_dev,
+              int64_t num_pages, const int32_t *seq_lens_dev, const int32_t *page_indptr_dev,
+              const int32_t *page_indices_dev, const int32_t *dst_indptr_dev,
+              const int32_t *dst_indices_dev, int32_t page_size, const int32_t *budgets_dev,
+              int32_t sinks, int32_t recent, int32_t B, int32_t Hkv, int32_t d, int32_t *kept_dev,
+              int64_t kept_stride, int32_t *new_lens_dev, int32_t *status_dev,
+              hpa_stream_t stream) {
+  hpa::EvictParams p;
+  hpa::CompactParams mv;
+  int rc = evict_params(acc_dev, seq_lens_dev, page_indptr_dev, page_indices_dev, num_pages,
+                        page_size, budgets_dev, sinks, recent, B, Hkv, kept_dev, kept_stride,
+                        new_lens_dev, status_dev, &p);
+  if (rc == HPA_OK)
+    rc = compact_params(k_pool_dev, v_pool_dev, kv_dtype, acc_dev, num_pages, page_indptr_dev,
+                        page_indices_dev, dst_indptr_dev, dst_indices_dev, page_size, kept_dev,
+                        kept_stride, new_lens_dev, B, Hkv, d, status_dev, &mv);
+  if (rc != HPA_OK) return rc;
+  cudaError_t e = hpa::launch_evict_select(p, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess)
+    e = hpa::launch_evict_compact(mv, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? HPA_OK : cuda_fail(e);
 }
 

@@ -91,6 +91,8 @@ def lib():
                                       P], ctypes.c_int),
                 "hpa_evict_compact": ([P, P, I32, P, I64, P, P, P, P, I32, P, I64, P, I32, I32,
                                        I32, P, P], ctypes.c_int),
+                "hpa_evict": ([P, P, I32, P, I64, P, P, P, P, P, I32, P, I32, I32, I32, I32, I32, P,
+                               I64, P, P, P], ctypes.c_int),
                 "hpa_error_string": ([ctypes.c_int], ctypes.c_char_p),
                 "hpa_last_cuda_error": ([], ctypes.c_int),
             }
@@ -515,7 +517,7 @@ def _one_device(*tensors):
     """The library launches on the current device: every tensor has to live there."""
     here = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.device.index != here:
+        if t is not None and t.get_device() != here:
             raise HpaError("tensors must be on the current device (cuda:%d), got %s" %
                            (here, t.device))
 
@@ -532,6 +534,24 @@ def _page_table(indptr, indices, B, what="page"):
     _dev(indices, what + "_indices", torch.int32)
     if indptr.numel() != B + 1:
         raise HpaError("%s_indptr must have B + 1 = %d entries" % (what, B + 1))
+
+
+def _dst_table(indptr, indices, B):
+    if (indptr is None) != (indices is None):
+        raise HpaError("dst_indptr and dst_indices go together")
+    if indptr is not None:
+        _page_table(indptr, indices, B, "dst")
+
+
+def _pools(k_pool, v_pool):
+    """(kv, P, Hkv, page, d) of the two pools of one cache."""
+    _dev(k_pool, "k_pool")
+    _dev(v_pool, "v_pool", k_pool.dtype)
+    if k_pool.dim() != 4 or v_pool.shape != k_pool.shape:
+        raise HpaError("k_pool and v_pool must match, [P][Hkv][page][d]")
+    if k_pool.dtype not in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn):
+        raise HpaError("unsupported KV dtype %s" % k_pool.dtype)
+    return (KV_BF16 if k_pool.dtype == torch.bfloat16 else KV_E4M3, *k_pool.shape)
 
 
 def hpa_key_weights(q, lse, k_pool, page_indptr, page_indices, taskmap, num_ctas: int, acc,
@@ -618,23 +638,13 @@ def hpa_evict_compact(k_pool, v_pool, page_indptr, page_indices, kept, new_lens,
                       dst_indptr=None, dst_indices=None, status=None, stream=None):
     """Moves the kept rows of K, V and acc to the front of each request's own pages, or to the
     pages that dst_indptr / dst_indices list (the old cache then stays as it was)."""
-    _dev(k_pool, "k_pool")
-    _dev(v_pool, "v_pool")
-    if k_pool.dim() != 4 or v_pool.dtype != k_pool.dtype or v_pool.shape != k_pool.shape:
-        raise HpaError("k_pool and v_pool must match, [P][Hkv][page][d]")
-    if k_pool.dtype not in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn):
-        raise HpaError("unsupported KV dtype %s" % k_pool.dtype)
-    kv = KV_BF16 if k_pool.dtype == torch.bfloat16 else KV_E4M3
-    P, Hkv, page, d = k_pool.shape
+    kv, P, Hkv, page, d = _pools(k_pool, v_pool)
     B = page_indptr.numel() - 1
     _page_table(page_indptr, page_indices, B)
     _kept(kept, new_lens, B, Hkv)
     if acc is not None:
         _acc_pool(acc, "acc", k_pool)
-    if (dst_indptr is None) != (dst_indices is None):
-        raise HpaError("dst_indptr and dst_indices go together")
-    if dst_indptr is not None:
-        _page_table(dst_indptr, dst_indices, B, "dst")
+    _dst_table(dst_indptr, dst_indices, B)
     if status is not None:
         _dev(status, "status", torch.int32)
     _one_device(k_pool, v_pool, page_indptr, page_indices, kept, new_lens, acc, dst_indptr,
@@ -645,16 +655,30 @@ def hpa_evict_compact(k_pool, v_pool, page_indptr, page_indices, kept, new_lens,
         Hkv, d, _ptr(status), _stream(stream)), "hpa_evict_compact")
 
 
-def evict_step(acc, k_pool, v_pool, seq_lens, page_indptr, page_indices, budgets, sinks: int,
-               recent: int, kept, new_lens, dst_indptr=None, dst_indices=None, status=None,
-               stream=None):
-    """hpa_evict_select -> hpa_evict_compact of K, V and acc, enqueued on one stream; the cache
-    then has new_lens[r] keys per request (-1: a request that `status` reports, untouched)."""
-    stream = _stream(stream)
-    hpa_evict_select(acc, seq_lens, page_indptr, page_indices, budgets, sinks, recent, kept,
-                     new_lens, status, stream)
-    hpa_evict_compact(k_pool, v_pool, page_indptr, page_indices, kept, new_lens, acc, dst_indptr,
-                      dst_indices, status, stream)
+def hpa_evict(acc, k_pool, v_pool, seq_lens, page_indptr, page_indices, budgets, sinks: int,
+              recent: int, kept, new_lens, dst_indptr=None, dst_indices=None, status=None,
+              stream=None):
+    """hpa_evict_select, then hpa_evict_compact of K, V and acc; the cache then has new_lens[r]
+    keys per request (-1: a request that `status` reports, untouched)."""
+    kv, P, Hkv, page, d = _pools(k_pool, v_pool)
+    _acc_pool(acc, "acc", k_pool)
+    _dev(seq_lens, "seq_lens", torch.int32)
+    _dev(budgets, "budgets", torch.int32)
+    B = seq_lens.numel()
+    if budgets.numel() != B:
+        raise HpaError("budgets needs one value per request")
+    _page_table(page_indptr, page_indices, B)
+    _dst_table(dst_indptr, dst_indices, B)
+    _kept(kept, new_lens, B, Hkv)
+    if status is not None:
+        _dev(status, "status", torch.int32)
+    _one_device(k_pool, v_pool, acc, seq_lens, budgets, page_indptr, page_indices, kept, new_lens,
+                dst_indptr, dst_indices, status)
+    _check(lib().hpa_evict(
+        _ptr(k_pool), _ptr(v_pool), kv, _ptr(acc), P, _ptr(seq_lens), _ptr(page_indptr),
+        _ptr(page_indices), _ptr(dst_indptr), _ptr(dst_indices), page, _ptr(budgets), sinks,
+        recent, B, Hkv, d, _ptr(kept), kept.shape[2], _ptr(new_lens), _ptr(status),
+        _stream(stream)), "hpa_evict")
 
 
 # ----------------------------------------------------------------------------- workspace helper
@@ -761,3 +785,12 @@ def decode_step(ws: Workspace, q, k_pool, v_pool, seq_lens, page_indptr, page_in
     if acc is not None:
         hpa_key_weights(q, out_lse, k_pool, page_indptr, page_indices, ws.taskmap, ws.num_ctas,
                         acc, k_scale=k_scale, decay=decay, sm_scale=sm_scale, stream=stream)
+
+
+def evict_step(acc, k_pool, v_pool, seq_lens, page_indptr, page_indices, budgets, sinks: int,
+               recent: int, kept, new_lens, dst_indptr=None, dst_indices=None, status=None,
+               stream=None):
+    """What follows a decode_step once caches have outgrown their budgets: selection and the
+    move of K, V and the accumulated weights, enqueued on one stream (hpa_evict)."""
+    hpa_evict(acc, k_pool, v_pool, seq_lens, page_indptr, page_indices, budgets, sinks, recent,
+              kept, new_lens, dst_indptr, dst_indices, status, stream)

@@ -248,11 +248,14 @@ def _cache(lens, kv, Hkv, spare=0, seed=0):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
-@pytest.mark.parametrize("lens,budget,Hkv", [([1], 1, 1), ([300], 100, 1), ([64, 700, 65, 30], 64, 3),
+@pytest.mark.parametrize("lens,budget,Hkv", [([1], 1, 1), ([300], 100, 1), ([300, 200], 250, 1), ([64, 700, 65, 30], 64, 3),
                                              ([5000, 130, 2500], 2049, 2),
-                                             (list(range(60, 260)), 90, 2)])
+                                             (list(range(60, 260)), 90, 2),
+                                             ([40000, 9000], 3001, 1),      # clusters
+                                             ([30000], 20000, 1)])
 @pytest.mark.parametrize("elsewhere", [False, True])
-def test_evict_step(kv, lens, budget, Hkv, elsewhere):
+@pytest.mark.parametrize("calls", [1, 2])
+def test_evict_step(kv, lens, budget, Hkv, elsewhere, calls):
     pages = [(min(L, budget) + 63) // 64 for L in lens]
     b, db, acc = _cache(lens, kv, Hkv, sum(pages) if elsewhere else 0, seed=len(lens) + budget)
     dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()  # noqa: E731
@@ -268,8 +271,13 @@ def test_evict_step(kv, lens, budget, Hkv, elsewhere):
     new = torch.zeros(len(lens), dtype=torch.int32, device="cuda")
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     sinks, recent = min(2, budget // 2), min(5, budget // 2)
-    hpa.evict_step(acc, db.k, db.v, db.lens, db.indptr, db.indices, dev(budgets), sinks, recent,
-                   kept, new, status=st, **dst)
+    if calls == 1:
+        hpa.evict_step(acc, db.k, db.v, db.lens, db.indptr, db.indices, dev(budgets), sinks,
+                       recent, kept, new, status=st, **dst)
+    else:
+        hpa.hpa_evict_select(acc, db.lens, db.indptr, db.indices, dev(budgets), sinks, recent,
+                             kept, new, st)
+        hpa.hpa_evict_compact(db.k, db.v, db.indptr, db.indices, kept, new, acc, status=st, **dst)
     torch.cuda.synchronize()
     assert int(st.item()) == 0
     ek, ev, ea = k0.clone(), v0.clone(), a0.clone()
