@@ -47,7 +47,9 @@ struct KwCfg {
   static constexpr int kPageBytes = KV == HPA_KV_BF16 ? 16384 : 8192;
   static constexpr int kStageBytes = kStepPages * kPageBytes;
   static constexpr int kN = KV == HPA_KV_E4M3 ? 2 * RP : RP < 16 ? 16 : RP;  // MMA columns
-  static constexpr int kStages = (kSmall ? 96 : 160) * 1024 / kStageBytes;
+  // Two CTAs share an SM with 64 KB of pages in flight each: with 96 KB, CTAs of equal
+  // budgets ended further apart (148 -> 154 us at 32 x 24000 E4M3, 49.5 -> 51 at 16 x 8192).
+  static constexpr int kStages = (kSmall ? 64 : 160) * 1024 / kStageBytes;
   static constexpr int kBufs = KV == HPA_KV_E4M3 && kSmall ? 2 : 4;  // S buffers in TMEM
   // Slots of the accumulator ring.  The copy for step n is issued once the MMAs of step
   // n - kStages are done, these once step n - kStages - kBufs has been read: with as many

@@ -128,7 +128,7 @@ def _ptr(t):
 def _dev(t, name, dtype=None):
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous()):
         raise HpaError("%s must be a contiguous CUDA tensor" % name)
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise HpaError("%s must be %s, got %s" % (name, dtype, t.dtype))
     return t
 
@@ -282,17 +282,27 @@ def hpa_decode_attn(q, k_pool, v_pool, page_indptr, page_indices, taskmap, num_c
     hpa_decode_attn picks the kernel by query rows per KV head (mma.sync up to 16,
     tcgen05 above); tc=True calls hpa_decode_attn_tc, mma=True hpa_decode_attn_mma and
     window=True hpa_decode_attn_window with the same arguments."""
-    kv, B, q_len, Hq, d, P, Hkv, page = _attn_args(q, k_pool, v_pool, page_indptr,
-                                                   page_indices, taskmap, k_scale, v_scale)
+    args = _attn_args(q, k_pool, v_pool, page_indptr, page_indices, taskmap, k_scale, v_scale)
+    _, B, q_len, Hq, d, _, _, _ = args
     _partials(partial_o, partial_lse, B, num_ctas, q_len, Hq, d)
+    _attn_call(args, q, k_pool, v_pool, page_indptr, page_indices, taskmap, num_ctas, partial_o,
+               partial_lse, k_scale, v_scale, sm_scale, _stream(stream), tc, mma, window)
+
+
+def _attn_call(args, q, k_pool, v_pool, page_indptr, page_indices, taskmap, num_ctas, partial_o,
+               partial_lse, k_scale, v_scale, sm_scale, stream, tc, mma, window):
+    """The attention call of the kernel asked for, on checked arguments."""
+    kv, B, q_len, Hq, d, P, Hkv, page = args
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(d)
     name = ("hpa_decode_attn_tc" if tc else "hpa_decode_attn_mma" if mma else
             "hpa_decode_attn_window" if window else "hpa_decode_attn")
-    _check(getattr(lib(), name)(
+    rc = getattr(lib(), name)(
         _ptr(q), _ptr(k_pool), _ptr(v_pool), kv, _ptr(k_scale), _ptr(v_scale), P,
-        _ptr(page_indptr), _ptr(page_indices), page, B, q_len, Hq, Hkv, d, float(sm_scale),
-        _ptr(taskmap), num_ctas, _ptr(partial_o), _ptr(partial_lse), _stream(stream)), name)
+        _ptr(page_indptr), _ptr(page_indices), page, B, q_len, Hq, Hkv, d, sm_scale,
+        _ptr(taskmap), num_ctas, _ptr(partial_o), _ptr(partial_lse), stream)
+    if rc != 0:
+        _check(rc, name)
 
 
 def hpa_decode_attn_mma(q, k_pool, v_pool, page_indptr, page_indices, taskmap, num_ctas: int,
@@ -429,9 +439,17 @@ def hpa_combine(partial_o, partial_lse, taskmap, num_ctas: int, out, out_lse=Non
     B, q_len, Hq, d = out.shape
     _outputs(out, out_lse, B, q_len, Hq, d)
     _partials(partial_o, partial_lse, B, num_ctas, q_len, Hq, d)
-    _check(lib().hpa_combine(_ptr(partial_o), _ptr(partial_lse), _ptr(taskmap), B, num_ctas,
-                             q_len, Hq, d, _ptr(out), _ptr(out_lse), _stream(stream)),
-           "hpa_combine")
+    _combine_call(partial_o, partial_lse, taskmap, num_ctas, out, out_lse, B, q_len, Hq, d,
+                  _stream(stream))
+
+
+def _combine_call(partial_o, partial_lse, taskmap, num_ctas, out, out_lse, B, q_len, Hq, d,
+                  stream):
+    """hpa_combine on checked arguments."""
+    rc = lib().hpa_combine(_ptr(partial_o), _ptr(partial_lse), _ptr(taskmap), B, num_ctas, q_len,
+                           Hq, d, _ptr(out), _ptr(out_lse), stream)
+    if rc != 0:
+        _check(rc, "hpa_combine")
 
 
 def hpa_selftest_wait_timeout(status, limit_ns: int, stream=None):
@@ -588,8 +606,9 @@ def hpa_key_weights(q, lse, k_pool, page_indptr, page_indices, taskmap, num_ctas
             _acc_pool(t, n, k_pool)
     _page_table(page_indptr, page_indices, B)
     _dev(taskmap, "taskmap")
-    # a static map holds num_ctas segment rows of 16 bytes, the others B + num_ctas - 1
-    if taskmap.numel() * taskmap.element_size() < hpa_taskmap_bytes(B, num_ctas) - 16 * (B - 1):
+    # int32 words of the smallest map of this shape, a static one: num_ctas segment rows
+    if taskmap.numel() * taskmap.element_size() < 4 * (((23 + 3 * B + 2 * num_ctas) & ~3) +
+                                                       4 * num_ctas):
         raise HpaError("taskmap is too small for %d requests over %d partitions" % (B, num_ctas))
     _one_device(q, lse, k_pool, k_scale, acc, out, page_indptr, page_indices, taskmap)
     if sm_scale is None:
@@ -776,12 +795,18 @@ def decode_step(ws: Workspace, q, k_pool, v_pool, seq_lens, page_indptr, page_in
         hpa_decode_attn_allheads(q, k_pool, v_pool, page_indptr, page_indices, ws.taskmap,
                                  ws.num_ctas, ws.partial_o, ws.partial_lse, k_scale, v_scale,
                                  sm_scale=sm_scale, stream=stream)
-    else:
-        hpa_decode_attn(q, k_pool, v_pool, page_indptr, page_indices, ws.taskmap, ws.num_ctas,
-                        ws.partial_o, ws.partial_lse, k_scale, v_scale, sm_scale=sm_scale,
-                        stream=stream, tc=tc, mma=mma, window=ws.window is not None)
-    if not fused:
         hpa_combine(ws.partial_o, ws.partial_lse, ws.taskmap, ws.num_ctas, out, out_lse, stream)
+    else:  # both calls after one round of checks
+        args = _attn_args(q, k_pool, v_pool, page_indptr, page_indices, ws.taskmap, k_scale,
+                          v_scale)
+        _, B, q_len, Hq, d, _, _, _ = args
+        _partials(ws.partial_o, ws.partial_lse, B, ws.num_ctas, q_len, Hq, d)
+        _outputs(out, out_lse, B, q_len, Hq, d)
+        _attn_call(args, q, k_pool, v_pool, page_indptr, page_indices, ws.taskmap, ws.num_ctas,
+                   ws.partial_o, ws.partial_lse, k_scale, v_scale, sm_scale, stream, tc, mma,
+                   ws.window is not None)
+        _combine_call(ws.partial_o, ws.partial_lse, ws.taskmap, ws.num_ctas, out, out_lse, B,
+                      q_len, Hq, d, stream)
     if acc is not None:
         hpa_key_weights(q, out_lse, k_pool, page_indptr, page_indices, ws.taskmap, ws.num_ctas,
                         acc, k_scale=k_scale, decay=decay, sm_scale=sm_scale, stream=stream)
