@@ -107,6 +107,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *__res
       const int need = kind == KIND_WINDOW ? win.q_len : 1;
       if (L < need) {
         atomicOr(&s_bad, HPA_STATUS_BAD_SEQLEN);
+      } else if (kind == KIND_WINDOW && L > INT_MAX - PAGE) {  // keys past the last page's end
+        atomicOr(&s_bad, HPA_STATUS_OVERFLOW);
       } else {
         keys = kind == KIND_WINDOW ? WinSpan::make(L, win.q_len, win.window, win.sinks).L : L;
         n = (keys - 1) / tile + 1;

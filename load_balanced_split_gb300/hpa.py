@@ -325,6 +325,8 @@ def hpa_decode_attn_window(q, k_pool, v_pool, page_indptr, page_indices, taskmap
                            partial_o, partial_lse, k_scale=None, v_scale=None,
                            sm_scale: float | None = None, stream=None):
     """hpa_decode_attn over a map of hpa_plan_window (sliding window and sink tokens)."""
+    _one_device(q, k_pool, v_pool, page_indptr, page_indices, taskmap, partial_o, partial_lse,
+                k_scale, v_scale)
     hpa_decode_attn(q, k_pool, v_pool, page_indptr, page_indices, taskmap, num_ctas, partial_o,
                     partial_lse, k_scale, v_scale, sm_scale, stream, window=True)
 
@@ -797,6 +799,9 @@ def decode_step(ws: Workspace, q, k_pool, v_pool, seq_lens, page_indptr, page_in
                                  sm_scale=sm_scale, stream=stream)
         hpa_combine(ws.partial_o, ws.partial_lse, ws.taskmap, ws.num_ctas, out, out_lse, stream)
     else:  # both calls after one round of checks
+        if ws.window is not None:
+            _one_device(q, k_pool, v_pool, seq_lens, page_indptr, page_indices, out, out_lse,
+                        k_scale, v_scale, ws.taskmap)
         args = _attn_args(q, k_pool, v_pool, page_indptr, page_indices, ws.taskmap, k_scale,
                           v_scale)
         _, B, q_len, Hq, d, _, _, _ = args
