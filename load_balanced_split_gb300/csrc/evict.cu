@@ -198,8 +198,18 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
             return j >= hi || j < lo ? (j < L ? kFixed : kAbsent) : weight_key(x);
           };
           const bool there = at + (lane >> 4) < cnt;  // an odd last page
+          const int key0 = (g + at) * PAGE;
+          const bool plain = at + 1 < cnt && key0 >= lo && hi - key0 >= 2 * PAGE;
           uint4 x = make_uint4(kAbsent, kAbsent, kAbsent, kAbsent);
-          if (there) {
+          // the usual turn: candidates alone, none of them negative or NaN
+          const bool usual =
+              plain &&
+              __all_sync(kFull, max(max(k[u].x, k[u].y), max(k[u].z, k[u].w)) <= 0x7f800000u);
+          if (usual) {
+            x = make_uint4(k[u].x | 0x80000000u, k[u].y | 0x80000000u, k[u].z | 0x80000000u,
+                           k[u].w | 0x80000000u);
+            if (KEEP) *reinterpret_cast<uint4 *>(keys + (g + at - w0) * PAGE + 4 * lane) = x;
+          } else if (there) {
             x = make_uint4(key(k[u].x, i), key(k[u].y, i + 1), key(k[u].z, i + 2),
                            key(k[u].w, i + 3));
             if (KEEP) *reinterpret_cast<uint4 *>(keys + (g + at - w0) * PAGE + 4 * lane) = x;
@@ -263,10 +273,11 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
     need = take - above;
     const uint32_t top1 = d1;
     // keys above the digit are counted; those that share it go on the list
+    const uint32_t low1 = top1 << 21, end1 = top1 == 2047 ? kFixed : low1 + (1u << 21);
     each([&](int, uint4 x) {
       auto see = [&](uint32_t k) {
-        gt_n += k >> 21 > top1 || k == kFixed;
-        if (k >> 21 == top1 && k != kFixed) {
+        gt_n += k >= end1;  // the fixed ones among them
+        if (k - low1 < end1 - low1) {
           atomicAdd(&hist1[(k >> 11) & 1023], 1);
           const int at = atomicAdd(&s_listed, 1);
           if (at < kList) list[at] = (k & 0x1fffffu) | static_cast<uint32_t>(wid) << 21;
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
     } else {
       each([&](int, uint4 x) {
         auto see = [&](uint32_t k) {
-          gt_n += k >> 21 == top1 && k != kFixed && k > T;
+          gt_n += k - low1 < end1 - low1 && k > T;
           eq_n += k == T;
         };
         see(x.x), see(x.y), see(x.z), see(x.w);
