@@ -22,6 +22,14 @@
 //    columns for V, so every shared-memory read is a 16-byte vector load;
 //  * every wait is bounded in time; a CTA that gives up flags the task map's
 //    status word, waits for its own copies in flight and returns.
+//
+// Sliding windows with sink tokens (WIN, hpa_decode_attn_window): the same kernel over a
+// map that counts only the pages the window reaches; the producer maps those to real pages
+// (WinSpan), and the consumers mask by position in the pages at the window's ends alone.
+// Bound by DRAM as the plain kernel is: 1.08 GB of E4M3 keys and values (128 requests,
+// window 4096) in 180 us of kernel, 6.0 TB/s; 135 MB (32 requests, window 1024, bf16) in
+// 28 us, of which 19 stream the pages and the rest is the wait for the map (4 us), the
+// reads up to the first page (2) and the segments' epilogues (3).
 #include <math_constants.h>
 
 #include <type_traits>
@@ -49,7 +57,6 @@ __host__ __device__ constexpr int merge_phys(int dd) { return dd + 4 * (dd >> 5)
 // accumulators are rescaled: P values stay <= 256, well inside bf16/f16 range.
 constexpr float kRescaleSlack = 8.f;
 constexpr int kThreads = (kConsumerWarps + 1) * 32;
-constexpr int kWinThreads = kThreads + 32;  // a staging warp beside the producer
 constexpr uint32_t kFull = 0xffffffffu;
 
 template <int KV>
@@ -117,9 +124,10 @@ __device__ __forceinline__ SegInfo seg_info(const AttnParams &p, int s, int tile
 }
 
 // ----------------------------------------------------------------------------- producer
-template <int KV, bool FUSED, bool ALLH>
+template <int KV, bool FUSED, bool ALLH, bool WIN>
 __device__ void producer(const AttnParams &p, const CUtensorMap *tmk, const CUtensorMap *tmv,
-                         uint8_t *smem, int s_begin, int s_end, int tile, int h0) {
+                         uint8_t *smem, int s_begin, int s_end, int tile, int h0, int window,
+                         int sinks) {
   using S = Smem<KV>;
   const int lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem);
@@ -140,7 +148,9 @@ __device__ void producer(const AttnParams &p, const CUtensorMap *tmk, const CUte
   const int hpc = ALLH ? p.heads_per_cta : 1, n_items = (s_end - s_begin) * hpc;
   for (int k = 0; k < n_items && ok; ++k) {
     const int s = s_begin + k / hpc, h = h0 + k % hpc;
-    const SegInfo f = seg_info<false>(p, s, tile, blockIdx.x, lane == 0 && h == h0);
+    const SegInfo f = seg_info<WIN>(p, s, tile, blockIdx.x, lane == 0 && h == h0);
+    WinSpan win = {};
+    if (WIN && f.pg0 < f.pg1) win = WinSpan::make(f.L, p.q_len, window, sinks);
     // stage the item's segment info and query rows for the consumers
     {
       const int slot = k & 1;
@@ -178,7 +188,8 @@ __device__ void producer(const AttnParams &p, const CUtensorMap *tmk, const CUte
       const int cnt = min(32, f.pg1 - pb);
       int id = 0;
       if (lane < cnt) {
-        id = pb + lane < pcount ? pidx[pb + lane] : -1;
+        const int pg = WIN ? win.real_page(pb + lane) : pb + lane;
+        id = pg < pcount ? pidx[pg] : -1;
         if (id < 0 || id >= p.num_pages) {  // bad id or too short a page list
           status_or(p.tm, HPA_STATUS_BAD_PAGE);
           id = 0;
@@ -215,167 +226,6 @@ __device__ void producer(const AttnParams &p, const CUtensorMap *tmk, const CUte
           phase ^= 1;
         }
       }
-    }
-  }
-  if (!ok && lane == 0) {
-    status_or(p.tm, HPA_STATUS_TIMEOUT);
-    *abort_flag = 1;
-    // never leave the CTA with copies still landing in its shared memory
-    for (int st = 0; st < S::kStages; ++st)
-      if (issued & (1u << st))
-        mbar_wait_bounded(full0 + 8 * st, (parity_bits >> st) & 1u, 1000000000ull);
-  }
-}
-
-// ----------------------------------------------------------------------------- window roles
-// Windows make short segments (a window of 4096 keys is 64 pages, where a long request has
-// thousands), and the reads that lead to a segment's first page -- its row, its length,
-// its page range, the page ids -- each wait for the one before, behind the page traffic.
-// So the window kernel gives the staging to a warp of its own that runs up to two segments
-// ahead, and the producer warp asks for the next 32 page ids, of the next segment where
-// this one ends, before it issues the pages it has.
-template <int KV>
-__device__ void win_stager(const AttnParams &p, uint8_t *smem, int s_begin, int s_end, int tile,
-                           int h, int window, int sinks) {
-  using S = Smem<KV>;
-  const int lane = threadIdx.x & 31, G = p.G, rb = row_base(), rows = group_rows(p);
-  const uint32_t base = smem_u32(smem);
-  const uint32_t qfull0 = base + S::kBars + 16 * S::kStages, qempty0 = qfull0 + 16;
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kFlag);
-  // this lane's 16-byte chunks of the group's rows (256 bytes each): chunk lane + 32 u
-  constexpr int kChunks = MAX_ROWS * 16 / 32;
-  int64_t off[kChunks];
-#pragma unroll
-  for (int u = 0; u < kChunks; ++u) {
-    const int row = (lane + 32 * u) >> 4, j = (rb + row) / G, g = (rb + row) - j * G;
-    off[u] = row < rows ? (static_cast<int64_t>(j) * p.Hq + h * G + g) * HEAD_DIM +
-                              ((lane + 32 * u) & 15) * 8
-                        : -1;
-  }
-  for (int s = s_begin; s < s_end; ++s) {
-    const int k = s - s_begin, slot = k & 1;
-    const SegInfo f = seg_info<true>(p, s, tile, blockIdx.x, lane == 0);
-    const int pstart = p.page_indptr[f.r], pcount = p.page_indptr[f.r + 1] - pstart;
-    WinSpan win = {};
-    if (f.pg0 < f.pg1) win = WinSpan::make(f.L, p.q_len, window, sinks);
-    const __nv_bfloat16 *q = p.q + static_cast<int64_t>(f.r) * p.q_len * p.Hq * HEAD_DIM;
-    int4 v[kChunks];
-#pragma unroll
-    for (int u = 0; u < kChunks; ++u)
-      if (off[u] >= 0) v[u] = *reinterpret_cast<const int4 *>(q + off[u]);
-    int good = 1;
-    if (lane == 0) good = !*abort_flag && mbar_wait_bounded(qempty0 + 8 * slot, ((k >> 1) & 1) ^ 1);
-    if (!__shfl_sync(kFull, good, 0)) {
-      if (lane == 0) {
-        status_or(p.tm, HPA_STATUS_TIMEOUT);
-        *abort_flag = 1;
-      }
-      return;
-    }
-    uint8_t *qs = smem + S::kQ + slot * kQSlotBytes;
-#pragma unroll
-    for (int u = 0; u < kChunks; ++u)
-      if (off[u] >= 0)
-        *reinterpret_cast<int4 *>(qs + ((lane + 32 * u) >> 4) * kQRowBytes +
-                                  ((lane + 32 * u) & 15) * 16) = v[u];
-    if (lane == 0) {
-      int4 *info = reinterpret_cast<int4 *>(smem + S::kInfo) + 2 * slot;
-      info[0] = make_int4(f.r, f.L, f.klo, f.khi);
-      info[1] = make_int4(pstart, pcount, win.sink_pages, win.hidden);
-    }
-    mbar_arrive(qfull0 + 8 * slot);  // every lane publishes its own stores
-  }
-}
-
-template <int KV>
-__device__ void win_producer(const AttnParams &p, const CUtensorMap *tmk, const CUtensorMap *tmv,
-                             uint8_t *smem, int n_seg, int h) {
-  using S = Smem<KV>;
-  const int lane = threadIdx.x & 31;
-  const uint32_t base = smem_u32(smem);
-  const uint32_t full0 = base + S::kBars, empty0 = full0 + 8 * S::kStages;
-  const uint32_t qfull0 = empty0 + 8 * S::kStages, qempty0 = qfull0 + 16;
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kFlag);
-  uint64_t pol = 0;
-  if (lane == 0) pol = l2_policy_evict_first();
-  int stage = 0;
-  uint32_t phase = 0, issued = 0, parity_bits = 0;
-  // The next 32 compact pages [pb, pb + 32) of the segment at hand, which ends at pg1; `id`:
-  // this lane's page id.  where: first page index, page count, sink pages, hidden pages.
-  int k = 0, pb = 0, pg1 = 0, id = 0;
-  int4 where = make_int4(0, 0, 0, 0);
-  bool ok = true, more = true;
-  // Takes the next staged segment where the one at hand is through, and asks for the ids.
-  // False if it is not staged yet (not with `wait`, unless the wait gave up: ok); `more`
-  // is cleared after the last segment.
-  auto ask = [&](bool wait) {
-    while (pb >= pg1) {  // again where a malformed segment has no pages
-      if (k == n_seg) {
-        more = false;
-        return true;
-      }
-      const uint32_t bar = qfull0 + 8 * (k & 1), parity = (k >> 1) & 1;
-      const bool staged = wait ? !*abort_flag && mbar_wait_bounded(bar, parity)
-                               : mbar_try_wait(bar, parity);
-      if (!__all_sync(kFull, staged)) {
-        ok = !wait;
-        return false;
-      }
-      const int4 *info = reinterpret_cast<const int4 *>(smem + S::kInfo) + 2 * (k & 1);
-      pb = info[0].z / PAGE;
-      pg1 = (info[0].w + PAGE - 1) / PAGE;
-      where = info[1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(qempty0 + 8 * (k & 1));
-      ++k;
-    }
-    id = 0;
-    if (pb + lane < pg1) {
-      const int pg = pb + lane < where.z ? pb + lane : pb + lane + where.w;
-      id = pg < where.y ? p.page_indices[where.x + pg] : -1;
-    }
-    return true;
-  };
-  bool asked = ask(true);
-  while (ok && more) {
-    const int cnt = min(32, pg1 - pb);
-    int ids = id;
-    pb += 32;
-    asked = ask(false);
-    if (lane < cnt && (ids < 0 || ids >= p.num_pages)) {  // bad id or too short a page list
-      status_or(p.tm, HPA_STATUS_BAD_PAGE);
-      ids = 0;
-    }
-    for (int i = 0; i < cnt; ++i) {
-      const int pid = __shfl_sync(kFull, ids, i);
-      int good = 1;
-      if (lane == 0) {
-        if (*abort_flag || !mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1)) {
-          good = 0;
-        } else {
-          const uint32_t fb = full0 + 8 * stage, dst = base + stage * S::kStageBytes;
-          const int z = pid * p.Hkv + h;
-          mbar_arrive_expect_tx(fb, S::kStageBytes);
-          if (KV == HPA_KV_BF16) {
-            tma_load_3d(dst, tmk, fb, 0, 0, z, pol);
-            tma_load_3d(dst + 8192, tmk, fb, 64, 0, z, pol);
-            tma_load_3d(dst + 16384, tmv, fb, 0, 0, z, pol);
-            tma_load_3d(dst + 24576, tmv, fb, 64, 0, z, pol);
-          } else {
-            tma_load_3d(dst, tmk, fb, 0, 0, z, pol);
-            tma_load_3d(dst + 8192, tmv, fb, 0, 0, z, pol);
-          }
-          issued |= 1u << stage;
-          parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
-        }
-      }
-      ok = __shfl_sync(kFull, good, 0) != 0;
-      if (!ok) break;
-      if (++stage == S::kStages) {
-        stage = 0;
-        phase ^= 1;
-      }
-      if (!asked) asked = ask(i + 1 == cnt);  // until the next segment is staged
     }
   }
   if (!ok && lane == 0) {
@@ -881,8 +731,8 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
       for (int pg = f.pg0; pg < f.pg1; ++pg)
         if (!page(pg, std::true_type())) break;
     } else {
-      // the clear pages' loop is a copy without the masks (191 -> 163 us of a 1.08 GB batch
-      // against one loop that tests each page)
+      // The clear pages run a copy of the loop without the masks, whose registers would
+      // spill in it (191 -> 162 us of attention at 16 x 32896 E4M3 keys, as the plain kernel).
       for (int pg = f.pg0; pg < f.pg1; ++pg) {
         const bool clear = pg >= clear0 && pg < clear1;
         if (clear ? !page(pg, std::false_type()) : !page(pg, std::true_type())) break;
@@ -1029,7 +879,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
 
 // ----------------------------------------------------------------------------- kernel
 template <int KV, bool FUSED, bool ALLH, bool WIN>
-__global__ void __launch_bounds__(WIN ? kWinThreads : kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 2)
     decode_attn_kernel(const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, const AttnParams p) {
   using S = Smem<KV>;
@@ -1044,10 +894,6 @@ __global__ void __launch_bounds__(WIN ? kWinThreads : kThreads, 2)
       p.trace ? p.trace + 4 * ((static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y) * p.C + c)
               : nullptr;
   if (trace && threadIdx.x == 0) trace[0] = globaltimer_ns();
-  if (WIN && threadIdx.x == 32) {
-    prefetch_tmap(&tmk);
-    prefetch_tmap(&tmv);
-  }
   // Nothing above this line reads memory that an earlier kernel writes: with
   // programmatic dependent launch the prologue overlaps the previous kernel.
   pdl_wait();
@@ -1084,8 +930,7 @@ __global__ void __launch_bounds__(WIN ? kWinThreads : kThreads, 2)
     }
     for (int sl = 0; sl < 2; ++sl) {
       mbar_init(base + S::kBars + 8 * (2 * S::kStages + sl), 32);                 // qfull
-      mbar_init(base + S::kBars + 8 * (2 * S::kStages + 2 + sl),
-                kConsumerWarps + (WIN ? 1 : 0));  // qempty (the window producer reads slots too)
+      mbar_init(base + S::kBars + 8 * (2 * S::kStages + 2 + sl), kConsumerWarps);  // qempty
     }
     *reinterpret_cast<int *>(smem + S::kFlag) = 0;
     fence_barrier_init();
@@ -1117,17 +962,12 @@ __global__ void __launch_bounds__(WIN ? kWinThreads : kThreads, 2)
     return;
   }
   const int tile = hdr[1], s_begin = hdr[2], s_end = hdr[3];
+  const int window = WIN ? hdr[4] : 0, sinks = WIN ? hdr[WIN ? 5 : 0] : 0;
 
   if (threadIdx.x >= kConsumerWarps * 32) {
-    if constexpr (!WIN)
-      producer<KV, FUSED, ALLH>(p, &tmk, &tmv, smem, s_begin, s_end, tile, h0);
-    else if (threadIdx.x < kThreads)
-      win_producer<KV>(p, &tmk, &tmv, smem, s_end - s_begin, h0);
-    else
-      win_stager<KV>(p, smem, s_begin, s_end, tile, h0, hdr[4], hdr[5]);
+    producer<KV, FUSED, ALLH, WIN>(p, &tmk, &tmv, smem, s_begin, s_end, tile, h0, window, sinks);
   } else {
-    consumer<KV, FUSED, ALLH, WIN>(p, smem, s_begin, s_end, tile, h0, WIN ? hdr[4] : 0,
-                                    WIN ? hdr[WIN ? 5 : 0] : 0);
+    consumer<KV, FUSED, ALLH, WIN>(p, smem, s_begin, s_end, tile, h0, window, sinks);
     if (trace && threadIdx.x == 0) trace[2] = globaltimer_ns();  // after the last epilogue
   }
 }
@@ -1147,7 +987,7 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &tmk, const CUtensorMa
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.C, ALLH ? 1 : p.Hkv, (p.rows + MAX_ROWS - 1) / MAX_ROWS);
-  cfg.blockDim = dim3(WIN ? kWinThreads : kThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Smem<KV>::kAlloc;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
