@@ -43,8 +43,8 @@ UNIT = "us/batch"
 # scaled to the full batch, since traffic grows with the KV read.
 TRAFFIC_PROFILE = {
     "config": 3,
-    "source_sha256": "67e86ff851789597537dc8fc07e83fbc9e8a369d6e98cd1044fef4e76cc1ff91",
-    "bytes_per_kv_byte": (2574309376 + 3269120) / 2572926976,
+    "source_sha256": "8d2bba05784dbcf245271c6ee2ef4d1093bc7d3bf3bc51a62a8a1f7a9e3d238d",
+    "bytes_per_kv_byte": (2574365184 + 3237888) / 2572926976,
     "workload": "mixed_45req_1k_128k_paged, first 12 requests (2.57 GB KV)",
 }
 

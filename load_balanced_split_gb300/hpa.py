@@ -264,12 +264,12 @@ def _partials(partial_o, partial_lse, B, num_ctas, q_len, Hq, d):
 
 def _outputs(out, out_lse, B, q_len, Hq, d):
     _dev(out, "out", torch.bfloat16)
-    if tuple(out.shape) != (B, q_len, Hq, d):
+    if out.shape != (B, q_len, Hq, d):
         raise HpaError("out must have q's shape %s, got %s" % ((B, q_len, Hq, d),
                                                                tuple(out.shape)))
     if out_lse is not None:
         _dev(out_lse, "out_lse", torch.float32)
-        if tuple(out_lse.shape) != (B, q_len, Hq):
+        if out_lse.shape != (B, q_len, Hq):
             raise HpaError("out_lse must have shape %s" % ((B, q_len, Hq),))
 
 
@@ -533,8 +533,16 @@ def hpa_store_kv_at(k_new, v_new, seq_lens, text_pos, page_indptr, page_indices,
 
 
 # ----------------------------------------------------------------------------- bounded cache
+_n_devices = 0
+
+
 def _one_device(*tensors):
     """The library launches on the current device: every tensor has to live there."""
+    global _n_devices
+    if not _n_devices:
+        _n_devices = torch.cuda.device_count()
+    if _n_devices == 1:
+        return
     here = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != here:
@@ -544,7 +552,7 @@ def _one_device(*tensors):
 
 def _acc_pool(t, name, k_pool):
     _dev(t, name, torch.float32)
-    if tuple(t.shape) != tuple(k_pool.shape[:3]):
+    if t.shape != k_pool.shape[:3]:
         raise HpaError("%s must have shape %s, one weight per cached key, got %s" %
                        (name, tuple(k_pool.shape[:3]), tuple(t.shape)))
 
@@ -600,7 +608,7 @@ def hpa_key_weights(q, lse, k_pool, page_indptr, page_indices, taskmap, num_ctas
     else:
         raise HpaError("unsupported KV dtype %s" % k_pool.dtype)
     _dev(lse, "lse", torch.float32)
-    if tuple(lse.shape) != (B, q_len, Hq):
+    if lse.shape != (B, q_len, Hq):
         raise HpaError("lse must have shape %s" % ((B, q_len, Hq),))
     out = acc if out is None else out
     for t, n in ((acc, "acc"), (out, "out")):
@@ -624,7 +632,8 @@ def hpa_key_weights(q, lse, k_pool, page_indptr, page_indices, taskmap, num_ctas
 def _kept(kept, new_lens, B, Hkv):
     _dev(kept, "kept", torch.int32)
     _dev(new_lens, "new_lens", torch.int32)
-    if kept.dim() != 3 or tuple(kept.shape[:2]) != (B, Hkv) or kept.shape[2] < 1:
+    shape = kept.shape
+    if len(shape) != 3 or shape[0] != B or shape[1] != Hkv or shape[2] < 1:
         raise HpaError("kept must be int32 [B][Hkv][at least the largest budget]")
     if new_lens.numel() != B:
         raise HpaError("new_lens needs one value per request")

@@ -49,7 +49,7 @@ def _weights(b, window=None, sinks=0, decay=1.0, C=None, splits=None, weighted=F
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("heads,q_len", [((8, 1), 1), ((16, 2), 2), ((5, 1), 1), ((12, 3), 1),
                                          ((8, 1), 3), ((8, 1), 8), ((32, 1), 2), ((17, 1), 1),
-                                         ((2, 2), 1), ((40, 8), 5)])
+                                         ((2, 2), 1), ((40, 8), 5), ((40, 1), 1), ((8, 1), 6)])
 def test_weights_head_layouts(kv, heads, q_len):
     b = W.make_batch([q_len, 64, 65, 300, 530], q_len=q_len, kv_dtype=kv, seed=heads[0] + q_len,
                      Hq=heads[0], Hkv=heads[1])

@@ -74,11 +74,9 @@ def test_wide_window_gives_the_full_step(kv):
     assert (lse.cpu().numpy() == full["lse"]).all()
 
 
-@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
-@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("kv,bad", [("bf16", float("nan")), ("bf16", float("inf")),
+                                    ("bf16", float("-inf")), ("e4m3", float("nan"))])
 def test_nonfinite_values_reach_only_the_rows_that_see_them(kv, bad):
-    if kv == "e4m3" and bad == bad:
-        pytest.skip("E4M3 has no infinity")
     window, sinks, q_len = 70, 5, 4
     b = W.make_batch([300, 33, 641], q_len=q_len, kv_dtype=kv, seed=6, Hq=8, Hkv=2)
     poison_hidden(b, window, sinks)
