@@ -173,8 +173,8 @@ int hpa_plan_static(const int32_t *seq_lens_dev, int32_t B, int32_t tile, int32_
  * q_len are kept in the map, and the calls that read it follow them:
  * hpa_decode_attn_window, hpa_combine and hpa_key_weights.  The other attention
  * calls report such a map as HPA_STATUS_BAD_MAP.  L_r < q_len sets
- * HPA_STATUS_BAD_SEQLEN, L_r > 2^31 - 65 HPA_STATUS_OVERFLOW.  Sizes as hpa_plan; a tile of 64 (one page) balances
- * short windows best.
+ * HPA_STATUS_BAD_SEQLEN, L_r > 2^31 - 65 HPA_STATUS_OVERFLOW.  Sizes as hpa_plan; a
+ * tile of 64 (one page) balances short windows best.
  */
 int hpa_plan_window(const int32_t *seq_lens_dev, int32_t B, int32_t q_len, int32_t window,
                     int32_t sinks, int32_t tile, int32_t num_ctas, void *taskmap_dev,
@@ -432,7 +432,8 @@ int hpa_store_kv_at(const void *k_new_dev, const void *v_new_dev, const int32_t 
  * their slots held.  Other slots are not written (with a window map: keys no token
  * sees; they keep their weight and do not decay).  acc_in_dev may equal acc_out_dev
  * (the usual, in place), be another pool that does not overlap it (draft tokens that may
- * yet be rejected) or be NULL for zero; decay 0 does not read it.  A row whose lse is -inf adds nothing.
+ * yet be rejected) or be NULL for zero; decay 0 does not read it.  A row whose lse is
+ * -inf adds nothing.
  * taskmap_dev: the map of the attention step, of any plan; num_ctas as planned.  Both
  * pools 16-byte aligned.  q, K, shapes and errors as hpa_decode_attn; the pages of a
  * bad page id and the keys of a request shorter than q_len are not written.

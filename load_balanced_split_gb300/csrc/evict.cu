@@ -1,5 +1,5 @@
 // Eviction from the paged cache by accumulated attention weight: which keys each KV head
-// keeps (evict_select_kernel), and the move of their rows to the front (evict_compact_kernel).
+// keeps (evict_select_kernel), and the move of their rows to the front.
 //
 // Selection.  A request longer than its budget keeps its first `sinks` keys, its last
 // `recent` keys and, of the others, the budget - sinks - recent with the largest weight,
@@ -10,15 +10,22 @@
 // distributed shared memory.  A pass with ballots and a scan over the warps and blocks
 // then writes the kept indices in ascending order.  The weights are read from memory once,
 // eight pages in flight per warp, and stay in the shared memory of the cluster (24 K keys
-// a block, 192 K a cluster; a longer request's rest is read again in each pass, from L2).  The second digit's
-// pass also counts what lies above and lists the few keys that share the first digit, so
-// the third digit and the final counts go over that list.
+// a block, 192 K a cluster; a longer request's rest is read again in each pass, from L2).
+// The second digit's pass also counts what lies above and lists the few keys that share
+// the first digit, so the third digit and the final counts go over that list.
+// Bound by instruction issue (half of the cycles) and the barriers between the passes,
+// not by memory: 18.6 us for 32 requests of 8 heads and up to 8192 keys cut to 2048, 77
+// for 64 of up to 24000 cut to 4096, 24 for one of 196608 cut to 16384.
 //
-// Compaction.  Row t of the new cache is row kept[t] of the old one, and kept is
-// ascending, so kept[t] >= t: a block that takes the rows of one (request, head) in order,
-// a batch at a time, and writes a batch after all of its rows are read never overwrites a
-// row that is still needed.  Columns of a row are independent, so with few (request, head)
-// pairs a row is split over several blocks; a move to other pages also splits the rows.
+// Compaction (evict_copy_kernel to other pages, evict_shift_kernel in place).  Row t of the
+// new cache is row kept[t] of the old one, and kept is ascending, so kept[t] >= t: in place,
+// a cluster that takes the rows of one (request, head) in order, a step at a time, and
+// writes a step after all of its rows are read never overwrites a row that is still needed.
+// Columns of a row are independent, so with few (request, head) pairs a row is split over
+// several blocks.  Bound by DRAM: to other pages 0.54 GB read and written in 86 us (6.2
+// TB/s) for the first of those, 1.09 GB (E4M3 rows) in 174 us, 68 MB in 14.3 for the last.
+// In place the same rows take 94, 187 and 28 us: a step's reads end before its writes
+// begin.  One block per (pair, slice) with no cluster took 108, 271 and 180.
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -399,58 +406,58 @@ __device__ __forceinline__ int64_t row_place(const CompactParams &p, const int32
   return static_cast<int64_t>(id) * p.Hkv * PAGE + t % PAGE;
 }
 
-// Block (pair, slice, z): tiles z, z + gridDim.z, ... of 256 rows of one (request, head),
-// columns [slice * lanes, (slice + 1) * lanes) of 16 bytes of K and V.  A thread finds one
-// row's source and destination (the next tile's while this one moves: an index, a page id
-// and the row are three dependent reads), then the block moves the tile in batches of
-// 8 pieces per thread.  In place there is one block per column and its batches go in
-// order, each read whole before it is written.
+// A request's two page tables: its own, and the one the new cache goes to.
+struct Places {
+  const int32_t *src_idx, *dst_idx;
+  int ps, pn, ds, dn;
+  __device__ Places(const CompactParams &p, int r, bool in_place) {
+    src_idx = p.page_indices;
+    ps = p.page_indptr[r], pn = p.page_indptr[r + 1] - ps;
+    dst_idx = in_place ? src_idx : p.dst_indices;
+    ds = in_place ? ps : p.dst_indptr[r];
+    dn = in_place ? pn : p.dst_indptr[r + 1] - ds;
+  }
+};
+
+// To other pages.  Block (pair, slice, z): tiles z, z + gridDim.z, ... of 256 rows of one
+// (request, head), columns [slice * lanes, (slice + 1) * lanes) of 16 bytes of K and V.  A
+// thread finds one row's source and destination (the next tile's while this one moves: an
+// index, a page id and the row are three dependent reads), then the block moves the tile
+// in batches of 8 pieces per thread.
 // Moving the rows in the selection's own blocks, to overlap one request's selection with
 // another's move, was slower: 108 -> 121 and 263 -> 302 us (32 x 8192 cut to 2048, 64 x
 // 24000 to 4096), the blocks that a selection wants being too few and too large to move.
-template <bool IN_PLACE>
 __global__ void __launch_bounds__(kCmpThreads)
-    evict_compact_kernel(const CompactParams p, int lanes) {
+    evict_copy_kernel(const CompactParams p, int lanes) {
   __shared__ int64_t s_src[kCmpThreads], s_dst[kCmpThreads];
   const int r = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv, tid = threadIdx.x;
   pdl_wait();  // the selection is usually the kernel just before
   const int n = p.new_lens[r];
   if (n <= 0 || n > p.kept_stride) return;  // left as it is (new_lens -1: a bad request)
   const int32_t *kept = p.kept + static_cast<int64_t>(blockIdx.x) * p.kept_stride;
-  const int ps = p.page_indptr[r], pn = p.page_indptr[r + 1] - ps;
-  const int ds = IN_PLACE ? ps : p.dst_indptr[r];
-  const int dn = IN_PLACE ? pn : p.dst_indptr[r + 1] - ds;
-  const int32_t *didx = IN_PLACE ? p.page_indices : p.dst_indices;
+  const Places at(p, r, false);
   const int row_ts = p.row_bytes / 16, col = blockIdx.y * lanes;
   const int sh = 31 - __clz(lanes);  // lanes is a power of two
   const int64_t head = static_cast<int64_t>(h) * PAGE;
   const int64_t step = static_cast<int64_t>(gridDim.z) * kCmpThreads;
 
   int64_t src = -1, dst = -1;
-  auto resolve = [&](int64_t at) {  // rows that stay where they are, and none, have src -1
+  auto resolve = [&](int64_t t) {  // rows that are not there have src -1
     src = dst = -1;
-    if (at < n) {
-      const int t = static_cast<int>(at);
-      const int k = kept[t];
-      if (!(IN_PLACE && k == t)) {
-        src = row_place(p, p.page_indices, ps, pn, k);
-        dst = row_place(p, didx, ds, dn, t);
-        if (dst < 0) src = -1;
-      }
+    if (t < n) {
+      src = row_place(p, at.src_idx, at.ps, at.pn, kept[t]);
+      dst = row_place(p, at.dst_idx, at.ds, at.dn, static_cast<int>(t));
+      if (dst < 0) src = -1;
     }
   };
   int64_t t0 = static_cast<int64_t>(blockIdx.z) * kCmpThreads;
-  if (t0 < n) resolve(t0 + tid);
+  resolve(t0 + tid);
   for (; t0 < n; t0 += step) {
     __syncthreads();  // the previous tile's places are no longer needed
     s_src[tid] = src < 0 ? -1 : src + head;
     s_dst[tid] = dst + head;
-    float a = 0.f;
-    const int64_t as = src + head, ad = dst + head;
-    const bool weigh = p.acc && blockIdx.y == 0 && src >= 0;
-    if (weigh) a = p.acc[as];
+    if (p.acc && blockIdx.y == 0 && src >= 0) p.acc[dst + head] = p.acc[src + head];
     __syncthreads();
-    if (weigh) p.acc[ad] = a;  // in place: read by every thread of the tile before this
     if (t0 + step < n) resolve(t0 + step + tid);
     const int pieces = static_cast<int>(n - t0 < kCmpThreads ? n - t0 : kCmpThreads) << sh;
 #pragma unroll 1
@@ -464,13 +471,81 @@ __global__ void __launch_bounds__(kCmpThreads)
           const int64_t from = e < pieces ? s_src[e >> sh] : -1;
           if (from >= 0) x[u] = pool[from * row_ts + col + (e & (lanes - 1))];
         }
-        if (IN_PLACE) __syncthreads();
 #pragma unroll
         for (int u = 0; u < kCmpFlight; ++u) {
           const int e = b + u * kCmpThreads + tid;
           if (e < pieces && s_src[e >> sh] >= 0)
             pool[s_dst[e >> sh] * row_ts + col + (e & (lanes - 1))] = x[u];
         }
+      }
+    }
+  }
+}
+
+// In place.  A cluster takes the rows of one (request, head) and column slice in order, a
+// step of `rows` rows for each of its blocks at a time: every block reads its rows of K, V
+// and the weights into registers, the cluster's barrier follows, and only then are they
+// written.  A row that is written at t is the source of no row after this step (kept[t'] >=
+// t' > t), and the sources of this step have been read.
+__global__ void __launch_bounds__(kCmpThreads, 2)
+    evict_shift_kernel(const CompactParams p, int lanes, int rows) {
+  __shared__ int64_t s_src[kCmpThreads], s_dst[kCmpThreads];
+  cg::cluster_group cl = cg::this_cluster();
+  const int r = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv, tid = threadIdx.x;
+  pdl_wait();
+  const int n = p.new_lens[r];
+  if (n <= 0 || n > p.kept_stride) return;  // the whole cluster
+  const int32_t *kept = p.kept + static_cast<int64_t>(blockIdx.x) * p.kept_stride;
+  const Places at(p, r, true);
+  const int row_ts = p.row_bytes / 16, col = blockIdx.y * lanes;
+  const int sh = 31 - __clz(lanes);
+  const int64_t head = static_cast<int64_t>(h) * PAGE;
+  const int64_t step = static_cast<int64_t>(cl.num_blocks()) * rows;
+  const int pieces = rows << sh;  // per pool, at most 8 per thread
+  uint4 *const kp = static_cast<uint4 *>(p.k_pool), *const vp = static_cast<uint4 *>(p.v_pool);
+
+  int64_t src = -1, dst = -1;
+  auto resolve = [&](int64_t t) {  // rows that stay where they are, and none, have src -1
+    src = dst = -1;
+    if (tid < rows && t < n) {
+      const int k = kept[t];
+      if (k != t) {
+        src = row_place(p, at.src_idx, at.ps, at.pn, k);
+        dst = row_place(p, at.dst_idx, at.ds, at.dn, static_cast<int>(t));
+        if (dst < 0) src = -1;
+      }
+    }
+  };
+  int64_t t0 = static_cast<int64_t>(cl.block_rank()) * rows;
+  resolve(t0 + tid);
+  for (int64_t first = 0; first < n; first += step, t0 += step) {
+    __syncthreads();  // the previous step's places are no longer needed
+    s_src[tid] = src < 0 ? -1 : src + head;
+    s_dst[tid] = dst + head;
+    const int64_t as = src + head, ad = dst + head;
+    const bool weigh = p.acc && blockIdx.y == 0 && src >= 0;
+    const float a = weigh ? p.acc[as] : 0.f;
+    __syncthreads();
+    uint4 k[kCmpFlight], v[kCmpFlight];
+#pragma unroll
+    for (int u = 0; u < kCmpFlight; ++u) {
+      const int e = u * kCmpThreads + tid;
+      const int64_t from = e < pieces ? s_src[e >> sh] : -1;
+      if (from >= 0) {
+        k[u] = kp[from * row_ts + col + (e & (lanes - 1))];
+        v[u] = vp[from * row_ts + col + (e & (lanes - 1))];
+      }
+    }
+    resolve(t0 + step + tid);
+    cl.sync();
+    if (weigh) p.acc[ad] = a;
+#pragma unroll
+    for (int u = 0; u < kCmpFlight; ++u) {
+      const int e = u * kCmpThreads + tid;
+      if (e < pieces && s_src[e >> sh] >= 0) {
+        const int64_t to = s_dst[e >> sh] * row_ts + col + (e & (lanes - 1));
+        kp[to] = k[u];
+        vp[to] = v[u];
       }
     }
   }
@@ -524,28 +599,43 @@ cudaError_t launch_evict_compact(const CompactParams &p, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int64_t pairs = static_cast<int64_t>(p.B) * p.Hkv;
-  const bool in_place = p.dst_indptr == nullptr;
-  int slices = 1, split = 1;
-  if (in_place) {  // columns of 32 bytes or more per block, until four blocks per SM
-    while (slices < p.row_bytes / 32 && pairs * slices < 4 * sms) slices *= 2;
-  } else {  // rows: as many tiles as the kept lists can hold, up to 32 blocks per SM
-    const int64_t tiles = (p.kept_stride + kCmpThreads - 1) / kCmpThreads;
-    const int64_t most = 1 + 32 * static_cast<int64_t>(sms) / pairs;
-    split = static_cast<int>(tiles < most ? tiles : most);
-    while (slices < p.row_bytes / 64 && pairs * split * slices < 2 * sms) slices *= 2;
-  }
-  const int lanes = p.row_bytes / 16 / slices;
+  const int row_ts = p.row_bytes / 16;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pairs), slices, split);
   cfg.blockDim = dim3(kCmpThreads);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return in_place ? cudaLaunchKernelEx(&cfg, evict_compact_kernel<true>, p, lanes)
-                  : cudaLaunchKernelEx(&cfg, evict_compact_kernel<false>, p, lanes);
+  int slices = 1;
+  if (p.dst_indptr != nullptr) {
+    // rows: as many tiles as the kept lists can hold, up to 32 blocks per SM (8 per SM: 174
+    // -> 183 us for 512 pairs of 4096 rows); with few of them, columns of 64 bytes or more
+    const int64_t tiles = (p.kept_stride + kCmpThreads - 1) / kCmpThreads;
+    const int64_t most = 1 + 32 * static_cast<int64_t>(sms) / pairs;
+    const int split = static_cast<int>(tiles < most ? tiles : most);
+    while (slices < row_ts / 4 && pairs * split * slices < 2 * sms) slices *= 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(pairs), slices, split);
+    return cudaLaunchKernelEx(&cfg, evict_copy_kernel, p, row_ts / slices);
+  }
+  // Blocks of a cluster as far as the kept lists have rows for them: 8 with few pairs (16384
+  // rows of 8 pairs: 28 us in 8, 42 in 4, 147 in one), 4 where these fill the GPU (512
+  // pairs of 4096 rows: 187 us in 4, 200 in 8, 192 in one); then columns of 32 bytes or
+  // more.
+  auto rows_of = [&](int lanes) { return lanes > kCmpFlight ? kCmpThreads / 2 : kCmpThreads; };
+  int ranks = 1;
+  while (ranks < (pairs * 4 < 2 * sms ? kMaxCluster : 4) &&
+         static_cast<int64_t>(ranks) * rows_of(row_ts) < p.kept_stride)
+    ranks *= 2;
+  while (slices < row_ts / 2 && pairs * slices * ranks < 2 * sms) slices *= 2;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = ranks;
+  cfg.numAttrs = 2;
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs), slices, ranks);
+  const int lanes = row_ts / slices;
+  return cudaLaunchKernelEx(&cfg, evict_shift_kernel, p, lanes, rows_of(lanes));
 }
 
 }  // namespace hpa

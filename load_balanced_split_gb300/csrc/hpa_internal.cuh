@@ -298,10 +298,6 @@ __device__ __forceinline__ void lds128(uint32_t addr, uint32_t &a, uint32_t &b, 
                : "r"(addr));
 }
 
-__device__ __forceinline__ void lds64(uint32_t addr, uint32_t &a, uint32_t &b) {
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
-}
-
 // D += A(16x16, row) * B(16x8, col); bf16 inputs, fp32 accumulate.
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
