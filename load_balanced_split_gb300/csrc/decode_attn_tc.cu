@@ -5,7 +5,7 @@
 // tiles of its partition from the task map and writes split-KV partial
 // results for the combine.  One CTA is (partition c, KV head h) and covers all
 // G * q_len query rows of h (up to 64) in one pass over the KV, where the
-// mma.sync kernel needs one pass per group of 16 rows.  This matters for MTP
+// mma.sync kernel needs one pass per group of up to 16 rows.  This matters for MTP
 // with several draft tokens, where the warp-level MMAs become the bound.
 //
 // Work per step = PPS pages (64 PPS keys) of one KV head, PPS = 4 for the 8-bit

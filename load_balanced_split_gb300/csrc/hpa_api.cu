@@ -152,7 +152,7 @@ int32_t hpa_default_num_ctas_mma(int32_t Hq, int32_t Hkv, int32_t q_len, int32_t
     return -1;
   }
   if (hpa::attn_ctas_per_sm(kv_dtype, q_len, &per_sm) != 0 || per_sm < 1) return -1;
-  // one CTA per (partition, KV head, group of 16 query rows)
+  // one CTA per (partition, KV head, group of up to 16 query rows)
   const int groups = ((Hq / Hkv) * q_len + hpa::MAX_ROWS - 1) / hpa::MAX_ROWS;
   const int c = sms * per_sm / (Hkv * groups);
   return c < 1 ? 1 : c;
@@ -258,6 +258,8 @@ static int decode_attn_impl(const void *q_dev, const void *k_pool_dev, const voi
   p.Hkv = Hkv;
   p.G = Hq / Hkv;
   p.rows = p.G * q_len;
+  const int groups = (p.rows + hpa::MAX_ROWS - 1) / hpa::MAX_ROWS;
+  p.group = (p.rows + groups - 1) / groups;
   p.heads_per_cta = all_heads ? Hkv : 1;
   p.window = window;
   p.scale_log2 = sm_scale * 1.4426950408889634f;
@@ -397,7 +399,7 @@ int32_t hpa_default_num_ctas_allheads(int32_t Hq, int32_t Hkv, int32_t q_len, in
     return -1;
   }
   if (hpa::attn_ctas_per_sm(kv_dtype, q_len, &per_sm) != 0 || per_sm < 1) return -1;
-  // one CTA per (partition, group of 16 query rows), each walking every KV head
+  // one CTA per (partition, group of up to 16 query rows), each walking every KV head
   const int groups = ((Hq / Hkv) * q_len + hpa::MAX_ROWS - 1) / hpa::MAX_ROWS;
   const int c = sms * per_sm / groups;
   return c < 1 ? 1 : c;

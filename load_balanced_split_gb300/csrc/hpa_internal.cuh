@@ -39,7 +39,7 @@ struct TaskMapLayout {
 constexpr int PAGE = 64;       // tokens per KV page
 constexpr int HEAD_DIM = 128;  // d
 constexpr int MAX_ROWS = 16;   // query rows per CTA (one m16 MMA tile)
-constexpr int MAX_ROWS_TOTAL = 64;  // G * q_len rows per KV head, in groups of 16
+constexpr int MAX_ROWS_TOTAL = 64;  // G * q_len rows per KV head, in groups of up to 16
 
 // The pages of one request that a sliding window of `window` keys with `sinks` first
 // keys reaches, as a shorter "compact" sequence of pages: the pages holding sinks, then
@@ -80,6 +80,7 @@ struct AttnParams {
   int64_t num_pages;
   TaskMapLayout lay;
   int B, C, q_len, Hq, Hkv, G, rows;
+  int group;          // query rows per CTA of the mma.sync kernel: rows in equal groups
   int heads_per_cta;  // KV heads one CTA walks per segment: 1 (grid over heads) or Hkv
   bool window;        // the map is one of hpa_plan_window
   float scale_log2;   // sm_scale * log2(e)

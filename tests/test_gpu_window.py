@@ -45,7 +45,8 @@ def test_lengths_around_every_border(kv, window, sinks, q_len):
 
 
 @pytest.mark.parametrize("heads,q_len", [((2, 2), 1), ((8, 1), 8), ((5, 1), 1), ((40, 8), 4),
-                                         ((32, 2), 1), ((48, 4), 2), ((12, 3), 5)])
+                                         ((32, 2), 1), ((48, 4), 2), ((12, 3), 5),
+                                         ((64, 8), 5)])
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_head_layouts(kv, heads, q_len):
     _run([q_len, 90, 400, 777], q_len, kv, 130, 7, heads, seed=heads[0])
