@@ -67,7 +67,8 @@ typedef struct CUstream_st *hpa_stream_t;
 #define HPA_STATUS_MISMATCH 2   /* map built for another B / num_ctas / tile */
 #define HPA_STATUS_BAD_PAGE 4   /* a page id outside [0, num_pages); page 0 was read instead */
 #define HPA_STATUS_TIMEOUT 8    /* a shared-memory pipeline wait exceeded ~2 s; CTA gave up */
-#define HPA_STATUS_OVERFLOW 16  /* total tile count does not fit int32 */
+#define HPA_STATUS_OVERFLOW 16  /* total tile count does not fit int32; hpa_plan_window and
+                                   hpa_evict_select: a length whose positions do not */
 #define HPA_STATUS_BAD_MAP 32   /* a malformed map: a partition's segment range, a segment row
                                    (request, owner, tile range) or a request's segment range
                                    out of bounds; the row was skipped, never followed */
@@ -454,10 +455,11 @@ int hpa_key_weights(const void *q_dev, const float *lse_dev, const void *k_pool_
  * order to kept_dev[(r * Hkv + h) * kept_stride + t], t < new_lens_dev[r] =
  * min(L_r, budget); entries past that are left as they were.  A request that cannot
  * be served gets new_lens -1, which hpa_evict_compact passes over, and sets bits in
- * status_dev (optional int32, 4-byte aligned): L_r < 1 HPA_STATUS_BAD_SEQLEN; a budget
- * below 1, min(L_r, budget) > kept_stride, or sinks + recent > budget < L_r
- * HPA_STATUS_BAD_BUDGET; a missing or out-of-range page HPA_STATUS_BAD_PAGE.
- * kept_dev: int32, B * Hkv * kept_stride.  new_lens_dev: int32 [B], neither
+ * status_dev (optional int32, 4-byte aligned): L_r < 1 HPA_STATUS_BAD_SEQLEN; L_r above
+ * 2^31 - 65537 HPA_STATUS_OVERFLOW; a budget below 1, min(L_r, budget) > kept_stride, or
+ * sinks + recent > budget < L_r HPA_STATUS_BAD_BUDGET; a missing or out-of-range page
+ * HPA_STATUS_BAD_PAGE.
+ * kept_dev: int32, B * Hkv * kept_stride.  new_lens_dev: int32 [B], overlapping neither
  * seq_lens_dev nor budgets_dev.  acc_dev 16-byte aligned.
  */
 int hpa_evict_select(const float *acc_dev, const int32_t *seq_lens_dev,
@@ -478,7 +480,7 @@ int hpa_evict_select(const float *acc_dev, const int32_t *seq_lens_dev,
  * the same as before.  kept must ascend, as hpa_evict_select writes it.  new_lens[r]
  * below 1 or beyond kept_stride: the request is passed over.  A position without a
  * valid page sets HPA_STATUS_BAD_PAGE in status_dev (optional), and that row is not
- * moved.  k_pool_dev, v_pool_dev 16-byte aligned.
+ * moved.  k_pool_dev, v_pool_dev 16-byte aligned, apart from each other.
  */
 int hpa_evict_compact(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, float *acc_dev,
                       int64_t num_pages, const int32_t *page_indptr_dev,

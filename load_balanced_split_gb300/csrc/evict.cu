@@ -46,6 +46,7 @@ constexpr int kBlockPages = kSelWarps * kWarpPages;
 constexpr int kBins = 2048, kBins2 = 1024;                    // first and third digit; second
 constexpr int kList = 1024;                                  // keys that share the first digit
 constexpr int kMaxCluster = 8;
+constexpr int kMaxLen = INT_MAX - 65536;  // the loops over keys run past the end by less
 constexpr int64_t kMinKeys = 4096;                           // per block before a cluster grows
 constexpr int kSelSmem = kBlockPages * PAGE * 4 + (kBins + kBins2 + kList) * 4;
 constexpr int kSelBlocks = 2;                                // per SM: 112 KB of shared memory each
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
   const int n = min(L, budget);
   int bad = 0;  // the same in every block of the cluster
   if (L < 1) bad = HPA_STATUS_BAD_SEQLEN;
+  else if (L > kMaxLen) bad = HPA_STATUS_OVERFLOW;
   else if (budget < 1 || n > p.kept_stride ||
            (L > budget && static_cast<int64_t>(p.sinks) + p.recent > budget))
     bad = HPA_STATUS_BAD_BUDGET;

@@ -30,6 +30,12 @@ using hpa::cuda_fail;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether [a, a + na) and [b, b + nb) share a byte (null pointers share none).
+bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
+  const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && (x < y ? y - x < na : x - y < nb);
+}
+
 constexpr int32_t kMaxB = 1 << 24;
 constexpr int32_t kMaxC = 1 << 20;
 
@@ -551,8 +557,12 @@ int hpa_key_weights(const void *q_dev, const float *lse_dev, const void *k_pool_
     return HPA_ERR_UNSUPPORTED;
   if (num_pages * Hkv > INT_MAX) return HPA_ERR_UNSUPPORTED;
   if (!aligned(q_dev, 16) || !aligned(k_pool_dev, 16) || !aligned(taskmap_dev, 16) ||
-      !aligned(acc_in_dev, 16) || !aligned(acc_out_dev, 16) || !aligned(lse_dev, 4))
+      !aligned(acc_in_dev, 16) || !aligned(acc_out_dev, 16) || !aligned(lse_dev, 4) ||
+      !aligned(k_scale_dev, 4) || !aligned(page_indptr_dev, 4) || !aligned(page_indices_dev, 4))
     return HPA_ERR_ALIGN;
+  const uint64_t acc_bytes = static_cast<uint64_t>(num_pages) * Hkv * hpa::PAGE * 4;
+  if (acc_in_dev != acc_out_dev && overlap(acc_in_dev, acc_bytes, acc_out_dev, acc_bytes))
+    return HPA_ERR_INVALID;
   CUtensorMap tmk;
   const int rc = pool_map(k_pool_dev, num_pages, Hkv, kv_dtype, &tmk);
   if (rc != HPA_OK) return rc;
@@ -593,12 +603,16 @@ static int evict_params(const float *acc_dev, const int32_t *seq_lens_dev,
   if (B < 1 || B > kMaxB || Hkv < 1 || Hkv > 65535 || num_pages < 1 || sinks < 0 ||
       recent < 0 || kept_stride < 1)
     return HPA_ERR_INVALID;
-  // the blocks of a request's other heads may still read what the first one writes
-  if (new_lens_dev == seq_lens_dev || new_lens_dev == budgets_dev) return HPA_ERR_INVALID;
   if (page_size != hpa::PAGE || int64_t(B) * Hkv > INT_MAX) return HPA_ERR_UNSUPPORTED;
   if (!aligned(acc_dev, 16) || !aligned(kept_dev, 4) || !aligned(new_lens_dev, 4) ||
-      (status_dev && !aligned(status_dev, 4)))
+      !aligned(seq_lens_dev, 4) || !aligned(budgets_dev, 4) || !aligned(page_indptr_dev, 4) ||
+      !aligned(page_indices_dev, 4) || (status_dev && !aligned(status_dev, 4)))
     return HPA_ERR_ALIGN;
+  // the blocks of a request's other heads may still read what the first one writes
+  const uint64_t lens_bytes = static_cast<uint64_t>(B) * 4;
+  if (overlap(new_lens_dev, lens_bytes, seq_lens_dev, lens_bytes) ||
+      overlap(new_lens_dev, lens_bytes, budgets_dev, lens_bytes))
+    return HPA_ERR_INVALID;
   *p = hpa::EvictParams{acc_dev,   seq_lens_dev, page_indptr_dev, page_indices_dev,
                         budgets_dev, num_pages,  sinks,           recent,
                         B,         Hkv,          kept_dev,        kept_stride,
@@ -614,7 +628,7 @@ static int compact_params(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, 
                           const int32_t *new_lens_dev, int32_t B, int32_t Hkv, int32_t d,
                           int32_t *status_dev, hpa::CompactParams *p) {
   if (!k_pool_dev || !v_pool_dev || !page_indptr_dev || !page_indices_dev || !kept_dev ||
-      !new_lens_dev || !dst_indptr_dev != !dst_indices_dev || k_pool_dev == v_pool_dev)
+      !new_lens_dev || !dst_indptr_dev != !dst_indices_dev)
     return HPA_ERR_INVALID;
   if (kv_dtype != HPA_KV_BF16 && kv_dtype != HPA_KV_E4M3) return HPA_ERR_INVALID;
   if (B < 1 || B > kMaxB || Hkv < 1 || Hkv > 65535 || num_pages < 1 || kept_stride < 1)
@@ -622,14 +636,19 @@ static int compact_params(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, 
   if (d != hpa::HEAD_DIM || page_size != hpa::PAGE || int64_t(B) * Hkv > INT_MAX)
     return HPA_ERR_UNSUPPORTED;
   if (!aligned(k_pool_dev, 16) || !aligned(v_pool_dev, 16) || !aligned(acc_dev, 4) ||
-      (status_dev && !aligned(status_dev, 4)))
+      !aligned(kept_dev, 4) || !aligned(new_lens_dev, 4) || !aligned(page_indptr_dev, 4) ||
+      !aligned(page_indices_dev, 4) || !aligned(dst_indptr_dev, 4) ||
+      !aligned(dst_indices_dev, 4) || (status_dev && !aligned(status_dev, 4)))
     return HPA_ERR_ALIGN;
+  const int row_bytes = d * (kv_dtype == HPA_KV_BF16 ? 2 : 1);
+  const uint64_t bytes = static_cast<uint64_t>(num_pages) * Hkv * hpa::PAGE * row_bytes;
+  if (overlap(k_pool_dev, bytes, v_pool_dev, bytes)) return HPA_ERR_INVALID;
   if (dst_indptr_dev == page_indptr_dev && dst_indices_dev == page_indices_dev)
     dst_indptr_dev = dst_indices_dev = nullptr;  // the request's own pages: in place
   *p = hpa::CompactParams{k_pool_dev,     v_pool_dev,      acc_dev,   page_indptr_dev,
                           page_indices_dev, dst_indptr_dev, dst_indices_dev, num_pages,
                           kept_dev,       new_lens_dev,    kept_stride, B,
-                          Hkv,            d * (kv_dtype == HPA_KV_BF16 ? 2 : 1), status_dev};
+                          Hkv,            row_bytes,       status_dev};
   return HPA_OK;
 }
 

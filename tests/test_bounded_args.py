@@ -58,6 +58,11 @@ def test_key_weights_argument_checks():
     assert call(P=1 << 29) == -2 and call(Hq=63) == -2
     for name in ("a0", "a1", "k", "tm"):
         assert call(**{name: FAKE + 8}) == -4, name
+    for name in ("lse", "ip", "ix"):
+        assert call(**{name: FAKE + 2}) == -4, name
+    size = 100 * 8 * 64 * 4                          # a pool of weights that overlaps the other
+    for a0, a1 in ((FAKE, FAKE + size - 16), (FAKE + size - 16, FAKE)):
+        assert call(a0=a0, a1=a1) == -1
 
 
 def test_evict_select_argument_checks():
@@ -76,13 +81,17 @@ def test_evict_select_argument_checks():
         assert call(**bad) == -1, bad
     assert call(page=32) == -2 and call(B=1 << 24, Hkv=1000) == -2
     assert call(acc=FAKE + 4) == -4 and call(st=FAKE + 2) == -4
+    for name in ("lens", "ip", "ix", "budgets", "kept"):
+        assert call(**{name: FAKE + 66}) == -4, name
+    assert call(new=FAKE + 130) == -4
+    assert call(new=FAKE + 8) == -1 and call(new=FAKE + 60) == -1  # overlaps lens, budgets
 
 
 def test_evict_compact_argument_checks():
     L = hpa.lib()
 
     def call(**kw):
-        a = dict(k=FAKE, v=FAKE + 64, kv=0, acc=None, P=100, ip=FAKE, ix=FAKE, dip=None, dix=None,
+        a = dict(k=FAKE, v=2 * FAKE + (100 << 17), kv=0, acc=None, P=100, ip=FAKE, ix=FAKE, dip=None, dix=None,
                  page=64, kept=FAKE, stride=100, new=FAKE, B=3, Hkv=8, d=128, st=None)
         a.update(kw)
         return L.hpa_evict_compact(*a.values(), None)
@@ -90,7 +99,12 @@ def test_evict_compact_argument_checks():
     for name in ("k", "v", "ip", "ix", "kept", "new"):
         assert call(**{name: None}) == -1, name
     assert call(dip=FAKE) == -1 and call(dix=FAKE) == -1           # one half of a page table
-    assert call(v=FAKE) == -1 and call(kv=3) == -1 and call(stride=0) == -1
+    assert call(v=FAKE) == -1 and call(v=FAKE + (100 << 17) - 16) == -1   # one pool over the other
+    assert call(k=FAKE + (100 << 17), v=2 * FAKE) == -1
+    for name in ("ip", "ix", "kept", "new", "acc"):
+        assert call(**{name: FAKE + 2}) == -4, name
+    assert call(dip=FAKE + 2, dix=FAKE) == -4 and call(dip=FAKE, dix=FAKE + 2) == -4
+    assert call(kv=3) == -1 and call(stride=0) == -1
     assert call(d=64) == -2 and call(page=128) == -2
     assert call(k=FAKE + 8) == -4
 

@@ -233,6 +233,10 @@ def test_select_refusals():
             hpa.hpa_evict_select(acc, one(n), one(0, len(indices)), one(*indices), one(budget), 0,
                                  0, kept, new, st)
             assert int(st.item()) == 4 and int(new.item()) == -1 and (kept == -9).all()
+    for n in (2 ** 31 - 1, 2 ** 31 - 65536):        # positions that int32 does not hold
+        new, st = one(5), one(0)
+        hpa.hpa_evict_select(acc, one(n), one(0, 2), one(0, 1), one(40), 0, 0, kept, new, st)
+        assert int(st.item()) == 16 and int(new.item()) == -1 and (kept == -9).all()
 
 
 # ----------------------------------------------------------------------------- compaction
