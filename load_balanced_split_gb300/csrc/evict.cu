@@ -11,11 +11,11 @@
 // then writes the kept indices in ascending order.  The weights are read from memory once,
 // eight pages in flight per warp, and stay in the shared memory of the cluster (24 K keys
 // a block, 192 K a cluster; a longer request's rest is read again in each pass, from L2).
-// The second digit's pass also counts what lies above and lists the few keys that share
-// the first digit, so the third digit and the final counts go over that list.
+// The third digit's pass also counts what lies above and lists the few keys that share
+// both digits before, so the final counts go over that list.
 // Bound by instruction issue (half of the cycles) and the barriers between the passes,
-// not by memory: 18.6 us for 32 requests of 8 heads and up to 8192 keys cut to 2048, 77
-// for 64 of up to 24000 cut to 4096, 24 for one of 196608 cut to 16384.
+// not by memory: 15 us for 32 requests of 8 heads and about 8192 keys cut to 2048, 53 for
+// 64 of about 24000 cut to 4096, 23 for one of 196608 cut to 16384.
 //
 // Compaction (evict_copy_kernel to other pages, evict_shift_kernel in place).  Row t of the
 // new cache is row kept[t] of the old one, and kept is ascending, so kept[t] >= t: in place,
@@ -44,7 +44,7 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kWarpPages = 24;                               // pages a warp holds in shared memory
 constexpr int kBlockPages = kSelWarps * kWarpPages;
 constexpr int kBins = 2048, kBins2 = 1024;                    // first and third digit; second
-constexpr int kList = 1024;                                  // keys that share the first digit
+constexpr int kList = 1024;                                  // keys that share two digits
 constexpr int kMaxCluster = 8;
 constexpr int kMaxLen = INT_MAX - 65536;  // the loops over keys run past the end by less
 constexpr int64_t kMinKeys = 4096;                           // per block before a cluster grows
@@ -99,19 +99,18 @@ __device__ void find_bin(cg::cluster_group &cl, int *hist, int k, int &bin, int 
   }
   if (lane == 31) wsum[wid] = v;
   __syncthreads();
-  int before = v - mine;
-#pragma unroll
-  for (int x = 0; x < kSelWarps; ++x) before += x < wid ? wsum[x] : 0;
+  const int before = v - mine + __reduce_add_sync(kFull, lane < wid ? wsum[lane] : 0);
   if (before < k && before + mine >= k) {
+    int up = before;  // entries in the bins above bin x
     bool found = false;
 #pragma unroll
     for (int x = N - 1; x >= 0; --x) {
-      if (!found && before + c[x] >= k) {
+      if (!found && up + c[x] >= k) {
         s_bin = low + x;
-        s_above = before;
+        s_above = up;
         found = true;
       }
-      before += c[x];
+      up += c[x];
     }
   }
   __syncthreads();
@@ -127,20 +126,37 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
   const int ranks = cl.num_blocks(), rank = cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   int *hist0 = reinterpret_cast<int *>(sel_smem + kBlockPages * PAGE), *hist1 = hist0 + kBins;
-  // keys that share the first digit: their other 21 bits, and the warp above them
+  // keys that share the first two digits: their other 11 bits, and the warp above them
   uint32_t *list = reinterpret_cast<uint32_t *>(hist1 + kBins2);
   uint32_t *keys = sel_smem + wid * (kWarpPages * PAGE);   // this warp's first pages
-  const int pair = blockIdx.x / ranks, r = pair / p.Hkv, h = pair % p.Hkv;
+  const int slot = blockIdx.x / ranks / p.Hkv, h = blockIdx.x / ranks % p.Hkv;
+  // No early launch of the kernel after this one: compaction blocks that wait on the SMs
+  // settle unevenly around these (174 -> 251 us of compaction on 64 requests cut to 4096).
+  pdl_wait();
+  int r = slot;
+  if (p.longest_first) {  // the request that has `slot` longer ones; four threads count for each
+    __shared__ int s_r;
+    int *lens = reinterpret_cast<int *>(sel_smem);
+    for (int i = tid; i < p.B; i += kSelThreads) lens[i] = p.seq_lens[i];
+    __syncthreads();
+    const int q = tid >> 2;
+    int longer = 0;
+    if (q < p.B)
+      for (int u = tid & 3; u < p.B; u += 4)
+        longer += lens[u] > lens[q] || (lens[u] == lens[q] && u < q);
+    longer += __shfl_xor_sync(kFull, longer, 1);
+    longer += __shfl_xor_sync(kFull, longer, 2);
+    if (q < p.B && (tid & 3) == 0 && longer == slot) s_r = q;
+    __syncthreads();
+    r = s_r;
+  }
+  const int L = p.seq_lens[r], budget = p.budgets[r];
+  const int pstart = p.page_indptr[r], pcount = p.page_indptr[r + 1] - pstart;
+  const int n = min(L, budget);
   if (tid == 0) s_bad = s_listed = 0;
   if (tid < kSelWarps) s_gt[tid] = s_eq[tid] = 0;
   for (int i = tid; i < (kBins + kBins2) / 4; i += kSelThreads)  // both histograms
     reinterpret_cast<int4 *>(hist0)[i] = make_int4(0, 0, 0, 0);
-  // No early launch of the kernel after this one: compaction blocks that wait on the SMs
-  // settle unevenly around these (174 -> 251 us of compaction on 64 requests cut to 4096).
-  pdl_wait();
-  const int L = p.seq_lens[r], budget = p.budgets[r];
-  const int pstart = p.page_indptr[r], pcount = p.page_indptr[r + 1] - pstart;
-  const int n = min(L, budget);
   int bad = 0;  // the same in every block of the cluster
   if (L < 1) bad = HPA_STATUS_BAD_SEQLEN;
   else if (L > kMaxLen) bad = HPA_STATUS_OVERFLOW;
@@ -161,7 +177,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
     return;
   }
   __syncthreads();
-  int32_t *kept = p.kept + static_cast<int64_t>(pair) * p.kept_stride;
+  int32_t *kept = p.kept + (static_cast<int64_t>(r) * p.Hkv + h) * p.kept_stride;
   const int32_t *pidx = p.page_indices + pstart;
   const bool cut = L > budget;
   const int npages = (L - 1) / PAGE + 1;
@@ -281,50 +297,49 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
     find_bin<kBins>(cl, hist0, take, d1, above);
     need = take - above;
     const uint32_t top1 = d1;
-    // keys above the digit are counted; those that share it go on the list
     const uint32_t low1 = top1 << 21, end1 = top1 == 2047 ? kFixed : low1 + (1u << 21);
     each([&](int, uint4 x) {
       auto see = [&](uint32_t k) {
-        gt_n += k >= end1;  // the fixed ones among them
-        if (k - low1 < end1 - low1) {
-          atomicAdd(&hist1[(k >> 11) & 1023], 1);
-          const int at = atomicAdd(&s_listed, 1);
-          if (at < kList) list[at] = (k & 0x1fffffu) | static_cast<uint32_t>(wid) << 21;
-        }
+        if (k - low1 < end1 - low1) atomicAdd(&hist1[(k >> 11) & 1023], 1);
       };
       see(x.x), see(x.y), see(x.z), see(x.w);
     });
     cluster_sync();
-    const int listed = s_listed;  // of this block: beyond kList its keys are walked again
     find_bin<kBins2>(cl, hist1, need, d2, above);
     need -= above;
     // every block has read hist0 (before the barrier above): it takes the last digit
     for (int i = tid; i < kBins / 4; i += kSelThreads)
       reinterpret_cast<int4 *>(hist0)[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    const uint32_t top2 = top1 << 10 | static_cast<uint32_t>(d2);
-    auto third = [&](uint32_t k) {
-      if (k >> 11 == top2 && k != kFixed) atomicAdd(&hist0[k & 2047], 1);
-    };
-    if (listed <= kList) {
-      for (int i = tid; i < listed; i += kSelThreads) third(top1 << 21 | (list[i] & 0x1fffffu));
-    } else {
-      each([&](int, uint4 x) { third(x.x), third(x.y), third(x.z), third(x.w); });
-    }
+    // keys above both digits are counted; the few that share them go on the list
+    const uint32_t top2 = top1 << 10 | static_cast<uint32_t>(d2), low2 = top2 << 11;
+    const uint32_t end2 = top2 == 0x1fffffu ? kFixed : low2 + 2048u;
+    each([&](int, uint4 x) {
+      auto see = [&](uint32_t k) {
+        gt_n += k >= end2;  // the fixed ones among them
+        if (k - low2 < end2 - low2) {
+          atomicAdd(&hist0[k & 2047], 1);
+          const int at = atomicAdd(&s_listed, 1);
+          if (at < kList) list[at] = (k & 2047u) | static_cast<uint32_t>(wid) << 11;
+        }
+      };
+      see(x.x), see(x.y), see(x.z), see(x.w);
+    });
     cluster_sync();
+    const int listed = s_listed;  // of this block: beyond kList its keys are walked again
     find_bin<kBins>(cl, hist0, need, d3, above);
     need -= above;  // keys equal to T that stay
-    T = top2 << 11 | static_cast<uint32_t>(d3);
+    T = low2 | static_cast<uint32_t>(d3);
     if (listed <= kList) {
       for (int i = tid; i < listed; i += kSelThreads) {
-        const uint32_t k = top1 << 21 | (list[i] & 0x1fffffu), w = list[i] >> 21;
-        if (k > T) atomicAdd(&s_gt[w], 1);
-        else if (k == T) atomicAdd(&s_eq[w], 1);
+        const int k = list[i] & 2047u, w = list[i] >> 11;
+        if (k > d3) atomicAdd(&s_gt[w], 1);
+        else if (k == d3) atomicAdd(&s_eq[w], 1);
       }
     } else {
       each([&](int, uint4 x) {
         auto see = [&](uint32_t k) {
-          gt_n += k - low1 < end1 - low1 && k > T;
+          gt_n += k > T && k < end2;
           eq_n += k == T;
         };
         see(x.x), see(x.y), see(x.z), see(x.w);
@@ -339,14 +354,14 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
   eq_n = __reduce_add_sync(kFull, eq_n);
   if (lane == 0) atomicAdd(&s_gt[wid], gt_n), atomicAdd(&s_eq[wid], eq_n);
   __syncthreads();
-  int gt_at = 0, eq_at = 0, gt_all = 0, eq_all = 0;  // before this warp, and in the block
-#pragma unroll
-  for (int x = 0; x < kSelWarps; ++x) {
-    gt_at += x < wid ? s_gt[x] : 0, eq_at += x < wid ? s_eq[x] : 0;
-    gt_all += s_gt[x], eq_all += s_eq[x];
-  }
+  const int gt_w = lane < kSelWarps ? s_gt[lane] : 0, eq_w = lane < kSelWarps ? s_eq[lane] : 0;
+  int gt_at = __reduce_add_sync(kFull, lane < wid ? gt_w : 0);  // before this warp
+  int eq_at = __reduce_add_sync(kFull, lane < wid ? eq_w : 0);
   if (ranks > 1) {
-    if (tid == 0) s_total[0] = gt_all, s_total[1] = eq_all;
+    if (wid == 0) {
+      const int gt_all = __reduce_add_sync(kFull, gt_w), eq_all = __reduce_add_sync(kFull, eq_w);
+      if (lane == 0) s_total[0] = gt_all, s_total[1] = eq_all;
+    }
     cl.sync();
 #pragma unroll
     for (int x = 0; x < kMaxCluster - 1; ++x)
@@ -568,16 +583,17 @@ cudaError_t launch_evict_select(const EvictParams &p, cudaStream_t s) {
     if (dev < 64) configured[dev] = 1;
   }
   // Blocks per (request, head), by a request of the pool's average length (the lengths
-  // themselves are on the device): enough to hold its weights, and up to filling the GPU
-  // once as long as a block has kMinKeys of them (a request of 1024 keys: 6 us in one
-  // block, 18 in eight, each of whose barriers costs a microsecond).
+  // themselves are on the device): more as long as the clusters find room on the GPU
+  // together and a block has kMinKeys (a request of 1024 keys: 6 us in one block, 18 in
+  // eight, each of whose barriers costs a microsecond); one step past that room if the
+  // weights are not held otherwise (20 x 196608: 164 against 189 us), not where they fill
+  // it already (64 x 24000: 51 in one block, 62 in two; 40 x 100000: 166, 245 in four).
   const int64_t pairs = static_cast<int64_t>(p.B) * p.Hkv;
-  const int64_t mean = p.num_pages * PAGE / p.B;
+  const int64_t mean = p.num_pages * PAGE / p.B, room = kSelBlocks * sms;
   int ranks = 1;
   while (ranks < kMaxCluster &&
-         ((pairs * ranks * 2 <= kSelBlocks * sms && ranks * kMinKeys < mean) ||
-          static_cast<int64_t>(ranks) * kBlockPages * PAGE < mean) &&
-         pairs * ranks * 2 <= INT_MAX)
+         ((pairs * ranks * 2 <= room && ranks * kMinKeys < mean) ||
+          (pairs * ranks <= room && static_cast<int64_t>(ranks) * kBlockPages * PAGE < mean)))
     ranks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(pairs * ranks));
@@ -592,7 +608,11 @@ cudaError_t launch_evict_select(const EvictParams &p, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+  EvictParams q = p;
+  // More blocks than the GPU holds: the longest requests first, or one of them begins last
+  // (64 x 24000, lognormal: 74 -> 65 us; 58 -> 61 if all are of one length).
+  q.longest_first = p.B > 1 && p.B <= kSelThreads / 4 && pairs * ranks > room;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel, q);
 }
 
 cudaError_t launch_evict_compact(const CompactParams &p, cudaStream_t s) {

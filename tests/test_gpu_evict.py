@@ -217,6 +217,19 @@ def test_select_one_long_among_many():
         assert list(kept[r, 0, :n]) == bounded.kept_keys(weights[r][0], n, 2, 30)
 
 
+@pytest.mark.parametrize("B,Hkv", [(2, 160), (57, 8), (127, 3), (128, 3), (129, 3)])
+def test_select_more_blocks_than_the_gpu_holds(B, Hkv):
+    """The longest requests go first then: equal lengths, none and every other order."""
+    g = np.random.default_rng(B)
+    lens = [int(x) for x in g.choice([1, 64, 65, 100, 100, 190, 300], size=B)]
+    weights = [g.random((Hkv, L)).astype(np.float32) for L in lens]
+    _check_select(weights, lens, [70] * B, 1, 10, Hkv=Hkv)
+    lens[B // 2] = 0
+    kept, new, st = _select(weights, lens, [70] * B, 1, 10, Hkv=Hkv)
+    assert st == 1 and list(new) == [min(L, 70) if L else -1 for L in lens]
+    assert (kept[B // 2] == -9).all()
+
+
 def test_select_refusals():
     g = np.random.default_rng(9)
     lens = [100, 100, 100, 100, 0]
