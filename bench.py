@@ -43,8 +43,8 @@ UNIT = "us/batch"
 # scaled to the full batch, since traffic grows with the KV read.
 TRAFFIC_PROFILE = {
     "config": 3,
-    "source_sha256": "cbfa31ba505bfa8627e482d674017696da442f5a2f453701d9b0c1733de05ba1",
-    "bytes_per_kv_byte": (2574311936 + 3182336) / 2572926976,
+    "source_sha256": "dcfe60cece72ecdb6fc9363c755a82f8e5f22e654e23c7e8010271f9a5e851b6",
+    "bytes_per_kv_byte": (2574310400 + 3255296) / 2572926976,
     "workload": "mixed_45req_1k_128k_paged, first 12 requests (2.57 GB KV)",
 }
 

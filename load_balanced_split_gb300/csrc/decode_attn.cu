@@ -98,9 +98,11 @@ struct Smem {
 
 // Query rows are handled in groups of at most 16 (one m16 MMA tile): CTA z of a
 // (partition, head) pair takes rows [z * group, (z + 1) * group) of the G * q_len rows,
-// so MTP with more draft tokens (up to 64 rows) reuses the same kernel.  The groups are
-// of equal size: CTAs that read the same pages then keep pace and find them in L2 (16
-// requests of 4096 keys in the window, 20 rows of 8 heads: 10 + 10 73 us, 16 + 4 93).
+// so MTP with more draft tokens (up to 64 rows) reuses the same kernel.  With a window
+// the groups are of equal size: CTAs that read the same pages then keep pace and find them
+// in L2 (16 requests of 4096 keys in the window, 20 rows of 8 heads: 10 + 10 73 us, 16 + 4
+// 93).  Without one they are full but for the last (32 x 8192, 24 rows: 16 + 8 195 us, 12 +
+// 12 196).
 __device__ __forceinline__ int row_base(const AttnParams &p) {
   return p.group * static_cast<int>(blockIdx.z);
 }

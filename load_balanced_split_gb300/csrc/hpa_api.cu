@@ -265,7 +265,7 @@ static int decode_attn_impl(const void *q_dev, const void *k_pool_dev, const voi
   p.G = Hq / Hkv;
   p.rows = p.G * q_len;
   const int groups = (p.rows + hpa::MAX_ROWS - 1) / hpa::MAX_ROWS;
-  p.group = (p.rows + groups - 1) / groups;
+  p.group = window ? (p.rows + groups - 1) / groups : hpa::MAX_ROWS;
   p.heads_per_cta = all_heads ? Hkv : 1;
   p.window = window;
   p.scale_log2 = sm_scale * 1.4426950408889634f;

@@ -80,7 +80,7 @@ struct AttnParams {
   int64_t num_pages;
   TaskMapLayout lay;
   int B, C, q_len, Hq, Hkv, G, rows;
-  int group;          // query rows per CTA of the mma.sync kernel: rows in equal groups
+  int group;          // query rows per CTA of the mma.sync kernel, at most MAX_ROWS
   int heads_per_cta;  // KV heads one CTA walks per segment: 1 (grid over heads) or Hkv
   bool window;        // the map is one of hpa_plan_window
   float scale_log2;   // sm_scale * log2(e)
