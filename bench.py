@@ -43,8 +43,8 @@ UNIT = "us/batch"
 # scaled to the full batch, since traffic grows with the KV read.
 TRAFFIC_PROFILE = {
     "config": 3,
-    "source_sha256": "dcfe60cece72ecdb6fc9363c755a82f8e5f22e654e23c7e8010271f9a5e851b6",
-    "bytes_per_kv_byte": (2574310400 + 3255296) / 2572926976,
+    "source_sha256": "66a06c432afe56678c828a21c6ede1dcaa440278670e32ade6e77a7ea16fae0c",
+    "bytes_per_kv_byte": (2574349568 + 3353344) / 2572926976,
     "workload": "mixed_45req_1k_128k_paged, first 12 requests (2.57 GB KV)",
 }
 

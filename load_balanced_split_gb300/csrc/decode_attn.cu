@@ -103,11 +103,15 @@ struct Smem {
 // in L2 (16 requests of 4096 keys in the window, 20 rows of 8 heads: 10 + 10 73 us, 16 + 4
 // 93).  Without one they are full but for the last (32 x 8192, 24 rows: 16 + 8 195 us, 12 +
 // 12 196).
+// The fused combine has no windows; with its groups not known to the compiler its E4M3 form
+// took 1362 us, not 1307 (64 requests of 68K tokens).
+template <bool FUSED>
 __device__ __forceinline__ int row_base(const AttnParams &p) {
-  return p.group * static_cast<int>(blockIdx.z);
+  return (FUSED ? MAX_ROWS : p.group) * static_cast<int>(blockIdx.z);
 }
+template <bool FUSED>
 __device__ __forceinline__ int group_rows(const AttnParams &p) {
-  return min(p.group, p.rows - row_base(p));
+  return min(FUSED ? MAX_ROWS : p.group, p.rows - row_base<FUSED>(p));
 }
 
 struct SegInfo {
@@ -168,8 +172,8 @@ __device__ void producer(const AttnParams &p, const CUtensorMap *tmk, const CUte
         break;
       }
       uint8_t *qs = smem + S::kQ + slot * kQSlotBytes;
-      const int G = p.G, rb = row_base(p);
-      for (int ch = lane; ch < group_rows(p) * 16; ch += 32) {  // 16-B chunks of 256-B rows
+      const int G = p.G, rb = row_base<FUSED>(p);
+      for (int ch = lane; ch < group_rows<FUSED>(p) * 16; ch += 32) {  // 16-B chunks of 256-B rows
         const int row = ch >> 4, c16 = ch & 15, j = (rb + row) / G, g = (rb + row) % G;
         const int4 v = reinterpret_cast<const int4 *>(
             p.q + ((static_cast<int64_t>(f.r) * p.q_len + j) * p.Hq + h * G + g) * HEAD_DIM)[c16];
@@ -445,9 +449,9 @@ __device__ __forceinline__ void store_bf16x4(__nv_bfloat16 *dst, float4 v) {
 template <int KV>
 __device__ void merge_request(const AttnParams &p, int r, int h, int seg_first, int nseg,
                               int tid) {
-  const int G = p.G, q_len = p.q_len, rb = row_base(p);
+  const int G = p.G, q_len = p.q_len, rb = row_base<true>(p);
   const int64_t per_seg = static_cast<int64_t>(q_len) * p.Hq;
-  for (int v = tid; v < group_rows(p) * (HEAD_DIM / 4); v += kConsumerWarps * 32) {
+  for (int v = tid; v < group_rows<true>(p) * (HEAD_DIM / 4); v += kConsumerWarps * 32) {
     const int row = rb + v / (HEAD_DIM / 4), c4 = v % (HEAD_DIM / 4);
     const int64_t col = static_cast<int64_t>(row / G) * p.Hq + h * G + row % G;
     float M = -CUDART_INF_F;
@@ -500,7 +504,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kFlag);
 
   // rows of this CTA's group: local index row, global query row rb + row
-  const int G = p.G, rows = group_rows(p), q_len = p.q_len, rb = row_base(p);
+  const int G = p.G, rows = group_rows<FUSED>(p), q_len = p.q_len, rb = row_base<FUSED>(p);
   const int row0 = r8, row1 = r8 + 8;
   const bool v0 = row0 < rows, v1 = row1 < rows;
   const int j0 = (rb + row0) / G, j1 = (rb + row1) / G;
@@ -953,11 +957,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       // CTA (c, h) covers requests c, c + C, ... for the query heads of its KV heads
       const float nan = CUDART_NAN_F;
       for (int r = c; r < p.B; r += p.C)
-        for (int v = threadIdx.x; v < (ALLH ? p.Hkv : 1) * group_rows(p) * (HEAD_DIM / 4);
+        for (int v = threadIdx.x; v < (ALLH ? p.Hkv : 1) * group_rows<FUSED>(p) * (HEAD_DIM / 4);
              v += kThreads) {
-          const int hh = h0 + v / (group_rows(p) * (HEAD_DIM / 4));
-          const int vr = v % (group_rows(p) * (HEAD_DIM / 4));
-          const int row = row_base(p) + vr / (HEAD_DIM / 4), c4 = vr % (HEAD_DIM / 4);
+          const int hh = h0 + v / (group_rows<FUSED>(p) * (HEAD_DIM / 4));
+          const int vr = v % (group_rows<FUSED>(p) * (HEAD_DIM / 4));
+          const int row = row_base<FUSED>(p) + vr / (HEAD_DIM / 4), c4 = vr % (HEAD_DIM / 4);
           const int64_t col = static_cast<int64_t>(row / p.G) * p.Hq + hh * p.G + row % p.G;
           const int64_t orow = static_cast<int64_t>(r) * p.q_len * p.Hq + col;
           store_bf16x4(p.out + orow * HEAD_DIM + 4 * c4, make_float4(nan, nan, nan, nan));
