@@ -107,6 +107,9 @@ __device__ __forceinline__ KwSeg kw_seg(const KeyWeightsParams &p, const MapHead
 // ----------------------------------------------------------------------------- stagers
 // Each segment's query rows as the MMA's B operand (K-major, 128-byte swizzle), and each
 // row's score factor and log-sum-exp in base 2: a weight is 2^(factor * S - lse).
+// Four lanes share a row.  With every lane in all of a warp's eight rows, twice the code,
+// which a launch fetches cold, 16 E4M3 rows were staged 8.5 us after the map was there and
+// 64 bf16 ones 7.5; so 3.7 and 3.1, before the first pages land.
 template <int KV, int RP>
 __device__ void kw_stager(const KeyWeightsParams &p, uint8_t *smem, const MapHead &m, int ws) {
   using S = KwCfg<KV, RP>;
@@ -135,43 +138,58 @@ __device__ void kw_stager(const KeyWeightsParams &p, uint8_t *smem, const MapHea
     const int64_t row_at = static_cast<int64_t>(f.r) * p.q_len * p.Hq + h * G;
 #pragma unroll 1
     for (int row0 = 8 * ws; row0 < (KV == HPA_KV_BF16 ? S::kN : RP); row0 += 8 * S::kStagers) {
-      uint2 x[8];
-      float lse = 0.f;  // lane i < 8: of row row0 + i
+      // four lanes to a row: 32 dims each, in 16-byte pieces of the operand
+      const int row = row0 + (lane >> 2), qd = lane & 3;
+      uint4 x[4] = {};
+      float lse = 0.f, mine = factor;
+      if (row < p.rows) {
+        const int j = jrow[row];
+        const int64_t at = row_at + static_cast<int64_t>(j) * p.Hq + (row - j * G);
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + at * HEAD_DIM);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {  // eight rows' loads in flight; lane: dims [4 lane, 4 lane + 4)
-        const int row = row0 + i;
-        x[i] = make_uint2(0u, 0u);
-        if (row < p.rows) {
-          const int j = jrow[row];
-          const int64_t at = row_at + static_cast<int64_t>(j) * p.Hq + (row - j * G);
-          x[i] = reinterpret_cast<const uint2 *>(p.q + at * HEAD_DIM)[lane];
-          if (lane == i) lse = p.lse[at];
-        }
+        for (int c = 0; c < 4; ++c)
+          x[c] = src[KV == HPA_KV_BF16 ? 4 * c + qd : 8 * (c >> 1) + 2 * qd + (c & 1)];
+        lse = p.lse[at];
       }
-      float mine = factor;  // lane i: row i's score factor
+      if (KV == HPA_KV_BF16) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = row0 + i;
-        if (KV == HPA_KV_BF16) {
-          *reinterpret_cast<uint2 *>(qs + kmaj(row, 8 * lane, S::kN * 128)) = x[i];
-        } else {
-          const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x[i].x));
-          const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x[i].y));
-          const float v[4] = {a.x, a.y, b.x, b.y};
-          const float sq = pow2_to_128(
-              warp_max(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y)))));
-          uint32_t hi, lo;
-          e4m3_two_terms(v, sq, hi, lo);
-          *reinterpret_cast<uint32_t *>(qs + kmaj(row, 4 * lane, 0)) = hi;
-          *reinterpret_cast<uint32_t *>(qs + RP * 128 + kmaj(row, 4 * lane, 0)) = lo;
-          if (lane == i) mine = factor / sq;
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4 *>(qs + kmaj(row, 16 * (4 * c + qd), S::kN * 128)) = x[c];
+      } else {
+        float2 f[4][4];
+        float amax = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t u[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[c][e] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u[e]));
+            amax = fmaxf(amax, fmaxf(fabsf(f[c][e].x), fabsf(f[c][e].y)));
+          }
         }
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+        const float sq = pow2_to_128(fmaxf(amax, __shfl_xor_sync(kFull, amax, 2)));
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = f[2 * half + (e >> 1)][2 * (e & 1)];
+            const float2 b = f[2 * half + (e >> 1)][2 * (e & 1) + 1];
+            const float v[4] = {a.x, a.y, b.x, b.y};
+            e4m3_two_terms(v, sq, hi[e], lo[e]);
+          }
+          uint8_t *to = qs + kmaj(row, 16 * (4 * half + qd), 0);
+          *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4 *>(to + RP * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        mine = factor / sq;
       }
-      if (lane < 8 && row0 + lane < RP) {
+      if (qd == 0 && row < RP) {
         const float l2 = lse * 1.4426950408889634f;
         // rows that pad the tile, and rows that see no key (lse -inf), weigh nothing
-        const bool none = row0 + lane >= p.rows || l2 == -CUDART_INF_F;
-        rc[row0 + lane] = none ? make_float2(0.f, CUDART_INF_F) : make_float2(mine, l2);
+        const bool none = row >= p.rows || l2 == -CUDART_INF_F;
+        rc[row] = none ? make_float2(0.f, CUDART_INF_F) : make_float2(mine, l2);
       }
     }
     if (ws == 0 && lane == 0)
