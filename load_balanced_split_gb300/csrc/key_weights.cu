@@ -24,9 +24,9 @@
 //  * up to 16 rows two CTAs share an SM, above one with a deeper ring: the partition
 //    counts of hpa_default_num_ctas for these row counts.
 // Bound by DRAM.  Plan and weights together: 0.89 GB (32 requests of about 24000 E4M3 keys,
-// two tokens) in 143 us, 6.2 TB/s; 0.27 GB (16 of about 8192, bf16, one token) in 47, of
-// which 41 stream the pages; 0.14 GB (one of 65536, bf16, 64 rows a KV head) in 32, with
-// 64 exponentials per key beside the loads.  On mma.sync, where a key's rows lie in four
+// two tokens) in 141 us, 6.4 TB/s; 0.27 GB (16 of about 8192, bf16, one token) in 47, of
+// which 41 stream the pages; 0.14 GB (one of 65536, bf16, 64 rows a KV head) in 30, of
+// which 18 do.  On mma.sync, where a key's rows lie in four
 // lanes and 16 rows make a pass: 219, 52 and 72 us.
 // Every wait is bounded in time, as in the attention kernels.
 #include <math_constants.h>
