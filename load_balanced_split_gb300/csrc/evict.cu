@@ -62,16 +62,16 @@ __device__ __forceinline__ uint32_t weight_key(uint32_t u) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// Over the whole cluster: the bin of the k-th largest entry (1 <= k <= the entries
+// Over the n blocks of the cluster that take part: the bin of the k-th largest entry (1 <= k <= the entries
 // counted) and the number of entries in higher bins.  The caller has synchronised the
 // cluster after the last count into `hist`.
 template <int BINS>
-__device__ void find_bin(cg::cluster_group &cl, int *hist, int k, int &bin, int &above) {
+__device__ void find_bin(cg::cluster_group &cl, int n, int *hist, int k, int &bin, int &above) {
   constexpr int N = BINS / kSelThreads;  // bins per thread: 4 or 2
   typedef typename std::conditional<N == 4, int4, int2>::type Bins;
   static_assert(sizeof(Bins) == 4 * N, "one load per block");
   __shared__ int wsum[kSelWarps], s_bin, s_above;
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, n = cl.num_blocks();
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   // thread t owns bins [low, low + N), low = BINS - N (t + 1): a scan from the highest bin
   const int low = BINS - N * (tid + 1);
   int c[N];
@@ -123,13 +123,14 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
   extern __shared__ __align__(16) uint32_t sel_smem[];
   __shared__ int s_bad, s_listed, s_total[2], s_gt[kSelWarps], s_eq[kSelWarps];
   cg::cluster_group cl = cg::this_cluster();
-  const int ranks = cl.num_blocks(), rank = cl.block_rank();
+  int ranks = cl.num_blocks();
+  const int rank = cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   int *hist0 = reinterpret_cast<int *>(sel_smem + kBlockPages * PAGE), *hist1 = hist0 + kBins;
   // keys that share the first two digits: their other 11 bits, and the warp above them
   uint32_t *list = reinterpret_cast<uint32_t *>(hist1 + kBins2);
   uint32_t *keys = sel_smem + wid * (kWarpPages * PAGE);   // this warp's first pages
-  const int slot = blockIdx.x / ranks / p.Hkv, h = blockIdx.x / ranks % p.Hkv;
+  const int pair = blockIdx.x / ranks, slot = pair / p.Hkv, h = pair % p.Hkv;
   // No early launch of the kernel after this one: compaction blocks that wait on the SMs
   // settle unevenly around these (174 -> 251 us of compaction on 64 requests cut to 4096).
   pdl_wait();
@@ -176,6 +177,10 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
     refuse(bad);
     return;
   }
+  // A short request is the first blocks' alone (4 of 1024 keys in a large pool: 27 us in
+  // eight blocks each, 11 so); the cluster's barrier does not wait for blocks that have left.
+  while (ranks > 1 && static_cast<int64_t>(ranks / 2) * kMinKeys >= L) ranks /= 2;
+  if (rank >= ranks) return;
   __syncthreads();
   int32_t *kept = p.kept + (static_cast<int64_t>(r) * p.Hkv + h) * p.kept_stride;
   const int32_t *pidx = p.page_indices + pstart;
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
   int need = 0, gt_n = 0, eq_n = 0;
   if (take > 0) {
     int d1, d2, d3, above;
-    find_bin<kBins>(cl, hist0, take, d1, above);
+    find_bin<kBins>(cl, ranks, hist0, take, d1, above);
     need = take - above;
     const uint32_t top1 = d1;
     const uint32_t low1 = top1 << 21, end1 = top1 == 2047 ? kFixed : low1 + (1u << 21);
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
       see(x.x), see(x.y), see(x.z), see(x.w);
     });
     cluster_sync();
-    find_bin<kBins2>(cl, hist1, need, d2, above);
+    find_bin<kBins2>(cl, ranks, hist1, need, d2, above);
     need -= above;
     // every block has read hist0 (before the barrier above): it takes the last digit
     for (int i = tid; i < kBins / 4; i += kSelThreads)
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocks)
     });
     cluster_sync();
     const int listed = s_listed;  // of this block: beyond kList its keys are walked again
-    find_bin<kBins>(cl, hist0, need, d3, above);
+    find_bin<kBins>(cl, ranks, hist0, need, d3, above);
     need -= above;  // keys equal to T that stay
     T = low2 | static_cast<uint32_t>(d3);
     if (listed <= kList) {
@@ -582,14 +587,17 @@ cudaError_t launch_evict_select(const EvictParams &p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 64) configured[dev] = 1;
   }
-  // Blocks per (request, head), by a request of the pool's average length (the lengths
-  // themselves are on the device): more as long as the clusters find room on the GPU
+  // Blocks per (request, head), by a request of the pool's average length, or 64 times the
+  // longest list if that is less (the lengths themselves are on the device; a request that
+  // is shorter leaves blocks idle: 16 x 8192 cut to 512 in a pool of 20 times their pages
+  // 31 us by the average alone, 19 so): more as long as the clusters find room on the GPU
   // together and a block has kMinKeys (a request of 1024 keys: 6 us in one block, 18 in
   // eight, each of whose barriers costs a microsecond); one step past that room if the
   // weights are not held otherwise (20 x 196608: 164 against 189 us), not where they fill
   // it already (64 x 24000: 51 in one block, 62 in two; 40 x 100000: 166, 245 in four).
   const int64_t pairs = static_cast<int64_t>(p.B) * p.Hkv;
-  const int64_t mean = p.num_pages * PAGE / p.B, room = kSelBlocks * sms;
+  const int64_t share = p.num_pages * PAGE / p.B, room = kSelBlocks * sms;
+  const int64_t mean = p.kept_stride < share / 64 ? 64 * p.kept_stride : share;
   int ranks = 1;
   while (ranks < kMaxCluster &&
          ((pairs * ranks * 2 <= room && ranks * kMinKeys < mean) ||

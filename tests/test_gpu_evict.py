@@ -129,11 +129,11 @@ def test_weights_device_side_refusals():
 
 
 # ----------------------------------------------------------------------------- selection
-def _select(weights, lens, budgets, sinks, recent, stride=None, Hkv=2, seed=0):
-    """weights: per request [Hkv][L] fp32."""
+def _select(weights, lens, budgets, sinks, recent, stride=None, Hkv=2, seed=0, spare=0):
+    """weights: per request [Hkv][L] fp32; spare: pages of the pool that no request has."""
     _, indices, P = W.page_table(seed, np.maximum(np.array(lens), 1), 64, True)
     indptr = np.concatenate([[0], np.cumsum((np.maximum(lens, 1) + 63) // 64)]).astype(np.int32)
-    acc = np.full((P, Hkv, 64), 1e30, np.float32)
+    acc = np.full((P + spare, Hkv, 64), 1e30, np.float32)
     for r, L in enumerate(lens):
         for i in range(L):
             acc[indices[indptr[r] + i // 64], :, i % 64] = weights[r][:, i]
@@ -228,6 +228,21 @@ def test_select_more_blocks_than_the_gpu_holds(B, Hkv):
     kept, new, st = _select(weights, lens, [70] * B, 1, 10, Hkv=Hkv)
     assert st == 1 and list(new) == [min(L, 70) if L else -1 for L in lens]
     assert (kept[B // 2] == -9).all()
+
+
+def test_select_short_requests_in_a_large_pool():
+    """Blocks are launched by the pool's size; those that a request does not need leave."""
+    g = np.random.default_rng(11)
+    lens = [1, 100, 4096, 4097, 8192, 8193, 16385, 0, 32768, 33000]
+    weights = [g.random((1, L)).astype(np.float32) for L in lens]
+    budgets = [50, 50, 2000, 2000, 8192, 1, 16384, 5, 7000, 32999]
+    kept, new, st = _select(weights, lens, budgets, 0, 0, Hkv=1, spare=8192)
+    assert st == 1
+    for r, L in enumerate(lens):
+        n = min(L, budgets[r])
+        assert new[r] == (n if L else -1) and (kept[r, 0, n:] == -9).all()
+        order = np.lexsort((np.arange(L), -weights[r][0].astype(np.float64)))
+        assert (kept[r, 0, :n] == np.sort(order[:n])).all()
 
 
 def test_select_refusals():
