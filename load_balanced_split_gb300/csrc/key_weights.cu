@@ -31,6 +31,8 @@
 // Every wait is bounded in time, as in the attention kernels.
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "tcgen05.cuh"
 
 namespace hpa {
@@ -42,6 +44,9 @@ constexpr int kGroups = 2;
 constexpr int kCompute = kGroups * kGroupWarps;
 constexpr int kStepPages = 2;
 constexpr int kAccBytes = PAGE * 4;
+// The lse of a row that adds nothing, and its token: one that sees no key at all
+constexpr float kNoWeight = 3.402823466e38f;
+constexpr int kNoToken = -(1 << 30);
 
 // RP: query rows, padded to 8, 16, 32, 48 or 64.
 template <int KV, int RP>
@@ -72,7 +77,8 @@ struct KwCfg {
   static constexpr int kAcc = kQ + 2 * kQSlot;                  // float[kAccs][2][64]
   static constexpr int kRow = kAcc + kAccs * kStepPages * kAccBytes;  // float2[2][RP]
   static constexpr int kJRow = kRow + 2 * RP * 8;               // int[RP]: token j of a row
-  static constexpr int kInfo = (kJRow + RP * 4 + 15) & ~15;     // int4[2]
+  static constexpr int kJSee = kJRow + RP * 4;                  // int[2][RP]: the same, or kNoToken
+  static constexpr int kInfo = (kJSee + 2 * RP * 4 + 15) & ~15; // int4[2]: nothing adds, L, pages
   static constexpr int kPid = kInfo + 32;                       // int2[kAccs]
   // kv_full[kStages] kv_empty[kStages] s_full[kBufs] s_free[kBufs] acc_full[kAccs]
   // q_full[2] q_empty[2] drain
@@ -107,6 +113,12 @@ __device__ __forceinline__ KwSeg kw_seg(const KeyWeightsParams &p, const MapHead
 // ----------------------------------------------------------------------------- stagers
 // Each segment's query rows as the MMA's B operand (K-major, 128-byte swizzle), and each
 // row's score factor and log-sum-exp in base 2: a weight is 2^(factor * S - lse).
+// Rows that pad the tile and rows of lse -inf add nothing.  They are copies of the first row
+// that does add, with an lse of kNoWeight: a query of zeros would make NaN of an infinite
+// key (0 inf), and the key's weight with it.  A copy's score is not finite only where the
+// row's own is not, and 2^(factor * S - kNoWeight) is then 0, infinite or NaN as the row's
+// own weight is.  That holds where the row sees the key; the compute warps' masked path
+// takes copies out by their token, and runs for every key if no row of the segment adds.
 // Four lanes share a row.  With every lane in all of a warp's eight rows, twice the code,
 // which a launch fetches cold, 16 E4M3 rows were staged 8.5 us after the map was there and
 // 64 bf16 ones 7.5; so 3.7 and 3.1, before the first pages land.
@@ -117,6 +129,8 @@ __device__ void kw_stager(const KeyWeightsParams &p, uint8_t *smem, const MapHea
   const uint32_t base = smem_u32(smem);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kAbort);
   const int *jrow = reinterpret_cast<const int *>(smem + S::kJRow);
+  constexpr int kHalves = RP > 32 ? 2 : 1;
+  using Rows = typename std::conditional<(RP > 32), unsigned long long, uint32_t>::type;
   float factor = p.scale_log2;
   if (KV == HPA_KV_E4M3) factor *= p.k_scale[h];
   for (int k = 0; k < m.s_end - m.s_begin; ++k) {
@@ -135,22 +149,39 @@ __device__ void kw_stager(const KeyWeightsParams &p, uint8_t *smem, const MapHea
     }
     uint8_t *qs = smem + S::kQ + slot * S::kQSlot;
     float2 *rc = reinterpret_cast<float2 *>(smem + S::kRow) + slot * RP;
+    int *jsee = reinterpret_cast<int *>(smem + S::kJSee) + slot * RP;
     const int64_t row_at = static_cast<int64_t>(f.r) * p.q_len * p.Hq + h * G;
+    auto place = [&](int row) {
+      const int j = jrow[row];
+      return row_at + static_cast<int64_t>(j) * p.Hq + (row - j * G);
+    };
+    float z[kHalves];  // every row's lse, a row (or two) per lane
+#pragma unroll
+    for (int u = 0; u < kHalves; ++u)
+      z[u] = lane + 32 * u < p.rows ? p.lse[place(lane + 32 * u)] : -CUDART_INF_F;
+    Rows adds = 0;  // rows that add a weight
 #pragma unroll 1
     for (int row0 = 8 * ws; row0 < (KV == HPA_KV_BF16 ? S::kN : RP); row0 += 8 * S::kStagers) {
       // four lanes to a row: 32 dims each, in 16-byte pieces of the operand
       const int row = row0 + (lane >> 2), qd = lane & 3;
       uint4 x[4] = {};
-      float lse = 0.f, mine = factor;
-      if (row < p.rows) {
-        const int j = jrow[row];
-        const int64_t at = row_at + static_cast<int64_t>(j) * p.Hq + (row - j * G);
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + at * HEAD_DIM);
+      float mine = factor;
+      int src = row < p.rows ? row : 0;
+#pragma unroll 1
+      while (row0 < RP) {  // columns beyond RP are not read back
+        const uint4 *from = reinterpret_cast<const uint4 *>(p.q + place(src) * HEAD_DIM);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          x[c] = src[KV == HPA_KV_BF16 ? 4 * c + qd : 8 * (c >> 1) + 2 * qd + (c & 1)];
-        lse = p.lse[at];
+          x[c] = from[KV == HPA_KV_BF16 ? 4 * c + qd : 8 * (c >> 1) + 2 * qd + (c & 1)];
+        adds = __ballot_sync(kFull, z[0] != -CUDART_INF_F);
+        if constexpr (kHalves > 1)
+          adds |= static_cast<Rows>(__ballot_sync(kFull, z[1] != -CUDART_INF_F)) << 32;
+        const int want = adds == 0 || (adds >> src & 1) ? src : __ffsll(adds) - 1;
+        if (__all_sync(kFull, want == src)) break;
+        src = want;
       }
+      const float lse = __shfl_sync(kFull, kHalves > 1 && row0 >= 32 ? z[kHalves - 1] : z[0],
+                                    row & 31);
       if (KV == HPA_KV_BF16) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -186,14 +217,13 @@ __device__ void kw_stager(const KeyWeightsParams &p, uint8_t *smem, const MapHea
         mine = factor / sq;
       }
       if (qd == 0 && row < RP) {
-        const float l2 = lse * 1.4426950408889634f;
-        // rows that pad the tile, and rows that see no key (lse -inf), weigh nothing
-        const bool none = row >= p.rows || l2 == -CUDART_INF_F;
-        rc[row] = none ? make_float2(0.f, CUDART_INF_F) : make_float2(mine, l2);
+        const bool add = adds >> row & 1;
+        rc[row] = make_float2(mine, add ? lse * 1.4426950408889634f : kNoWeight);
+        jsee[row] = add ? jrow[row] : kNoToken;
       }
     }
     if (ws == 0 && lane == 0)
-      reinterpret_cast<int4 *>(smem + S::kInfo)[slot] = make_int4(f.r, f.L, f.pg0, f.pg1);
+      reinterpret_cast<int4 *>(smem + S::kInfo)[slot] = make_int4(adds == 0, f.L, f.pg0, f.pg1);
     fence_proxy_async_smem();  // the MMA reads the slot through the async proxy
     mbar_arrive(base + S::kQFull + 8 * slot);  // every lane publishes its own stores
   }
@@ -353,7 +383,6 @@ __device__ void kw_compute(const KeyWeightsParams &p, uint8_t *smem, const MapHe
   const uint32_t base = smem_u32(smem);
   const uint32_t lane_t = tmem + (static_cast<uint32_t>(32 * w) << 16);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kAbort);
-  const int *jrow = reinterpret_cast<const int *>(smem + S::kJRow);
   const bool windowed = head.windowed;
   const int sinks = head.sinks, q_len = p.q_len, n_seg = head.s_end - head.s_begin;
   int n = 0;  // step of the CTA
@@ -368,8 +397,10 @@ __device__ void kw_compute(const KeyWeightsParams &p, uint8_t *smem, const MapHe
     const int steps = (pg1 - pg0 + kStepPages - 1) / kStepPages;
     WinSpan win = {};
     if (windowed && steps > 0) win = WinSpan::make(L, q_len, head.window, sinks);
-    const int lim_min = L - q_len + 1;  // first key hidden from some row
+    // first key hidden from some row (from all of them if no row adds a weight)
+    const int lim_min = info.x ? 0 : L - q_len + 1;
     const uint32_t rows = base + S::kRow + slot * RP * 8;
+    const int *jsee = reinterpret_cast<const int *>(smem + S::kJSee) + slot * RP;
     for (int i = (group + kGroups - n % kGroups) % kGroups; i < steps; i += kGroups) {
       const int m = n + i, buf = m % S::kBufs, sa = m % S::kAccs;
       ok = __all_sync(kFull,
@@ -417,8 +448,8 @@ __device__ void kw_compute(const KeyWeightsParams &p, uint8_t *smem, const MapHe
             auto hidden = [&](int j) {
               return key >= lim_min + j || (windowed && key >= sinks && key < win.start + j);
             };
-            if (hidden(jrow[r0 + e])) a = 0.f;
-            if (hidden(jrow[r0 + e + 1])) b = 0.f;
+            if (hidden(jsee[r0 + e])) a = 0.f;
+            if (hidden(jsee[r0 + e + 1])) b = 0.f;
           }
           sum = add2(sum, pk(a, b));
         }
