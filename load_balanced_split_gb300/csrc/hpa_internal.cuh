@@ -17,7 +17,7 @@ namespace hpa {
 // ----------------------------------------------------------------------------- task map
 enum : int {
   TM_T = 0, TM_BASE, TM_REM, TM_C, TM_B, TM_S, TM_STATUS, TM_TILE, TM_KIND, TM_SPLITS,
-  TM_SCAP, TM_WINDOW, TM_SINKS, TM_QLEN, TM_HEADER_WORDS = 16
+  TM_SCAP, TM_WINDOW, TM_SINKS, TM_QLEN, TM_RAISED, TM_HEADER_WORDS = 16
 };
 constexpr int KIND_WINDOW = 3;  // the map kind of hpa_plan_window
 
@@ -409,6 +409,16 @@ __device__ __forceinline__ void status_or(int32_t *tm, int bits) {
   atomicOr(reinterpret_cast<int *>(tm + TM_STATUS), bits);
 }
 
+// As status_or, for errors that hpa_key_weights itself finds.  TM_RAISED has the bit before
+// the status does, so a block that starts later and meets the status can tell it from an
+// earlier kernel's (read_map_head): one request's error must not stop the updates of others,
+// which would then depend on when their blocks run.
+__device__ __forceinline__ void status_or_raised(int32_t *tm, int bits) {
+  atomicOr(reinterpret_cast<int *>(tm + TM_RAISED), bits);
+  __threadfence();
+  status_or(tm, bits);
+}
+
 // One segment row of a task map, checked before use: request in [0, B), owned by
 // partition c, 0 <= tile_lo < tile_hi <= ceil(L_r / tile).  A row that fails (a
 // map corrupted after hpa_plan wrote it) is reported as HPA_STATUS_BAD_MAP when
@@ -420,7 +430,7 @@ __device__ __forceinline__ void status_or(int32_t *tm, int bits) {
 struct SegRow {
   int r, L, klo, khi;  // request, its length, key range [klo, khi)
 };
-template <bool WIN = false>
+template <bool WIN = false, bool RAISED = false>
 __device__ __forceinline__ SegRow read_seg_row(int32_t *tm, const TaskMapLayout &lay, int B,
                                                int s, int c, int tile, bool report) {
   const int4 sg = reinterpret_cast<const int4 *>(tm + lay.segs)[s];
@@ -435,7 +445,8 @@ __device__ __forceinline__ SegRow read_seg_row(int32_t *tm, const TaskMapLayout 
       }
     }
   }
-  if (report) status_or(tm, HPA_STATUS_BAD_MAP);
+  if (report && RAISED) status_or_raised(tm, HPA_STATUS_BAD_MAP);
+  else if (report) status_or(tm, HPA_STATUS_BAD_MAP);
   return SegRow{0, 1 << 30, 0, 0};
 }
 
@@ -455,13 +466,14 @@ __device__ __forceinline__ bool map_ranges_ok(const int32_t *tm, const TaskMapLa
 // header (the words lie behind the plan's kernel in L2, and a check at a time costs a round
 // trip each) and one of the partition's segment range.  With need_window a map of another
 // kind is malformed; without, all kinds are read.  A map for another shape or q_len is
-// reported by the CTA with `report`, a malformed one by every CTA that finds it.
+// reported by the CTA with `report`, a malformed one by every CTA that finds it.  With raised
+// (hpa_key_weights) the bits that this kernel has set do not stop it.
 struct MapHead {
   int go, tile, s_begin, s_end, windowed, window, sinks;
 };
 __device__ __forceinline__ MapHead read_map_head(int32_t *tm, const TaskMapLayout &lay, int B,
                                                  int C, int c, int q_len, bool need_window,
-                                                 bool report) {
+                                                 bool report, bool raised = false) {
   const int4 *h = reinterpret_cast<const int4 *>(tm);
   const int4 a = h[0], b = h[1], d = h[2], e = h[3];
   static_assert(TM_C == 3 && TM_B == 4 && TM_S == 5 && TM_STATUS == 6 && TM_TILE == 7 &&
@@ -469,7 +481,12 @@ __device__ __forceinline__ MapHead read_map_head(int32_t *tm, const TaskMapLayou
                     TM_QLEN == 13,
                 "header words");
   MapHead m = {0, b.w, 0, 0, d.x == KIND_WINDOW, d.w, e.x};
-  if (b.z != 0) return m;
+  int status = b.z;
+  if (raised && status != 0) {
+    __threadfence();  // TM_RAISED after the status: see status_or_raised
+    status &= ~*reinterpret_cast<volatile const int32_t *>(tm + TM_RAISED);
+  }
+  if (status != 0) return m;
   if (a.w != C || b.x != B || m.tile <= 0 || m.tile % PAGE != 0 ||
       (m.windowed && e.y != q_len)) {
     if (report) status_or(tm, HPA_STATUS_MISMATCH);
@@ -482,7 +499,8 @@ __device__ __forceinline__ MapHead read_map_head(int32_t *tm, const TaskMapLayou
                                   : !need_window && d.x >= 0 && d.x <= 2;
   if (!kind_ok || d.z != cap || S < 0 || S > cap || m.s_begin < 0 || m.s_begin > m.s_end ||
       m.s_end > S) {
-    status_or(tm, HPA_STATUS_BAD_MAP);
+    if (raised) status_or_raised(tm, HPA_STATUS_BAD_MAP);
+    else status_or(tm, HPA_STATUS_BAD_MAP);
     m.s_begin = m.s_end = 0;
     return m;
   }

@@ -78,7 +78,7 @@ struct KwCfg {
   static constexpr int kRow = kAcc + kAccs * kStepPages * kAccBytes;  // float2[2][RP]
   static constexpr int kJRow = kRow + 2 * RP * 8;               // int[RP]: token j of a row
   static constexpr int kJSee = kJRow + RP * 4;                  // int[2][RP]: the same, or kNoToken
-  static constexpr int kInfo = (kJSee + 2 * RP * 4 + 15) & ~15; // int4[2]: nothing adds, L, pages
+  static constexpr int kInfo = (kJSee + 2 * RP * 4 + 15) & ~15;  // int4[2]: none adds, L, pages
   static constexpr int kPid = kInfo + 32;                       // int2[kAccs]
   // kv_full[kStages] kv_empty[kStages] s_full[kBufs] s_free[kBufs] acc_full[kAccs]
   // q_full[2] q_empty[2] drain
@@ -99,12 +99,12 @@ struct KwSeg {
 };
 __device__ __forceinline__ KwSeg kw_seg(const KeyWeightsParams &p, const MapHead &m, int s,
                                         bool report) {
-  const SegRow sr = m.windowed
-                        ? read_seg_row<true>(p.tm, p.lay, p.B, s, blockIdx.x, m.tile, report)
-                        : read_seg_row<false>(p.tm, p.lay, p.B, s, blockIdx.x, m.tile, report);
+  const SegRow sr =
+      m.windowed ? read_seg_row<true, true>(p.tm, p.lay, p.B, s, blockIdx.x, m.tile, report)
+                 : read_seg_row<false, true>(p.tm, p.lay, p.B, s, blockIdx.x, m.tile, report);
   KwSeg f = {sr.r, sr.L, sr.klo / PAGE, (sr.khi + PAGE - 1) / PAGE};
   if (sr.L < p.q_len) {
-    if (report) status_or(p.tm, HPA_STATUS_BAD_SEQLEN);
+    if (report) status_or_raised(p.tm, HPA_STATUS_BAD_SEQLEN);
     f.pg1 = f.pg0;
   }
   return f;
@@ -260,7 +260,7 @@ __device__ void kw_producer(const KeyWeightsParams &p, const CUtensorMap *tmk, u
           const int pg = windowed ? win.real_page(v) : v;
           id[u] = pg < pcount ? p.page_indices[pstart + pg] : -1;
           if (id[u] < 0 || id[u] >= p.num_pages) {
-            status_or(p.tm, HPA_STATUS_BAD_PAGE);
+            status_or_raised(p.tm, HPA_STATUS_BAD_PAGE);
             id[u] = -1;  // page 0 is read in its place and nothing is written
           }
         }
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(KwCfg<KV, RP>::kThreads, RP <= 16 ? 2 : 1)
   if (threadIdx.x == 32) prefetch_tmap(&tmk);
   pdl_wait();  // nothing above reads what an earlier kernel writes
   if (threadIdx.x == 0) {
-    head = read_map_head(p.tm, p.lay, p.B, p.C, c, p.q_len, false, c == 0 && blockIdx.y == 0);
+    head = read_map_head(p.tm, p.lay, p.B, p.C, c, p.q_len, false, c == 0 && blockIdx.y == 0, true);
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(base + S::kKvFull + 8 * i, 1);   // TMA bytes
       mbar_init(base + S::kKvEmpty + 8 * i, 1);  // MMA commit
