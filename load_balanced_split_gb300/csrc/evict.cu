@@ -47,7 +47,10 @@ constexpr int kBins = 2048, kBins2 = 1024;                    // first and third
 constexpr int kList = 1024;                                  // keys that share two digits
 constexpr int kMaxCluster = 8;
 constexpr int kMaxLen = INT_MAX - 65536;  // the loops over keys run past the end by less
-constexpr int64_t kMinKeys = 4096;                           // per block before a cluster grows
+// Keys per block before a cluster grows, half of what a block holds: each of a cluster's
+// barriers costs a microsecond (72 pairs of 12000 keys: 16 us in one block each, 21 in four;
+// 8 of 16384: 17 in two and in four; 8 of 1024: 6 in one, 18 in eight)
+constexpr int64_t kMinKeys = 12288;
 constexpr int kSelSmem = kBlockPages * PAGE * 4 + (kBins + kBins2 + kList) * 4;
 constexpr int kSelBlocks = 2;                                // per SM: 112 KB of shared memory each
 constexpr int kFlight = 4;                                   // page pairs in flight per warp
@@ -587,21 +590,21 @@ cudaError_t launch_evict_select(const EvictParams &p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 64) configured[dev] = 1;
   }
-  // Blocks per (request, head), by a request of the pool's average length, or 64 times the
-  // longest list if that is less (the lengths themselves are on the device; a request that
-  // is shorter leaves blocks idle: 16 x 8192 cut to 512 in a pool of 20 times their pages
-  // 31 us by the average alone, 19 so): more as long as the clusters find room on the GPU
-  // together and a block has kMinKeys (a request of 1024 keys: 6 us in one block, 18 in
-  // eight, each of whose barriers costs a microsecond); one step past that room if the
-  // weights are not held otherwise (20 x 196608: 164 against 189 us), not where they fill
-  // it already (64 x 24000: 51 in one block, 62 in two; 40 x 100000: 166, 245 in four).
+  // Blocks per (request, head).  The lengths are on the device; the launch goes by the pool's
+  // average and not by the budget, which says nothing of the length (one request of 196608
+  // cut to 64 by one block each: 138 us, by eight 27), and blocks that a shorter request does
+  // not need leave.  More blocks as long as the clusters find room on the GPU together and a
+  // block has kMinKeys; past that room (up to 1.4 times) only where the weights are far more
+  // than the blocks hold (160 pairs of 196608: 171 us in two blocks each, 195 in one; 160 of
+  // 55000: 60 and 56; 64 of 191721: 74 in eight, 58 in four; 256 of 30000: 46 in two, 33 in
+  // one).
   const int64_t pairs = static_cast<int64_t>(p.B) * p.Hkv;
   const int64_t share = p.num_pages * PAGE / p.B, room = kSelBlocks * sms;
-  const int64_t mean = p.kept_stride < share / 64 ? 64 * p.kept_stride : share;
+  const int64_t held = kBlockPages * PAGE;
   int ranks = 1;
   while (ranks < kMaxCluster &&
-         ((pairs * ranks * 2 <= room && ranks * kMinKeys < mean) ||
-          (pairs * ranks <= room && static_cast<int64_t>(ranks) * kBlockPages * PAGE < mean)))
+         ((pairs * ranks * 2 <= room && ranks * kMinKeys < share) ||
+          (pairs * ranks * 2 <= room * 7 / 5 && ranks * held * 3 < share)))
     ranks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(pairs * ranks));
