@@ -496,8 +496,10 @@ int hpa_evict_compact(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, floa
 
 /*
  * hpa_evict -- hpa_evict_select followed by hpa_evict_compact of K, V and the weights
- * (acc_dev, not NULL) in one call, with their arguments, results and checks (all made
- * before the first launch).
+ * (acc_dev, not NULL) in one call, with their arguments, results and checks (those of the
+ * arguments all made before the first launch).  With a second table the selection checks it
+ * too: a request whose new pages are not all listed with valid ids gets new_lens -1 and
+ * HPA_STATUS_BAD_PAGE, and none of its rows moves.
  */
 int hpa_evict(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, float *acc_dev,
               int64_t num_pages, const int32_t *seq_lens_dev, const int32_t *page_indptr_dev,

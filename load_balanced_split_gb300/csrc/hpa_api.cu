@@ -616,7 +616,7 @@ static int evict_params(const float *acc_dev, const int32_t *seq_lens_dev,
   *p = hpa::EvictParams{acc_dev,   seq_lens_dev, page_indptr_dev, page_indices_dev,
                         budgets_dev, num_pages,  sinks,           recent,
                         B,         Hkv,          kept_dev,        kept_stride,
-                        new_lens_dev, status_dev};
+                        new_lens_dev, status_dev,    nullptr,         nullptr};
   return HPA_OK;
 }
 
@@ -700,6 +700,8 @@ int hpa_evict(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, float *acc_d
                         page_indices_dev, dst_indptr_dev, dst_indices_dev, page_size, kept_dev,
                         kept_stride, new_lens_dev, B, Hkv, d, status_dev, &mv);
   if (rc != HPA_OK) return rc;
+  p.dst_indptr = mv.dst_indptr;
+  p.dst_indices = mv.dst_indices;
   cudaError_t e = hpa::launch_evict_select(p, reinterpret_cast<cudaStream_t>(stream));
   if (e == cudaSuccess)
     e = hpa::launch_evict_compact(mv, reinterpret_cast<cudaStream_t>(stream));

@@ -134,6 +134,7 @@ struct EvictParams {
   int64_t kept_stride;
   int32_t *new_lens;
   int32_t *status;
+  const int32_t *dst_indptr, *dst_indices;  // where hpa_evict moves to (nullptr: in place)
   bool longest_first;  // requests in the order of their lengths (set by the launch)
 };
 cudaError_t launch_evict_select(const EvictParams &p, cudaStream_t s);

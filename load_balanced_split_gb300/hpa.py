@@ -689,7 +689,8 @@ def hpa_evict(acc, k_pool, v_pool, seq_lens, page_indptr, page_indices, budgets,
               recent: int, kept, new_lens, dst_indptr=None, dst_indices=None, status=None,
               stream=None):
     """hpa_evict_select, then hpa_evict_compact of K, V and acc; the cache then has new_lens[r]
-    keys per request (-1: a request that `status` reports, untouched)."""
+    keys per request (-1: a request that `status` reports, for a bad destination list as well;
+    nothing of it is moved)."""
     kv, P, Hkv, page, d = _pools(k_pool, v_pool)
     _acc_pool(acc, "acc", k_pool)
     _dev(seq_lens, "seq_lens", torch.int32)
