@@ -62,10 +62,12 @@ struct KwCfg {
   static constexpr int kStages = (kSmall ? 64 : 160) * 1024 / kStageBytes;
   static constexpr int kBufs = KV == HPA_KV_E4M3 && kSmall ? 2 : 4;  // S buffers in TMEM
   // Slots of the accumulator ring.  The copy for step n is issued once the MMAs of step
-  // n - kStages are done, these once step n - kStages - kBufs has been read: with as many
-  // slots, none is overwritten early.
+  // n - kStages are done, and these once the scores of step n - kStages - kBufs have left
+  // TMEM.  The group of that step reads its accumulators only after it has released the
+  // scores, but its step before, n - kStages - kBufs - kGroups, it has finished: a slot may
+  // be taken again that many steps later.
   static constexpr int kAccs = kSmall ? 8 : 16;
-  static_assert(kStages + kBufs <= kAccs && kAccs % kGroups == 0, "accumulator ring");
+  static_assert(kStages + kBufs + kGroups <= kAccs && kAccs % kGroups == 0, "accumulator ring");
   static constexpr int kTmem = kBufs * kN <= 32    ? 32
                                : kBufs * kN <= 64  ? 64
                                : kBufs * kN <= 128 ? 128
