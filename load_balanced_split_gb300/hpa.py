@@ -219,6 +219,7 @@ def hpa_plan_window(seq_lens, q_len: int, window: int, sinks: int, tile: int, nu
     i > a - window or i < sinks."""
     _dev(seq_lens, "seq_lens", torch.int32)
     _dev(taskmap, "taskmap")
+    _one_device(seq_lens, taskmap)
     _check(lib().hpa_plan_window(_ptr(seq_lens), seq_lens.numel(), q_len, window, sinks, tile,
                                  num_ctas, _ptr(taskmap),
                                  taskmap.numel() * taskmap.element_size(), _stream(stream)),
@@ -249,6 +250,8 @@ def _attn_args(q, k_pool, v_pool, page_indptr, page_indices, taskmap, k_scale, v
     P, Hkv, page, d2 = k_pool.shape
     if d2 != d:
         raise HpaError("head dim mismatch")
+    if page_indptr.numel() < B + 1:
+        raise HpaError("page_indptr must have B + 1 = %d entries" % (B + 1))
     if kv == KV_E4M3 and (k_scale.numel() < Hkv or v_scale.numel() < Hkv):
         raise HpaError("k_scale / v_scale need one fp32 value per KV head")
     return kv, B, q_len, Hq, d, P, Hkv, page
@@ -492,18 +495,28 @@ def _store_kv(name, k_new, v_new, seq_lens, text_pos, page_indptr, page_indices,
     for t, n in ((seq_lens, "seq_lens"), (page_indptr, "page_indptr"),
                  (page_indices, "page_indices")):
         _dev(t, n, torch.int32)
-    _dev(k_pool, "k_pool")
-    _dev(v_pool, "v_pool")
-    kv = KV_BF16 if k_pool.dtype == torch.bfloat16 else KV_E4M3
+    kv, P, Hkv2, page, _ = _pools(k_pool, v_pool)
+    if k_new.dim() != 4 or v_new.shape != k_new.shape:
+        raise HpaError("k_new and v_new must match, [B][q_len][Hkv][d]")
     B, q_len, Hkv, d = k_new.shape
-    P, Hkv2, page, _ = k_pool.shape
-    if Hkv2 != Hkv:
-        raise HpaError("KV head count mismatch")
+    if Hkv2 != Hkv or k_pool.shape[3] != d:
+        raise HpaError("KV head count or head dim mismatch")
+    if page_indptr.numel() < B + 1 or seq_lens.numel() < B:
+        raise HpaError("page_indptr needs B + 1 = %d entries and seq_lens B" % (B + 1))
+    if cos_sin.dim() < 2 or cos_sin.numel() < cos_sin.shape[0] * d or norm_w.numel() < d:
+        raise HpaError("cos_sin must be [max_pos][d] and norm_w [d]")
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if kv == KV_E4M3 and _dev(t, n, torch.float32).numel() < Hkv:
+            raise HpaError("%s needs one fp32 value per KV head" % n)
+    if status is not None:
+        _dev(status, "status", torch.int32)
     at = ()
     if name == "hpa_store_kv_at":
         _dev(text_pos, "text_pos", torch.int32)
         if text_pos.numel() != B or seq_lens.numel() != B:
             raise HpaError("text_pos and seq_lens need one value per request")
+        _one_device(k_new, v_new, seq_lens, text_pos, page_indptr, page_indices, cos_sin, norm_w,
+                    k_pool, v_pool, k_scale, v_scale, status)
         at = (_ptr(text_pos),)
     _check(getattr(lib(), name)(
         _ptr(k_new), _ptr(v_new), _ptr(seq_lens), *at, _ptr(page_indptr), _ptr(page_indices), P,
