@@ -85,8 +85,8 @@ typedef struct CUstream_st *hpa_stream_t;
  * serves every layer of a decode step ([HPC-Ops §二.1]).  Layout (int32 words):
  *   [0,16)  header: T, base, rem, C, B, S (segments), status, tile, kind
  *           (0 dynamic / 1 static / 2 token-weighted / 3 window), splits, S_cap,
- *           then window, sinks, q_len of a window map, the status bits that
- *           hpa_key_weights has set, 0
+ *           then window, sinks, q_len of a window map, and two words that
+ *           hpa_key_weights uses while it runs (0 before and after)
  *   lens[B]            copy of the sequence lengths
  *   cu_tiles[B+1]      exclusive running sum of tiles per request
  *   cta_begin[C+1]     first stream tile of each partition
@@ -439,10 +439,10 @@ int hpa_store_kv_at(const void *k_new_dev, const void *v_new_dev, const int32_t 
  * taskmap_dev: the map of the attention step, of any plan; num_ctas as planned.  Both
  * pools 16-byte aligned.  q, K, shapes and errors as hpa_decode_attn; the pages of a
  * bad page id, the keys of a request shorter than q_len and those of a malformed segment
- * are not written, all others are updated in full.  A status that an earlier call left in
- * the map (the plan or the attention step) stops the whole call, nothing being written; the
- * bits that hpa_key_weights has set itself do not, HPA_STATUS_TIMEOUT excepted, after which
- * the accumulators are undefined.
+ * are not written, all others are updated in full, and the bits are in the status once the
+ * call has run.  A status that an earlier call left in the map (the plan, the attention
+ * step, hpa_key_weights) stops the whole call: nothing is written.  After
+ * HPA_STATUS_TIMEOUT the accumulators are undefined.
  */
 int hpa_key_weights(const void *q_dev, const float *lse_dev, const void *k_pool_dev,
                     int32_t kv_dtype, const float *k_scale_dev, int64_t num_pages,

@@ -17,7 +17,7 @@ namespace hpa {
 // ----------------------------------------------------------------------------- task map
 enum : int {
   TM_T = 0, TM_BASE, TM_REM, TM_C, TM_B, TM_S, TM_STATUS, TM_TILE, TM_KIND, TM_SPLITS,
-  TM_SCAP, TM_WINDOW, TM_SINKS, TM_QLEN, TM_RAISED, TM_HEADER_WORDS = 16
+  TM_SCAP, TM_WINDOW, TM_SINKS, TM_QLEN, TM_RAISED, TM_DONE, TM_HEADER_WORDS = 16
 };
 constexpr int KIND_WINDOW = 3;  // the map kind of hpa_plan_window
 
@@ -410,14 +410,19 @@ __device__ __forceinline__ void status_or(int32_t *tm, int bits) {
   atomicOr(reinterpret_cast<int *>(tm + TM_STATUS), bits);
 }
 
-// As status_or, for errors that hpa_key_weights itself finds.  TM_RAISED has the bit before
-// the status does, so a block that starts later and meets the status can tell it from an
-// earlier kernel's (read_map_head): one request's error must not stop the updates of others,
-// which would then depend on when their blocks run.
-__device__ __forceinline__ void status_or_raised(int32_t *tm, int bits) {
+// hpa_key_weights updates in place, so which requests it updates must not hang on when its
+// blocks run: all of them have to go by the status as it was before the launch.  The errors
+// that it finds gather in TM_RAISED, and the last block to get past its own (each of the
+// launch's n blocks calls raised_done once, after its last raise) moves them to the status.
+__device__ __forceinline__ void status_raise(int32_t *tm, int bits) {
   atomicOr(reinterpret_cast<int *>(tm + TM_RAISED), bits);
   __threadfence();
-  status_or(tm, bits);
+}
+__device__ __forceinline__ void raised_done(int32_t *tm, unsigned n) {
+  __threadfence();
+  if (atomicInc(reinterpret_cast<unsigned *>(tm + TM_DONE), n - 1) != n - 1) return;
+  const int bits = atomicExch(reinterpret_cast<int *>(tm + TM_RAISED), 0);
+  if (bits != 0) status_or(tm, bits);
 }
 
 // One segment row of a task map, checked before use: request in [0, B), owned by
@@ -446,7 +451,7 @@ __device__ __forceinline__ SegRow read_seg_row(int32_t *tm, const TaskMapLayout 
       }
     }
   }
-  if (report && RAISED) status_or_raised(tm, HPA_STATUS_BAD_MAP);
+  if (report && RAISED) status_raise(tm, HPA_STATUS_BAD_MAP);
   else if (report) status_or(tm, HPA_STATUS_BAD_MAP);
   return SegRow{0, 1 << 30, 0, 0};
 }
@@ -467,8 +472,8 @@ __device__ __forceinline__ bool map_ranges_ok(const int32_t *tm, const TaskMapLa
 // header (the words lie behind the plan's kernel in L2, and a check at a time costs a round
 // trip each) and one of the partition's segment range.  With need_window a map of another
 // kind is malformed; without, all kinds are read.  A map for another shape or q_len is
-// reported by the CTA with `report`, a malformed one by every CTA that finds it.  With raised
-// (hpa_key_weights) the bits that this kernel has set do not stop it.
+// reported by the CTA with `report`, a malformed one by every CTA that finds it, with `raised`
+// through status_raise.
 struct MapHead {
   int go, tile, s_begin, s_end, windowed, window, sinks;
 };
@@ -482,12 +487,7 @@ __device__ __forceinline__ MapHead read_map_head(int32_t *tm, const TaskMapLayou
                     TM_QLEN == 13,
                 "header words");
   MapHead m = {0, b.w, 0, 0, d.x == KIND_WINDOW, d.w, e.x};
-  int status = b.z;
-  if (raised && status != 0) {
-    __threadfence();  // TM_RAISED after the status: see status_or_raised
-    status &= ~*reinterpret_cast<volatile const int32_t *>(tm + TM_RAISED);
-  }
-  if (status != 0) return m;
+  if (b.z != 0) return m;
   if (a.w != C || b.x != B || m.tile <= 0 || m.tile % PAGE != 0 ||
       (m.windowed && e.y != q_len)) {
     if (report) status_or(tm, HPA_STATUS_MISMATCH);
@@ -500,7 +500,7 @@ __device__ __forceinline__ MapHead read_map_head(int32_t *tm, const TaskMapLayou
                                   : !need_window && d.x >= 0 && d.x <= 2;
   if (!kind_ok || d.z != cap || S < 0 || S > cap || m.s_begin < 0 || m.s_begin > m.s_end ||
       m.s_end > S) {
-    if (raised) status_or_raised(tm, HPA_STATUS_BAD_MAP);
+    if (raised) status_raise(tm, HPA_STATUS_BAD_MAP);
     else status_or(tm, HPA_STATUS_BAD_MAP);
     m.s_begin = m.s_end = 0;
     return m;

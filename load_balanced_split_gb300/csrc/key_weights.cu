@@ -106,7 +106,7 @@ __device__ __forceinline__ KwSeg kw_seg(const KeyWeightsParams &p, const MapHead
                  : read_seg_row<false, true>(p.tm, p.lay, p.B, s, blockIdx.x, m.tile, report);
   KwSeg f = {sr.r, sr.L, sr.klo / PAGE, (sr.khi + PAGE - 1) / PAGE};
   if (sr.L < p.q_len) {
-    if (report) status_or_raised(p.tm, HPA_STATUS_BAD_SEQLEN);
+    if (report) status_raise(p.tm, HPA_STATUS_BAD_SEQLEN);
     f.pg1 = f.pg0;
   }
   return f;
@@ -262,7 +262,7 @@ __device__ void kw_producer(const KeyWeightsParams &p, const CUtensorMap *tmk, u
           const int pg = windowed ? win.real_page(v) : v;
           id[u] = pg < pcount ? p.page_indices[pstart + pg] : -1;
           if (id[u] < 0 || id[u] >= p.num_pages) {
-            status_or_raised(p.tm, HPA_STATUS_BAD_PAGE);
+            status_raise(p.tm, HPA_STATUS_BAD_PAGE);
             id[u] = -1;  // page 0 is read in its place and nothing is written
           }
         }
@@ -307,6 +307,8 @@ __device__ void kw_producer(const KeyWeightsParams &p, const CUtensorMap *tmk, u
       }
     }
   }
+  __syncwarp();
+  if (lane == 0) raised_done(p.tm, gridDim.x * gridDim.y);  // this warp alone raises errors
   if (!ok && lane == 0) {
     status_or(p.tm, HPA_STATUS_TIMEOUT);
     *abort_flag = 1;
@@ -510,7 +512,10 @@ __global__ void __launch_bounds__(KwCfg<KV, RP>::kThreads, RP <= 16 ? 2 : 1)
   if (threadIdx.x < RP) reinterpret_cast<int *>(smem + S::kJRow)[threadIdx.x] = threadIdx.x / p.G;
   __syncthreads();
   pdl_launch_dependents();
-  if (!head.go) return;
+  if (!head.go) {
+    if (threadIdx.x == 0) raised_done(p.tm, gridDim.x * gridDim.y);
+    return;
+  }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      base + S::kTmemAt),

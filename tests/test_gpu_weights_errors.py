@@ -30,10 +30,11 @@ def _weights(db, lse, acc0, lens=None, indices=None, corrupt=None, calls=1):
         corrupt(tm)
         ws.taskmap.copy_(tm)
     acc = acc0.clone()
-    for _ in range(calls):
+    for _ in range(calls):                                  # an error stops those that follow
         hpa.hpa_key_weights(db.q, lse, db.k, db.indptr, db.indices if indices is None else indices,
                             ws.taskmap, C, acc, decay=0.5)
     torch.cuda.synchronize()
+    assert ws.taskmap[14:16].tolist() == [0, 0]
     return ws.status(), acc
 
 
@@ -41,7 +42,7 @@ def _weights(db, lse, acc0, lens=None, indices=None, corrupt=None, calls=1):
 @pytest.mark.parametrize("what", ["page", "length", "segment"])
 def test_other_requests_are_updated_in_full(what, calls):
     b, db, lse, acc0 = _state()
-    st, want = _weights(db, lse, acc0, calls=calls)
+    st, want = _weights(db, lse, acc0)
     assert st == 0
     touched = np.ones(b.num_pages, bool)
     if what == "page":
@@ -92,3 +93,21 @@ def test_the_attention_step_still_reports_what_key_weights_found():
     hpa.decode_step(ws, db.q, db.k, db.v, db.lens, db.indptr, db.indices, out, tile=64)
     torch.cuda.synchronize()
     assert ws.status() == 0 and not out.isnan().any()        # a new plan starts afresh
+
+
+def test_a_step_after_an_error_adds_nothing():
+    """Layer after layer on one plan: the first one's weights meet a bad page of their own, the
+    attention of the next gives NaN, and its weights leave every accumulator as it was."""
+    b, db, lse, acc0 = _state()
+    ws = hpa.Workspace(B, 2, 2 * HKV, 128, num_ctas=C, Hkv=HKV)
+    ws.plan(db.lens, tile=64)
+    bad = db.indices.clone()
+    bad[3] = -1
+    hpa.hpa_key_weights(db.q, lse, db.k, db.indptr, bad, ws.taskmap, C, acc0.clone())
+    out = torch.zeros((B, 2, 2 * HKV, 128), dtype=torch.bfloat16, device="cuda")
+    for _ in range(2):
+        acc = acc0.clone()
+        hpa.decode_step(ws, db.q, db.k, db.v, db.lens, db.indptr, db.indices, out, lse, acc=acc,
+                        plan=False)
+        torch.cuda.synchronize()
+        assert ws.status() == 4 and lse.isnan().all() and torch.equal(acc, acc0)
