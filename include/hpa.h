@@ -212,6 +212,8 @@ int hpa_plan_window(const int32_t *seq_lens_dev, int32_t B, int32_t q_len, int32
  *               query converts exactly, down to 2^-28 of its row's largest.
  * page_indptr_dev: int32 [B+1]; page_indices_dev: int32; key i of request r
  *               is slot i % page_size of page page_indices[page_indptr[r] + i / page_size].
+ *               page_indptr has to be right when the kernel reads it: no call is told how
+ *               many indices there are (page ids themselves are checked).
  * Supported: d == 128, page_size == 64, Hq % Hkv == 0, (Hq / Hkv) * q_len <= 64,
  *               num_pages * Hkv < 2^31.  Row groups past the first re-read the
  *               pages (through L2 when they run together).
@@ -274,7 +276,10 @@ int32_t hpa_default_num_ctas_tc(int32_t Hq, int32_t Hkv, int32_t q_len, int32_t 
  * only their pages.  Arguments, layouts, supported shapes, partials and errors are
  * those of hpa_decode_attn; q_len is the one the map was planned with
  * (HPA_STATUS_MISMATCH).  What lies in hidden places of a page, NaN included, does
- * not enter the result.  hpa_combine merges the partials.
+ * not enter the result.  hpa_combine merges the partials.  The kernel is that of
+ * hpa_decode_attn_mma, and a window that hides nothing gives its bits: sums and softmax
+ * statistics are fp32, and the probabilities are rounded to the type of the second product
+ * (bf16 pages: bf16, each off by at most 2^-8 of itself; E4M3 pages: f16, 2^-11).
  */
 int hpa_decode_attn_window(const void *q_dev, const void *k_pool_dev, const void *v_pool_dev,
                            int32_t kv_dtype, const float *k_scale_dev, const float *v_scale_dev,
@@ -432,12 +437,15 @@ int hpa_store_kv_at(const void *k_new_dev, const void *v_new_dev, const int32_t 
  *                exp(sm_scale * q . k_i - lse[j][g]),
  * in fp32, the same order on every run.  The q_len new keys start from zero, whatever
  * their slots held.  Other slots are not written (with a window map: keys no token
- * sees; they keep their weight and do not decay).  acc_in_dev may equal acc_out_dev
+ * sees; they keep their weight and do not decay, so an eviction by these weights may keep
+ * keys that no window shows any more).  acc_in_dev may equal acc_out_dev
  * (the usual, in place), be another pool that does not overlap it (draft tokens that may
  * yet be rejected) or be NULL for zero; decay 0 does not read it.  A row whose lse is
  * -inf adds nothing.
  * taskmap_dev: the map of the attention step, of any plan; num_ctas as planned.  Both
- * pools 16-byte aligned.  q, K, shapes and errors as hpa_decode_attn; the pages of a
+ * pools 16-byte aligned.  q, K, shapes and errors as hpa_decode_attn, but with E4M3 pages
+ * the query rows are carried as in hpa_decode_attn_tc at every row count: exactly down to
+ * about 2^-12 of a row's largest element, then to an absolute 2^-21 of it.  The pages of a
  * bad page id, the keys of a request shorter than q_len and those of a malformed segment
  * are not written, all others are updated in full, and the bits are in the status once the
  * call has run.  A status that an earlier call left in the map (the plan, the attention
@@ -481,8 +489,9 @@ int hpa_evict_select(const float *acc_dev, const int32_t *seq_lens_dev,
  * dst_indices_dev NULL the new cache is the front of the request's own pages; the pages
  * past ceil(new_len / page_size) are then free.  Otherwise it is the pages that this
  * second table lists, none of them among the pages being read: the old cache stays as
- * it was (a shared prefix, say).  Order is kept, so windows, sinks and causal masks mean
- * the same as before.  kept must ascend, as hpa_evict_select writes it.  new_lens[r]
+ * it was (a shared prefix, say).  Order is kept, so sinks and causal masks mean the same as
+ * before; a window counts cache slots, so after an eviction it reaches further back in the
+ * text than its number of keys (no call masks by text position).  kept must ascend, as hpa_evict_select writes it.  new_lens[r]
  * below 1 or beyond kept_stride: the request is passed over.  A position without a
  * valid page sets HPA_STATUS_BAD_PAGE in status_dev (optional), and that row is not
  * moved.  k_pool_dev, v_pool_dev 16-byte aligned, apart from each other.

@@ -715,6 +715,10 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, int s_begin, int s_
             return key < (row ? lim1 : lim0) && (key < sinks || key >= win.start + j);
           }, [&](int key) { return (key >= pl && key < ph) || (key >= lim_min && key < f.L); }, wk);
       }
+      // The probabilities in the type of V's operand, since one MMA has one type: bf16 for
+      // bf16 pages (off by up to 2^-8 of each, in a sum whose own result is rounded as
+      // much: 2.2e-3 largest difference from 64 bits where fp32 probabilities give 1.7e-3),
+      // f16 for E4M3 ones (2^-11).  Their sums l are taken in fp32 before the rounding.
       uint32_t pa[4];
       if (KV == HPA_KV_BF16) {
         pa[0] = pack_bf16(sc[0][0], sc[0][1]);

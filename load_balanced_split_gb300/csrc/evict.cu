@@ -13,9 +13,10 @@
 // a block, 192 K a cluster; a longer request's rest is read again in each pass, from L2).
 // The third digit's pass also counts what lies above and lists the few keys that share
 // both digits before, so the final counts go over that list.
-// Bound by instruction issue (half of the cycles) and the barriers between the passes,
-// not by memory: 15 us for 32 requests of 8 heads and about 8192 keys cut to 2048, 53 for
-// 64 of about 24000 cut to 4096, 23 for one of 196608 cut to 16384.
+// Bound by instructions (44 % of the issue slots busy over the whole launch, the wait for
+// their fetch the first stall) and the barriers between the passes, not by memory: 15 us for
+// 32 requests of 8 heads and about 8192 keys cut to 2048, 54 for 64 of about 24000 cut to
+// 4096, 23 for one of 196608 cut to 16384.
 //
 // Compaction (evict_copy_kernel to other pages, evict_shift_kernel in place).  Row t of the
 // new cache is row kept[t] of the old one, and kept is ascending, so kept[t] >= t: in place,
@@ -65,9 +66,9 @@ __device__ __forceinline__ uint32_t weight_key(uint32_t u) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// Over the n blocks of the cluster that take part: the bin of the k-th largest entry (1 <= k <= the entries
-// counted) and the number of entries in higher bins.  The caller has synchronised the
-// cluster after the last count into `hist`.
+// Over the n blocks of the cluster that take part: the bin of the k-th largest entry (1 <= k
+// <= the entries counted) and the number of entries in higher bins.  The caller has
+// synchronised the cluster after the last count into `hist`.
 template <int BINS>
 __device__ void find_bin(cg::cluster_group &cl, int n, int *hist, int k, int &bin, int &above) {
   constexpr int N = BINS / kSelThreads;  // bins per thread: 4 or 2
