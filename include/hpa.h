@@ -450,7 +450,9 @@ int hpa_store_kv_at(const void *k_new_dev, const void *v_new_dev, const int32_t 
  * are not written, all others are updated in full, and the bits are in the status once the
  * call has run.  A status that an earlier call left in the map (the plan, the attention
  * step, hpa_key_weights) stops the whole call: nothing is written.  After
- * HPA_STATUS_TIMEOUT the accumulators are undefined.
+ * HPA_STATUS_TIMEOUT the accumulators are undefined.  Calls that run at the same time over
+ * one map need the same Hkv, as they count their blocks in it together, and an error in one
+ * of them may stop blocks of the others.
  */
 int hpa_key_weights(const void *q_dev, const float *lse_dev, const void *k_pool_dev,
                     int32_t kv_dtype, const float *k_scale_dev, int64_t num_pages,

@@ -111,3 +111,43 @@ def test_a_step_after_an_error_adds_nothing():
                         plan=False)
         torch.cuda.synchronize()
         assert ws.status() == 4 and lse.isnan().all() and torch.equal(acc, acc0)
+
+
+def test_calls_over_one_map_on_two_streams():
+    """Two layers' weights at once, over and over: each as if alone, the map's two words zero
+    again, and an error in a later call still reported."""
+    b, db, lse, acc0 = _state()
+    _, want = _weights(db, lse, acc0)
+    ws = hpa.Workspace(B, 2, 2 * HKV, 128, num_ctas=C, Hkv=HKV)
+    ws.plan(db.lens, tile=64)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    accs = [[acc0.clone() for _ in range(4)] for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for s, a in zip(streams, accs):
+            hpa.hpa_key_weights(db.q, lse, db.k, db.indptr, db.indices, ws.taskmap, C, a[i],
+                                decay=0.5, stream=s)
+    torch.cuda.synchronize()
+    assert ws.status() == 0 and ws.taskmap[14:16].tolist() == [0, 0]
+    assert all(torch.equal(a, want) for group in accs for a in group)
+    bad = db.indices.clone()
+    bad[-1] = -1                                            # the last blocks' page
+    hpa.hpa_key_weights(db.q, lse, db.k, db.indptr, bad, ws.taskmap, C, acc0.clone())
+    assert ws.status() == 4
+
+
+def test_calls_of_other_head_counts_one_after_the_other():
+    """The blocks of a call are counted in the map: a call of another size begins from zero."""
+    b, db, lse, acc0 = _state()
+    ws = hpa.Workspace(B, 2, 2 * HKV, 128, num_ctas=C, Hkv=HKV)
+    ws.plan(db.lens, tile=64)
+    for heads in (1, 3, HKV):
+        k, a = db.k[:, :heads].contiguous(), acc0[:, :heads].contiguous()
+        hpa.hpa_key_weights(db.q[:, :, :2 * heads].contiguous(),
+                            lse[:, :, :2 * heads].contiguous(), k, db.indptr, db.indices,
+                            ws.taskmap, C, a)
+        assert ws.status() == 0 and ws.taskmap[14:16].tolist() == [0, 0]
+    bad = db.indices.clone()
+    bad[-1] = -1
+    hpa.hpa_key_weights(db.q, lse, db.k, db.indptr, bad, ws.taskmap, C, acc0.clone())
+    assert ws.status() == 4 and ws.taskmap[14:16].tolist() == [0, 0]
