@@ -43,8 +43,8 @@ UNIT = "us/batch"
 # scaled to the full batch, since traffic grows with the KV read.
 TRAFFIC_PROFILE = {
     "config": 3,
-    "source_sha256": "66a06c432afe56678c828a21c6ede1dcaa440278670e32ade6e77a7ea16fae0c",
-    "bytes_per_kv_byte": (2574349568 + 3353344) / 2572926976,
+    "source_sha256": "8be854326d3dd9a57b4db80e10f4a789e2b8c02b731122054bb4c33a68306fbf",
+    "bytes_per_kv_byte": (2574498560 + 3051520) / 2572926976,
     "workload": "mixed_45req_1k_128k_paged, first 12 requests (2.57 GB KV)",
 }
 
