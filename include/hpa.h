@@ -78,6 +78,15 @@ typedef struct CUstream_st *hpa_stream_t;
 /* ---- KV element types ---- */
 #define HPA_KV_BF16 0 /* bfloat16 */
 #define HPA_KV_E4M3 1 /* OCP FP8 E4M3 code; value = code * scale[kv head] */
+#define HPA_KV_E2M1 2 /* 4-bit: OCP FP4 E2M1 code; value = code * block scale * scale[kv head],
+                         with an E4M3 block scale for every 16 elements of a row */
+
+/* A 4-bit pool holds, for each page and KV head, HPA_E2M1_PAGE_BYTES bytes: 64 rows of 64 bytes
+ * of codes (byte i of a row: element 2i in the low nibble, 2i + 1 in the high one), then the
+ * block scales, 64 rows of 8 bytes (byte j of a row: elements [16j, 16j + 16)).  Taken by
+ * hpa_decode_attn, hpa_decode_attn_window, hpa_decode_attn_combine_noalloc, hpa_store_qkv and
+ * hpa_default_num_ctas(_window); every other call with a kv_dtype refuses it. */
+#define HPA_E2M1_PAGE_BYTES 4608
 
 /*
  * Task map: an opaque int32 blob in device memory, written by hpa_plan or
@@ -210,6 +219,12 @@ int hpa_plan_window(const int32_t *seq_lens_dev, int32_t B, int32_t q_len, int32
  *               scaled by a power of two that puts its largest |element| in
  *               [2^14, 2^15) (taken back out of the scores), so any finite bf16
  *               query converts exactly, down to 2^-28 of its row's largest.
+ *               With HPA_KV_E2M1 pages (layout above, pools 16-byte aligned) a kernel of
+ *               their own runs at every row count, in row groups of up to 16, with the
+ *               precision of E4M3 pages here: codes times block scales and queries enter the
+ *               products exactly, in f16, sums and softmax statistics are fp32 and the
+ *               probabilities are rounded to f16 (2^-11).  NaN block scales of keys that a
+ *               row does not see do not reach it; a row that sees one is NaN in the result.
  * page_indptr_dev: int32 [B+1]; page_indices_dev: int32; key i of request r
  *               is slot i % page_size of page page_indices[page_indptr[r] + i / page_size].
  *               page_indptr has to be right when the kernel reads it: no call is told how

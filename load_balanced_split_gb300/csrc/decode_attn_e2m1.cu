@@ -1,0 +1,733 @@
+// Split-KV GQA decode attention over a paged KV cache held in 4 bits (HPA_KV_E2M1), driven by
+// the same task maps as the 16- and 8-bit kernels.
+//
+// A page of one KV head is one block of 4608 bytes: 64 rows of 64 bytes of E2M1 codes (the even
+// element of a pair in the low nibble), then 64 x 8 E4M3 scales, one for every 16 elements of a
+// row.  With c the code's value, b its block's scale and s_h the head's scale,
+//   x = c * b * s_h,   out = sum_i softmax(sm_scale * q . k_i) v_i   over the keys a token sees.
+//
+// What bounds it: at 4.5 bits an element the DRAM delivers 42 elements a clock to each SM, so
+// the widening to f16 has about three instruction slots an element before it, not the memory,
+// is what the kernel waits for.  The layout keeps to about half of them:
+//  * the products run as m16n8k16 MMAs with the KEYS (S = K Q^T) and the HEAD DIMS (O^T = V^T P^T)
+//    as the 16 rows and 8 query rows as the 8 columns, so an MMA takes 256 cache elements for 8
+//    query rows, where queries on the 16 rows would take 128 and leave half of the tile empty;
+//  * a thread reads 32 consecutive dims of a key with one 16-byte load and widens two codes per
+//    conversion; the head dims are permuted alike in Q and K, so nothing is shuffled.  The
+//    product of a code and its block scale has 6 significant bits and is exact in f16;
+//  * V needs its pairs along the keys.  Two keys' words are interleaved by nibbles (four logic
+//    operations for 16 elements), so that a converted byte already is a pair of keys;
+//  * P moves from the first product's accumulator layout to the second's operand by movmatrix;
+//  * the softmax's running maximum moves only when a score passes it by 2^8 (as in the 8-bit
+//    kernel), so a page costs one vote and no exchange of maxima;
+//  * a warp takes whole pages, every fourth of its CTA: one wait, one vote and one release for
+//    64 keys.  One producer warp keeps a ring of pages in flight with bulk copies, two a page
+//    (codes and scales lie together).
+// Sums, softmax statistics and outputs are fp32.  Queries enter as f16, each row scaled by a power
+// of two that puts its largest element into [2^14, 2^15) (exact down to 2^-28 of it), and the
+// probabilities are rounded to f16 (2^-11 of each) as the second product's operand.
+//
+// Windows with sink tokens (WIN): the producer maps the map's compact pages to real ones
+// (WinSpan), and pages at the window's ends mask by position.  Pages without a hidden key run a
+// copy of the loop without masks.  A code cannot be NaN but a block scale can: V scales of keys
+// that no token sees are taken as zero, and a key that some tokens see and others do not is
+// added for the rows that see it alone if its scales hold a NaN.
+#include <math_constants.h>
+
+#include <type_traits>
+
+#include "hpa_internal.cuh"
+
+namespace hpa {
+namespace {
+
+constexpr int kWarps = 4;  // consumer warps
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kUnit = E2M1_UNIT;  // bytes of one page and KV head of K or V
+constexpr int kStageBytes = 2 * kUnit;
+constexpr int kStages = 8;  // a multiple of kWarps: a warp meets the same stages again
+constexpr float kRescaleSlack = 8.f;
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kQRowBytes = 272;  // 256 of a query row, padded against bank conflicts
+constexpr int kMergeStride = HEAD_DIM + 4;
+
+template <int NT>
+struct Smem {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kQSlot = kRows * kQRowBytes;
+  static constexpr int kMerge = kStages * kStageBytes;               // float[2][kRows][stride]
+  static constexpr int kStats = kMerge + 2 * kRows * kMergeStride * 4;  // m, l: [warps][kRows]
+  static constexpr int kQ = kStats + 2 * kWarps * kRows * 4;         // two query slots
+  static constexpr int kInfo = kQ + 2 * kQSlot;                      // int4[2]
+  static constexpr int kBars = kInfo + 2 * 16;  // full[stages] empty[stages] qfull[2] qempty[2]
+  static constexpr int kFlag = kBars + (2 * kStages + 4) * 8;
+  static constexpr int kBytes = kFlag + 16;
+  static constexpr int kAlloc = kBytes + 128;  // room to align the base
+};
+
+// Which of a group's 8 keys stands at index k of the MMAs' key dimension: the keys that the
+// four lanes of a quad read together for V (k = 0, 2, 4, 6 and 1, 3, 5, 7) then lie in both
+// halves of the 128 bytes that shared memory serves at once.
+__device__ __forceinline__ constexpr int key_at(int k) { return k ^ ((k >> 1) & 1); }
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+// The four bytes of w, two E2M1 codes each, as f16 pairs (low nibble in the low half; exact).
+__device__ __forceinline__ void widen8(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Transpose of an 8x8 matrix of 16-bit elements held a row of pairs per lane quad.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+__device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void *src, uint32_t bytes,
+                                               uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ float absmax8_bf16(uint4 v) {
+  float m = 0.f;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[i] << 16)),
+                       fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+  return m;
+}
+
+__device__ __forceinline__ bool e4m3_nan(uint32_t byte) { return (byte & 0x7fu) == 0x7fu; }
+
+struct Seg {
+  int r, L, klo, khi, pg0, pg1;
+};
+
+template <bool WIN>
+__device__ __forceinline__ Seg read_seg(const AttnParams &p, int s, int tile, bool report) {
+  const SegRow sr = read_seg_row<WIN>(p.tm, p.lay, p.B, s, blockIdx.x, tile, report);
+  return Seg{sr.r, sr.L, sr.klo, sr.khi, sr.klo / PAGE, (sr.khi + PAGE - 1) / PAGE};
+}
+
+__device__ __forceinline__ int row_base(const AttnParams &p) {
+  return p.group * static_cast<int>(blockIdx.z);
+}
+__device__ __forceinline__ int group_rows(const AttnParams &p) {
+  return min(p.group, p.rows - row_base(p));
+}
+
+// ----------------------------------------------------------------------------- producer
+template <int NT, bool WIN>
+__device__ void producer(const AttnParams &p, const uint8_t *k_pool, const uint8_t *v_pool,
+                         uint8_t *smem, const MapHead &head) {
+  using S = Smem<NT>;
+  const int lane = threadIdx.x & 31, h = blockIdx.y;
+  const uint32_t base = smem_u32(smem);
+  const uint32_t full0 = base + S::kBars, empty0 = full0 + 8 * kStages;
+  const uint32_t qfull0 = empty0 + 8 * kStages, qempty0 = qfull0 + 16;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kFlag);
+  const uint64_t pol = l2_policy_evict_first();
+  int stage = 0;
+  uint32_t phase = 0, issued = 0, parity_bits = 0;
+  bool ok = true;
+  for (int s = head.s_begin; s < head.s_end && ok; ++s) {
+    const Seg f = read_seg<WIN>(p, s, head.tile, lane == 0);
+    WinSpan win = {};
+    if (WIN && f.pg0 < f.pg1) win = WinSpan::make(f.L, p.q_len, head.window, head.sinks);
+    {  // the segment's place and query rows, two segments ahead of the consumers at most
+      const int k = s - head.s_begin, slot = k & 1;
+      int good = 1;
+      if (lane == 0)
+        good = !*abort_flag && mbar_wait_bounded(qempty0 + 8 * slot, ((k >> 1) & 1) ^ 1);
+      if (!__shfl_sync(kFull, good, 0)) {
+        ok = false;
+        break;
+      }
+      uint8_t *qs = smem + S::kQ + slot * S::kQSlot;
+      const int G = p.G, rb = row_base(p);
+      for (int ch = lane; ch < group_rows(p) * 16; ch += 32) {  // 16-byte chunks of 256-byte rows
+        const int row = ch >> 4, c16 = ch & 15, j = (rb + row) / G, g = (rb + row) % G;
+        const int4 v = reinterpret_cast<const int4 *>(
+            p.q + ((static_cast<int64_t>(f.r) * p.q_len + j) * p.Hq + h * G + g) * HEAD_DIM)[c16];
+        *reinterpret_cast<int4 *>(qs + row * kQRowBytes + c16 * 16) = v;
+      }
+      if (lane == 0)
+        reinterpret_cast<int4 *>(smem + S::kInfo)[slot] = make_int4(f.r, f.L, f.klo, f.khi);
+      mbar_arrive(qfull0 + 8 * slot);  // every lane publishes its own stores
+    }
+    const int pstart = p.page_indptr[f.r], pcount = p.page_indptr[f.r + 1] - pstart;
+    const int32_t *pidx = p.page_indices + pstart;
+    for (int pb = f.pg0; pb < f.pg1 && ok; pb += 32) {
+      const int cnt = min(32, f.pg1 - pb);
+      int id = 0;
+      if (lane < cnt) {
+        const int pg = WIN ? win.real_page(pb + lane) : pb + lane;
+        id = pg < pcount ? pidx[pg] : -1;
+        if (id < 0 || id >= p.num_pages) {  // bad id or too short a page list
+          status_or(p.tm, HPA_STATUS_BAD_PAGE);
+          id = 0;
+        }
+      }
+      for (int i = 0; i < cnt; ++i) {
+        const int pid = __shfl_sync(kFull, id, i);
+        int good = 1;
+        if (lane == 0) {
+          if (*abort_flag || !mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1)) {
+            good = 0;
+          } else {
+            const uint32_t fb = full0 + 8 * stage, dst = base + stage * kStageBytes;
+            const int64_t at = (static_cast<int64_t>(pid) * p.Hkv + h) * kUnit;
+            mbar_arrive_expect_tx(fb, kStageBytes);
+            bulk_load_hint(dst, k_pool + at, kUnit, fb, pol);
+            bulk_load_hint(dst + kUnit, v_pool + at, kUnit, fb, pol);
+            issued |= 1u << stage;
+            parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
+          }
+        }
+        ok = __shfl_sync(kFull, good, 0) != 0;
+        if (!ok) break;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  }
+  if (!ok && lane == 0) {
+    status_or(p.tm, HPA_STATUS_TIMEOUT);
+    *abort_flag = 1;
+    // never leave the CTA with copies still landing in its shared memory
+    for (int st = 0; st < kStages; ++st)
+      if (issued & (1u << st))
+        mbar_wait_bounded(full0 + 8 * st, (parity_bits >> st) & 1u, 1000000000ull);
+  }
+}
+
+// ----------------------------------------------------------------------------- consumer
+// V^T operand of 16 keys for one k half (8 keys: a pair per lane): the words of two keys, both
+// 16 dims of the lane, as f16 pairs along the keys; r[2 t] belongs to dim 16 g + 2 t, r[2 t + 1]
+// to the next.
+__device__ __forceinline__ void v_pairs(uint32_t lo_key, uint32_t hi_key, uint32_t scale,
+                                        uint32_t (&even)[4], uint32_t (&odd)[4]) {
+  widen8((lo_key & 0x0f0f0f0fu) | ((hi_key << 4) & 0xf0f0f0f0u), even);
+  widen8(((lo_key >> 4) & 0x0f0f0f0fu) | (hi_key & 0xf0f0f0f0u), odd);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    even[i] = mul_f16x2(even[i], scale);
+    odd[i] = mul_f16x2(odd[i], scale);
+  }
+}
+
+template <int NT, bool WIN>
+__device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head) {
+  using S = Smem<NT>;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
+  const int g = lane >> 2, c = lane & 3;
+  const uint32_t base = smem_u32(smem);
+  const uint32_t full0 = base + S::kBars, empty0 = full0 + 8 * kStages;
+  const uint32_t qfull0 = empty0 + 8 * kStages, qempty0 = qfull0 + 16;
+  float *mbuf = reinterpret_cast<float *>(smem + S::kMerge);
+  float *sm_m = reinterpret_cast<float *>(smem + S::kStats);
+  float *sm_l = sm_m + kWarps * S::kRows;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kFlag);
+
+  const int G = p.G, q_len = p.q_len, rows = group_rows(p), rb = row_base(p);
+  const float sl2 = p.scale_log2 * p.k_scale[h], vsc = p.v_scale[h];
+  // the two accumulator columns of each n-tile: query rows 8 nt + 2 c + {0, 1}, their tokens
+  int tok[2 * NT];
+#pragma unroll
+  for (int i = 0; i < 2 * NT; ++i) {
+    const int row = 8 * (i >> 1) + 2 * c + (i & 1);
+    tok[i] = row < rows ? (rb + row) / G : q_len - 1;
+  }
+  // where this lane's shares of a page lie: K rows key_at(g) (+8), dims 32 c..; V keys of the
+  // quad's lane c, dims 16 g..; their scales
+  const uint32_t k_off = key_at(g) * 64 + c * 16;
+  const uint32_t ks_off = 4096 + key_at(g) * 8 + 2 * c;
+  const int vk0 = key_at(2 * c), vk1 = key_at(2 * c + 1);
+
+  int count = 0;  // pages of this CTA so far: page n goes to warp n % kWarps, stage n % kStages
+  const int n_items = head.s_end - head.s_begin;
+  for (int k = 0; k < n_items; ++k) {
+    const int s = head.s_begin + k, slot = k & 1;
+    bool ok = !*abort_flag && mbar_wait_bounded(qfull0 + 8 * slot, (k >> 1) & 1);
+    ok = __all_sync(kFull, ok);
+    Seg f;
+    {
+      const int4 inf = reinterpret_cast<const int4 *>(smem + S::kInfo)[slot];
+      f.r = inf.x;
+      f.L = inf.y;
+      f.klo = inf.z;
+      f.khi = inf.w;
+      f.pg0 = f.klo / PAGE;
+      f.pg1 = ok ? (f.khi + PAGE - 1) / PAGE : f.pg0;  // no pages if the wait gave up
+    }
+    if (ok && f.L < q_len && w == 0 && lane == 0) status_or(p.tm, HPA_STATUS_BAD_SEQLEN);
+    // Row of token j sees key i < lim_min + j, and with a window i < sinks or i >= start + j.
+    // Pages [clear0, clear1) of the map hold no key that some row does not see.
+    const int lim_min = f.L - q_len + 1;
+    WinSpan win = {};
+    int clear0 = 0, clear1 = lim_min / PAGE;
+    if (WIN && f.pg0 < f.pg1) {
+      win = WinSpan::make(f.L, q_len, head.window, head.sinks);
+      const int first = win.start + q_len - 1;  // where the last row's window starts
+      clear0 = first > 0 ? (first - 1) / PAGE + 1 - win.hidden : 0;
+      clear1 = lim_min / PAGE - win.hidden;
+    }
+
+    // Query rows as the B operand: lane (g, c) holds dims [32 c, 32 c + 32) of rows 8 nt + g,
+    // scaled by 2^e of the row; sl holds what takes the scores of its columns to log2 units.
+    uint32_t qf[NT][8][2];
+    float sl[2 * NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = 8 * nt + g;
+      const uint32_t qa = base + S::kQ + slot * S::kQSlot + row * kQRowBytes + c * 64;
+      uint4 raw[4];
+      float am = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < rows) lds128(qa + 16 * i, raw[i].x, raw[i].y, raw[i].z, raw[i].w);
+        am = fmaxf(am, absmax8_bf16(raw[i]));
+      }
+      am = fmaxf(am, __shfl_xor_sync(kFull, am, 1));
+      am = fmaxf(am, __shfl_xor_sync(kFull, am, 2));
+      const int e = f16_row_exponent(am);
+      const float up = exp2i(e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u)  // elements 8 i + 2 u, + 1: k-step 2 i + u / 2, register u % 2
+          qf[nt][2 * i + (u >> 1)][u & 1] = pack_f16(__uint_as_float(x[u] << 16) * up,
+                                                     __uint_as_float(x[u] & 0xffff0000u) * up);
+      }
+      const float down = sl2 * exp2i(-e);
+      sl[2 * nt] = __shfl_sync(kFull, down, 8 * c);
+      sl[2 * nt + 1] = __shfl_sync(kFull, down, 8 * c + 4);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(qempty0 + 8 * slot);  // the slot may be refilled
+
+    float m[2 * NT], l[2 * NT], o[NT][8][4];
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) m[i] = -CUDART_INF_F, l[i] = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][t][e] = 0.f;
+
+    // One page of this warp; EDGE looks for keys that some row does not see.
+    auto page = [&](int pg, int stage, uint32_t phase, auto edge_tag) {
+      constexpr bool EDGE = decltype(edge_tag)::value;
+      const bool got = !(*abort_flag) && mbar_wait_bounded(full0 + 8 * stage, phase);
+      if (!__all_sync(kFull, got)) {
+        ok = false;
+        return;
+      }
+      const uint32_t kt = base + stage * kStageBytes, vt = kt + kUnit;
+      const int key0 = (WIN ? win.real_page(pg) : pg) * PAGE;
+
+      // S = K Q^T, 16 keys at a time
+      float x[4][NT][4];
+#pragma unroll
+      for (int kg = 0; kg < 4; ++kg) {
+        uint32_t kw[2][4], sc[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {  // keys key_at(g) and key_at(g) + 8 of the group
+          lds128(kt + k_off + (16 * kg + 8 * u) * 64, kw[u][0], kw[u][1], kw[u][2], kw[u][3]);
+          const uint32_t two = e4m3x2_to_f16x2(
+              static_cast<uint16_t>(lds_u16(kt + ks_off + (16 * kg + 8 * u) * 8)));
+          sc[u][0] = __byte_perm(two, 0u, 0x1010);
+          sc[u][1] = __byte_perm(two, 0u, 0x3232);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[kg][nt][e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // a word: 8 dims, two k-steps
+          uint32_t a[2][4];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            widen8(kw[u][i], a[u]);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) a[u][b] = mul_f16x2(a[u][b], sc[u][i >> 1]);
+          }
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            const uint32_t af[4] = {a[0][2 * st], a[1][2 * st], a[0][2 * st + 1], a[1][2 * st + 1]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(x[kg][nt], af, qf[nt][2 * i + st][0], qf[nt][2 * i + st][1]);
+          }
+        }
+      }
+      // to log2 units, and what a row does not see to -inf
+#pragma unroll
+      for (int kg = 0; kg < 4; ++kg)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v = x[kg][nt][e] * sl[2 * nt + (e & 1)];
+            if (EDGE) {
+              const int key = key0 + 16 * kg + key_at(g) + 8 * (e >> 1), j = tok[2 * nt + (e & 1)];
+              bool see = key < lim_min + j;
+              if (WIN) see = see && (key < head.sinks || key >= win.start + j);
+              v = see ? v : -CUDART_INF_F;
+            }
+            x[kg][nt][e] = v;
+          }
+      // running maximum: moves when a score passes it by more than the slack
+      bool over = false;
+      float top[2 * NT];
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i) {
+        top[i] = fmaxf(x[0][i >> 1][i & 1], x[0][i >> 1][2 + (i & 1)]);
+#pragma unroll
+        for (int kg = 1; kg < 4; ++kg)
+          top[i] = fmaxf(top[i], fmaxf(x[kg][i >> 1][i & 1], x[kg][i >> 1][2 + (i & 1)]));
+        over |= top[i] > m[i] + kRescaleSlack;
+      }
+      if (__any_sync(kFull, over)) {
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(kFull, top[i], d));
+          const float mn = top[i] > m[i] + kRescaleSlack ? top[i] : m[i];
+          const float a = mn == -CUDART_INF_F ? 1.f : exp2f(m[i] - mn);
+          m[i] = mn;
+          l[i] *= a;
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            o[i >> 1][t][i & 1] *= a;
+            o[i >> 1][t][2 + (i & 1)] *= a;
+          }
+        }
+      }
+      // probabilities; their sums in fp32 before the rounding to f16
+      uint32_t pb[4][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float b0 = m[2 * nt] == -CUDART_INF_F ? 0.f : m[2 * nt];
+        const float b1 = m[2 * nt + 1] == -CUDART_INF_F ? 0.f : m[2 * nt + 1];
+#pragma unroll
+        for (int kg = 0; kg < 4; ++kg) {
+          const float p0 = exp2f(x[kg][nt][0] - b0), p1 = exp2f(x[kg][nt][1] - b1);
+          const float p2 = exp2f(x[kg][nt][2] - b0), p3 = exp2f(x[kg][nt][3] - b1);
+          l[2 * nt] += p0 + p2;
+          l[2 * nt + 1] += p1 + p3;
+          pb[kg][nt][0] = transpose8(pack_f16(p0, p1));
+          pb[kg][nt][1] = transpose8(pack_f16(p2, p3));
+        }
+      }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int kg = 0; kg < 4; ++kg) {
+        const int kb = 16 * kg;
+        const uint2 v0 = lds64(vt + (kb + vk0) * 64 + 8 * g), v1 = lds64(vt + (kb + vk1) * 64 + 8 * g);
+        const uint2 v2 = lds64(vt + (kb + 8 + vk0) * 64 + 8 * g);
+        const uint2 v3 = lds64(vt + (kb + 8 + vk1) * 64 + 8 * g);
+        const uint32_t sb = vt + 4096 + g;
+        uint32_t b0 = lds_u8(sb + (kb + vk0) * 8), b1 = lds_u8(sb + (kb + vk1) * 8);
+        uint32_t b2 = lds_u8(sb + (kb + 8 + vk0) * 8), b3 = lds_u8(sb + (kb + 8 + vk1) * 8);
+        const int keys[4] = {key0 + kb + vk0, key0 + kb + vk1, key0 + kb + 8 + vk0,
+                             key0 + kb + 8 + vk1};
+        auto scales = [](uint32_t lo, uint32_t hi) {
+          return e4m3x2_to_f16x2(static_cast<uint16_t>(lo | (hi << 8)));
+        };
+        auto sees = [&](int key, int j) {
+          return key < lim_min + j && (!WIN || key < head.sinks || key >= win.start + j);
+        };
+        if (EDGE) {
+          auto hide = [&](int key, uint32_t b) {  // seen by no token: the scale is taken as zero
+            return key >= f.L || (WIN && key >= head.sinks && key < win.low) ? 0u : b;
+          };
+          b0 = hide(keys[0], b0), b1 = hide(keys[1], b1);
+          b2 = hide(keys[2], b2), b3 = hide(keys[3], b3);
+          if (q_len > 1) {
+            auto odd_one = [&](int key, uint32_t b) {  // a NaN that only some tokens see
+              return e4m3_nan(b) && !(sees(key, 0) && sees(key, q_len - 1));
+            };
+            if (__any_sync(kFull, odd_one(keys[0], b0) || odd_one(keys[1], b1) ||
+                                      odd_one(keys[2], b2) || odd_one(keys[3], b3))) {
+              // 0 * NaN would reach every row: a pass for each token, kept by its rows alone
+#pragma unroll 1
+              for (int j = 0; j < q_len; ++j) {
+                uint32_t a0[2][4], a1[2][4], a2[2][4], a3[2][4];
+                const uint32_t s01 = scales(sees(keys[0], j) ? b0 : 0u, sees(keys[1], j) ? b1 : 0u);
+                const uint32_t s23 = scales(sees(keys[2], j) ? b2 : 0u, sees(keys[3], j) ? b3 : 0u);
+                v_pairs(v0.x, v1.x, s01, a0[0], a1[0]);
+                v_pairs(v0.y, v1.y, s01, a0[1], a1[1]);
+                v_pairs(v2.x, v3.x, s23, a2[0], a3[0]);
+                v_pairs(v2.y, v3.y, s23, a2[1], a3[1]);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                  const uint32_t af[4] = {a0[t >> 2][t & 3], a1[t >> 2][t & 3], a2[t >> 2][t & 3],
+                                          a3[t >> 2][t & 3]};
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_f16(part, af, pb[kg][nt][0], pb[kg][nt][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                      if (tok[2 * nt + (e & 1)] == j) o[nt][t][e] += part[e];
+                  }
+                }
+              }
+              continue;
+            }
+          }
+        }
+        const uint32_t s01 = scales(b0, b1), s23 = scales(b2, b3);
+#pragma unroll
+        for (int hw = 0; hw < 2; ++hw) {
+          uint32_t a0[4], a1[4], a2[4], a3[4];
+          v_pairs(hw ? v0.y : v0.x, hw ? v1.y : v1.x, s01, a0, a1);
+          v_pairs(hw ? v2.y : v2.x, hw ? v3.y : v3.x, s23, a2, a3);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t af[4] = {a0[t], a1[t], a2[t], a3[t]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(o[nt][4 * hw + t], af, pb[kg][nt][0], pb[kg][nt][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty0 + 8 * stage);
+    };
+    // this warp's pages of the segment: page n of the CTA with n % kWarps == w
+    const int skip = (w - count) & (kWarps - 1), n_pages = f.pg1 - f.pg0;
+    for (int i = skip; i < n_pages && ok; i += kWarps) {
+      const int n = count + i, stage = n % kStages, pg = f.pg0 + i;
+      const uint32_t phase = (n / kStages) & 1;
+      if (pg >= clear0 && pg < clear1) page(pg, stage, phase, std::false_type());
+      else page(pg, stage, phase, std::true_type());
+    }
+    count += n_pages;
+    // A warp that gave up flags the map and raises the CTA's abort flag; it still takes part
+    // in the named barriers below.  Later waits see the flag and fail at once.
+    if (!ok && lane == 0) {
+      status_or(p.tm, HPA_STATUS_TIMEOUT);
+      *abort_flag = 1;
+    }
+
+    // ---- segment end: merge the four warps' (m, l, O) and store the partial
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[i] += __shfl_xor_sync(kFull, l[i], d);
+      const int row = 8 * (i >> 1) + 2 * c + (i & 1);
+      if (g == 0) {
+        sm_m[w * S::kRows + row] = m[i];
+        sm_l[w * S::kRows + row] = l[i];
+      }
+    }
+    named_barrier(1, kWarps * 32);
+    auto row_stats = [&](int row, float &M, float &Lsum) {
+      M = -CUDART_INF_F;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) M = fmaxf(M, sm_m[v * S::kRows + row]);
+      M = M == -CUDART_INF_F ? 0.f : M;
+      Lsum = 0.f;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v)
+        Lsum += sm_l[v * S::kRows + row] * exp2f(sm_m[v * S::kRows + row] - M);
+    };
+    float fs[2 * NT];
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) {
+      float M, Lsum;
+      row_stats(8 * (i >> 1) + 2 * c + (i & 1), M, Lsum);
+      fs[i] = Lsum == 0.f ? 0.f : exp2f(m[i] - M) / Lsum * vsc;
+    }
+    float *mine = mbuf + (w & 1) * (S::kRows * kMergeStride);
+    auto merge = [&](auto add_tag) {  // warps 0 / 1 store, then warps 2 / 3 add
+      constexpr bool ADD = decltype(add_tag)::value;
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i) {
+        const int row = 8 * (i >> 1) + 2 * c + (i & 1);
+        float4 *d = reinterpret_cast<float4 *>(mine + row * kMergeStride + 16 * g);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float(&oa)[4] = o[i >> 1][2 * t], (&ob)[4] = o[i >> 1][2 * t + 1];
+          const int e = i & 1;
+          float4 nv = make_float4(oa[e] * fs[i], oa[2 + e] * fs[i], ob[e] * fs[i], ob[2 + e] * fs[i]);
+          if (ADD) {
+            const float4 old = d[t];
+            nv.x += old.x, nv.y += old.y, nv.z += old.z, nv.w += old.w;
+          }
+          d[t] = nv;
+        }
+      }
+    };
+    if (w < 2) merge(std::false_type());
+    named_barrier(1, kWarps * 32);
+    if (w >= 2) merge(std::true_type());
+    named_barrier(1, kWarps * 32);
+    const int tid = threadIdx.x;
+    for (int v = tid; v < rows * (HEAD_DIM / 4); v += kWarps * 32) {
+      const int row = v / (HEAD_DIM / 4), c4 = v % (HEAD_DIM / 4);
+      const int j = (rb + row) / G, gq = (rb + row) % G;
+      const int64_t dst = (static_cast<int64_t>(s) * q_len + j) * p.Hq + h * G + gq;
+      const float4 a = reinterpret_cast<const float4 *>(mbuf + row * kMergeStride)[c4];
+      const float4 b = reinterpret_cast<const float4 *>(mbuf + (S::kRows + row) * kMergeStride)[c4];
+      reinterpret_cast<float4 *>(p.partial_o + dst * HEAD_DIM)[c4] =
+          make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+    }
+    if (tid < rows) {
+      float M, Lsum;
+      row_stats(tid, M, Lsum);
+      const int j = (rb + tid) / G, gq = (rb + tid) % G;
+      // a row that sees a NaN has no sum: +inf, beside which no other partial counts, makes the
+      // combine's result NaN (it passes over -inf and NaN)
+      p.partial_lse[(static_cast<int64_t>(s) * q_len + j) * p.Hq + h * G + gq] =
+          Lsum == 0.f ? -CUDART_INF_F
+          : Lsum > 0.f ? (M + log2f(Lsum)) * 0.69314718055994531f
+                       : CUDART_INF_F;
+    }
+    named_barrier(1, kWarps * 32);
+  }
+}
+
+template <int NT, bool WIN>
+__global__ void __launch_bounds__(kThreads, 2)
+    decode_attn_e2m1_kernel(const uint8_t *__restrict__ k_pool, const uint8_t *__restrict__ v_pool,
+                            const AttnParams p) {
+  using S = Smem<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+  __shared__ MapHead head;
+  const int c = blockIdx.x;
+  const uint32_t base = smem_u32(smem);
+  if (threadIdx.x == 0) {
+    for (int st = 0; st < kStages; ++st) {
+      mbar_init(base + S::kBars + 8 * st, 1);
+      mbar_init(base + S::kBars + 8 * (kStages + st), 1);
+    }
+    for (int sl = 0; sl < 2; ++sl) {
+      mbar_init(base + S::kBars + 8 * (2 * kStages + sl), 32);           // qfull
+      mbar_init(base + S::kBars + 8 * (2 * kStages + 2 + sl), kWarps);   // qempty
+    }
+    *reinterpret_cast<int *>(smem + S::kFlag) = 0;
+    fence_barrier_init();
+  }
+  // Nothing above reads memory that an earlier kernel writes: the prologue overlaps it.
+  pdl_wait();
+  if (threadIdx.x == 0) {
+    MapHead m = read_map_head(p.tm, p.lay, p.B, p.C, c, p.q_len, WIN, c == 0 && blockIdx.y == 0);
+    if (!WIN && m.windowed) {  // a map of hpa_plan_window belongs to hpa_decode_attn_window
+      status_or(p.tm, HPA_STATUS_BAD_MAP);
+      m.go = 0;
+    }
+    head = m;
+  }
+  __syncthreads();
+  pdl_launch_dependents();  // the combine kernel may be scheduled; it waits for this grid
+  if (!head.go) return;     // bad map, or a partition with no tiles
+  const MapHead m = head;
+  if (threadIdx.x >= kWarps * 32) producer<NT, WIN>(p, k_pool, v_pool, smem, m);
+  else consumer<NT, WIN>(p, smem, m);
+}
+
+template <int NT, bool WIN>
+cudaError_t configure() {
+  static int configured[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && configured[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(decode_attn_e2m1_kernel<NT, WIN>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<NT>::kAlloc);
+  if (e == cudaSuccess && dev < 64) configured[dev] = 1;
+  return e;
+}
+
+template <int NT, bool WIN>
+cudaError_t launch(const AttnParams &p, const void *k_pool, const void *v_pool, cudaStream_t s) {
+  cudaError_t e = configure<NT, WIN>();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.C, p.Hkv, (p.rows + p.group - 1) / p.group);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Smem<NT>::kAlloc;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_attn_e2m1_kernel<NT, WIN>,
+                            static_cast<const uint8_t *>(k_pool),
+                            static_cast<const uint8_t *>(v_pool), p);
+}
+
+template <int NT>
+int occupancy(int *ctas) {
+  if (configure<NT, false>() != cudaSuccess) return -1;
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, decode_attn_e2m1_kernel<NT, false>,
+                                                       kThreads, Smem<NT>::kAlloc) == cudaSuccess
+             ? 0
+             : -1;
+}
+
+}  // namespace
+
+// Query rows of a KV head in groups of equal size, up to 16: CTAs that share pages keep pace and
+// find them in L2.
+int attn_e2m1_group(int rows) {
+  const int groups = (rows + MAX_ROWS - 1) / MAX_ROWS;
+  return (rows + groups - 1) / groups;
+}
+
+cudaError_t launch_decode_attn_e2m1(const AttnParams &p, const void *k_pool, const void *v_pool,
+                                    cudaStream_t s) {
+  if (p.group <= 8)
+    return p.window ? launch<1, true>(p, k_pool, v_pool, s) : launch<1, false>(p, k_pool, v_pool, s);
+  return p.window ? launch<2, true>(p, k_pool, v_pool, s) : launch<2, false>(p, k_pool, v_pool, s);
+}
+
+int attn_e2m1_ctas_per_sm(int rows, int *ctas) {
+  return attn_e2m1_group(rows) <= 8 ? occupancy<1>(ctas) : occupancy<2>(ctas);
+}
+
+}  // namespace hpa

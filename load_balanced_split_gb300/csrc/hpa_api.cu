@@ -226,8 +226,10 @@ static int decode_attn_impl(const void *q_dev, const void *k_pool_dev, const voi
   if (!q_dev || !k_pool_dev || !v_pool_dev || !page_indptr_dev || !page_indices_dev ||
       !taskmap_dev || !partial_o_dev || !partial_lse_dev)
     return HPA_ERR_INVALID;
-  if (kv_dtype != HPA_KV_BF16 && kv_dtype != HPA_KV_E4M3) return HPA_ERR_INVALID;
-  if (kv_dtype == HPA_KV_E4M3 && (!k_scale_dev || !v_scale_dev)) return HPA_ERR_INVALID;
+  const bool e2m1 = kv_dtype == HPA_KV_E2M1;
+  if (kv_dtype != HPA_KV_BF16 && kv_dtype != HPA_KV_E4M3 && !e2m1) return HPA_ERR_INVALID;
+  if (kv_dtype != HPA_KV_BF16 && (!k_scale_dev || !v_scale_dev)) return HPA_ERR_INVALID;
+  if (e2m1 && (tc || all_heads || trace_dev || out_dev)) return HPA_ERR_UNSUPPORTED;
   if (B < 1 || B > kMaxB || num_ctas < 1 || num_ctas > kMaxC || q_len < 1 || Hq < 1 ||
       Hkv < 1 || Hkv > 65535 || num_pages < 1 || !std::isfinite(sm_scale))
     return HPA_ERR_INVALID;
@@ -239,9 +241,11 @@ static int decode_attn_impl(const void *q_dev, const void *k_pool_dev, const voi
       !aligned(taskmap_dev, 16) || !aligned(partial_o_dev, 16) || !aligned(partial_lse_dev, 4))
     return HPA_ERR_ALIGN;
   CUtensorMap tmk, tmv;
-  int rc = pool_map(k_pool_dev, num_pages, Hkv, kv_dtype, &tmk);
-  if (rc == HPA_OK) rc = pool_map(v_pool_dev, num_pages, Hkv, kv_dtype, &tmv);
-  if (rc != HPA_OK) return rc;
+  if (!e2m1) {  // 4-bit pages are whole blocks of memory and need no tensor map
+    int rc = pool_map(k_pool_dev, num_pages, Hkv, kv_dtype, &tmk);
+    if (rc == HPA_OK) rc = pool_map(v_pool_dev, num_pages, Hkv, kv_dtype, &tmv);
+    if (rc != HPA_OK) return rc;
+  }
   hpa::AttnParams p;
   p.q = static_cast<const __nv_bfloat16 *>(q_dev);
   p.tm = static_cast<int32_t *>(taskmap_dev);
@@ -265,13 +269,17 @@ static int decode_attn_impl(const void *q_dev, const void *k_pool_dev, const voi
   p.G = Hq / Hkv;
   p.rows = p.G * q_len;
   const int groups = (p.rows + hpa::MAX_ROWS - 1) / hpa::MAX_ROWS;
-  p.group = window ? (p.rows + groups - 1) / groups : hpa::MAX_ROWS;
+  p.group = e2m1     ? hpa::attn_e2m1_group(p.rows)
+            : window ? (p.rows + groups - 1) / groups
+                     : hpa::MAX_ROWS;
   p.heads_per_cta = all_heads ? Hkv : 1;
   p.window = window;
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   cudaError_t e =
-      tc ? hpa::launch_decode_attn_tc(p, tmk, tmv, kv_dtype, reinterpret_cast<cudaStream_t>(stream))
-         : hpa::launch_decode_attn(p, tmk, tmv, kv_dtype, reinterpret_cast<cudaStream_t>(stream));
+      e2m1 ? hpa::launch_decode_attn_e2m1(p, k_pool_dev, v_pool_dev,
+                                          reinterpret_cast<cudaStream_t>(stream))
+      : tc ? hpa::launch_decode_attn_tc(p, tmk, tmv, kv_dtype, reinterpret_cast<cudaStream_t>(stream))
+           : hpa::launch_decode_attn(p, tmk, tmv, kv_dtype, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? HPA_OK : cuda_fail(e);
 }
 
@@ -313,6 +321,7 @@ int hpa_decode_attn_mma(const void *q_dev, const void *k_pool_dev, const void *v
                         int32_t q_len, int32_t Hq, int32_t Hkv, int32_t d, float sm_scale,
                         void *taskmap_dev, int32_t num_ctas, float *partial_o_dev,
                         float *partial_lse_dev, hpa_stream_t stream) {
+  if (kv_dtype == HPA_KV_E2M1) return HPA_ERR_UNSUPPORTED;  // a kernel of the wider types
   return decode_attn_impl(q_dev, k_pool_dev, v_pool_dev, kv_dtype, k_scale_dev, v_scale_dev,
                           num_pages, page_indptr_dev, page_indices_dev, page_size, B, q_len, Hq,
                           Hkv, d, sm_scale, taskmap_dev, num_ctas, partial_o_dev,
@@ -333,14 +342,35 @@ int hpa_decode_attn_window(const void *q_dev, const void *k_pool_dev, const void
                           false, true);
 }
 
-int32_t hpa_default_num_ctas_window(int32_t Hq, int32_t Hkv, int32_t q_len, int32_t kv_dtype) {
-  return hpa_default_num_ctas_mma(Hq, Hkv, q_len, kv_dtype);
-}
-
 // More than 16 query rows per KV head (MTP with several draft tokens) go to the
 // tcgen05 kernel, which takes all rows in one pass over the keys.
-static bool routes_to_tc(int32_t Hq, int32_t Hkv, int32_t q_len) {
-  return Hkv >= 1 && Hq % Hkv == 0 && int64_t(Hq / Hkv) * q_len > hpa::MAX_ROWS;
+// (4-bit pages have one kernel, in groups of up to 16 rows.)
+static bool routes_to_tc(int32_t Hq, int32_t Hkv, int32_t q_len, int32_t kv_dtype) {
+  return kv_dtype != HPA_KV_E2M1 && Hkv >= 1 && Hq % Hkv == 0 &&
+         int64_t(Hq / Hkv) * q_len > hpa::MAX_ROWS;
+}
+
+// Partitions per KV head that fill the device once with the kernel of 4-bit pages.
+static int32_t default_num_ctas_e2m1(int32_t Hq, int32_t Hkv, int32_t q_len) {
+  if (Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || q_len < 1 ||
+      int64_t(Hq / Hkv) * q_len > hpa::MAX_ROWS_TOTAL)
+    return -1;
+  int dev = 0, sms = 0, per_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) {
+    cuda_fail(e);
+    return -1;
+  }
+  const int rows = (Hq / Hkv) * q_len, group = hpa::attn_e2m1_group(rows);
+  if (hpa::attn_e2m1_ctas_per_sm(rows, &per_sm) != 0 || per_sm < 1) return -1;
+  const int c = sms * per_sm / (Hkv * ((rows + group - 1) / group));
+  return c < 1 ? 1 : c;
+}
+
+int32_t hpa_default_num_ctas_window(int32_t Hq, int32_t Hkv, int32_t q_len, int32_t kv_dtype) {
+  if (kv_dtype == HPA_KV_E2M1) return default_num_ctas_e2m1(Hq, Hkv, q_len);
+  return hpa_default_num_ctas_mma(Hq, Hkv, q_len, kv_dtype);
 }
 
 int hpa_decode_attn(const void *q_dev, const void *k_pool_dev, const void *v_pool_dev,
@@ -354,12 +384,14 @@ int hpa_decode_attn(const void *q_dev, const void *k_pool_dev, const void *v_poo
                           num_pages, page_indptr_dev, page_indices_dev, page_size, B, q_len, Hq,
                           Hkv, d, sm_scale, taskmap_dev, num_ctas, partial_o_dev,
                           partial_lse_dev, nullptr, nullptr, nullptr, nullptr, stream,
-                          routes_to_tc(Hq, Hkv, q_len));
+                          routes_to_tc(Hq, Hkv, q_len, kv_dtype));
 }
 
 int32_t hpa_default_num_ctas(int32_t Hq, int32_t Hkv, int32_t q_len, int32_t kv_dtype) {
-  return routes_to_tc(Hq, Hkv, q_len) ? hpa_default_num_ctas_tc(Hq, Hkv, q_len, kv_dtype)
-                                      : hpa_default_num_ctas_mma(Hq, Hkv, q_len, kv_dtype);
+  if (kv_dtype == HPA_KV_E2M1) return default_num_ctas_e2m1(Hq, Hkv, q_len);
+  return routes_to_tc(Hq, Hkv, q_len, kv_dtype)
+             ? hpa_default_num_ctas_tc(Hq, Hkv, q_len, kv_dtype)
+             : hpa_default_num_ctas_mma(Hq, Hkv, q_len, kv_dtype);
 }
 
 int hpa_decode_attn_traced(const void *q_dev, const void *k_pool_dev, const void *v_pool_dev,
@@ -375,7 +407,7 @@ int hpa_decode_attn_traced(const void *q_dev, const void *k_pool_dev, const void
                           num_pages, page_indptr_dev, page_indices_dev, page_size, B, q_len, Hq,
                           Hkv, d, sm_scale, taskmap_dev, num_ctas, partial_o_dev,
                           partial_lse_dev, trace_dev, nullptr, nullptr, nullptr, stream,
-                          routes_to_tc(Hq, Hkv, q_len));
+                          routes_to_tc(Hq, Hkv, q_len, kv_dtype));
 }
 
 int hpa_decode_attn_allheads(const void *q_dev, const void *k_pool_dev, const void *v_pool_dev,

@@ -39,6 +39,11 @@ struct TaskMapLayout {
 constexpr int PAGE = 64;       // tokens per KV page
 constexpr int HEAD_DIM = 128;  // d
 constexpr int MAX_ROWS = 16;   // query rows per CTA (one m16 MMA tile)
+// One page and KV head of a 4-bit pool: 64 rows of 64 bytes of E2M1 codes, then 64 x 8 E4M3
+// scales, one for each 16 elements.
+constexpr int E2M1_BLOCK = 16;
+constexpr int E2M1_UNIT = PAGE * HEAD_DIM / 2 + PAGE * HEAD_DIM / E2M1_BLOCK;
+static_assert(E2M1_UNIT == HPA_E2M1_PAGE_BYTES, "as the header states");
 constexpr int MAX_ROWS_TOTAL = 64;  // G * q_len rows per KV head, in groups of up to 16
 
 // The pages of one request that a sliding window of `window` keys with `sinks` first
@@ -107,6 +112,10 @@ int attn_ctas_per_sm(int kv_dtype, int q_len, int *ctas);  // occupancy query (h
 cudaError_t launch_decode_attn_tc(const AttnParams &p, const CUtensorMap &tmk,
                                   const CUtensorMap &tmv, int kv_dtype, cudaStream_t s);
 int attn_tc_ctas_per_sm(int kv_dtype, int rows, int *ctas);  // occupancy query (host)
+cudaError_t launch_decode_attn_e2m1(const AttnParams &p, const void *k_pool, const void *v_pool,
+                                    cudaStream_t s);
+int attn_e2m1_group(int rows);                         // query rows per CTA
+int attn_e2m1_ctas_per_sm(int rows, int *ctas);        // occupancy query (host)
 cudaError_t launch_selftest_wait(int32_t *status, long long limit_ns, cudaStream_t s);
 
 struct KeyWeightsParams {

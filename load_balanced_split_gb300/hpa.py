@@ -17,7 +17,8 @@ import torch
 
 from . import build as _build
 
-KV_BF16, KV_E4M3 = 0, 1
+KV_BF16, KV_E4M3, KV_E2M1 = 0, 1, 2
+E2M1_PAGE_BYTES = 4608   # one page and KV head of a 4-bit pool: 64 x 64 of codes, 64 x 8 scales
 STATUS_BITS = {1: "BAD_SEQLEN", 2: "MISMATCH", 4: "BAD_PAGE", 8: "TIMEOUT", 16: "OVERFLOW",
                32: "BAD_MAP", 64: "BAD_BUDGET"}
 HEADER_WORDS = 16
@@ -226,15 +227,21 @@ def hpa_plan_window(seq_lens, q_len: int, window: int, sinks: int, tile: int, nu
            "hpa_plan_window")
 
 
+def _is_e2m1(pool):
+    """Whether a pool is one of 4-bit pages, uint8 [P][Hkv][E2M1_PAGE_BYTES]."""
+    return pool.dim() == 3 and pool.dtype is torch.uint8 and pool.shape[2] == E2M1_PAGE_BYTES
+
+
 def _attn_args(q, k_pool, v_pool, page_indptr, page_indices, taskmap, k_scale, v_scale):
     """Checks shared by every attention call; returns (kv, B, q_len, Hq, d, P, Hkv, page)."""
     _dev(q, "q", torch.bfloat16)
     _dev(k_pool, "k_pool")
     _dev(v_pool, "v_pool")
+    e2m1 = _is_e2m1(k_pool)
     if k_pool.dtype == torch.bfloat16:
         kv = KV_BF16
     elif k_pool.dtype in (torch.uint8, torch.float8_e4m3fn):
-        kv = KV_E4M3
+        kv = KV_E2M1 if e2m1 else KV_E4M3
         _dev(k_scale, "k_scale", torch.float32)
         _dev(v_scale, "v_scale", torch.float32)
     else:
@@ -244,15 +251,18 @@ def _attn_args(q, k_pool, v_pool, page_indptr, page_indices, taskmap, k_scale, v
     for t, n in ((page_indptr, "page_indptr"), (page_indices, "page_indices")):
         _dev(t, n, torch.int32)
     _dev(taskmap, "taskmap")
-    if q.dim() != 4 or k_pool.dim() != 4:
-        raise HpaError("q must be [B][q_len][Hq][d] and the pools [P][Hkv][page][d]")
+    if q.dim() != 4 or (k_pool.dim() != 4 and not e2m1):
+        raise HpaError("q must be [B][q_len][Hq][d] and the pools [P][Hkv][page][d] "
+                       "(4-bit pools: uint8 [P][Hkv][%d])" % E2M1_PAGE_BYTES)
     B, q_len, Hq, d = q.shape
-    P, Hkv, page, d2 = k_pool.shape
+    P, Hkv, page, d2 = (*k_pool.shape[:2], 64, 128) if e2m1 else k_pool.shape
     if d2 != d:
         raise HpaError("head dim mismatch")
     if page_indptr.numel() < B + 1:
         raise HpaError("page_indptr must have B + 1 = %d entries" % (B + 1))
-    if kv == KV_E4M3 and (k_scale.numel() < Hkv or v_scale.numel() < Hkv):
+    if e2m1:
+        _one_device(q, k_pool, v_pool, page_indptr, page_indices, taskmap, k_scale, v_scale)
+    if kv != KV_BF16 and (k_scale.numel() < Hkv or v_scale.numel() < Hkv):
         raise HpaError("k_scale / v_scale need one fp32 value per KV head")
     return kv, B, q_len, Hq, d, P, Hkv, page
 
@@ -280,7 +290,8 @@ def hpa_decode_attn(q, k_pool, v_pool, page_indptr, page_indices, taskmap, num_c
                     partial_o, partial_lse, k_scale=None, v_scale=None,
                     sm_scale: float | None = None, stream=None, tc: bool = False,
                     mma: bool = False, window: bool = False):
-    """q bf16 [B][q_len][Hq][d]; k/v pools bf16 or uint8 (E4M3) [P][Hkv][page][d].
+    """q bf16 [B][q_len][Hq][d]; k/v pools bf16 or uint8 (E4M3) [P][Hkv][page][d], or 4-bit
+    (E2M1 with block scales) uint8 [P][Hkv][E2M1_PAGE_BYTES].
 
     hpa_decode_attn picks the kernel by query rows per KV head (mma.sync up to 16,
     tcgen05 above); tc=True calls hpa_decode_attn_tc, mma=True hpa_decode_attn_mma and
@@ -809,6 +820,8 @@ def decode_step(ws: Workspace, q, k_pool, v_pool, seq_lens, page_indptr, page_in
         raise HpaError("accumulating key weights needs out_lse")
     if acc is not None and allheads:
         raise HpaError("hpa_key_weights needs a map per KV head, which the all-heads one is not")
+    if acc is not None and _is_e2m1(k_pool):
+        raise HpaError("hpa_key_weights has no 4-bit form")
     stream = _stream(stream)
     if plan:
         ws.plan(seq_lens, tile, stream)

@@ -19,14 +19,17 @@ import math
 
 import numpy as np
 
-from . import scheduler
+from . import fourbit, scheduler
 
 PAGE = 64
 
 
 def pool_values(pool, kv_dtype, scale=None):
-    """fp64 values of a pool [P][Hkv][page][d] (torch tensor, bf16 or E4M3 codes)."""
+    """fp64 values of a pool [P][Hkv][page][d] (torch tensor, bf16 or E4M3 codes, or 4-bit
+    pages [P][Hkv][bytes])."""
     import torch
+    if kv_dtype == "e2m1":
+        return fourbit.values(pool.cpu().numpy(), scale)
     if kv_dtype == "bf16":
         return pool.cpu().to(torch.float64).numpy()
     x = pool.cpu().view(torch.float8_e4m3fn).to(torch.float64).numpy()
