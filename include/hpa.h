@@ -74,6 +74,7 @@ typedef struct CUstream_st *hpa_stream_t;
                                    out of bounds; the row was skipped, never followed */
 #define HPA_STATUS_BAD_BUDGET 64 /* hpa_evict_select: a budget below 1, below sinks + recent of a
                                     longer request, or beyond kept_stride */
+#define HPA_STATUS_NO_PAGES 128 /* hpa_assign_pages: a request asked for more pages than are free */
 
 /* ---- KV element types ---- */
 #define HPA_KV_BF16 0 /* bfloat16 */
@@ -534,6 +535,55 @@ int hpa_evict(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, float *acc_d
               int32_t sinks, int32_t recent, int32_t B, int32_t Hkv, int32_t d, int32_t *kept_dev,
               int64_t kept_stride, int32_t *new_lens_dev, int32_t *status_dev,
               hpa_stream_t stream);
+
+/*
+ * hpa_assign_pages -- page tables and slot maps from request lengths, on the device (the pages
+ * have no counterpart to it).  The state of a pool of num_pages pages:
+ *   table_dev       int32 [num_rows][table_stride]: the pages that each row (a session) holds,
+ *                   in order;
+ *   held            int32 [num_rows]: how many;
+ *   free_pages_dev  int32 [num_pages]: a stack of the pages that no row holds;
+ *   free_count      int32: its height.
+ * A page belongs to one row or to the stack, so one that several sessions share (a prefix) is
+ * not for this call.  One step, for the B requests of a batch in rows rows_dev[r] (NULL: row r):
+ *   n_r = ceil(L_r / page_size) pages from now on, for L_r = seq_lens_dev[r] >= 0 tokens, the
+ *   new ones included (0: the session has ended).  Pages past n_r go back on the stack, in the
+ *   order of the requests and of their pages; then missing ones come off it, request by request,
+ *   the top first.  A request that asks for more than is left after the requests before it
+ *   gets none and keeps what it holds, as does every later one that needs a page
+ *   (HPA_STATUS_NO_PAGES).
+ * held_in_dev and held_out_dev, free_count_in_dev and free_count_out_dev may each be one array
+ * (the usual, in place).  Where they differ, the state before the step stays whole -- entries
+ * of the table past a row's count and of the stack past its height mean nothing -- so that a
+ * step can be taken again from it with other lengths (draft tokens that were rejected).
+ * held_out is written for the rows of the batch alone.  Results:
+ *   page_indptr_dev [B+1], page_indices_dev [indices_cap]: the page lists of the batch, as the
+ *                   attention calls read them; entries past the last are left as they were;
+ *   with new_tokens_dev (int32 [B], 0 <= new_tokens[r] <= L_r, the last tokens of r; or NULL)
+ *   slots_dev (int64) and positions_dev (int32) [max_tokens]: for each of them, request by
+ *                   request, page * page_size + place in the page, and L_r - new_tokens[r] + j
+ *                   plus pos_offset_dev[r] (NULL: 0; the tokens that evictions removed).  A
+ *                   refused request's tokens have slot -1; behind the last token slots are -1
+ *                   and positions 0, so a captured step can be replayed with fewer tokens.
+ * status_dev (optional int32) gets bits, and the request in question keeps its pages:
+ * HPA_STATUS_BAD_SEQLEN (L_r < 0, new_tokens outside [0, L_r]), HPA_STATUS_OVERFLOW (n_r beyond
+ * table_stride; page lists beyond indices_cap or tokens beyond max_tokens, which are cut),
+ * HPA_STATUS_BAD_MAP (a row outside [0, num_rows), one that an earlier request of the batch
+ * lists, a count outside its range), HPA_STATUS_BAD_PAGE (a page id out of range in the state).
+ * workspace_dev: >= hpa_assign_pages_workspace(B, num_rows) bytes, 16-byte aligned; calls that
+ * may run at the same time need one each.  page_size == 64.  slots_dev 8-byte aligned.  The
+ * arrays written overlap neither each other nor those read.
+ */
+size_t hpa_assign_pages_workspace(int32_t B, int32_t num_rows);
+int hpa_assign_pages(const int32_t *seq_lens_dev, const int32_t *new_tokens_dev,
+                     const int32_t *rows_dev, const int32_t *pos_offset_dev, int32_t B,
+                     int32_t num_rows, int32_t *table_dev, int32_t table_stride,
+                     const int32_t *held_in_dev, int32_t *held_out_dev, int32_t *free_pages_dev,
+                     const int32_t *free_count_in_dev, int32_t *free_count_out_dev,
+                     int32_t num_pages, int32_t page_size, int32_t *page_indptr_dev,
+                     int32_t *page_indices_dev, int32_t indices_cap, int64_t *slots_dev,
+                     int32_t *positions_dev, int32_t max_tokens, void *workspace_dev,
+                     size_t workspace_bytes, int32_t *status_dev, hpa_stream_t stream);
 
 /*
  * hpa_selftest_wait_timeout -- diagnostic for the failure path of the

@@ -569,6 +569,99 @@ int hpa_store_kv_at(const void *k_new_dev, const void *v_new_dev, const int32_t 
                        status_dev, text_pos_dev, stream);
 }
 
+size_t hpa_assign_pages_workspace(int32_t B, int32_t num_rows) {
+  if (B < 1 || B > kMaxB || num_rows < 1) return 0;
+  return static_cast<size_t>(hpa::assign_workspace_words(B, num_rows)) * 4;
+}
+
+int hpa_assign_pages(const int32_t *seq_lens_dev, const int32_t *new_tokens_dev,
+                     const int32_t *rows_dev, const int32_t *pos_offset_dev, int32_t B,
+                     int32_t num_rows, int32_t *table_dev, int32_t table_stride,
+                     const int32_t *held_in_dev, int32_t *held_out_dev, int32_t *free_pages_dev,
+                     const int32_t *free_count_in_dev, int32_t *free_count_out_dev,
+                     int32_t num_pages, int32_t page_size, int32_t *page_indptr_dev,
+                     int32_t *page_indices_dev, int32_t indices_cap, int64_t *slots_dev,
+                     int32_t *positions_dev, int32_t max_tokens, void *workspace_dev,
+                     size_t workspace_bytes, int32_t *status_dev, hpa_stream_t stream) {
+  if (!seq_lens_dev || !table_dev || !held_in_dev || !held_out_dev || !free_pages_dev ||
+      !free_count_in_dev || !free_count_out_dev || !page_indptr_dev || !page_indices_dev ||
+      !workspace_dev)
+    return HPA_ERR_INVALID;
+  if (new_tokens_dev && (!slots_dev || !positions_dev)) return HPA_ERR_INVALID;
+  if (B < 1 || B > kMaxB || num_rows < 1 || table_stride < 1 || num_pages < 1 || indices_cap < 0 ||
+      (new_tokens_dev && max_tokens < 0))
+    return HPA_ERR_INVALID;
+  if (!rows_dev && B > num_rows) return HPA_ERR_INVALID;
+  if (page_size != hpa::PAGE) return HPA_ERR_UNSUPPORTED;
+  if (!aligned(workspace_dev, 16) || !aligned(slots_dev, 8)) return HPA_ERR_ALIGN;
+  for (const void *p : {static_cast<const void *>(seq_lens_dev), static_cast<const void *>(new_tokens_dev),
+                        static_cast<const void *>(rows_dev), static_cast<const void *>(pos_offset_dev),
+                        static_cast<const void *>(table_dev), static_cast<const void *>(held_in_dev),
+                        static_cast<const void *>(held_out_dev), static_cast<const void *>(free_pages_dev),
+                        static_cast<const void *>(free_count_in_dev),
+                        static_cast<const void *>(free_count_out_dev),
+                        static_cast<const void *>(page_indptr_dev),
+                        static_cast<const void *>(page_indices_dev),
+                        static_cast<const void *>(positions_dev), static_cast<const void *>(status_dev)})
+    if (!aligned(p, 4)) return HPA_ERR_ALIGN;
+  if (workspace_bytes < hpa_assign_pages_workspace(B, num_rows)) return HPA_ERR_WORKSPACE;
+  // the arrays that the call writes lie apart from each other and from what it reads; the state
+  // may be updated in place
+  struct Range {
+    const void *p;
+    uint64_t bytes;
+  };
+  const uint64_t b4 = 4ull * B;
+  const Range written[] = {{table_dev, 4ull * num_rows * table_stride},
+                           {free_pages_dev, 4ull * num_pages},
+                           {page_indptr_dev, b4 + 4},
+                           {page_indices_dev, 4ull * indices_cap},
+                           {new_tokens_dev ? slots_dev : nullptr, 8ull * max_tokens},
+                           {new_tokens_dev ? positions_dev : nullptr, 4ull * max_tokens},
+                           {held_out_dev, 4ull * num_rows},
+                           {free_count_out_dev, 4},
+                           {workspace_dev, workspace_bytes}};
+  const Range read[] = {{seq_lens_dev, b4}, {new_tokens_dev, b4}, {rows_dev, b4},
+                        {pos_offset_dev, b4}};
+  constexpr int kWritten = sizeof(written) / sizeof(written[0]);
+  for (int i = 0; i < kWritten; ++i) {
+    for (const Range &r : read)
+      if (overlap(written[i].p, written[i].bytes, r.p, r.bytes)) return HPA_ERR_INVALID;
+    for (int j = 0; j < i; ++j)
+      if (overlap(written[i].p, written[i].bytes, written[j].p, written[j].bytes))
+        return HPA_ERR_INVALID;
+    if (held_in_dev != held_out_dev || written[i].p != held_out_dev)
+      if (overlap(written[i].p, written[i].bytes, held_in_dev, 4ull * num_rows)) return HPA_ERR_INVALID;
+    if (free_count_in_dev != free_count_out_dev || written[i].p != free_count_out_dev)
+      if (overlap(written[i].p, written[i].bytes, free_count_in_dev, 4)) return HPA_ERR_INVALID;
+  }
+  hpa::AssignParams p;
+  p.seq_lens = seq_lens_dev;
+  p.new_tokens = new_tokens_dev;
+  p.rows = rows_dev;
+  p.pos_offset = pos_offset_dev;
+  p.B = B;
+  p.num_rows = num_rows;
+  p.table = table_dev;
+  p.stride = table_stride;
+  p.held_in = held_in_dev;
+  p.held_out = held_out_dev;
+  p.free_pages = free_pages_dev;
+  p.free_in = free_count_in_dev;
+  p.free_out = free_count_out_dev;
+  p.num_pages = num_pages;
+  p.page_indptr = page_indptr_dev;
+  p.page_indices = page_indices_dev;
+  p.indices_cap = indices_cap;
+  p.slots = slots_dev;
+  p.positions = positions_dev;
+  p.max_tokens = new_tokens_dev ? max_tokens : 0;
+  p.ws = static_cast<int32_t *>(workspace_dev);
+  p.status = status_dev;
+  cudaError_t e = hpa::launch_assign_pages(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HPA_OK : cuda_fail(e);
+}
+
 int hpa_key_weights(const void *q_dev, const float *lse_dev, const void *k_pool_dev,
                     int32_t kv_dtype, const float *k_scale_dev, int64_t num_pages,
                     const int32_t *page_indptr_dev, const int32_t *page_indices_dev,

@@ -177,6 +177,27 @@ struct StoreKvParams {
 };
 cudaError_t launch_store_kv(const StoreKvParams &p, cudaStream_t s);
 
+struct AssignParams {
+  const int32_t *seq_lens, *new_tokens, *rows, *pos_offset;  // the last three optional
+  int B, num_rows;
+  int32_t *table;  // [num_rows][stride]
+  int stride;
+  const int32_t *held_in;
+  int32_t *held_out, *free_pages;
+  const int32_t *free_in;
+  int32_t *free_out;
+  int num_pages;
+  int32_t *page_indptr, *page_indices;
+  int indices_cap;
+  int64_t *slots;
+  int32_t *positions;
+  int max_tokens;
+  int32_t *ws;
+  int32_t *status;
+};
+int64_t assign_workspace_words(int64_t B, int64_t num_rows);
+cudaError_t launch_assign_pages(const AssignParams &p, cudaStream_t s);
+
 // ----------------------------------------------------------------------------- PTX wrappers
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -20,7 +20,7 @@ from . import build as _build
 KV_BF16, KV_E4M3, KV_E2M1 = 0, 1, 2
 E2M1_PAGE_BYTES = 4608   # one page and KV head of a 4-bit pool: 64 x 64 of codes, 64 x 8 scales
 STATUS_BITS = {1: "BAD_SEQLEN", 2: "MISMATCH", 4: "BAD_PAGE", 8: "TIMEOUT", 16: "OVERFLOW",
-               32: "BAD_MAP", 64: "BAD_BUDGET"}
+               32: "BAD_MAP", 64: "BAD_BUDGET", 128: "NO_PAGES"}
 HEADER_WORDS = 16
 
 _lock = threading.Lock()
@@ -94,6 +94,9 @@ def lib():
                                        I32, P, P], ctypes.c_int),
                 "hpa_evict": ([P, P, I32, P, I64, P, P, P, P, P, I32, P, I32, I32, I32, I32, I32, P,
                                I64, P, P, P], ctypes.c_int),
+                "hpa_assign_pages_workspace": ([I32, I32], SZ),
+                "hpa_assign_pages": ([P, P, P, P, I32, I32, P, I32, P, P, P, P, P, I32, I32, P, P,
+                                      I32, P, P, I32, P, SZ, P, P], ctypes.c_int),
                 "hpa_error_string": ([ctypes.c_int], ctypes.c_char_p),
                 "hpa_last_cuda_error": ([], ctypes.c_int),
             }
@@ -734,6 +737,114 @@ def hpa_evict(acc, k_pool, v_pool, seq_lens, page_indptr, page_indices, budgets,
         _ptr(page_indices), _ptr(dst_indptr), _ptr(dst_indices), page, _ptr(budgets), sinks,
         recent, B, Hkv, d, _ptr(kept), kept.shape[2], _ptr(new_lens), _ptr(status),
         _stream(stream)), "hpa_evict")
+
+
+# ----------------------------------------------------------------------------- page tables
+def hpa_assign_pages_workspace(B: int, num_rows: int) -> int:
+    return int(lib().hpa_assign_pages_workspace(B, num_rows))
+
+
+def _i32(t, name, n=None):
+    _dev(t, name, torch.int32)
+    if n is not None and t.numel() != n:
+        raise HpaError("%s needs %d entries, got %d" % (name, n, t.numel()))
+    return t
+
+
+def hpa_assign_pages(seq_lens, new_tokens, table, held, free_pages, free_count, page_indptr,
+                     page_indices, slots, positions, workspace, rows=None, pos_offset=None,
+                     held_out=None, free_count_out=None, status=None, stream=None):
+    """One step of a paged cache's tables, on the device: the pages that seq_lens (int32 [B], 0
+    for an ended session) ask for are taken from the free stack or given back, and the batch's
+    page_indptr [B+1] and page_indices and the slots (int64) and positions (int32) of its
+    new_tokens (int32 [B], or None with slots and positions None) are written.
+
+    State: table int32 [num_rows][max pages], held int32 [num_rows], free_pages int32
+    [num_pages], free_count int32 [1]; updated in place, or held and free_count into held_out and
+    free_count_out.  rows (int32 [B]): the table row of each request, by default 0 .. B - 1."""
+    B = _i32(seq_lens, "seq_lens").numel()
+    _dev(table, "table", torch.int32)
+    if table.dim() != 2:
+        raise HpaError("table must be int32 [num_rows][max pages]")
+    num_rows, stride = table.shape
+    held_out = held if held_out is None else held_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    _i32(held, "held", num_rows)
+    _i32(held_out, "held_out", num_rows)
+    _i32(free_count, "free_count", 1)
+    _i32(free_count_out, "free_count_out", 1)
+    _i32(free_pages, "free_pages")
+    _i32(page_indptr, "page_indptr", B + 1)
+    _i32(page_indices, "page_indices")
+    if rows is not None:
+        _i32(rows, "rows", B)
+    elif B > num_rows:
+        raise HpaError("%d requests without rows in a table of %d rows" % (B, num_rows))
+    if pos_offset is not None:
+        _i32(pos_offset, "pos_offset", B)
+    if (new_tokens is None) != (slots is None) or (slots is None) != (positions is None):
+        raise HpaError("new_tokens, slots and positions go together")
+    tokens = 0
+    if new_tokens is not None:
+        _i32(new_tokens, "new_tokens", B)
+        _dev(slots, "slots", torch.int64)
+        tokens = slots.numel()
+        _i32(positions, "positions", tokens)
+    _dev(workspace, "workspace")
+    if status is not None:
+        _i32(status, "status")
+    _one_device(seq_lens, new_tokens, table, held, held_out, free_pages, free_count,
+                free_count_out, page_indptr, page_indices, slots, positions, workspace, rows,
+                pos_offset, status)
+    rc = lib().hpa_assign_pages(
+        _ptr(seq_lens), _ptr(new_tokens), _ptr(rows), _ptr(pos_offset), B, num_rows, _ptr(table),
+        stride, _ptr(held), _ptr(held_out), _ptr(free_pages), _ptr(free_count),
+        _ptr(free_count_out), free_pages.numel(), 64, _ptr(page_indptr), _ptr(page_indices),
+        page_indices.numel(), _ptr(slots), _ptr(positions), tokens, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+    if rc != 0:
+        _check(rc, "hpa_assign_pages")
+
+
+class PageTable:
+    """The page tables of a pool of num_pages pages and what hpa_assign_pages writes for a step.
+
+    num_rows sessions of up to max_pages pages each; steps of up to max_batch requests and
+    max_tokens new tokens.  After assign(...), page_indptr and page_indices are the batch's lists,
+    and slots and positions hold its new tokens (slot -1 behind the last); `status` gathers the
+    bits of steps that could not serve a request (HPA_STATUS_NO_PAGES and others)."""
+
+    def __init__(self, num_pages, num_rows, max_pages, max_batch=None, max_tokens=None,
+                 device="cuda"):
+        max_batch = num_rows if max_batch is None else max_batch
+        max_tokens = max_batch if max_tokens is None else max_tokens
+
+        def i32(*shape):
+            return torch.zeros(shape, dtype=torch.int32, device=device)
+        nbytes = hpa_assign_pages_workspace(max_batch, num_rows)
+        if nbytes == 0 or num_pages < 1 or max_pages < 1 or max_tokens < 0:
+            raise HpaError("page table sizes out of range")
+        self.table, self.held = i32(num_rows, max_pages), i32(num_rows)
+        # page 0 on top
+        self.free_pages = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.free_count = i32(1) + num_pages
+        self._indptr = i32(max_batch + 1)
+        self.page_indptr, self.page_indices = self._indptr, i32(num_pages)
+        self.slots = torch.full((max_tokens,), -1, dtype=torch.int64, device=device)
+        self.positions = i32(max_tokens)
+        self.workspace = i32((nbytes + 3) // 4)
+        self.status = i32(1)
+
+    def assign(self, seq_lens, new_tokens=None, rows=None, pos_offset=None, stream=None):
+        B = seq_lens.numel()
+        if B + 1 > self._indptr.numel():
+            raise HpaError("a batch of %d requests, and room for %d" % (B, self._indptr.numel() - 1))
+        self.page_indptr = self._indptr[:B + 1]
+        slots, positions = (None, None) if new_tokens is None else (self.slots, self.positions)
+        hpa_assign_pages(seq_lens, new_tokens, self.table, self.held, self.free_pages,
+                         self.free_count, self.page_indptr, self.page_indices, slots, positions,
+                         self.workspace, rows=rows, pos_offset=pos_offset, status=self.status,
+                         stream=stream)
 
 
 # ----------------------------------------------------------------------------- workspace helper
