@@ -537,6 +537,50 @@ int hpa_evict(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, float *acc_d
               hpa_stream_t stream);
 
 /*
+ * hpa_store_qkv -- queries and the cache from the projections of num_tokens tokens in one pass:
+ * RMSNorm of every query and key head, position rotation in the same pass, an optional
+ * transform, and the quantised paged store.  hpa_store_kv ("Hy3 Preview AI Infra 推理优化精读
+ * 笔记", §4.1) does the keys and values of [B][q_len] tokens; this call takes any list of tokens
+ * (prompt chunks, decode steps, both) by the slots and positions of hpa_assign_pages, does the
+ * queries too, and writes 4-bit caches.  Token t, head h, row x of d = 128 elements:
+ *   query, key: norm and rotation, the norm first, or last with HPA_QKV_NORM_AFTER (the order of
+ *           hpa_store_kv).  Norm: x / sqrt(mean(x^2) + eps) * w, w = q_norm or k_norm (fp32 [d],
+ *           NULL: no norm).  Rotation of the first rot_dim elements (0, 16, 32, 64 or 128):
+ *           pair i, (x_i, x_{i + rot_dim/2}) or with HPA_QKV_INTERLEAVED (x_2i, x_{2i+1}), turned
+ *           by cos_sin[positions[t]][i] (cosine) and [rot_dim/2 + i] (sine).  With
+ *           HPA_QKV_HADAMARD then the orthonormal Sylvester transform of order d, on queries and
+ *           keys alike, which leaves their products as they were;
+ *   query:  rounded to bf16 into q_out[t][h];
+ *   key, value: into place slots[t] % 64 of page slots[t] / 64 of the pools: bf16; E4M3 codes of
+ *           x / scale[h] (round to nearest even, saturating); or 4-bit: with y = x / scale[h], for
+ *           every 16 elements the block scale b = E4M3(max |y| / 6) and codes E2M1(y / b), both to
+ *           nearest even and saturating (codes 0 where b is 0; a NaN makes b NaN).
+ * All arithmetic is fp32; nothing is rounded between the steps.
+ * q_dev, k_dev, v_dev: bf16, token t's heads from t * stride elements on (so they may be parts
+ * of one packed projection), 16-byte aligned, strides multiples of 8.  q_out_dev likewise; it may
+ * be q_dev with its stride (in place).  q_dev NULL: no queries; k_dev and v_dev NULL: no cache
+ * (num_pages then only bounds the slots).  positions_dev int32, slots_dev int64 [num_tokens].
+ * cos_sin_dev: fp32 [max_pos][rot_dim], 16-byte aligned.
+ * A token of slot -1 is passed over, its q_out row left as it was (rows of a captured batch that
+ * hold no token, requests that got no pages); so is one of another slot outside the pool
+ * (HPA_STATUS_BAD_PAGE in status_dev, optional int32) or of a position outside [0, max_pos)
+ * (HPA_STATUS_BAD_SEQLEN).  Two tokens of one slot: which one its row holds, or parts of both,
+ * is unspecified.  d == 128, page_size == 64; num_tokens may be 0.
+ */
+#define HPA_QKV_NORM_AFTER 1
+#define HPA_QKV_INTERLEAVED 2
+#define HPA_QKV_HADAMARD 4
+int hpa_store_qkv(const void *q_dev, int64_t q_stride, const void *k_dev, int64_t k_stride,
+                  const void *v_dev, int64_t v_stride, int32_t num_tokens, int32_t Hq, int32_t Hkv,
+                  int32_t d, const int32_t *positions_dev, const int64_t *slots_dev,
+                  const float *cos_sin_dev, int32_t max_pos, int32_t rot_dim,
+                  const float *q_norm_dev, const float *k_norm_dev, float eps, int32_t flags,
+                  void *q_out_dev, int64_t q_out_stride, int32_t kv_dtype,
+                  const float *k_scale_dev, const float *v_scale_dev, void *k_pool_dev,
+                  void *v_pool_dev, int64_t num_pages, int32_t page_size, int32_t *status_dev,
+                  hpa_stream_t stream);
+
+/*
  * hpa_assign_pages -- page tables and slot maps from request lengths, on the device (the pages
  * have no counterpart to it).  The state of a pool of num_pages pages:
  *   table_dev       int32 [num_rows][table_stride]: the pages that each row (a session) holds,

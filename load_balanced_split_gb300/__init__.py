@@ -5,7 +5,7 @@ csrc/); `hpa` is its ctypes binding.  Nothing here computes on the CPU.
 """
 from .hpa import (E2M1_PAGE_BYTES, KV_BF16, KV_E2M1, KV_E4M3, HpaError,  # noqa: F401
                   PageTable, Workspace, decode_step, evict_step, hpa_assign_pages,
-                  hpa_assign_pages_workspace,
+                  hpa_assign_pages_workspace, hpa_store_qkv,
                   hpa_decode_attn_window, hpa_default_num_ctas_window, hpa_evict, hpa_evict_compact,
                   hpa_evict_select, hpa_key_weights, hpa_plan_window, hpa_store_kv_at,
                   hpa_arrivals_elems, hpa_combine, hpa_decode_attn, hpa_decode_attn_allheads,

@@ -569,6 +569,85 @@ int hpa_store_kv_at(const void *k_new_dev, const void *v_new_dev, const int32_t 
                        status_dev, text_pos_dev, stream);
 }
 
+int hpa_store_qkv(const void *q_dev, int64_t q_stride, const void *k_dev, int64_t k_stride,
+                  const void *v_dev, int64_t v_stride, int32_t num_tokens, int32_t Hq, int32_t Hkv,
+                  int32_t d, const int32_t *positions_dev, const int64_t *slots_dev,
+                  const float *cos_sin_dev, int32_t max_pos, int32_t rot_dim,
+                  const float *q_norm_dev, const float *k_norm_dev, float eps, int32_t flags,
+                  void *q_out_dev, int64_t q_out_stride, int32_t kv_dtype,
+                  const float *k_scale_dev, const float *v_scale_dev, void *k_pool_dev,
+                  void *v_pool_dev, int64_t num_pages, int32_t page_size, int32_t *status_dev,
+                  hpa_stream_t stream) {
+  constexpr int32_t kFlags = HPA_QKV_NORM_AFTER | HPA_QKV_INTERLEAVED | HPA_QKV_HADAMARD;
+  const bool has_q = q_dev != nullptr, has_kv = k_dev != nullptr;
+  if ((k_dev == nullptr) != (v_dev == nullptr) || (!has_q && !has_kv)) return HPA_ERR_INVALID;
+  if (!positions_dev || !slots_dev || (rot_dim != 0 && !cos_sin_dev) || (has_q && !q_out_dev) ||
+      (has_kv && (!k_pool_dev || !v_pool_dev)))
+    return HPA_ERR_INVALID;
+  if (kv_dtype != HPA_KV_BF16 && kv_dtype != HPA_KV_E4M3 && kv_dtype != HPA_KV_E2M1)
+    return HPA_ERR_INVALID;
+  if (has_kv && kv_dtype != HPA_KV_BF16 && (!k_scale_dev || !v_scale_dev)) return HPA_ERR_INVALID;
+  if (num_tokens < 0 || (has_q && Hq < 1) || (has_kv && Hkv < 1) || Hq > 65535 || Hkv > 65535 ||
+      num_pages < 1 || (rot_dim != 0 && max_pos < 1) || !(eps >= 0.f) || !std::isfinite(eps) ||
+      (flags & ~kFlags) != 0)
+    return HPA_ERR_INVALID;
+  if (d != hpa::HEAD_DIM || page_size != hpa::PAGE || num_pages * 64 > (int64_t(1) << 40) ||
+      (rot_dim != 0 && rot_dim != 16 && rot_dim != 32 && rot_dim != 64 && rot_dim != 128))
+    return HPA_ERR_UNSUPPORTED;
+  if (has_kv && num_pages > INT_MAX / Hkv) return HPA_ERR_UNSUPPORTED;
+  if (num_pages > INT_MAX) return HPA_ERR_UNSUPPORTED;
+  // tokens apart by at least their heads, rows on 16-byte boundaries
+  if ((has_q && (q_stride < int64_t(Hq) * d || q_out_stride < int64_t(Hq) * d)) ||
+      (has_kv && (k_stride < int64_t(Hkv) * d || v_stride < int64_t(Hkv) * d)))
+    return HPA_ERR_INVALID;
+  if ((has_q && (q_stride % 8 || q_out_stride % 8 || !aligned(q_dev, 16) || !aligned(q_out_dev, 16))) ||
+      (has_kv && (k_stride % 8 || v_stride % 8 || !aligned(k_dev, 16) || !aligned(v_dev, 16) ||
+                  !aligned(k_pool_dev, 16) || !aligned(v_pool_dev, 16))) ||
+      !aligned(positions_dev, 4) || !aligned(slots_dev, 8) || !aligned(cos_sin_dev, 16) ||
+      !aligned(q_norm_dev, 4) || !aligned(k_norm_dev, 4) || !aligned(k_scale_dev, 4) ||
+      !aligned(v_scale_dev, 4) || !aligned(status_dev, 4))
+    return HPA_ERR_ALIGN;
+  if (num_tokens == 0) return HPA_OK;
+  const auto span = [&](int64_t stride) {  // bytes from the first query to the last one's end
+    return 2ull * (stride * (num_tokens - 1) + int64_t(Hq) * d);
+  };
+  if (has_q && (q_dev != q_out_dev || (q_stride != q_out_stride && num_tokens > 1)) &&
+      overlap(q_dev, span(q_stride), q_out_dev, span(q_out_stride)))
+    return HPA_ERR_INVALID;
+  hpa::StoreQkvParams p;
+  p.q = static_cast<const __nv_bfloat16 *>(q_dev);
+  p.k = static_cast<const __nv_bfloat16 *>(k_dev);
+  p.v = static_cast<const __nv_bfloat16 *>(v_dev);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out_stride = q_out_stride;
+  p.num_tokens = num_tokens;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.positions = positions_dev;
+  p.slots = slots_dev;
+  p.cos_sin = cos_sin_dev;
+  p.max_pos = max_pos;
+  p.rot_dim = rot_dim;
+  p.q_norm = q_norm_dev;
+  p.k_norm = k_norm_dev;
+  p.eps = eps;
+  p.norm_after = (flags & HPA_QKV_NORM_AFTER) != 0;
+  p.interleaved = (flags & HPA_QKV_INTERLEAVED) != 0;
+  p.use_hadamard = (flags & HPA_QKV_HADAMARD) != 0;
+  p.q_out = static_cast<__nv_bfloat16 *>(q_out_dev);
+  p.kv_dtype = kv_dtype;
+  p.k_scale = k_scale_dev;
+  p.v_scale = v_scale_dev;
+  p.k_pool = k_pool_dev;
+  p.v_pool = v_pool_dev;
+  p.num_pages = num_pages;
+  p.status = status_dev;
+  cudaError_t e = hpa::launch_store_qkv(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HPA_OK : cuda_fail(e);
+}
+
 size_t hpa_assign_pages_workspace(int32_t B, int32_t num_rows) {
   if (B < 1 || B > kMaxB || num_rows < 1) return 0;
   return static_cast<size_t>(hpa::assign_workspace_words(B, num_rows)) * 4;

@@ -177,6 +177,26 @@ struct StoreKvParams {
 };
 cudaError_t launch_store_kv(const StoreKvParams &p, cudaStream_t s);
 
+struct StoreQkvParams {
+  const __nv_bfloat16 *q, *k, *v;  // q or (k and v) may be nullptr
+  int64_t q_stride, k_stride, v_stride, q_out_stride;  // elements between tokens
+  int num_tokens, Hq, Hkv;
+  const int32_t *positions;
+  const int64_t *slots;
+  const float *cos_sin;
+  int max_pos, rot_dim;
+  const float *q_norm, *k_norm;  // optional
+  float eps;
+  bool norm_after, interleaved, use_hadamard;
+  __nv_bfloat16 *q_out;
+  int kv_dtype;
+  const float *k_scale, *v_scale;
+  void *k_pool, *v_pool;
+  int64_t num_pages;
+  int32_t *status;
+};
+cudaError_t launch_store_qkv(const StoreQkvParams &p, cudaStream_t s);
+
 struct AssignParams {
   const int32_t *seq_lens, *new_tokens, *rows, *pos_offset;  // the last three optional
   int B, num_rows;

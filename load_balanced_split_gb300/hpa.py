@@ -94,6 +94,9 @@ def lib():
                                        I32, P, P], ctypes.c_int),
                 "hpa_evict": ([P, P, I32, P, I64, P, P, P, P, P, I32, P, I32, I32, I32, I32, I32, P,
                                I64, P, P, P], ctypes.c_int),
+                "hpa_store_qkv": ([P, I64, P, I64, P, I64, I32, I32, I32, I32, P, P, P, I32, I32,
+                                   P, P, F, I32, P, I64, I32, P, P, P, P, I64, I32, P, P],
+                                  ctypes.c_int),
                 "hpa_assign_pages_workspace": ([I32, I32], SZ),
                 "hpa_assign_pages": ([P, P, P, P, I32, I32, P, I32, P, P, P, P, P, I32, I32, P, P,
                                       I32, P, P, I32, P, SZ, P, P], ctypes.c_int),
@@ -557,6 +560,102 @@ def hpa_store_kv_at(k_new, v_new, seq_lens, text_pos, page_indptr, page_indices,
     text_pos (int32 [B], the text position of each request's first new token) rotates them."""
     _store_kv("hpa_store_kv_at", k_new, v_new, seq_lens, text_pos, page_indptr, page_indices,
               cos_sin, norm_w, k_pool, v_pool, eps, use_hadamard, k_scale, v_scale, status, stream)
+
+
+def _heads(t, name, n):
+    """Checks a bf16 [n][heads][128] tensor whose tokens may lie apart; (heads, token stride)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise HpaError("%s must be a CUDA tensor" % name)
+    if t.dtype is not torch.bfloat16:
+        raise HpaError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != 128:
+        raise HpaError("%s must be [%d tokens][heads][128], got %s" % (name, n, tuple(t.shape)))
+    heads = t.shape[1]
+    st = t.stride()
+    if n and heads and (st[2] != 1 or (heads > 1 and st[1] != 128) or
+                        (n > 1 and (st[0] < heads * 128 or st[0] % 8))):
+        raise HpaError("%s: a token's heads must be contiguous, tokens a multiple of 8 elements "
+                       "apart, got strides %s" % (name, st))
+    return heads, st[0] if n > 1 else heads * 128
+
+
+def hpa_store_qkv(q, k, v, positions, slots, cos_sin, k_pool=None, v_pool=None, q_out=None,
+                  q_norm=None, k_norm=None, eps: float = 1e-6, norm_after: bool = False,
+                  interleaved: bool = False, use_hadamard: bool = False, k_scale=None,
+                  v_scale=None, status=None, stream=None, num_pages=None):
+    """Per-head RMSNorm, rotation, optional Hadamard transform and paged store of tokens'
+    projections, and their queries, in one pass.
+
+    q bf16 [n][Hq][128] (or None), k and v [n][Hkv][128] (or both None): tokens may be strided,
+    as the parts of a packed projection are; positions int32 [n], slots int64 [n] (-1: no token),
+    as hpa_assign_pages writes them; cos_sin fp32 [max_pos][rot_dim] (None: no rotation).  q_out:
+    like q, by default q itself (in place).  Pools bf16 or uint8 (E4M3) [P][Hkv][64][128] or 4-bit
+    uint8 [P][Hkv][E2M1_PAGE_BYTES]; without them num_pages bounds the slots."""
+    if q is None and k is None:
+        raise HpaError("neither queries nor keys and values")
+    if (k is None) != (v is None):
+        raise HpaError("k and v go together")
+    _dev(positions, "positions", torch.int32)
+    _dev(slots, "slots", torch.int64)
+    n = positions.numel()
+    if slots.numel() != n:
+        raise HpaError("positions and slots need one value per token")
+    Hq = Hkv = kv = 0
+    sq = sk = sv = so = 0
+    if q is not None:
+        Hq, sq = _heads(q, "q", n)
+        q_out = q if q_out is None else q_out
+        heads, so = _heads(q_out, "q_out", n)
+        if heads != Hq:
+            raise HpaError("q_out must have q's shape")
+    if k is not None:
+        Hkv, sk = _heads(k, "k", n)
+        heads, sv = _heads(v, "v", n)
+        if heads != Hkv:
+            raise HpaError("k and v must have the same heads")
+        if k_pool is None or v_pool is None:
+            raise HpaError("k and v need their pools")
+        if _is_e2m1(k_pool):
+            kv, num_pages = KV_E2M1, k_pool.shape[0]
+            _dev(k_pool, "k_pool")
+            _dev(v_pool, "v_pool", torch.uint8)
+            if v_pool.shape != k_pool.shape:
+                raise HpaError("k_pool and v_pool must match")
+            if k_pool.shape[1] != Hkv:
+                raise HpaError("KV head count mismatch")
+        else:
+            kv, num_pages, heads, page, d = _pools(k_pool, v_pool)
+            if heads != Hkv or page != 64 or d != 128:
+                raise HpaError("the pools must be [P][%d][64][128]" % Hkv)
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if kv != KV_BF16 and _dev(t, name, torch.float32).numel() < Hkv:
+                raise HpaError("%s needs one fp32 value per KV head" % name)
+    elif num_pages is None:
+        raise HpaError("without pools num_pages has to say how many there are")
+    rot = max_pos = 0
+    if cos_sin is not None:
+        _dev(cos_sin, "cos_sin", torch.float32)
+        if cos_sin.dim() != 2:
+            raise HpaError("cos_sin must be [max_pos][rot_dim]")
+        max_pos, rot = cos_sin.shape
+        if rot == 0:
+            raise HpaError("cos_sin must be [max_pos][rot_dim] (None: no rotation)")
+    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is not None and _dev(t, name, torch.float32).numel() != 128:
+            raise HpaError("%s must be [128]" % name)
+    if status is not None:
+        _dev(status, "status", torch.int32)
+    _one_device(q, k, v, positions, slots, cos_sin, k_pool, v_pool, q_out, q_norm, k_norm, k_scale,
+                v_scale, status)
+    if n == 0:                    # tensors without elements have no address to pass on
+        return
+    rc = lib().hpa_store_qkv(
+        _ptr(q), sq, _ptr(k), sk, _ptr(v), sv, n, Hq, Hkv, 128, _ptr(positions), _ptr(slots),
+        _ptr(cos_sin), max_pos, rot, _ptr(q_norm), _ptr(k_norm), eps,
+        norm_after | interleaved << 1 | use_hadamard << 2, _ptr(q_out), so, kv, _ptr(k_scale),
+        _ptr(v_scale), _ptr(k_pool), _ptr(v_pool), num_pages, 64, _ptr(status), _stream(stream))
+    if rc != 0:
+        _check(rc, "hpa_store_qkv")
 
 
 # ----------------------------------------------------------------------------- bounded cache

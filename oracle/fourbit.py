@@ -53,7 +53,7 @@ def encode(y):
     blocks = y.reshape(*y.shape[:-1], -1, BLOCK)
     s = encode_e4m3_value(np.abs(blocks).max(-1) / 6.0)
     with np.errstate(divide="ignore", invalid="ignore"):
-        z = np.where(s[..., None] > 0, blocks / s[..., None], 0.0 * blocks)
+        z = np.where(s[..., None] > 0, blocks / s[..., None], 0.0)
     return encode_e2m1(z).reshape(y.shape), s
 
 
