@@ -41,11 +41,21 @@
 namespace hpa {
 namespace {
 
-constexpr int kWarps = 4;  // consumer warps
-constexpr int kThreads = (kWarps + 1) * 32;
+// Up to 8 query rows (NT = 1): 5 consumer warps and 10 stages, two CTAs per SM, so 12 warps share
+// the register file at 168 each (4 and 8: 66 us on 32 x 8192 keys, 5 and 10: 62).  Up to 16
+// rows (NT = 2) the fewer warps leave the partitions twice as many CTAs.
+template <int NT>
+struct Cfg {
+  static constexpr int kWarps = NT == 1 ? 5 : 4;  // consumer warps
+  static constexpr int kStages = 2 * kWarps;
+  // A warp meets the same stages again.  Copies may land out of order, so a warp that came to a
+  // stage whose page before it, another warp's, had not landed would take that page's phase for
+  // the end of its own.
+  static_assert(kStages % kWarps == 0, "each stage belongs to one warp");
+  static constexpr int kThreads = (kWarps + 1) * 32;
+};
 constexpr int kUnit = E2M1_UNIT;  // bytes of one page and KV head of K or V
 constexpr int kStageBytes = 2 * kUnit;
-constexpr int kStages = 8;  // a multiple of kWarps: a warp meets the same stages again
 constexpr float kRescaleSlack = 8.f;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kQRowBytes = 272;  // 256 of a query row, padded against bank conflicts
@@ -53,38 +63,23 @@ constexpr int kMergeStride = HEAD_DIM + 4;
 
 template <int NT>
 struct Smem {
+  static constexpr int kWarps = Cfg<NT>::kWarps, kStages = Cfg<NT>::kStages;
   static constexpr int kRows = 8 * NT;
+  static constexpr int kBufs = kWarps > 4 ? 4 : 2;
   static constexpr int kQSlot = kRows * kQRowBytes;
-  static constexpr int kMerge = kStages * kStageBytes;               // float[2][kRows][stride]
-  static constexpr int kStats = kMerge + 2 * kRows * kMergeStride * 4;  // m, l: [warps][kRows]
+  static constexpr int kMerge = kStages * kStageBytes;               // float[kBufs][kRows][stride]
+  static constexpr int kStats = kMerge + kBufs * kRows * kMergeStride * 4;  // m, l: [warps][kRows]
   static constexpr int kQ = kStats + 2 * kWarps * kRows * 4;         // two query slots
   static constexpr int kInfo = kQ + 2 * kQSlot;                      // int4[2]
   static constexpr int kBars = kInfo + 2 * 16;  // full[stages] empty[stages] qfull[2] qempty[2]
   static constexpr int kFlag = kBars + (2 * kStages + 4) * 8;
-  static constexpr int kBytes = kFlag + 16;
-  static constexpr int kAlloc = kBytes + 128;  // room to align the base
+  static constexpr int kAlloc = kFlag + 16;
 };
 
 // Which of a group's 8 keys stands at index k of the MMAs' key dimension: the keys that the
 // four lanes of a quad read together for V (k = 0, 2, 4, 6 and 1, 3, 5, 7) then lie in both
 // halves of the 128 bytes that shared memory serves at once.
 __device__ __forceinline__ constexpr int key_at(int k) { return k ^ ((k >> 1) & 1); }
-
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
 
 // The four bytes of w, two E2M1 codes each, as f16 pairs (low nibble in the low half; exact).
 __device__ __forceinline__ void widen8(uint32_t w, uint32_t (&r)[4]) {
@@ -101,6 +96,15 @@ __device__ __forceinline__ void widen8(uint32_t w, uint32_t (&r)[4]) {
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// One half of an f16 pair in both halves (written so that a multiplication can take it in place).
+template <int HI>
+__device__ __forceinline__ uint32_t both_halves(uint32_t a) {
+  uint32_t d;
+  if (HI) asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(d) : "r"(a));
+  else asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(d) : "r"(a));
   return d;
 }
 
@@ -154,6 +158,7 @@ template <int NT, bool WIN>
 __device__ void producer(const AttnParams &p, const uint8_t *k_pool, const uint8_t *v_pool,
                          uint8_t *smem, const MapHead &head) {
   using S = Smem<NT>;
+  constexpr int kStages = S::kStages;
   const int lane = threadIdx.x & 31, h = blockIdx.y;
   const uint32_t base = smem_u32(smem);
   const uint32_t full0 = base + S::kBars, empty0 = full0 + 8 * kStages;
@@ -254,6 +259,7 @@ __device__ __forceinline__ void v_pairs(uint32_t lo_key, uint32_t hi_key, uint32
 template <int NT, bool WIN>
 __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head) {
   using S = Smem<NT>;
+  constexpr int kStages = S::kStages, kWarps = S::kWarps;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
   const int g = lane >> 2, c = lane & 3;
   const uint32_t base = smem_u32(smem);
@@ -275,8 +281,8 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
   }
   // where this lane's shares of a page lie: K rows key_at(g) (+8), dims 32 c..; V keys of the
   // quad's lane c, dims 16 g..; their scales
-  const uint32_t k_off = key_at(g) * 64 + c * 16;
-  const uint32_t ks_off = 4096 + key_at(g) * 8 + 2 * c;
+  const int k_off = key_at(g) * 64 + c * 16;
+  const int ks_off = 4096 + key_at(g) * 8 + 2 * c;
   const int vk0 = key_at(2 * c), vk1 = key_at(2 * c + 1);
 
   int count = 0;  // pages of this CTA so far: page n goes to warp n % kWarps, stage n % kStages
@@ -327,7 +333,8 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
       am = fmaxf(am, __shfl_xor_sync(kFull, am, 1));
       am = fmaxf(am, __shfl_xor_sync(kFull, am, 2));
       const int e = f16_row_exponent(am);
-      const float up = exp2i(e);
+      // the sign of the score factor goes to the query, so that the larger score is the larger sum
+      const float up = sl2 == 0.f ? 0.f : copysignf(exp2i(e), sl2);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -336,7 +343,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
           qf[nt][2 * i + (u >> 1)][u & 1] = pack_f16(__uint_as_float(x[u] << 16) * up,
                                                      __uint_as_float(x[u] & 0xffff0000u) * up);
       }
-      const float down = sl2 * exp2i(-e);
+      const float down = sl2 == 0.f ? 1.f : fabsf(sl2) * exp2i(-e);
       sl[2 * nt] = __shfl_sync(kFull, down, 8 * c);
       sl[2 * nt + 1] = __shfl_sync(kFull, down, 8 * c + 4);
     }
@@ -356,65 +363,77 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
     // One page of this warp; EDGE looks for keys that some row does not see.
     auto page = [&](int pg, int stage, uint32_t phase, auto edge_tag) {
       constexpr bool EDGE = decltype(edge_tag)::value;
+      constexpr int KG = 4;          // groups of 16 keys that share a softmax step
+      constexpr int KP = NT == 1 ? 1 : 2;  // and those whose chains of MMAs run side by side
       const bool got = !(*abort_flag) && mbar_wait_bounded(full0 + 8 * stage, phase);
       if (!__all_sync(kFull, got)) {
         ok = false;
         return;
       }
-      const uint32_t kt = base + stage * kStageBytes, vt = kt + kUnit;
+      const uint8_t *kt = smem + stage * kStageBytes, *vt = kt + kUnit;
       const int key0 = (WIN ? win.real_page(pg) : pg) * PAGE;
 
+#pragma unroll
+      for (int k0 = 0; k0 < 4; k0 += KG) {
       // S = K Q^T, 16 keys at a time
-      float x[4][NT][4];
+      float x[KG][NT][4];
 #pragma unroll
-      for (int kg = 0; kg < 4; ++kg) {
-        uint32_t kw[2][4], sc[2][2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {  // keys key_at(g) and key_at(g) + 8 of the group
-          lds128(kt + k_off + (16 * kg + 8 * u) * 64, kw[u][0], kw[u][1], kw[u][2], kw[u][3]);
-          const uint32_t two = e4m3x2_to_f16x2(
-              static_cast<uint16_t>(lds_u16(kt + ks_off + (16 * kg + 8 * u) * 8)));
-          sc[u][0] = __byte_perm(two, 0u, 0x1010);
-          sc[u][1] = __byte_perm(two, 0u, 0x3232);
-        }
+      for (int kg = 0; kg < KG; ++kg)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[kg][nt][e] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // a word: 8 dims, two k-steps
-          uint32_t a[2][4];
+      for (int kp = 0; kp < KG; kp += KP) {  // groups whose chains of MMAs run side by side
+        uint4 kw[KP][2];
+        uint32_t sc[KP][2][2];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            widen8(kw[u][i], a[u]);
+        for (int kq = 0; kq < KP; ++kq)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) a[u][b] = mul_f16x2(a[u][b], sc[u][i >> 1]);
+          for (int u = 0; u < 2; ++u) {  // keys key_at(g) and key_at(g) + 8 of the group
+            const int row = 16 * (k0 + kp + kq) + 8 * u;
+            kw[kq][u] = *reinterpret_cast<const uint4 *>(kt + k_off + row * 64);
+            const uint32_t two =
+                e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(kt + ks_off + row * 8));
+            sc[kq][u][0] = both_halves<0>(two);
+            sc[kq][u][1] = both_halves<1>(two);
           }
 #pragma unroll
-          for (int st = 0; st < 2; ++st) {
-            const uint32_t af[4] = {a[0][2 * st], a[1][2 * st], a[0][2 * st + 1], a[1][2 * st + 1]};
+        for (int i = 0; i < 4; ++i)  // a word: 8 dims, two k-steps
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16(x[kg][nt], af, qf[nt][2 * i + st][0], qf[nt][2 * i + st][1]);
-          }
-        }
-      }
-      // to log2 units, and what a row does not see to -inf
+          for (int kq = 0; kq < KP; ++kq) {
+            uint32_t a[2][4];
 #pragma unroll
-      for (int kg = 0; kg < 4; ++kg)
+            for (int u = 0; u < 2; ++u) {
+              const uint4 v = kw[kq][u];
+              widen8(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w, a[u]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v = x[kg][nt][e] * sl[2 * nt + (e & 1)];
-            if (EDGE) {
-              const int key = key0 + 16 * kg + key_at(g) + 8 * (e >> 1), j = tok[2 * nt + (e & 1)];
-              bool see = key < lim_min + j;
-              if (WIN) see = see && (key < head.sinks || key >= win.start + j);
-              v = see ? v : -CUDART_INF_F;
+              for (int b = 0; b < 4; ++b) a[u][b] = mul_f16x2(a[u][b], sc[kq][u][i >> 1]);
             }
-            x[kg][nt][e] = v;
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+              const uint32_t af[4] = {a[0][2 * st], a[1][2 * st], a[0][2 * st + 1],
+                                      a[1][2 * st + 1]};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(x[kp + kq][nt], af, qf[nt][2 * i + st][0], qf[nt][2 * i + st][1]);
+            }
           }
+      }
+      // what a row does not see to -inf (x is the plain sum; x * sl the score in log2 units)
+      if (EDGE) {
+#pragma unroll
+        for (int kg = 0; kg < KG; ++kg)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + 16 * (k0 + kg) + key_at(g) + 8 * (e >> 1);
+              const int j = tok[2 * nt + (e & 1)];
+              if (!(key < lim_min + j && (!WIN || key < head.sinks || key >= win.start + j)))
+                x[kg][nt][e] = -CUDART_INF_F;
+            }
+      }
       // running maximum: moves when a score passes it by more than the slack
       bool over = false;
       float top[2 * NT];
@@ -422,8 +441,9 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
       for (int i = 0; i < 2 * NT; ++i) {
         top[i] = fmaxf(x[0][i >> 1][i & 1], x[0][i >> 1][2 + (i & 1)]);
 #pragma unroll
-        for (int kg = 1; kg < 4; ++kg)
+        for (int kg = 1; kg < KG; ++kg)
           top[i] = fmaxf(top[i], fmaxf(x[kg][i >> 1][i & 1], x[kg][i >> 1][2 + (i & 1)]));
+        top[i] *= sl[i];
         over |= top[i] > m[i] + kRescaleSlack;
       }
       if (__any_sync(kFull, over)) {
@@ -443,15 +463,16 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
         }
       }
       // probabilities; their sums in fp32 before the rounding to f16
-      uint32_t pb[4][NT][2];
+      uint32_t pb[KG][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float b0 = m[2 * nt] == -CUDART_INF_F ? 0.f : m[2 * nt];
-        const float b1 = m[2 * nt + 1] == -CUDART_INF_F ? 0.f : m[2 * nt + 1];
+        const float s0 = sl[2 * nt], s1 = sl[2 * nt + 1];
+        const float b0 = m[2 * nt] == -CUDART_INF_F ? 0.f : -m[2 * nt];
+        const float b1 = m[2 * nt + 1] == -CUDART_INF_F ? 0.f : -m[2 * nt + 1];
 #pragma unroll
-        for (int kg = 0; kg < 4; ++kg) {
-          const float p0 = exp2f(x[kg][nt][0] - b0), p1 = exp2f(x[kg][nt][1] - b1);
-          const float p2 = exp2f(x[kg][nt][2] - b0), p3 = exp2f(x[kg][nt][3] - b1);
+        for (int kg = 0; kg < KG; ++kg) {
+          const float p0 = exp2f(fmaf(x[kg][nt][0], s0, b0)), p1 = exp2f(fmaf(x[kg][nt][1], s1, b1));
+          const float p2 = exp2f(fmaf(x[kg][nt][2], s0, b0)), p3 = exp2f(fmaf(x[kg][nt][3], s1, b1));
           l[2 * nt] += p0 + p2;
           l[2 * nt + 1] += p1 + p3;
           pb[kg][nt][0] = transpose8(pack_f16(p0, p1));
@@ -460,14 +481,14 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
       }
       // O^T += V^T P^T
 #pragma unroll
-      for (int kg = 0; kg < 4; ++kg) {
-        const int kb = 16 * kg;
-        const uint2 v0 = lds64(vt + (kb + vk0) * 64 + 8 * g), v1 = lds64(vt + (kb + vk1) * 64 + 8 * g);
-        const uint2 v2 = lds64(vt + (kb + 8 + vk0) * 64 + 8 * g);
-        const uint2 v3 = lds64(vt + (kb + 8 + vk1) * 64 + 8 * g);
-        const uint32_t sb = vt + 4096 + g;
-        uint32_t b0 = lds_u8(sb + (kb + vk0) * 8), b1 = lds_u8(sb + (kb + vk1) * 8);
-        uint32_t b2 = lds_u8(sb + (kb + 8 + vk0) * 8), b3 = lds_u8(sb + (kb + 8 + vk1) * 8);
+      for (int kg = 0; kg < KG; ++kg) {
+        const int kb = 16 * (k0 + kg);
+        auto words = [&](int key) { return *reinterpret_cast<const uint2 *>(vt + key * 64 + 8 * g); };
+        const uint2 v0 = words(kb + vk0), v1 = words(kb + vk1);
+        const uint2 v2 = words(kb + 8 + vk0), v3 = words(kb + 8 + vk1);
+        const uint8_t *sb = vt + 4096 + g;
+        uint32_t b0 = sb[(kb + vk0) * 8], b1 = sb[(kb + vk1) * 8];
+        uint32_t b2 = sb[(kb + 8 + vk0) * 8], b3 = sb[(kb + 8 + vk1) * 8];
         const int keys[4] = {key0 + kb + vk0, key0 + kb + vk1, key0 + kb + 8 + vk0,
                              key0 + kb + 8 + vk1};
         auto scales = [](uint32_t lo, uint32_t hi) {
@@ -483,36 +504,29 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
           b0 = hide(keys[0], b0), b1 = hide(keys[1], b1);
           b2 = hide(keys[2], b2), b3 = hide(keys[3], b3);
           if (q_len > 1) {
-            auto odd_one = [&](int key, uint32_t b) {  // a NaN that only some tokens see
-              return e4m3_nan(b) && !(sees(key, 0) && sees(key, q_len - 1));
+            // A NaN that some tokens see and others do not: 0 * NaN would reach every row, so
+            // the scale is taken as zero and the block's 16 dims, which are this quad's o, become
+            // NaN for the rows that see the key.
+            uint32_t odd = 0;
+            auto take = [&](int u, uint32_t b) {
+              if (!e4m3_nan(b) || (sees(keys[u], 0) && sees(keys[u], q_len - 1))) return b;
+              odd |= 1u << u;
+              return 0u;
             };
-            if (__any_sync(kFull, odd_one(keys[0], b0) || odd_one(keys[1], b1) ||
-                                      odd_one(keys[2], b2) || odd_one(keys[3], b3))) {
-              // 0 * NaN would reach every row: a pass for each token, kept by its rows alone
+            b0 = take(0, b0), b1 = take(1, b1), b2 = take(2, b2), b3 = take(3, b3);
+            if (__any_sync(kFull, odd != 0)) {
 #pragma unroll 1
-              for (int j = 0; j < q_len; ++j) {
-                uint32_t a0[2][4], a1[2][4], a2[2][4], a3[2][4];
-                const uint32_t s01 = scales(sees(keys[0], j) ? b0 : 0u, sees(keys[1], j) ? b1 : 0u);
-                const uint32_t s23 = scales(sees(keys[2], j) ? b2 : 0u, sees(keys[3], j) ? b3 : 0u);
-                v_pairs(v0.x, v1.x, s01, a0[0], a1[0]);
-                v_pairs(v0.y, v1.y, s01, a0[1], a1[1]);
-                v_pairs(v2.x, v3.x, s23, a2[0], a3[0]);
-                v_pairs(v2.y, v3.y, s23, a2[1], a3[1]);
+              for (int v = 0; v < 16; ++v) {  // the quad's 16 keys
+                const uint32_t bits = __shfl_sync(kFull, odd, (lane & 28) | (v >> 2));
+                if (!((bits >> (v & 3)) & 1)) continue;
+                const int at = key0 + kb + key_at(2 * (v >> 2) + (v & 1)) + 8 * ((v & 3) >> 1);
 #pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                  const uint32_t af[4] = {a0[t >> 2][t & 3], a1[t >> 2][t & 3], a2[t >> 2][t & 3],
-                                          a3[t >> 2][t & 3]};
+                for (int i = 0; i < 2 * NT; ++i)
+                  if (sees(at, tok[i]))
 #pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) {
-                    float part[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_f16(part, af, pb[kg][nt][0], pb[kg][nt][1]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                      if (tok[2 * nt + (e & 1)] == j) o[nt][t][e] += part[e];
-                  }
-                }
+                    for (int t = 0; t < 8; ++t)
+                      o[i >> 1][t][i & 1] = o[i >> 1][t][2 + (i & 1)] = CUDART_NAN_F;
               }
-              continue;
             }
           }
         }
@@ -531,11 +545,12 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
           }
         }
       }
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty0 + 8 * stage);
     };
     // this warp's pages of the segment: page n of the CTA with n % kWarps == w
-    const int skip = (w - count) & (kWarps - 1), n_pages = f.pg1 - f.pg0;
+    const int skip = (w + kWarps - count % kWarps) % kWarps, n_pages = f.pg1 - f.pg0;
     for (int i = skip; i < n_pages && ok; i += kWarps) {
       const int n = count + i, stage = n % kStages, pg = f.pg0 + i;
       const uint32_t phase = (n / kStages) & 1;
@@ -579,7 +594,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
       row_stats(8 * (i >> 1) + 2 * c + (i & 1), M, Lsum);
       fs[i] = Lsum == 0.f ? 0.f : exp2f(m[i] - M) / Lsum * vsc;
     }
-    float *mine = mbuf + (w & 1) * (S::kRows * kMergeStride);
+    float *mine = mbuf + (w % S::kBufs) * (S::kRows * kMergeStride);
     auto merge = [&](auto add_tag) {  // warps 0 / 1 store, then warps 2 / 3 add
       constexpr bool ADD = decltype(add_tag)::value;
 #pragma unroll
@@ -599,19 +614,26 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
         }
       }
     };
-    if (w < 2) merge(std::false_type());
+    if (w < S::kBufs) merge(std::false_type());
     named_barrier(1, kWarps * 32);
-    if (w >= 2) merge(std::true_type());
-    named_barrier(1, kWarps * 32);
+#pragma unroll
+    for (int v = S::kBufs; v < kWarps; v += S::kBufs) {
+      if (w >= v && w < v + S::kBufs) merge(std::true_type());
+      named_barrier(1, kWarps * 32);
+    }
     const int tid = threadIdx.x;
     for (int v = tid; v < rows * (HEAD_DIM / 4); v += kWarps * 32) {
       const int row = v / (HEAD_DIM / 4), c4 = v % (HEAD_DIM / 4);
       const int j = (rb + row) / G, gq = (rb + row) % G;
       const int64_t dst = (static_cast<int64_t>(s) * q_len + j) * p.Hq + h * G + gq;
-      const float4 a = reinterpret_cast<const float4 *>(mbuf + row * kMergeStride)[c4];
-      const float4 b = reinterpret_cast<const float4 *>(mbuf + (S::kRows + row) * kMergeStride)[c4];
-      reinterpret_cast<float4 *>(p.partial_o + dst * HEAD_DIM)[c4] =
-          make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+      float4 a = reinterpret_cast<const float4 *>(mbuf + row * kMergeStride)[c4];
+#pragma unroll
+      for (int u = 1; u < S::kBufs; ++u) {
+        const float4 b =
+            reinterpret_cast<const float4 *>(mbuf + (u * S::kRows + row) * kMergeStride)[c4];
+        a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+      }
+      reinterpret_cast<float4 *>(p.partial_o + dst * HEAD_DIM)[c4] = a;
     }
     if (tid < rows) {
       float M, Lsum;
@@ -629,13 +651,12 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
 }
 
 template <int NT, bool WIN>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(Cfg<NT>::kThreads, 2)
     decode_attn_e2m1_kernel(const uint8_t *__restrict__ k_pool, const uint8_t *__restrict__ v_pool,
                             const AttnParams p) {
   using S = Smem<NT>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+  constexpr int kStages = S::kStages, kWarps = S::kWarps;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ MapHead head;
   const int c = blockIdx.x;
   const uint32_t base = smem_u32(smem);
@@ -688,7 +709,7 @@ cudaError_t launch(const AttnParams &p, const void *k_pool, const void *v_pool, 
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.C, p.Hkv, (p.rows + p.group - 1) / p.group);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Cfg<NT>::kThreads);
   cfg.dynamicSmemBytes = Smem<NT>::kAlloc;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -705,7 +726,7 @@ template <int NT>
 int occupancy(int *ctas) {
   if (configure<NT, false>() != cudaSuccess) return -1;
   return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, decode_attn_e2m1_kernel<NT, false>,
-                                                       kThreads, Smem<NT>::kAlloc) == cudaSuccess
+                                                       Cfg<NT>::kThreads, Smem<NT>::kAlloc) == cudaSuccess
              ? 0
              : -1;
 }
