@@ -140,6 +140,21 @@ def _dev(t, name, dtype=None):
     return t
 
 
+def _devs(dtype, names, tensors):
+    """_dev for several tensors of one type (None is passed over), at less host time each."""
+    try:
+        for t in tensors:
+            if t is not None and not (t.is_cuda and t.dtype is dtype and t.is_contiguous()):
+                break
+        else:
+            return
+    except AttributeError:
+        pass
+    for t, name in zip(tensors, names.split()):
+        if t is not None:
+            _dev(t, name, dtype)
+
+
 # ----------------------------------------------------------------------------- sizes
 def hpa_taskmap_bytes(B: int, num_ctas: int) -> int:
     return int(lib().hpa_taskmap_bytes(B, num_ctas))
@@ -564,14 +579,22 @@ def hpa_store_kv_at(k_new, v_new, seq_lens, text_pos, page_indptr, page_indices,
 
 def _heads(t, name, n):
     """Checks a bf16 [n][heads][128] tensor whose tokens may lie apart; (heads, token stride)."""
+    try:
+        if t.is_cuda and t.dtype is torch.bfloat16:
+            tokens, heads, d = t.shape
+            s0, s1, s2 = t.stride()
+            if tokens == n and d == 128 and s2 == 1 and s1 == 128 and s0 >= heads * 128:
+                if s0 % 8 == 0 or n <= 1:
+                    return heads, s0 if n > 1 else heads * 128
+    except (AttributeError, ValueError):
+        pass
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise HpaError("%s must be a CUDA tensor" % name)
     if t.dtype is not torch.bfloat16:
         raise HpaError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
     if t.dim() != 3 or t.shape[0] != n or t.shape[2] != 128:
         raise HpaError("%s must be [%d tokens][heads][128], got %s" % (name, n, tuple(t.shape)))
-    heads = t.shape[1]
-    st = t.stride()
+    heads, st = t.shape[1], t.stride()
     if n and heads and (st[2] != 1 or (heads > 1 and st[1] != 128) or
                         (n > 1 and (st[0] < heads * 128 or st[0] % 8))):
         raise HpaError("%s: a token's heads must be contiguous, tokens a multiple of 8 elements "
@@ -595,8 +618,10 @@ def hpa_store_qkv(q, k, v, positions, slots, cos_sin, k_pool=None, v_pool=None, 
         raise HpaError("neither queries nor keys and values")
     if (k is None) != (v is None):
         raise HpaError("k and v go together")
-    _dev(positions, "positions", torch.int32)
     _dev(slots, "slots", torch.int64)
+    _dev(positions, "positions", torch.int32)
+    _devs(torch.float32, "cos_sin q_norm k_norm k_scale v_scale",
+          (cos_sin, q_norm, k_norm, k_scale, v_scale))
     n = positions.numel()
     if slots.numel() != n:
         raise HpaError("positions and slots need one value per token")
@@ -627,22 +652,22 @@ def hpa_store_qkv(q, k, v, positions, slots, cos_sin, k_pool=None, v_pool=None, 
             kv, num_pages, heads, page, d = _pools(k_pool, v_pool)
             if heads != Hkv or page != 64 or d != 128:
                 raise HpaError("the pools must be [P][%d][64][128]" % Hkv)
-        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if kv != KV_BF16 and _dev(t, name, torch.float32).numel() < Hkv:
-                raise HpaError("%s needs one fp32 value per KV head" % name)
+        if kv != KV_BF16:
+            for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if (t if t is not None else _dev(t, name)).numel() < Hkv:
+                    raise HpaError("%s needs one fp32 value per KV head" % name)
     elif num_pages is None:
         raise HpaError("without pools num_pages has to say how many there are")
     rot = max_pos = 0
     if cos_sin is not None:
-        _dev(cos_sin, "cos_sin", torch.float32)
         if cos_sin.dim() != 2:
             raise HpaError("cos_sin must be [max_pos][rot_dim]")
         max_pos, rot = cos_sin.shape
         if rot == 0:
             raise HpaError("cos_sin must be [max_pos][rot_dim] (None: no rotation)")
-    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if t is not None and _dev(t, name, torch.float32).numel() != 128:
-            raise HpaError("%s must be [128]" % name)
+    if ((q_norm is not None and q_norm.numel() != 128) or
+            (k_norm is not None and k_norm.numel() != 128)):
+        raise HpaError("q_norm and k_norm must be [128]")
     if status is not None:
         _dev(status, "status", torch.int32)
     _one_device(q, k, v, positions, slots, cos_sin, k_pool, v_pool, q_out, q_norm, k_norm, k_scale,
@@ -652,7 +677,7 @@ def hpa_store_qkv(q, k, v, positions, slots, cos_sin, k_pool=None, v_pool=None, 
     rc = lib().hpa_store_qkv(
         _ptr(q), sq, _ptr(k), sk, _ptr(v), sv, n, Hq, Hkv, 128, _ptr(positions), _ptr(slots),
         _ptr(cos_sin), max_pos, rot, _ptr(q_norm), _ptr(k_norm), eps,
-        norm_after | interleaved << 1 | use_hadamard << 2, _ptr(q_out), so, kv, _ptr(k_scale),
+        (1 if norm_after else 0) + (2 if interleaved else 0) + (4 if use_hadamard else 0), _ptr(q_out), so, kv, _ptr(k_scale),
         _ptr(v_scale), _ptr(k_pool), _ptr(v_pool), num_pages, 64, _ptr(status), _stream(stream))
     if rc != 0:
         _check(rc, "hpa_store_qkv")
@@ -843,13 +868,6 @@ def hpa_assign_pages_workspace(B: int, num_rows: int) -> int:
     return int(lib().hpa_assign_pages_workspace(B, num_rows))
 
 
-def _i32(t, name, n=None):
-    _dev(t, name, torch.int32)
-    if n is not None and t.numel() != n:
-        raise HpaError("%s needs %d entries, got %d" % (name, n, t.numel()))
-    return t
-
-
 def hpa_assign_pages(seq_lens, new_tokens, table, held, free_pages, free_count, page_indptr,
                      page_indices, slots, positions, workspace, rows=None, pos_offset=None,
                      held_out=None, free_count_out=None, status=None, stream=None):
@@ -861,46 +879,53 @@ def hpa_assign_pages(seq_lens, new_tokens, table, held, free_pages, free_count, 
     State: table int32 [num_rows][max pages], held int32 [num_rows], free_pages int32
     [num_pages], free_count int32 [1]; updated in place, or held and free_count into held_out and
     free_count_out.  rows (int32 [B]): the table row of each request, by default 0 .. B - 1."""
-    B = _i32(seq_lens, "seq_lens").numel()
-    _dev(table, "table", torch.int32)
+    held_out = held if held_out is None else held_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    for t, name in ((seq_lens, "seq_lens"), (table, "table"), (held, "held"),
+                    (free_pages, "free_pages"), (free_count, "free_count"),
+                    (page_indptr, "page_indptr"), (page_indices, "page_indices")):
+        if t is None:
+            raise HpaError("%s must be a contiguous CUDA tensor" % name)
+    _devs(torch.int32, "seq_lens table held held_out free_pages free_count free_count_out "
+          "page_indptr page_indices new_tokens positions rows pos_offset status",
+          (seq_lens, table, held, held_out, free_pages, free_count, free_count_out, page_indptr,
+           page_indices, new_tokens, positions, rows, pos_offset, status))
+    _dev(workspace, "workspace")
+    B = seq_lens.numel()
     if table.dim() != 2:
         raise HpaError("table must be int32 [num_rows][max pages]")
     num_rows, stride = table.shape
-    held_out = held if held_out is None else held_out
-    free_count_out = free_count if free_count_out is None else free_count_out
-    _i32(held, "held", num_rows)
-    _i32(held_out, "held_out", num_rows)
-    _i32(free_count, "free_count", 1)
-    _i32(free_count_out, "free_count_out", 1)
-    _i32(free_pages, "free_pages")
-    _i32(page_indptr, "page_indptr", B + 1)
-    _i32(page_indices, "page_indices")
-    if rows is not None:
-        _i32(rows, "rows", B)
-    elif B > num_rows:
-        raise HpaError("%d requests without rows in a table of %d rows" % (B, num_rows))
-    if pos_offset is not None:
-        _i32(pos_offset, "pos_offset", B)
-    if (new_tokens is None) != (slots is None) or (slots is None) != (positions is None):
-        raise HpaError("new_tokens, slots and positions go together")
+    if held.numel() != num_rows or held_out.numel() != num_rows:
+        raise HpaError("held and held_out need one count for each of %d rows" % num_rows)
+    if free_count.numel() != 1 or free_count_out.numel() != 1:
+        raise HpaError("free_count and free_count_out are one number each")
+    if page_indptr.numel() != B + 1:
+        raise HpaError("page_indptr must have B + 1 = %d entries" % (B + 1))
+    if rows is None:
+        if B > num_rows:
+            raise HpaError("%d requests without rows in a table of %d rows" % (B, num_rows))
+    elif rows.numel() != B:
+        raise HpaError("rows needs one value per request")
+    if pos_offset is not None and pos_offset.numel() != B:
+        raise HpaError("pos_offset needs one value per request")
     tokens = 0
-    if new_tokens is not None:
-        _i32(new_tokens, "new_tokens", B)
+    if new_tokens is not None and slots is not None and positions is not None:
         _dev(slots, "slots", torch.int64)
         tokens = slots.numel()
-        _i32(positions, "positions", tokens)
-    _dev(workspace, "workspace")
-    if status is not None:
-        _i32(status, "status")
+        if new_tokens.numel() != B or positions.numel() != tokens:
+            raise HpaError("new_tokens needs one value per request, positions one per slot")
+    elif not (new_tokens is None and slots is None and positions is None):
+        raise HpaError("new_tokens, slots and positions go together")
     _one_device(seq_lens, new_tokens, table, held, held_out, free_pages, free_count,
                 free_count_out, page_indptr, page_indices, slots, positions, workspace, rows,
                 pos_offset, status)
     rc = lib().hpa_assign_pages(
-        _ptr(seq_lens), _ptr(new_tokens), _ptr(rows), _ptr(pos_offset), B, num_rows, _ptr(table),
-        stride, _ptr(held), _ptr(held_out), _ptr(free_pages), _ptr(free_count),
-        _ptr(free_count_out), free_pages.numel(), 64, _ptr(page_indptr), _ptr(page_indices),
-        page_indices.numel(), _ptr(slots), _ptr(positions), tokens, _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+        seq_lens.data_ptr(), _ptr(new_tokens), _ptr(rows), _ptr(pos_offset), B, num_rows,
+        table.data_ptr(), stride, held.data_ptr(), held_out.data_ptr(), free_pages.data_ptr(),
+        free_count.data_ptr(), free_count_out.data_ptr(), free_pages.numel(), 64,
+        page_indptr.data_ptr(), page_indices.data_ptr(), page_indices.numel(), _ptr(slots),
+        _ptr(positions), tokens, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _ptr(status), _stream(stream))
     if rc != 0:
         _check(rc, "hpa_assign_pages")
 
