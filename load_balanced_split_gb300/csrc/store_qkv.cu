@@ -67,36 +67,39 @@ __device__ __forceinline__ uint32_t pack_e2m1(const float (&v)[8]) {
   return r;
 }
 
+// A warp's items follow one another: token by token, its chunks of q, k and v heads in turn.
 struct Item {
-  int tok, kind, h0, nh;  // token, q / k / v, first head, heads
+  int tok, ch;            // token, chunk of it
+  int kind, h0, nh;       // q / k / v, first head, heads
   int pos, place;         // position; slot % PAGE
   int page;               // -1: the token is skipped
+  bool fresh;             // the warp's first item of its token: it brings the table row
 };
 
-struct Walk {
-  int n_chunks, cq, ck, d_tok, d_ch, n;
+struct Chunks {
+  int cq, ck, n;  // chunks of q and of k (or v) heads, and of a token
 };
 
-__device__ __forceinline__ Item item_at(const StoreQkvParams &p, const Walk &w, int tok, int ch,
-                                        bool report) {
-  Item x;
-  x.tok = tok;
-  x.kind = ch < w.cq ? KIND_Q : ch < w.cq + w.ck ? KIND_K : KIND_V;
-  const int c = x.kind == KIND_Q ? ch : x.kind == KIND_K ? ch - w.cq : ch - w.cq - w.ck;
+__device__ __forceinline__ void set_chunk(const StoreQkvParams &p, const Chunks &w, Item &x) {
+  x.kind = x.ch < w.cq ? KIND_Q : x.ch < w.cq + w.ck ? KIND_K : KIND_V;
+  const int c = x.ch - (x.kind == KIND_Q ? 0 : x.kind == KIND_K ? w.cq : w.cq + w.ck);
   x.h0 = c * kChunkHeads;
   x.nh = min(kChunkHeads, (x.kind == KIND_Q ? p.Hq : p.Hkv) - x.h0);
-  const long long slot = p.slots[tok];
-  x.pos = p.positions[tok];
+}
+
+__device__ __forceinline__ void set_token(const StoreQkvParams &p, Item &x, bool report) {
+  const long long slot = p.slots[x.tok];
+  x.pos = p.positions[x.tok];
   x.place = static_cast<int>(slot & (PAGE - 1));
   const bool page_ok = slot >= 0 && slot / PAGE < p.num_pages;
   const bool pos_ok = p.rot_dim == 0 || (x.pos >= 0 && x.pos < p.max_pos);
   x.page = page_ok && pos_ok ? static_cast<int>(slot / PAGE) : -1;
-  if (report && ch == 0 && p.status && slot != -1 && x.page < 0)
+  x.fresh = true;
+  if (report && x.ch == 0 && p.status && slot != -1 && x.page < 0)
     atomicOr(reinterpret_cast<int *>(p.status), page_ok ? HPA_STATUS_BAD_SEQLEN : HPA_STATUS_BAD_PAGE);
-  return x;
 }
 
-// Start an item's rows and its token's table row on their way into a slot.
+// Start an item's rows and, with its token's first, the table row on their way into a slot.
 template <int ROPE>
 __device__ __forceinline__ void fetch(const StoreQkvParams &p, const Item &x, uint32_t slot,
                                       int lane) {
@@ -104,9 +107,15 @@ __device__ __forceinline__ void fetch(const StoreQkvParams &p, const Item &x, ui
   const __nv_bfloat16 *src = (x.kind == KIND_Q   ? p.q + x.tok * p.q_stride
                               : x.kind == KIND_K ? p.k + x.tok * p.k_stride
                                                  : p.v + x.tok * p.v_stride) +
-                             x.h0 * HEAD_DIM;
-  for (int c = lane; c < x.nh * (kRowBytes / 16); c += 32) cp_async16(slot + 16 * c, src + 8 * c);
-  if (ROPE != ROPE_NONE && x.kind != KIND_V && lane < p.rot_dim / 4)
+                             x.h0 * HEAD_DIM + 8 * lane;
+  if (x.nh == kChunkHeads) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) cp_async16(slot + 16 * lane + 512 * u, src + 256 * u);
+  } else {
+    for (int c = lane; c < x.nh * (kRowBytes / 16); c += 32)
+      cp_async16(slot + 16 * c, src + 8 * (c - lane));
+  }
+  if (ROPE != ROPE_NONE && x.fresh && x.kind != KIND_V && lane < p.rot_dim / 4)
     cp_async16(slot + kCosOff + 16 * lane,
                p.cos_sin + static_cast<int64_t>(x.pos) * p.rot_dim + 4 * lane);
 }
@@ -298,21 +307,28 @@ __device__ __forceinline__ void store_row(void *pool, int kv_dtype, int64_t unit
   }
 }
 
+// What a lane keeps from item to item: its table entries and its norm weights.
 template <int ROPE>
-__device__ __forceinline__ void work(const StoreQkvParams &p, const Item &x, uint32_t slot,
-                                     uint32_t norms, int lane) {
+struct Kept {
+  Turn<ROPE> t;
+  f32x2 w[8];
+  int w_kind;
+};
+
+template <int ROPE>
+__device__ __forceinline__ void work(const StoreQkvParams &p, const Item &x, Kept<ROPE> &kept,
+                                     uint32_t slot, uint32_t norms, int lane) {
   const int k = lane % kLanesPerHead, hp = lane / kLanesPerHead;
   const bool key_like = x.kind != KIND_V;
   const bool has_norm = x.kind == KIND_Q ? p.q_norm != nullptr : p.k_norm != nullptr;
-  Turn<ROPE> t;
-  f32x2 w[8];
-  if (key_like) {
-    load_turn<ROPE>(t, slot + kCosOff, k, p.rot_dim);
-    if (has_norm) {
-      const uint32_t at = norms + (x.kind == KIND_K) * (HEAD_DIM * 4) + 32 * k;
-      lds_f32x8(at, reinterpret_cast<f32x2(&)[4]>(w[0]));
-      lds_f32x8(at + 256, reinterpret_cast<f32x2(&)[4]>(w[4]));
-    }
+  Turn<ROPE> &t = kept.t;
+  f32x2(&w)[8] = kept.w;
+  if (key_like && x.fresh) load_turn<ROPE>(t, slot + kCosOff, k, p.rot_dim);
+  if (key_like && has_norm && kept.w_kind != x.kind) {
+    const uint32_t at = norms + (x.kind == KIND_K) * (HEAD_DIM * 4) + 32 * k;
+    lds_f32x8(at, reinterpret_cast<f32x2(&)[4]>(w[0]));
+    lds_f32x8(at + 256, reinterpret_cast<f32x2(&)[4]>(w[4]));
+    kept.w_kind = x.kind;
   }
 #pragma unroll 1
   for (int ps = 0; ps * kHeadsPerPass < x.nh; ++ps) {
@@ -364,7 +380,10 @@ __device__ __forceinline__ void work(const StoreQkvParams &p, const Item &x, uin
 }
 
 template <int ROPE>
-__global__ void __launch_bounds__(kWarps * 32, 2) store_qkv_kernel(const StoreQkvParams p) {
+#ifndef SMB
+#define SMB 2
+#endif
+__global__ void __launch_bounds__(kWarps * 32, SMB) store_qkv_kernel(const StoreQkvParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
@@ -376,33 +395,43 @@ __global__ void __launch_bounds__(kWarps * 32, 2) store_qkv_kernel(const StoreQk
   __syncthreads();
   const uint32_t norms = smem_u32(smem);
   const uint32_t slots = norms + kNormBytes + warp * kSlots * kSlotBytes;
-  Walk w;
+  Chunks w;
   w.cq = p.q ? (p.Hq + kChunkHeads - 1) / kChunkHeads : 0;
   w.ck = p.k ? (p.Hkv + kChunkHeads - 1) / kChunkHeads : 0;
-  w.n_chunks = w.cq + 2 * w.ck;
-  const int64_t n_items = static_cast<int64_t>(p.num_tokens) * w.n_chunks;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
-  int64_t it = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  if (it >= n_items) return;
-  w.d_tok = static_cast<int>(stride / w.n_chunks);
-  w.d_ch = static_cast<int>(stride % w.n_chunks);
-  int tok = static_cast<int>(it / w.n_chunks), ch = static_cast<int>(it % w.n_chunks);
-  Item cur = item_at(p, w, tok, ch, lane == 0);
+  w.n = w.cq + 2 * w.ck;
+  // equal shares of the items, each a run of its own: a token's table row, place and weights are
+  // then read once for its (usually ten) items
+  const int64_t n_items = static_cast<int64_t>(p.num_tokens) * w.n;
+  const int64_t n_warps = static_cast<int64_t>(gridDim.x) * kWarps;
+  const int64_t mine = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  const int64_t begin = n_items * mine / n_warps;
+  const int count = static_cast<int>(n_items * (mine + 1) / n_warps - begin);
+  if (count <= 0) return;
+  Item cur;
+  cur.tok = static_cast<int>(begin / w.n);
+  cur.ch = static_cast<int>(begin % w.n);
+  set_chunk(p, w, cur);
+  set_token(p, cur, lane == 0);
   fetch<ROPE>(p, cur, slots, lane);
   cp_async_commit();
-  for (int buf = 0; it < n_items; it += stride, buf ^= 1) {
+  Kept<ROPE> kept;
+  kept.w_kind = -1;
+  for (int i = 0, buf = 0; i < count; ++i, buf ^= 1) {
     Item nxt = cur;
-    if (it + stride < n_items) {
-      tok += w.d_tok;
-      ch += w.d_ch;
-      if (ch >= w.n_chunks) ch -= w.n_chunks, ++tok;
-      nxt = item_at(p, w, tok, ch, lane == 0);
+    if (i + 1 < count) {
+      nxt.fresh = false;
+      if (++nxt.ch == w.n) {
+        nxt.ch = 0;
+        ++nxt.tok;
+        set_token(p, nxt, lane == 0);
+      }
+      set_chunk(p, w, nxt);
       fetch<ROPE>(p, nxt, slots + (buf ^ 1) * kSlotBytes, lane);
     }
     cp_async_commit();
     cp_async_wait<1>();  // this item's group has landed (the next one may still fly)
     __syncwarp();
-    if (cur.page >= 0) work<ROPE>(p, cur, slots + buf * kSlotBytes, norms, lane);
+    if (cur.page >= 0) work<ROPE>(p, cur, kept, slots + buf * kSlotBytes, norms, lane);
     __syncwarp();  // every lane is done with this slot before it is refilled
     cur = nxt;
   }
