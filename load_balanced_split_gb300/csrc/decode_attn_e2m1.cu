@@ -41,18 +41,26 @@
 namespace hpa {
 namespace {
 
-// Up to 8 query rows (NT = 1): 5 consumer warps and 10 stages, two CTAs per SM, so 12 warps share
-// the register file at 168 each (4 and 8: 66 us on 32 x 8192 keys, 5 and 10: 62).  Up to 16
-// rows (NT = 2) the fewer warps leave the partitions twice as many CTAs.
+// Query rows in tiles of 8 columns, and what was measured best for each number of them (32 x
+// 8192 keys with 8 rows; 64 x 20000 with 16; 13 x 20011 with 20):
+//   1 tile:  5 consumer warps, two CTAs per SM, 168 registers (4 warps 66 us, 5 warps 62);
+//   2 tiles: 4 and two; the query fragments in shared memory and the softmax over two groups of
+//            16 keys at a time, for the registers' sake (353 -> 347 us);
+//   3 tiles: 7 and one, 255 registers: one pass for up to 24 rows (two passes of 2 tiles 153 us,
+//            4 warps at 168 registers with spills 184, this 101).
 template <int NT>
 struct Cfg {
-  static constexpr int kWarps = NT == 1 ? 5 : 4;  // consumer warps
+  static constexpr int kWarps = NT == 1 ? 5 : NT == 2 ? 4 : 7;  // consumer warps
+  static constexpr int kBlocks = NT == 3 ? 1 : 2;                // CTAs per SM
   static constexpr int kStages = 2 * kWarps;
   // A warp meets the same stages again.  Copies may land out of order, so a warp that came to a
   // stage whose page before it, another warp's, had not landed would take that page's phase for
   // the end of its own.
   static_assert(kStages % kWarps == 0, "each stage belongs to one warp");
   static constexpr int kThreads = (kWarps + 1) * 32;
+  static constexpr int kGroups = NT == 2 ? 2 : 4;  // groups of 16 keys that share a softmax step
+  static constexpr int kSide = NT == 1 ? 1 : 2;    // and those whose chains of MMAs run side by side
+  static constexpr bool kSharedQ = NT > 1;         // query fragments in shared memory
 };
 constexpr int kUnit = E2M1_UNIT;  // bytes of one page and KV head of K or V
 constexpr int kStageBytes = 2 * kUnit;
@@ -65,13 +73,14 @@ template <int NT>
 struct Smem {
   static constexpr int kWarps = Cfg<NT>::kWarps, kStages = Cfg<NT>::kStages;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kBufs = kWarps > 4 ? 4 : 2;
+  static constexpr int kBufs = NT == 1 ? 4 : 2;  // merge buffers
   static constexpr int kQSlot = kRows * kQRowBytes;
   static constexpr int kMerge = kStages * kStageBytes;               // float[kBufs][kRows][stride]
   static constexpr int kStats = kMerge + kBufs * kRows * kMergeStride * 4;  // m, l: [warps][kRows]
   static constexpr int kQ = kStats + 2 * kWarps * kRows * 4;         // two query slots
   static constexpr int kInfo = kQ + 2 * kQSlot;                      // int4[2]
-  static constexpr int kBars = kInfo + 2 * 16;  // full[stages] empty[stages] qfull[2] qempty[2]
+  static constexpr int kFrag = kInfo + 2 * 16;                       // query fragments, factors
+  static constexpr int kBars = kFrag + (Cfg<NT>::kSharedQ ? NT * 8 * 256 + kRows * 4 : 0);  // full[stages] empty[stages] qfull[2] qempty[2]
   static constexpr int kFlag = kBars + (2 * kStages + 4) * 8;
   static constexpr int kAlloc = kFlag + 16;
 };
@@ -106,6 +115,13 @@ __device__ __forceinline__ uint32_t both_halves(uint32_t a) {
   if (HI) asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(d) : "r"(a));
   else asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(d) : "r"(a));
   return d;
+}
+
+__device__ __forceinline__ void lds64(uint32_t addr, uint32_t &a, uint32_t &b) {
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
+}
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
 // Transpose of an 8x8 matrix of 16-bit elements held a row of pairs per lane quad.
@@ -316,11 +332,16 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
 
     // Query rows as the B operand: lane (g, c) holds dims [32 c, 32 c + 32) of rows 8 nt + g,
     // scaled by 2^e of the row; sl holds what takes the scores of its columns to log2 units.
-    uint32_t qf[NT][8][2];
+    // From 9 rows on the fragments lie in shared memory, one warp's work for all.
+    constexpr bool QS = Cfg<NT>::kSharedQ;
+    uint32_t qf[QS ? 1 : NT][8][2];
+    const uint32_t frag = base + S::kFrag + lane * 8;
+    float *factor = reinterpret_cast<float *>(smem + S::kFrag + NT * 8 * 256);
     float sl[2 * NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = 8 * nt + g;
+      if (QS && w != nt) continue;
+      const int row = 8 * nt + g, at = QS ? 0 : nt;
       const uint32_t qa = base + S::kQ + slot * S::kQSlot + row * kQRowBytes + c * 64;
       uint4 raw[4];
       float am = 0.f;
@@ -340,12 +361,23 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
         const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
         for (int u = 0; u < 4; ++u)  // elements 8 i + 2 u, + 1: k-step 2 i + u / 2, register u % 2
-          qf[nt][2 * i + (u >> 1)][u & 1] = pack_f16(__uint_as_float(x[u] << 16) * up,
+          qf[at][2 * i + (u >> 1)][u & 1] = pack_f16(__uint_as_float(x[u] << 16) * up,
                                                      __uint_as_float(x[u] & 0xffff0000u) * up);
       }
       const float down = sl2 == 0.f ? 1.f : fabsf(sl2) * exp2i(-e);
-      sl[2 * nt] = __shfl_sync(kFull, down, 8 * c);
-      sl[2 * nt + 1] = __shfl_sync(kFull, down, 8 * c + 4);
+      if (QS) {
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) sts64(frag + (nt * 8 + ks) * 256, qf[0][ks][0], qf[0][ks][1]);
+        if (c == 0) factor[row] = down;
+      } else {
+        sl[2 * nt] = __shfl_sync(kFull, down, 8 * c);
+        sl[2 * nt + 1] = __shfl_sync(kFull, down, 8 * c + 4);
+      }
+    }
+    if (QS) {
+      named_barrier(1, kWarps * 32);
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i) sl[i] = factor[8 * (i >> 1) + 2 * c + (i & 1)];
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(qempty0 + 8 * slot);  // the slot may be refilled
@@ -363,8 +395,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
     // One page of this warp; EDGE looks for keys that some row does not see.
     auto page = [&](int pg, int stage, uint32_t phase, auto edge_tag) {
       constexpr bool EDGE = decltype(edge_tag)::value;
-      constexpr int KG = 4;          // groups of 16 keys that share a softmax step
-      constexpr int KP = NT == 1 ? 1 : 2;  // and those whose chains of MMAs run side by side
+      constexpr int KG = Cfg<NT>::kGroups, KP = Cfg<NT>::kSide;
       const bool got = !(*abort_flag) && mbar_wait_bounded(full0 + 8 * stage, phase);
       if (!__all_sync(kFull, got)) {
         ok = false;
@@ -399,7 +430,15 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
             sc[kq][u][1] = both_halves<1>(two);
           }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // a word: 8 dims, two k-steps
+        for (int i = 0; i < 4; ++i) {  // a word: 8 dims, two k-steps
+          uint32_t qb[2][NT][2];
+#pragma unroll
+          for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (QS) lds64(frag + (nt * 8 + 2 * i + st) * 256, qb[st][nt][0], qb[st][nt][1]);
+              else qb[st][nt][0] = qf[nt][2 * i + st][0], qb[st][nt][1] = qf[nt][2 * i + st][1];
+            }
 #pragma unroll
           for (int kq = 0; kq < KP; ++kq) {
             uint32_t a[2][4];
@@ -416,9 +455,10 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
                                       a[1][2 * st + 1]};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma_f16(x[kp + kq][nt], af, qf[nt][2 * i + st][0], qf[nt][2 * i + st][1]);
+                mma_f16(x[kp + kq][nt], af, qb[st][nt][0], qb[st][nt][1]);
             }
           }
+        }
       }
       // what a row does not see to -inf (x is the plain sum; x * sl the score in log2 units)
       if (EDGE) {
@@ -651,7 +691,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
 }
 
 template <int NT, bool WIN>
-__global__ void __launch_bounds__(Cfg<NT>::kThreads, 2)
+__global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kBlocks)
     decode_attn_e2m1_kernel(const uint8_t *__restrict__ k_pool, const uint8_t *__restrict__ v_pool,
                             const AttnParams p) {
   using S = Smem<NT>;
@@ -733,10 +773,10 @@ int occupancy(int *ctas) {
 
 }  // namespace
 
-// Query rows of a KV head in groups of equal size, up to 16: CTAs that share pages keep pace and
+// Query rows of a KV head in groups of equal size, up to 24: CTAs that share pages keep pace and
 // find them in L2.
 int attn_e2m1_group(int rows) {
-  const int groups = (rows + MAX_ROWS - 1) / MAX_ROWS;
+  const int groups = (rows + 23) / 24;
   return (rows + groups - 1) / groups;
 }
 
@@ -744,11 +784,14 @@ cudaError_t launch_decode_attn_e2m1(const AttnParams &p, const void *k_pool, con
                                     cudaStream_t s) {
   if (p.group <= 8)
     return p.window ? launch<1, true>(p, k_pool, v_pool, s) : launch<1, false>(p, k_pool, v_pool, s);
-  return p.window ? launch<2, true>(p, k_pool, v_pool, s) : launch<2, false>(p, k_pool, v_pool, s);
+  if (p.group <= 16)
+    return p.window ? launch<2, true>(p, k_pool, v_pool, s) : launch<2, false>(p, k_pool, v_pool, s);
+  return p.window ? launch<3, true>(p, k_pool, v_pool, s) : launch<3, false>(p, k_pool, v_pool, s);
 }
 
 int attn_e2m1_ctas_per_sm(int rows, int *ctas) {
-  return attn_e2m1_group(rows) <= 8 ? occupancy<1>(ctas) : occupancy<2>(ctas);
+  const int group = attn_e2m1_group(rows);
+  return group <= 8 ? occupancy<1>(ctas) : group <= 16 ? occupancy<2>(ctas) : occupancy<3>(ctas);
 }
 
 }  // namespace hpa
