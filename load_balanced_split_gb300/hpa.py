@@ -1059,6 +1059,8 @@ def decode_step(ws: Workspace, q, k_pool, v_pool, seq_lens, page_indptr, page_in
         raise HpaError("hpa_key_weights has no 4-bit form")
     stream = _stream(stream)
     if plan:
+        if tile is None and ws.window is None and _is_e2m1(k_pool):
+            tile = 256      # 4-bit pages: as long a read as 128 keys of 8 bits (1 x 100000: 35 -> 33 us)
         ws.plan(seq_lens, tile, stream)
     if fused:
         hpa_decode_attn_fused(q, k_pool, v_pool, page_indptr, page_indices, ws.taskmap,

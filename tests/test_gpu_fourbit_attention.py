@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import load_balanced_split_gb300 as hpa
-from bounded_helpers import check_attention
+from bounded_helpers import check_attention, lse_bound, out_bound
 from fourbit_helpers import make_batch, poison_hidden, rows_of, step
 from gpu_helpers import DeviceBatch
 from oracle import bounded
@@ -48,3 +48,232 @@ def test_one_long_request_and_a_large_batch():
     _run([70000], 2, heads=(8, 1), seed=3)
     g = np.random.default_rng(4)
     _run(list(g.integers(1, 300, size=400)), 1, heads=(4, 1), seed=4)
+
+
+@pytest.mark.parametrize("window,sinks", [(None, 0), (70, 0), (5, 130)])
+@pytest.mark.parametrize("heads,q_len", [((8, 2), 3), ((8, 1), 2), ((40, 8), 4)])
+def test_nan_scales_reach_only_the_rows_that_see_them(window, sinks, heads, q_len):
+    """A NaN block scale of a value marks its 16 dims of the rows that see the key, one of a key
+    the whole row; all other rows are as without it."""
+    lens = [200, 131, 64 + q_len]
+    for which in ("v", "k"):
+        b = make_batch(lens, q_len, heads, seed=21)
+        poison_hidden(b, window, sinks)
+        bad = []
+        for r, L in enumerate(lens):
+            # the last key (one token sees it), the first token's, and one at the windows' start
+            for i in {L - 1, L - q_len, max(0, L - (window or 0) - 1), max(0, L - (window or 0))}:
+                h, block = i % b.Hkv, (5 * i + r) % 8
+                page = int(b.page_indices[int(b.page_indptr[r]) + i // 64])
+                bad.append((r, i, h, block, page))
+        ref = bounded.attention_rows(b, window, sinks)
+        for r, i, h, block, page in bad:
+            rows_of(b.k_pool if which == "k" else b.v_pool)[1][page, h, i % 64, block] = 0x7F
+        ws, out, lse = step(b, DeviceBatch(b), window, sinks)
+        torch.cuda.synchronize()
+        assert ws.status() == 0
+        want, seen = ref[0].copy(), np.zeros(ref[1].shape, bool)
+        G = b.Hq // b.Hkv
+        for r, i, h, block, page in bad:
+            for j in range(q_len):
+                if bounded.sees(lens[r], q_len, j, i, window, sinks):
+                    dims = slice(16 * block, 16 * block + 16) if which == "v" else slice(None)
+                    want[r, j, h * G:(h + 1) * G, dims] = np.nan
+                    seen[r, j, h * G:(h + 1) * G] = which == "k"
+        got, l = out.float().cpu().numpy(), lse.cpu().numpy()
+        assert (np.isnan(got) == np.isnan(want)).all()
+        fine = ~np.isnan(want)
+        bound = out_bound(ref[0], ref[2], ref[3], "e2m1")
+        assert (np.abs(got - want)[fine] <= bound[fine]).all()
+        assert (np.abs(l - ref[1])[~seen] <= lse_bound(ref[1], ref[3])[~seen]).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_query_row_stays_alone(bad):
+    b = make_batch([300, 70], 2, (16, 2), seed=22)
+    ref = bounded.attention_rows(b)
+    b.q[0, 1, 3, 77] = bad
+    b.q[1, 0, 12, 0] = bad
+    ws, out, lse = step(b, DeviceBatch(b))
+    got = out.float().cpu().numpy()
+    hit = np.zeros(got.shape[:3], bool)
+    hit[0, 1, 3] = hit[1, 0, 12] = True
+    assert np.isnan(got[hit]).all()
+    bound = out_bound(ref[0], ref[2], ref[3], "e2m1")
+    assert (np.abs(got - ref[0])[~hit] <= bound[~hit]).all()
+
+
+@pytest.mark.parametrize("case", ["large", "tiny", "mixed_rows", "negative", "zero"])
+def test_query_scales(case):
+    b = make_batch([500, 64, 130], 2, (16, 2), seed=23)
+    sm, q = 1 / np.sqrt(128), b.q.float()
+    if case == "large":
+        q, sm = q * 1e5, sm / 1e5
+    elif case == "tiny":
+        q, sm = q * 1e-6, sm * 1e6
+    elif case == "mixed_rows":
+        q[:, :, ::3] *= 1e5
+        q[:, :, 1::3] *= 1e-6
+    else:
+        sm = -sm if case == "negative" else 0.0
+    b.q = q.to(torch.bfloat16)
+    ws, out, lse = step(b, DeviceBatch(b), sm_scale=sm)
+    torch.cuda.synchronize()
+    check_attention(b, out, lse, bounded.attention_rows(b, sm_scale=sm), "e2m1")
+
+
+@pytest.mark.parametrize("kind", ["static", "weighted"])
+def test_other_plans(kind):
+    b = make_batch([900, 33, 1500, 64], 1, (16, 2), seed=24)
+    db = DeviceBatch(b)
+    more = dict(splits=3) if kind == "static" else dict(num_ctas=7, weighted=True)
+    ws = hpa.Workspace(b.B, 1, b.Hq, 128, Hkv=b.Hkv, **more)
+    out = torch.empty(b.q.shape, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(b.q.shape[:3], device="cuda")
+    hpa.decode_step(ws, db.q, db.k, db.v, db.lens, db.indptr, db.indices, out, lse, db.ks, db.vs,
+                    tile=128)
+    check_attention(b, out, lse, bounded.attention_rows(b), "e2m1")
+
+
+def test_same_bits_again_and_without_allocation():
+    b = make_batch([3000, 200, 64, 1000], 2, (16, 2), seed=25)
+    db = DeviceBatch(b)
+    ws, out, lse = step(b, db)
+    first = out.clone(), lse.clone()
+    for _ in range(3):
+        hpa.decode_step(ws, db.q, db.k, db.v, db.lens, db.indptr, db.indices, out, lse, db.ks, db.vs)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    out.zero_()
+    hpa.hpa_decode_attn_combine_noalloc(db.q, db.k, db.v, db.indptr, db.indices, ws.taskmap,
+                                        ws.num_ctas, out, lse, db.ks, db.vs)
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+def test_captured_and_on_two_streams():
+    b, b2 = make_batch([700, 90], 1, (16, 2), seed=26), make_batch([400, 1300], 3, (16, 2), seed=27)
+    db, db2 = DeviceBatch(b), DeviceBatch(b2)
+    refs = bounded.attention_rows(b), bounded.attention_rows(b2)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        r1, r2 = step(b, db, stream=s1), step(b2, db2, stream=s2)
+    torch.cuda.synchronize()
+    check_attention(b, r1[1], r1[2], refs[0], "e2m1")
+    check_attention(b2, r2[1], r2[2], refs[1], "e2m1")
+    ws, out, lse = r1
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s1):
+        hpa.decode_step(ws, db.q, db.k, db.v, db.lens, db.indptr, db.indices, out, lse, db.ks, db.vs)
+    out.zero_(), lse.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    check_attention(b, out, lse, refs[0], "e2m1")
+
+
+def test_pages_past_32_bit_offsets():
+    """A pool of 4.8 GB whose last pages and those past 2^31 and 2^32 bytes are read."""
+    b = make_batch([400, 300], 1, (8, 8), seed=28)
+    P, unit = 130000, 8 * 4608
+    far = [P - 1, (1 << 31) // unit, (1 << 31) // unit + 1, (1 << 32) // unit, (1 << 32) // unit + 1, 0]
+    far += [P - 2 - i for i in range(len(b.page_indices) - len(far))]
+    ref = bounded.attention_rows(b)
+    db = DeviceBatch(b)
+    big = []
+    for pool in (db.k, db.v):
+        t = torch.full((P, 8, 4608), 0x7F, dtype=torch.uint8, device="cuda")
+        for old, new in zip(b.page_indices.tolist(), far):
+            t[new] = pool[old]
+        big.append(t)
+    db.k, db.v = big
+    db.indices = torch.tensor(far, dtype=torch.int32, device="cuda")
+    ws, out, lse = step(b, db)
+    check_attention(b, out, lse, ref, "e2m1")
+
+
+def test_errors_are_reported_and_the_result_is_nan():
+    def run(b, C=9, **kw):
+        db = DeviceBatch(b)
+        for k, v in kw.items():
+            setattr(db, k, v)
+        ws, out, lse = step(b, db, C=C)
+        torch.cuda.synchronize()
+        return ws.status(), out
+
+    b = make_batch([300, 70], 1, (16, 2), seed=29)
+    ix = torch.from_numpy(b.page_indices).cuda()
+    for at, bad in ((1, b.num_pages), (2, -1), (4, 2 ** 31 - 1)):
+        x = ix.clone()
+        x[at] = bad
+        status, out = run(b, indices=x)
+        assert status == 4 and torch.isnan(out).all()
+    short = torch.from_numpy(b.page_indptr).cuda()
+    short[1] -= 1                                  # a page list too short for its request
+    status, out = run(b, indptr=short)
+    assert status & 4 and torch.isnan(out).all()
+    b.seq_lens[1] = 2
+    b3 = make_batch([300, 70], 3, (16, 2), seed=29)
+    b3.seq_lens[1] = 2                             # fewer keys than new tokens
+    status, out = run(b3)
+    assert status == 1 and torch.isnan(out).all()
+
+
+def test_maps_of_other_calls_are_refused():
+    b = make_batch([300, 70], 2, (16, 2), seed=30)
+    db = DeviceBatch(b)
+    win, out, lse = step(b, db, 50, 3, C=6)
+    plain, _, _ = step(b, db, C=6)
+    torch.cuda.synchronize()
+    args = (db.q, db.k, db.v, db.indptr, db.indices)
+    for ws, kw, bit in ((win, {}, 32), (plain, dict(window=True), 32)):
+        ws.plan(db.lens)
+        hpa.hpa_decode_attn(*args, ws.taskmap, 6, ws.partial_o, ws.partial_lse, db.ks, db.vs, **kw)
+        assert ws.status() == bit
+    ws = plain
+    ws.plan(db.lens)
+    ws.taskmap[3] = 5                              # planned for another count
+    hpa.hpa_decode_attn(*args, ws.taskmap, 6, ws.partial_o, ws.partial_lse, db.ks, db.vs)
+    assert ws.status() == 2
+
+
+def test_guard_bands():
+    """Nothing is written outside the partials and the results."""
+    b = make_batch([800, 90, 64, 1], 3, (40, 8), seed=31)
+    db = DeviceBatch(b)
+    C = 11
+    ws = hpa.Workspace(b.B, b.q_len, b.Hq, 128, num_ctas=C, Hkv=b.Hkv)
+    n = ws.partial_lse.numel()
+    po = torch.full((n * 128 + 512,), 3.25, device="cuda")
+    pl = torch.full((n + 512,), 3.25, device="cuda")
+    ws.plan(db.lens)
+    hpa.hpa_decode_attn(db.q, db.k, db.v, db.indptr, db.indices, ws.taskmap, C, po[256:-256],
+                        pl[256:-256], db.ks, db.vs)
+    torch.cuda.synchronize()
+    S = int(ws.taskmap[5])
+    assert (po[:256] == 3.25).all() and (po[-256:] == 3.25).all()
+    assert (pl[:256] == 3.25).all() and (pl[-256:] == 3.25).all()
+    rows = b.q_len * b.Hq
+    assert (po[256 + S * rows * 128:] == 3.25).all() and (pl[256 + S * rows:] == 3.25).all()
+    assert not (pl[256:256 + S * rows] == 3.25).any()
+
+
+def test_calls_without_a_4bit_form_refuse_it():
+    b = make_batch([300, 70], 1, (16, 2), seed=32)
+    db = DeviceBatch(b)
+    ws = hpa.Workspace(b.B, 1, b.Hq, 128, num_ctas=5, Hkv=b.Hkv)
+    out = torch.empty(b.q.shape, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(b.q.shape[:3], device="cuda")
+    base = (db.q, db.k, db.v, db.lens, db.indptr, db.indices, out, lse, db.ks, db.vs)
+    for kw in (dict(fused=True), dict(tc=True), dict(mma=True), dict(allheads=True)):
+        with pytest.raises(hpa.HpaError, match="failed"):
+            hpa.decode_step(ws, *base, **kw)
+    acc = torch.zeros(b.num_pages, b.Hkv, 64, device="cuda")
+    with pytest.raises(hpa.HpaError, match="no 4-bit form"):
+        hpa.decode_step(ws, *base, acc=acc)
+    with pytest.raises(hpa.HpaError):
+        hpa.hpa_key_weights(db.q, lse, db.k, db.indptr, db.indices, ws.taskmap, 5, acc)
+    kept = torch.zeros(b.B, b.Hkv, 64, dtype=torch.int32, device="cuda")
+    with pytest.raises(hpa.HpaError):
+        hpa.hpa_evict_compact(db.k, db.v, db.indptr, db.indices, kept, db.lens.clone())
+    trace = torch.zeros(4 * 5 * 2, dtype=torch.int64, device="cuda")
+    with pytest.raises(hpa.HpaError, match="failed"):
+        hpa.hpa_decode_attn_traced(db.q, db.k, db.v, db.indptr, db.indices, ws.taskmap, 5,
+                                   ws.partial_o, ws.partial_lse, trace, db.ks, db.vs)
