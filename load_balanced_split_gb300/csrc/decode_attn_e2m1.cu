@@ -20,9 +20,9 @@
 //  * P moves from the first product's accumulator layout to the second's operand by movmatrix;
 //  * the softmax's running maximum moves only when a score passes it by 2^8 (as in the 8-bit
 //    kernel), so a page costs one vote and no exchange of maxima;
-//  * a warp takes whole pages, every fourth of its CTA: one wait, one vote and one release for
-//    64 keys.  One producer warp keeps a ring of pages in flight with bulk copies, two a page
-//    (codes and scales lie together).
+//  * a warp takes 32 or 64 keys of a page at a time, with one wait, vote and release.  One
+//    producer warp keeps a ring of pages in flight with bulk copies, two a page (codes and scales
+//    lie together).
 // Sums, softmax statistics and outputs are fp32.  Queries enter as f16, each row scaled by a power
 // of two that puts its largest element into [2^14, 2^15) (exact down to 2^-28 of it), and the
 // probabilities are rounded to f16 (2^-11 of each) as the second product's operand.
@@ -30,8 +30,8 @@
 // Windows with sink tokens (WIN): the producer maps the map's compact pages to real ones
 // (WinSpan), and pages at the window's ends mask by position.  Pages without a hidden key run a
 // copy of the loop without masks.  A code cannot be NaN but a block scale can: V scales of keys
-// that no token sees are taken as zero, and a key that some tokens see and others do not is
-// added for the rows that see it alone if its scales hold a NaN.
+// that no token sees are taken as zero, and a key that some tokens see and others do not marks
+// the rows that see it alone if its scales hold a NaN.
 #include <math_constants.h>
 
 #include <type_traits>
@@ -41,26 +41,32 @@
 namespace hpa {
 namespace {
 
-// Query rows in tiles of 8 columns, and what was measured best for each number of them (32 x
-// 8192 keys with 8 rows; 64 x 20000 with 16; 13 x 20011 with 20):
-//   1 tile:  5 consumer warps, two CTAs per SM, 168 registers (4 warps 66 us, 5 warps 62);
-//   2 tiles: 4 and two; the query fragments in shared memory and the softmax over two groups of
-//            16 keys at a time, for the registers' sake (353 -> 347 us);
-//   3 tiles: 7 and one, 255 registers: one pass for up to 24 rows (two passes of 2 tiles 153 us,
-//            4 warps at 168 registers with spills 184, this 101).
+// Query rows in tiles of 8 columns, and what was measured best for each number of them, in us (32 x
+// 8192 keys with 8 rows and 128 x 4096 in a window; 64 x 20000 with 16 rows and 64 x 2000 in a window;
+// 13 x 20011 with 20 rows):
+//   1 tile:  4 consumer warps in pairs that share a page, three CTAs per SM at 128 registers, 61 and
+//            113 (5 warps with a page each, two CTAs: 62 and 127; four to a page: 72 and 127);
+//   2 tiles: the same pairs, two CTAs at 168 registers, query fragments in shared memory, 351
+//            and 57 (a page each: 346, but 95 with the window: a segment's last pages, and its
+//            start, then leave warps idle for a page's time);
+//   3 tiles: 7 warps with a page each, one CTA at 255 registers: one pass for up to 24 rows, 101
+//            (two passes of 2 tiles 153, 4 warps at 168 registers with spills 184, pairs 127).
 template <int NT>
 struct Cfg {
-  static constexpr int kWarps = NT == 1 ? 5 : NT == 2 ? 4 : 7;  // consumer warps
-  static constexpr int kBlocks = NT == 3 ? 1 : 2;                // CTAs per SM
-  static constexpr int kStages = 2 * kWarps;
-  // A warp meets the same stages again.  Copies may land out of order, so a warp that came to a
-  // stage whose page before it, another warp's, had not landed would take that page's phase for
+  static constexpr int kWarps = NT == 3 ? 7 : 4;                 // consumer warps
+  static constexpr int kShare = NT == 3 ? 1 : 2;                 // warps of a team, which share a page
+  static constexpr int kTeams = kWarps / kShare;
+  static constexpr int kBlocks = NT == 1 ? 3 : NT == 2 ? 2 : 1;  // CTAs per SM
+  static constexpr int kStages = NT == 1 ? 6 : NT == 2 ? 8 : 14;
+  // A team meets the same stages again.  Copies may land out of order, so a warp that came to a
+  // stage whose page before it, another team's, had not landed would take that page's phase for
   // the end of its own.
-  static_assert(kStages % kWarps == 0, "each stage belongs to one warp");
+  static_assert(kWarps % kShare == 0 && kStages % kTeams == 0, "each stage belongs to one team");
   static constexpr int kThreads = (kWarps + 1) * 32;
-  static constexpr int kGroups = NT == 2 ? 2 : 4;  // groups of 16 keys that share a softmax step
-  static constexpr int kSide = NT == 1 ? 1 : 2;    // and those whose chains of MMAs run side by side
-  static constexpr bool kSharedQ = NT > 1;         // query fragments in shared memory
+  static constexpr int kMine = 4 / kShare;             // a page's groups of 16 keys for a warp
+  static constexpr int kGroups = NT == 3 ? 4 : 2;      // groups that share a softmax step
+  static constexpr int kSide = NT == 1 ? 1 : 2;        // groups whose chains of MMAs run side by side
+  static constexpr bool kSharedQ = NT > 1;             // query fragments in shared memory
 };
 constexpr int kUnit = E2M1_UNIT;  // bytes of one page and KV head of K or V
 constexpr int kStageBytes = 2 * kUnit;
@@ -73,7 +79,7 @@ template <int NT>
 struct Smem {
   static constexpr int kWarps = Cfg<NT>::kWarps, kStages = Cfg<NT>::kStages;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kBufs = NT == 1 ? 4 : 2;  // merge buffers
+  static constexpr int kBufs = 2;  // merge buffers
   static constexpr int kQSlot = kRows * kQRowBytes;
   static constexpr int kMerge = kStages * kStageBytes;               // float[kBufs][kRows][stride]
   static constexpr int kStats = kMerge + kBufs * kRows * kMergeStride * 4;  // m, l: [warps][kRows]
@@ -301,7 +307,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
   const int ks_off = 4096 + key_at(g) * 8 + 2 * c;
   const int vk0 = key_at(2 * c), vk1 = key_at(2 * c + 1);
 
-  int count = 0;  // pages of this CTA so far: page n goes to warp n % kWarps, stage n % kStages
+  int count = 0;  // pages of this CTA so far: page n goes to team n % kTeams, stage n % kStages
   const int n_items = head.s_end - head.s_begin;
   for (int k = 0; k < n_items; ++k) {
     const int s = head.s_begin + k, slot = k & 1;
@@ -405,7 +411,8 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
       const int key0 = (WIN ? win.real_page(pg) : pg) * PAGE;
 
 #pragma unroll
-      for (int k0 = 0; k0 < 4; k0 += KG) {
+      for (int kc = 0; kc < Cfg<NT>::kMine; kc += KG) {
+      const int k0 = (w % Cfg<NT>::kShare) * Cfg<NT>::kMine + kc;
       // S = K Q^T, 16 keys at a time
       float x[KG][NT][4];
 #pragma unroll
@@ -589,9 +596,10 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
       __syncwarp();
       if (lane == 0) mbar_arrive(empty0 + 8 * stage);
     };
-    // this warp's pages of the segment: page n of the CTA with n % kWarps == w
-    const int skip = (w + kWarps - count % kWarps) % kWarps, n_pages = f.pg1 - f.pg0;
-    for (int i = skip; i < n_pages && ok; i += kWarps) {
+    // this team's pages of the segment: page n of the CTA with n % kTeams == team
+    constexpr int kTeams = Cfg<NT>::kTeams;
+    const int skip = (w / Cfg<NT>::kShare + kTeams - count % kTeams) % kTeams, n_pages = f.pg1 - f.pg0;
+    for (int i = skip; i < n_pages && ok; i += kTeams) {
       const int n = count + i, stage = n % kStages, pg = f.pg0 + i;
       const uint32_t phase = (n / kStages) & 1;
       if (pg >= clear0 && pg < clear1) page(pg, stage, phase, std::false_type());
@@ -703,7 +711,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kBlocks)
   if (threadIdx.x == 0) {
     for (int st = 0; st < kStages; ++st) {
       mbar_init(base + S::kBars + 8 * st, 1);
-      mbar_init(base + S::kBars + 8 * (kStages + st), 1);
+      mbar_init(base + S::kBars + 8 * (kStages + st), Cfg<NT>::kShare);
     }
     for (int sl = 0; sl < 2; ++sl) {
       mbar_init(base + S::kBars + 8 * (2 * kStages + sl), 32);           // qfull
