@@ -67,6 +67,10 @@ struct Cfg {
   static constexpr int kGroups = NT == 3 ? 4 : 2;      // groups that share a softmax step
   static constexpr int kSide = NT == 1 ? 1 : 2;        // groups whose chains of MMAs run side by side
   static constexpr bool kSharedQ = NT > 1;             // query fragments in shared memory
+  // With 16 rows they fill the MMA's 16: S = Q K^T has P in the layout that the second product
+  // wants, without movmatrix, and a lane has 2 rows' statistics, not 4 (351 -> RMUS us).
+  static constexpr bool kRowsOnM = NT == 2;
+  static constexpr int kStats = kRowsOnM ? 2 : 2 * NT;
 };
 constexpr int kUnit = E2M1_UNIT;  // bytes of one page and KV head of K or V
 constexpr int kStageBytes = 2 * kUnit;
@@ -128,6 +132,10 @@ __device__ __forceinline__ void lds64(uint32_t addr, uint32_t &a, uint32_t &b) {
 }
 __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t a) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
 }
 
 // Transpose of an 8x8 matrix of 16-bit elements held a row of pairs per lane quad.
@@ -301,11 +309,24 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
     const int row = 8 * (i >> 1) + 2 * c + (i & 1);
     tok[i] = row < rows ? (rb + row) / G : q_len - 1;
   }
+  // The rows of the softmax's statistics, and of score e of x[.][i]: those columns, or with the
+  // rows on M 8 i + g; the key of that score, in its group of 16
+  constexpr bool RM = Cfg<NT>::kRowsOnM;
+  constexpr int NS = Cfg<NT>::kStats;
+  auto stat_row = [&](int i) { return RM ? 8 * i + g : 8 * (i >> 1) + 2 * c + (i & 1); };
+  auto stat_of = [](int i, int e) { return RM ? e >> 1 : 2 * i + (e & 1); };
+  int stat_tok[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+    stat_tok[i] = !RM ? tok[i % (2 * NT)] : stat_row(i) < rows ? (rb + stat_row(i)) / G : q_len - 1;
   // where this lane's shares of a page lie: K rows key_at(g) (+8), dims 32 c..; V keys of the
   // quad's lane c, dims 16 g..; their scales
   const int k_off = key_at(g) * 64 + c * 16;
   const int ks_off = 4096 + key_at(g) * 8 + 2 * c;
   const int vk0 = key_at(2 * c), vk1 = key_at(2 * c + 1);
+  auto key_of = [&](int i, int e) {
+    return RM ? 8 * i + (e & 1 ? vk1 : vk0) : key_at(g) + 8 * (e >> 1);
+  };
 
   int count = 0;  // pages of this CTA so far: page n goes to team n % kTeams, stage n % kStages
   const int n_items = head.s_end - head.s_begin;
@@ -341,9 +362,9 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
     // From 9 rows on the fragments lie in shared memory, one warp's work for all.
     constexpr bool QS = Cfg<NT>::kSharedQ;
     uint32_t qf[QS ? 1 : NT][8][2];
-    const uint32_t frag = base + S::kFrag + lane * 8;
+    const uint32_t frag = base + S::kFrag + lane * (RM ? 16 : 8);
     float *factor = reinterpret_cast<float *>(smem + S::kFrag + NT * 8 * 256);
-    float sl[2 * NT];
+    float sl[NS];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if (QS && w != nt) continue;
@@ -373,24 +394,31 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
       const float down = sl2 == 0.f ? 1.f : fabsf(sl2) * exp2i(-e);
       if (QS) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) sts64(frag + (nt * 8 + ks) * 256, qf[0][ks][0], qf[0][ks][1]);
+        for (int ks = 0; ks < 8; ++ks) {
+          if (RM) {  // registers nt and nt + 2 of the A operand
+            sts32(frag + ks * 512 + 4 * nt, qf[0][ks][0]);
+            sts32(frag + ks * 512 + 8 + 4 * nt, qf[0][ks][1]);
+          } else {
+            sts64(frag + (nt * 8 + ks) * 256, qf[0][ks][0], qf[0][ks][1]);
+          }
+        }
         if (c == 0) factor[row] = down;
       } else {
-        sl[2 * nt] = __shfl_sync(kFull, down, 8 * c);
-        sl[2 * nt + 1] = __shfl_sync(kFull, down, 8 * c + 4);
+        sl[(2 * nt) % NS] = __shfl_sync(kFull, down, 8 * c);
+        sl[(2 * nt + 1) % NS] = __shfl_sync(kFull, down, 8 * c + 4);
       }
     }
     if (QS) {
       named_barrier(1, kWarps * 32);
 #pragma unroll
-      for (int i = 0; i < 2 * NT; ++i) sl[i] = factor[8 * (i >> 1) + 2 * c + (i & 1)];
+      for (int i = 0; i < NS; ++i) sl[i] = factor[stat_row(i)];
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(qempty0 + 8 * slot);  // the slot may be refilled
 
-    float m[2 * NT], l[2 * NT], o[NT][8][4];
+    float m[NS], l[NS], o[NT][8][4];
 #pragma unroll
-    for (int i = 0; i < 2 * NT; ++i) m[i] = -CUDART_INF_F, l[i] = 0.f;
+    for (int i = 0; i < NS; ++i) m[i] = -CUDART_INF_F, l[i] = 0.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -412,186 +440,215 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
 
 #pragma unroll
       for (int kc = 0; kc < Cfg<NT>::kMine; kc += KG) {
-      const int k0 = (w % Cfg<NT>::kShare) * Cfg<NT>::kMine + kc;
-      // S = K Q^T, 16 keys at a time
-      float x[KG][NT][4];
-#pragma unroll
-      for (int kg = 0; kg < KG; ++kg)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[kg][nt][e] = 0.f;
-#pragma unroll
-      for (int kp = 0; kp < KG; kp += KP) {  // groups whose chains of MMAs run side by side
-        uint4 kw[KP][2];
-        uint32_t sc[KP][2][2];
-#pragma unroll
-        for (int kq = 0; kq < KP; ++kq)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {  // keys key_at(g) and key_at(g) + 8 of the group
-            const int row = 16 * (k0 + kp + kq) + 8 * u;
-            kw[kq][u] = *reinterpret_cast<const uint4 *>(kt + k_off + row * 64);
-            const uint32_t two =
-                e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(kt + ks_off + row * 8));
-            sc[kq][u][0] = both_halves<0>(two);
-            sc[kq][u][1] = both_halves<1>(two);
-          }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // a word: 8 dims, two k-steps
-          uint32_t qb[2][NT][2];
-#pragma unroll
-          for (int st = 0; st < 2; ++st)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (QS) lds64(frag + (nt * 8 + 2 * i + st) * 256, qb[st][nt][0], qb[st][nt][1]);
-              else qb[st][nt][0] = qf[nt][2 * i + st][0], qb[st][nt][1] = qf[nt][2 * i + st][1];
-            }
-#pragma unroll
-          for (int kq = 0; kq < KP; ++kq) {
-            uint32_t a[2][4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint4 v = kw[kq][u];
-              widen8(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w, a[u]);
-#pragma unroll
-              for (int b = 0; b < 4; ++b) a[u][b] = mul_f16x2(a[u][b], sc[kq][u][i >> 1]);
-            }
-#pragma unroll
-            for (int st = 0; st < 2; ++st) {
-              const uint32_t af[4] = {a[0][2 * st], a[1][2 * st], a[0][2 * st + 1],
-                                      a[1][2 * st + 1]};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16(x[kp + kq][nt], af, qb[st][nt][0], qb[st][nt][1]);
-            }
-          }
-        }
-      }
-      // what a row does not see to -inf (x is the plain sum; x * sl the score in log2 units)
-      if (EDGE) {
+        const int k0 = (w % Cfg<NT>::kShare) * Cfg<NT>::kMine + kc;
+        // S = K Q^T, 16 keys at a time
+        float x[KG][NT][4];
 #pragma unroll
         for (int kg = 0; kg < KG; ++kg)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = key0 + 16 * (k0 + kg) + key_at(g) + 8 * (e >> 1);
-              const int j = tok[2 * nt + (e & 1)];
-              if (!(key < lim_min + j && (!WIN || key < head.sinks || key >= win.start + j)))
-                x[kg][nt][e] = -CUDART_INF_F;
+            for (int e = 0; e < 4; ++e) x[kg][nt][e] = 0.f;
+#pragma unroll
+        for (int kp = 0; kp < KG; kp += KP) {  // groups whose chains of MMAs run side by side
+          uint4 kw[KP][2];
+          uint32_t sc[KP][2][2];
+#pragma unroll
+          for (int kq = 0; kq < KP; ++kq)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {  // keys key_at(g) and key_at(g) + 8 of the group
+              const int row = 16 * (k0 + kp + kq) + 8 * u;
+              kw[kq][u] = *reinterpret_cast<const uint4 *>(kt + k_off + row * 64);
+              const uint32_t two =
+                  e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(kt + ks_off + row * 8));
+              sc[kq][u][0] = both_halves<0>(two);
+              sc[kq][u][1] = both_halves<1>(two);
             }
-      }
-      // running maximum: moves when a score passes it by more than the slack
-      bool over = false;
-      float top[2 * NT];
 #pragma unroll
-      for (int i = 0; i < 2 * NT; ++i) {
-        top[i] = fmaxf(x[0][i >> 1][i & 1], x[0][i >> 1][2 + (i & 1)]);
+          for (int i = 0; i < 4; ++i) {  // a word: 8 dims, two k-steps
+            uint32_t qb[2][NT][2], qm[2][4];  // one of them: rows as B, or on M
 #pragma unroll
-        for (int kg = 1; kg < KG; ++kg)
-          top[i] = fmaxf(top[i], fmaxf(x[kg][i >> 1][i & 1], x[kg][i >> 1][2 + (i & 1)]));
-        top[i] *= sl[i];
-        over |= top[i] > m[i] + kRescaleSlack;
-      }
-      if (__any_sync(kFull, over)) {
+            for (int st = 0; st < 2; ++st) {
+              if constexpr (RM) {
+                lds128(frag + (2 * i + st) * 512, qm[st][0], qm[st][1], qm[st][2], qm[st][3]);
+              } else {
 #pragma unroll
-        for (int i = 0; i < 2 * NT; ++i) {
+                for (int nt = 0; nt < NT; ++nt) {
+                  if (QS) lds64(frag + (nt * 8 + 2 * i + st) * 256, qb[st][nt][0], qb[st][nt][1]);
+                  else qb[st][nt][0] = qf[nt][2 * i + st][0], qb[st][nt][1] = qf[nt][2 * i + st][1];
+                }
+              }
+            }
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(kFull, top[i], d));
-          const float mn = top[i] > m[i] + kRescaleSlack ? top[i] : m[i];
-          const float a = mn == -CUDART_INF_F ? 1.f : exp2f(m[i] - mn);
-          m[i] = mn;
-          l[i] *= a;
+            for (int kq = 0; kq < KP; ++kq) {
+              uint32_t a[2][4];
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            o[i >> 1][t][i & 1] *= a;
-            o[i >> 1][t][2 + (i & 1)] *= a;
-          }
-        }
-      }
-      // probabilities; their sums in fp32 before the rounding to f16
-      uint32_t pb[KG][NT][2];
+              for (int u = 0; u < 2; ++u) {
+                const uint4 v = kw[kq][u];
+                widen8(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w, a[u]);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float s0 = sl[2 * nt], s1 = sl[2 * nt + 1];
-        const float b0 = m[2 * nt] == -CUDART_INF_F ? 0.f : -m[2 * nt];
-        const float b1 = m[2 * nt + 1] == -CUDART_INF_F ? 0.f : -m[2 * nt + 1];
+                for (int b = 0; b < 4; ++b) a[u][b] = mul_f16x2(a[u][b], sc[kq][u][i >> 1]);
+              }
 #pragma unroll
-        for (int kg = 0; kg < KG; ++kg) {
-          const float p0 = exp2f(fmaf(x[kg][nt][0], s0, b0)), p1 = exp2f(fmaf(x[kg][nt][1], s1, b1));
-          const float p2 = exp2f(fmaf(x[kg][nt][2], s0, b0)), p3 = exp2f(fmaf(x[kg][nt][3], s1, b1));
-          l[2 * nt] += p0 + p2;
-          l[2 * nt + 1] += p1 + p3;
-          pb[kg][nt][0] = transpose8(pack_f16(p0, p1));
-          pb[kg][nt][1] = transpose8(pack_f16(p2, p3));
-        }
-      }
-      // O^T += V^T P^T
+              for (int st = 0; st < 2; ++st) {
+                const uint32_t af[4] = {a[0][2 * st], a[1][2 * st], a[0][2 * st + 1],
+                                        a[1][2 * st + 1]};
 #pragma unroll
-      for (int kg = 0; kg < KG; ++kg) {
-        const int kb = 16 * (k0 + kg);
-        auto words = [&](int key) { return *reinterpret_cast<const uint2 *>(vt + key * 64 + 8 * g); };
-        const uint2 v0 = words(kb + vk0), v1 = words(kb + vk1);
-        const uint2 v2 = words(kb + 8 + vk0), v3 = words(kb + 8 + vk1);
-        const uint8_t *sb = vt + 4096 + g;
-        uint32_t b0 = sb[(kb + vk0) * 8], b1 = sb[(kb + vk1) * 8];
-        uint32_t b2 = sb[(kb + 8 + vk0) * 8], b3 = sb[(kb + 8 + vk1) * 8];
-        const int keys[4] = {key0 + kb + vk0, key0 + kb + vk1, key0 + kb + 8 + vk0,
-                             key0 + kb + 8 + vk1};
-        auto scales = [](uint32_t lo, uint32_t hi) {
-          return e4m3x2_to_f16x2(static_cast<uint16_t>(lo | (hi << 8)));
-        };
-        auto sees = [&](int key, int j) {
-          return key < lim_min + j && (!WIN || key < head.sinks || key >= win.start + j);
-        };
-        if (EDGE) {
-          auto hide = [&](int key, uint32_t b) {  // seen by no token: the scale is taken as zero
-            return key >= f.L || (WIN && key >= head.sinks && key < win.low) ? 0u : b;
-          };
-          b0 = hide(keys[0], b0), b1 = hide(keys[1], b1);
-          b2 = hide(keys[2], b2), b3 = hide(keys[3], b3);
-          if (q_len > 1) {
-            // A NaN that some tokens see and others do not: 0 * NaN would reach every row, so
-            // the scale is taken as zero and the block's 16 dims, which are this quad's o, become
-            // NaN for the rows that see the key.
-            uint32_t odd = 0;
-            auto take = [&](int u, uint32_t b) {
-              if (!e4m3_nan(b) || (sees(keys[u], 0) && sees(keys[u], q_len - 1))) return b;
-              odd |= 1u << u;
-              return 0u;
-            };
-            b0 = take(0, b0), b1 = take(1, b1), b2 = take(2, b2), b3 = take(3, b3);
-            if (__any_sync(kFull, odd != 0)) {
-#pragma unroll 1
-              for (int v = 0; v < 16; ++v) {  // the quad's 16 keys
-                const uint32_t bits = __shfl_sync(kFull, odd, (lane & 28) | (v >> 2));
-                if (!((bits >> (v & 3)) & 1)) continue;
-                const int at = key0 + kb + key_at(2 * (v >> 2) + (v & 1)) + 8 * ((v & 3) >> 1);
-#pragma unroll
-                for (int i = 0; i < 2 * NT; ++i)
-                  if (sees(at, tok[i]))
-#pragma unroll
-                    for (int t = 0; t < 8; ++t)
-                      o[i >> 1][t][i & 1] = o[i >> 1][t][2 + (i & 1)] = CUDART_NAN_F;
+                for (int nt = 0; nt < NT; ++nt) {
+                  if (RM) mma_f16(x[kp + kq][nt], qm[st], a[nt & 1][2 * st], a[nt & 1][2 * st + 1]);
+                  else mma_f16(x[kp + kq][nt], af, qb[st][nt][0], qb[st][nt][1]);
+                }
               }
             }
           }
         }
-        const uint32_t s01 = scales(b0, b1), s23 = scales(b2, b3);
+        // what a row does not see to -inf (x is the plain sum; x * sl the score in log2 units)
+        if (EDGE) {
 #pragma unroll
-        for (int hw = 0; hw < 2; ++hw) {
-          uint32_t a0[4], a1[4], a2[4], a3[4];
-          v_pairs(hw ? v0.y : v0.x, hw ? v1.y : v1.x, s01, a0, a1);
-          v_pairs(hw ? v2.y : v2.x, hw ? v3.y : v3.x, s23, a2, a3);
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint32_t af[4] = {a0[t], a1[t], a2[t], a3[t]};
+          for (int kg = 0; kg < KG; ++kg)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_f16(o[nt][4 * hw + t], af, pb[kg][nt][0], pb[kg][nt][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = key0 + 16 * (k0 + kg) + key_of(nt, e), j = stat_tok[stat_of(nt, e)];
+                if (!(key < lim_min + j && (!WIN || key < head.sinks || key >= win.start + j)))
+                  x[kg][nt][e] = -CUDART_INF_F;
+              }
+        }
+        // running maximum: moves when a score passes it by more than the slack
+        bool over = false;
+        float top[NS];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int kg = 0; kg < KG; ++kg)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {  // the two scores of one row
+              const float a = x[kg][nt][RM ? 2 * u : u], b = x[kg][nt][RM ? 2 * u + 1 : u + 2];
+              const int i = stat_of(nt, RM ? 2 * u : u);
+              const bool fresh = kg == 0 && (!RM || nt == 0);
+              top[i] = fresh ? fmaxf(a, b) : fmaxf(top[i], fmaxf(a, b));
+            }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          top[i] *= sl[i];
+          over |= top[i] > m[i] + kRescaleSlack;
+        }
+        if (__any_sync(kFull, over)) {
+          float a[NS];
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+#pragma unroll
+            for (int d = RM ? 1 : 4; d < (RM ? 4 : 32); d <<= 1)
+              top[i] = fmaxf(top[i], __shfl_xor_sync(kFull, top[i], d));
+            const float mn = top[i] > m[i] + kRescaleSlack ? top[i] : m[i];
+            a[i] = mn == -CUDART_INF_F ? 1.f : exp2f(m[i] - mn);
+            m[i] = mn;
+            l[i] *= a[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 2 * NT; ++i) {  // the columns of o
+            const float f = RM ? __shfl_sync(kFull, a[(i >> 1) % NS], 8 * c + 4 * (i & 1)) : a[i % NS];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+              o[i >> 1][t][i & 1] *= f;
+              o[i >> 1][t][2 + (i & 1)] *= f;
+            }
           }
         }
-      }
+        // probabilities; their sums in fp32 before the rounding to f16
+        uint32_t pb[KG][NT][2];
+        float less[NS];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) less[i] = m[i] == -CUDART_INF_F ? 0.f : -m[i];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int kg = 0; kg < KG; ++kg) {
+            float pr[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = stat_of(nt, e);
+              pr[e] = exp2f(fmaf(x[kg][nt][e], sl[i], less[i]));
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              l[stat_of(nt, RM ? 2 * u : u)] += pr[RM ? 2 * u : u] + pr[RM ? 2 * u + 1 : u + 2];
+            const uint32_t lo = pack_f16(pr[0], pr[1]), hi = pack_f16(pr[2], pr[3]);
+            if constexpr (RM) {  // lo: rows 0 to 7, hi: rows 8 to 15; nt: the half of the 16 keys
+              pb[kg][0][nt] = lo;
+              pb[kg][1][nt] = hi;
+            } else {
+              pb[kg][nt][0] = transpose8(lo);
+              pb[kg][nt][1] = transpose8(hi);
+            }
+          }
+        // O^T += V^T P^T
+#pragma unroll
+        for (int kg = 0; kg < KG; ++kg) {
+          const int kb = 16 * (k0 + kg);
+          auto words = [&](int key) { return *reinterpret_cast<const uint2 *>(vt + key * 64 + 8 * g); };
+          const uint2 v0 = words(kb + vk0), v1 = words(kb + vk1);
+          const uint2 v2 = words(kb + 8 + vk0), v3 = words(kb + 8 + vk1);
+          const uint8_t *sb = vt + 4096 + g;
+          uint32_t b0 = sb[(kb + vk0) * 8], b1 = sb[(kb + vk1) * 8];
+          uint32_t b2 = sb[(kb + 8 + vk0) * 8], b3 = sb[(kb + 8 + vk1) * 8];
+          const int keys[4] = {key0 + kb + vk0, key0 + kb + vk1, key0 + kb + 8 + vk0,
+                               key0 + kb + 8 + vk1};
+          auto scales = [](uint32_t lo, uint32_t hi) {
+            return e4m3x2_to_f16x2(static_cast<uint16_t>(lo | (hi << 8)));
+          };
+          auto sees = [&](int key, int j) {
+            return key < lim_min + j && (!WIN || key < head.sinks || key >= win.start + j);
+          };
+          if (EDGE) {
+            auto hide = [&](int key, uint32_t b) {  // seen by no token: the scale is taken as zero
+              return key >= f.L || (WIN && key >= head.sinks && key < win.low) ? 0u : b;
+            };
+            b0 = hide(keys[0], b0), b1 = hide(keys[1], b1);
+            b2 = hide(keys[2], b2), b3 = hide(keys[3], b3);
+            if (q_len > 1) {
+              // A NaN that some tokens see and others do not: 0 * NaN would reach every row, so
+              // the scale is taken as zero and the block's 16 dims, which are this quad's o, become
+              // NaN for the rows that see the key.
+              uint32_t odd = 0;
+              auto take = [&](int u, uint32_t b) {
+                if (!e4m3_nan(b) || (sees(keys[u], 0) && sees(keys[u], q_len - 1))) return b;
+                odd |= 1u << u;
+                return 0u;
+              };
+              b0 = take(0, b0), b1 = take(1, b1), b2 = take(2, b2), b3 = take(3, b3);
+              if (__any_sync(kFull, odd != 0)) {
+#pragma unroll 1
+                for (int v = 0; v < 16; ++v) {  // the quad's 16 keys
+                  const uint32_t bits = __shfl_sync(kFull, odd, (lane & 28) | (v >> 2));
+                  if (!((bits >> (v & 3)) & 1)) continue;
+                  const int at = key0 + kb + key_at(2 * (v >> 2) + (v & 1)) + 8 * ((v & 3) >> 1);
+#pragma unroll
+                  for (int i = 0; i < 2 * NT; ++i)
+                    if (sees(at, tok[i]))
+#pragma unroll
+                      for (int t = 0; t < 8; ++t)
+                        o[i >> 1][t][i & 1] = o[i >> 1][t][2 + (i & 1)] = CUDART_NAN_F;
+                }
+              }
+            }
+          }
+          const uint32_t s01 = scales(b0, b1), s23 = scales(b2, b3);
+#pragma unroll
+          for (int hw = 0; hw < 2; ++hw) {
+            uint32_t a0[4], a1[4], a2[4], a3[4];
+            v_pairs(hw ? v0.y : v0.x, hw ? v1.y : v1.x, s01, a0, a1);
+            v_pairs(hw ? v2.y : v2.x, hw ? v3.y : v3.x, s23, a2, a3);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const uint32_t af[4] = {a0[t], a1[t], a2[t], a3[t]};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(o[nt][4 * hw + t], af, pb[kg][nt][0], pb[kg][nt][1]);
+            }
+          }
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty0 + 8 * stage);
@@ -615,13 +672,12 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
 
     // ---- segment end: merge the four warps' (m, l, O) and store the partial
 #pragma unroll
-    for (int i = 0; i < 2 * NT; ++i) {
+    for (int i = 0; i < NS; ++i) {
 #pragma unroll
-      for (int d = 4; d < 32; d <<= 1) l[i] += __shfl_xor_sync(kFull, l[i], d);
-      const int row = 8 * (i >> 1) + 2 * c + (i & 1);
-      if (g == 0) {
-        sm_m[w * S::kRows + row] = m[i];
-        sm_l[w * S::kRows + row] = l[i];
+      for (int d = RM ? 1 : 4; d < (RM ? 4 : 32); d <<= 1) l[i] += __shfl_xor_sync(kFull, l[i], d);
+      if (RM ? c == 0 : g == 0) {
+        sm_m[w * S::kRows + stat_row(i)] = m[i];
+        sm_l[w * S::kRows + stat_row(i)] = l[i];
       }
     }
     named_barrier(1, kWarps * 32);
@@ -638,9 +694,10 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
     float fs[2 * NT];
 #pragma unroll
     for (int i = 0; i < 2 * NT; ++i) {
+      const int row = 8 * (i >> 1) + 2 * c + (i & 1);
       float M, Lsum;
-      row_stats(8 * (i >> 1) + 2 * c + (i & 1), M, Lsum);
-      fs[i] = Lsum == 0.f ? 0.f : exp2f(m[i] - M) / Lsum * vsc;
+      row_stats(row, M, Lsum);
+      fs[i] = Lsum == 0.f ? 0.f : exp2f(sm_m[w * S::kRows + row] - M) / Lsum * vsc;
     }
     float *mine = mbuf + (w % S::kBufs) * (S::kRows * kMergeStride);
     auto merge = [&](auto add_tag) {  // warps 0 / 1 store, then warps 2 / 3 add
