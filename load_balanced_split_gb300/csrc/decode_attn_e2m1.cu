@@ -11,7 +11,8 @@
 // is what the kernel waits for.  The layout keeps to about half of them:
 //  * the products run as m16n8k16 MMAs with the KEYS (S = K Q^T) and the HEAD DIMS (O^T = V^T P^T)
 //    as the 16 rows and 8 query rows as the 8 columns, so an MMA takes 256 cache elements for 8
-//    query rows, where queries on the 16 rows would take 128 and leave half of the tile empty;
+//    query rows, where queries on the 16 rows would take 128 and leave half of the tile empty
+//    (9 to 16 rows fill it and stand there in the first product);
 //  * a thread reads 32 consecutive dims of a key with one 16-byte load and widens two codes per
 //    conversion; the head dims are permuted alike in Q and K, so nothing is shuffled.  The
 //    product of a code and its block scale has 6 significant bits and is exact in f16;
@@ -25,7 +26,8 @@
 //    lie together).
 // Sums, softmax statistics and outputs are fp32.  Queries enter as f16, each row scaled by a power
 // of two that puts its largest element into [2^14, 2^15) (exact down to 2^-28 of it), and the
-// probabilities are rounded to f16 (2^-11 of each) as the second product's operand.
+// probabilities are rounded to f16 as the second product's operand: 2^-11 of each, and of those
+// below 2^-21 of the row's largest 2^-32 of that one.
 //
 // Windows with sink tokens (WIN): the producer maps the map's compact pages to real ones
 // (WinSpan), and pages at the window's ends mask by position.  Pages without a hidden key run a
@@ -41,20 +43,21 @@
 namespace hpa {
 namespace {
 
-// Query rows in tiles of 8 columns, and what was measured best for each number of them, in us (32 x
-// 8192 keys with 8 rows and 128 x 4096 in a window; 64 x 20000 with 16 rows and 64 x 2000 in a window;
-// 13 x 20011 with 20 rows):
-//   1 tile:  4 consumer warps in pairs that share a page, three CTAs per SM at 128 registers, 61 and
-//            113 (5 warps with a page each, two CTAs: 62 and 127; four to a page: 72 and 127);
-//   2 tiles: the same pairs, two CTAs at 168 registers, query fragments in shared memory, 351
-//            and 57 (a page each: 346, but 95 with the window: a segment's last pages, and its
-//            start, then leave warps idle for a page's time);
+// Query rows in tiles of 8 columns, and what was measured best for each number of them, in us (32
+// x 8192 keys with 8 rows and 128 x 4096 in a window; 64 x 20000 with 16 rows and 64 x 2000 in a
+// window; 13 x 20011 with 20 rows):
+//   1 tile:  4 consumer warps in pairs that share a page, three CTAs per SM at 128 registers, 61
+//            and 113 (5 warps with a page each, two CTAs: 62 and 127; four to a page: 72 and 127);
+//   2 tiles: the same pairs, two CTAs at 168 registers, query fragments in shared memory, 343
+//            and 52 (a page each, with the keys on M: 346 to the pairs' 351, but 95 to their 57
+//            in the window: a segment's last pages, and its start, then leave warps idle for a
+//            page's time);
 //   3 tiles: 7 warps with a page each, one CTA at 255 registers: one pass for up to 24 rows, 101
 //            (two passes of 2 tiles 153, 4 warps at 168 registers with spills 184, pairs 127).
 template <int NT>
 struct Cfg {
   static constexpr int kWarps = NT == 3 ? 7 : 4;                 // consumer warps
-  static constexpr int kShare = NT == 3 ? 1 : 2;                 // warps of a team, which share a page
+  static constexpr int kShare = NT == 3 ? 1 : 2;                 // warps of a team: a page's
   static constexpr int kTeams = kWarps / kShare;
   static constexpr int kBlocks = NT == 1 ? 3 : NT == 2 ? 2 : 1;  // CTAs per SM
   static constexpr int kStages = NT == 1 ? 6 : NT == 2 ? 8 : 14;
@@ -65,16 +68,19 @@ struct Cfg {
   static constexpr int kThreads = (kWarps + 1) * 32;
   static constexpr int kMine = 4 / kShare;             // a page's groups of 16 keys for a warp
   static constexpr int kGroups = NT == 3 ? 4 : 2;      // groups that share a softmax step
-  static constexpr int kSide = NT == 1 ? 1 : 2;        // groups whose chains of MMAs run side by side
+  static constexpr int kSide = NT == 1 ? 1 : 2;        // groups whose MMA chains run side by side
   static constexpr bool kSharedQ = NT > 1;             // query fragments in shared memory
   // With 16 rows they fill the MMA's 16: S = Q K^T has P in the layout that the second product
-  // wants, without movmatrix, and a lane has 2 rows' statistics, not 4 (351 -> RMUS us).
+  // wants, without movmatrix, and a lane has 2 rows' statistics, not 4 (351 -> 343 us).
   static constexpr bool kRowsOnM = NT == 2;
   static constexpr int kStats = kRowsOnM ? 2 : 2 * NT;
 };
 constexpr int kUnit = E2M1_UNIT;  // bytes of one page and KV head of K or V
 constexpr int kStageBytes = 2 * kUnit;
 constexpr float kRescaleSlack = 8.f;
+// Probabilities are held times 2^7: with the slack up to 2^15 in f16, whose smallest step is then
+// 2^-31 of the row's largest, so that a million small ones beside it are not lost to rounding.
+constexpr float kLift = 7.f;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kQRowBytes = 272;  // 256 of a query row, padded against bank conflicts
 constexpr int kMergeStride = HEAD_DIM + 4;
@@ -90,7 +96,8 @@ struct Smem {
   static constexpr int kQ = kStats + 2 * kWarps * kRows * 4;         // two query slots
   static constexpr int kInfo = kQ + 2 * kQSlot;                      // int4[2]
   static constexpr int kFrag = kInfo + 2 * 16;                       // query fragments, factors
-  static constexpr int kBars = kFrag + (Cfg<NT>::kSharedQ ? NT * 8 * 256 + kRows * 4 : 0);  // full[stages] empty[stages] qfull[2] qempty[2]
+  // full[stages], empty[stages], qfull[2], qempty[2]
+  static constexpr int kBars = kFrag + (Cfg<NT>::kSharedQ ? NT * 8 * 256 + kRows * 4 : 0);
   static constexpr int kFlag = kBars + (2 * kStages + 4) * 8;
   static constexpr int kAlloc = kFlag + 16;
 };
@@ -122,8 +129,12 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 template <int HI>
 __device__ __forceinline__ uint32_t both_halves(uint32_t a) {
   uint32_t d;
-  if (HI) asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(d) : "r"(a));
-  else asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(d) : "r"(a));
+  if (HI)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}"
+        : "=r"(d) : "r"(a));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}"
+        : "=r"(d) : "r"(a));
   return d;
 }
 
@@ -391,7 +402,9 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
           qf[at][2 * i + (u >> 1)][u & 1] = pack_f16(__uint_as_float(x[u] << 16) * up,
                                                      __uint_as_float(x[u] & 0xffff0000u) * up);
       }
-      const float down = sl2 == 0.f ? 1.f : fabsf(sl2) * exp2i(-e);
+      // never zero, which would make NaN of a hidden key's -inf; at 2^-126 all scores are nothing
+      float down = sl2 == 0.f ? 1.f : fabsf(sl2) * exp2i(-e);
+      if (down < exp2i(-126)) down = exp2i(-126);
       if (QS) {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
@@ -548,7 +561,8 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
           }
 #pragma unroll
           for (int i = 0; i < 2 * NT; ++i) {  // the columns of o
-            const float f = RM ? __shfl_sync(kFull, a[(i >> 1) % NS], 8 * c + 4 * (i & 1)) : a[i % NS];
+            const float f = RM ? __shfl_sync(kFull, a[(i >> 1) % NS], 8 * c + 4 * (i & 1))
+                               : a[i % NS];
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
               o[i >> 1][t][i & 1] *= f;
@@ -560,7 +574,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
         uint32_t pb[KG][NT][2];
         float less[NS];
 #pragma unroll
-        for (int i = 0; i < NS; ++i) less[i] = m[i] == -CUDART_INF_F ? 0.f : -m[i];
+        for (int i = 0; i < NS; ++i) less[i] = m[i] == -CUDART_INF_F ? 0.f : kLift - m[i];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -587,7 +601,9 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
 #pragma unroll
         for (int kg = 0; kg < KG; ++kg) {
           const int kb = 16 * (k0 + kg);
-          auto words = [&](int key) { return *reinterpret_cast<const uint2 *>(vt + key * 64 + 8 * g); };
+          auto words = [&](int key) {
+            return *reinterpret_cast<const uint2 *>(vt + key * 64 + 8 * g);
+          };
           const uint2 v0 = words(kb + vk0), v1 = words(kb + vk1);
           const uint2 v2 = words(kb + 8 + vk0), v3 = words(kb + 8 + vk1);
           const uint8_t *sb = vt + 4096 + g;
@@ -655,7 +671,8 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
     };
     // this team's pages of the segment: page n of the CTA with n % kTeams == team
     constexpr int kTeams = Cfg<NT>::kTeams;
-    const int skip = (w / Cfg<NT>::kShare + kTeams - count % kTeams) % kTeams, n_pages = f.pg1 - f.pg0;
+    const int skip = (w / Cfg<NT>::kShare + kTeams - count % kTeams) % kTeams;
+    const int n_pages = f.pg1 - f.pg0;
     for (int i = skip; i < n_pages && ok; i += kTeams) {
       const int n = count + i, stage = n % kStages, pg = f.pg0 + i;
       const uint32_t phase = (n / kStages) & 1;
@@ -670,7 +687,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
       *abort_flag = 1;
     }
 
-    // ---- segment end: merge the four warps' (m, l, O) and store the partial
+    // ---- segment end: merge the warps' (m, l, O) and store the partial
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
 #pragma unroll
@@ -710,7 +727,8 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
         for (int t = 0; t < 4; ++t) {
           const float(&oa)[4] = o[i >> 1][2 * t], (&ob)[4] = o[i >> 1][2 * t + 1];
           const int e = i & 1;
-          float4 nv = make_float4(oa[e] * fs[i], oa[2 + e] * fs[i], ob[e] * fs[i], ob[2 + e] * fs[i]);
+          float4 nv = make_float4(oa[e] * fs[i], oa[2 + e] * fs[i],
+                                  ob[e] * fs[i], ob[2 + e] * fs[i]);
           if (ADD) {
             const float4 old = d[t];
             nv.x += old.x, nv.y += old.y, nv.z += old.z, nv.w += old.w;
@@ -748,7 +766,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
       // combine's result NaN (it passes over -inf and NaN)
       p.partial_lse[(static_cast<int64_t>(s) * q_len + j) * p.Hq + h * G + gq] =
           Lsum == 0.f ? -CUDART_INF_F
-          : Lsum > 0.f ? (M + log2f(Lsum)) * 0.69314718055994531f
+          : Lsum > 0.f ? (M - kLift + log2f(Lsum)) * 0.69314718055994531f
                        : CUDART_INF_F;
     }
     named_barrier(1, kWarps * 32);
@@ -830,10 +848,9 @@ cudaError_t launch(const AttnParams &p, const void *k_pool, const void *v_pool, 
 template <int NT>
 int occupancy(int *ctas) {
   if (configure<NT, false>() != cudaSuccess) return -1;
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, decode_attn_e2m1_kernel<NT, false>,
-                                                       Cfg<NT>::kThreads, Smem<NT>::kAlloc) == cudaSuccess
-             ? 0
-             : -1;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+      ctas, decode_attn_e2m1_kernel<NT, false>, Cfg<NT>::kThreads, Smem<NT>::kAlloc);
+  return e == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace
@@ -847,11 +864,10 @@ int attn_e2m1_group(int rows) {
 
 cudaError_t launch_decode_attn_e2m1(const AttnParams &p, const void *k_pool, const void *v_pool,
                                     cudaStream_t s) {
-  if (p.group <= 8)
-    return p.window ? launch<1, true>(p, k_pool, v_pool, s) : launch<1, false>(p, k_pool, v_pool, s);
-  if (p.group <= 16)
-    return p.window ? launch<2, true>(p, k_pool, v_pool, s) : launch<2, false>(p, k_pool, v_pool, s);
-  return p.window ? launch<3, true>(p, k_pool, v_pool, s) : launch<3, false>(p, k_pool, v_pool, s);
+  const auto run = p.group <= 8    ? (p.window ? launch<1, true> : launch<1, false>)
+                   : p.group <= 16 ? (p.window ? launch<2, true> : launch<2, false>)
+                                   : (p.window ? launch<3, true> : launch<3, false>);
+  return run(p, k_pool, v_pool, s);
 }
 
 int attn_e2m1_ctas_per_sm(int rows, int *ctas) {

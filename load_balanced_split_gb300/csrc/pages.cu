@@ -45,7 +45,8 @@ struct Sum2 {
 __device__ Sum2 block_scan2(Sum2 v, Sum2 *wbuf, Sum2 &total) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, warps = blockDim.x >> 5;
   for (int o = 1; o < 32; o <<= 1) {
-    const long long a = __shfl_up_sync(0xffffffffu, v.a, o), b = __shfl_up_sync(0xffffffffu, v.b, o);
+    const long long a = __shfl_up_sync(0xffffffffu, v.a, o);
+    const long long b = __shfl_up_sync(0xffffffffu, v.b, o);
     if (lane >= o) v.a += a, v.b += b;
   }
   if (warps == 1) {
@@ -58,7 +59,8 @@ __device__ Sum2 block_scan2(Sum2 v, Sum2 *wbuf, Sum2 &total) {
   if (wid == 0) {
     Sum2 s = lane < warps ? wbuf[lane] : Sum2{0, 0};
     for (int o = 1; o < 32; o <<= 1) {
-      const long long a = __shfl_up_sync(0xffffffffu, s.a, o), b = __shfl_up_sync(0xffffffffu, s.b, o);
+      const long long a = __shfl_up_sync(0xffffffffu, s.a, o);
+      const long long b = __shfl_up_sync(0xffffffffu, s.b, o);
       if (lane >= o) s.a += a, s.b += b;
     }
     if (lane < warps) wbuf[lane] = s;
@@ -184,7 +186,8 @@ __global__ void __launch_bounds__(1024) scan_kernel(const AssignParams p) {
   __syncthreads();
   if (tid == 0) {
     for (int w = 1; w < (n >> 5); ++w) given = max(given, wbuf[w].a);
-    if (done.a > p.indices_cap || (p.new_tokens && done.b > p.max_tokens)) s_bad |= HPA_STATUS_OVERFLOW;
+    if (done.a > p.indices_cap || (p.new_tokens && done.b > p.max_tokens))
+      s_bad |= HPA_STATUS_OVERFLOW;
     p.page_indptr[0] = 0;
     const long long left = avail - given;
     *p.free_out = static_cast<int32_t>(left < p.num_pages ? left : p.num_pages);

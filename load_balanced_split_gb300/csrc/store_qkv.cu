@@ -96,7 +96,8 @@ __device__ __forceinline__ void set_token(const StoreQkvParams &p, Item &x, bool
   x.page = page_ok && pos_ok ? static_cast<int>(slot / PAGE) : -1;
   x.fresh = true;
   if (report && x.ch == 0 && p.status && slot != -1 && x.page < 0)
-    atomicOr(reinterpret_cast<int *>(p.status), page_ok ? HPA_STATUS_BAD_SEQLEN : HPA_STATUS_BAD_PAGE);
+    atomicOr(reinterpret_cast<int *>(p.status),
+             page_ok ? HPA_STATUS_BAD_SEQLEN : HPA_STATUS_BAD_PAGE);
 }
 
 // Start an item's rows and, with its token's first, the table row on their way into a slot.
@@ -165,7 +166,10 @@ __device__ __forceinline__ void load_turn(Turn<ROPE> &t, uint32_t row, int k, in
         for (int j = 0; j < 4; ++j) s[j] = __uint_as_float(w[j]);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) t.c[4 * hf + j] = pk(c[j], c[j]), t.s[4 * hf + j] = pk(-s[j], s[j]);
+      for (int j = 0; j < 4; ++j) {
+        t.c[4 * hf + j] = pk(c[j], c[j]);
+        t.s[4 * hf + j] = pk(-s[j], s[j]);
+      }
     }
   }
 }

@@ -8,7 +8,7 @@ import load_balanced_split_gb300 as hpa
 from bounded_helpers import check_attention, lse_bound, out_bound
 from fourbit_helpers import make_batch, poison_hidden, rows_of, step
 from gpu_helpers import DeviceBatch
-from oracle import bounded
+from oracle import bounded, fourbit
 
 pytestmark = pytest.mark.gpu
 
@@ -120,6 +120,43 @@ def test_query_scales(case):
     ws, out, lse = step(b, DeviceBatch(b), sm_scale=sm)
     torch.cuda.synchronize()
     check_attention(b, out, lse, bounded.attention_rows(b, sm_scale=sm), "e2m1")
+
+
+@pytest.mark.parametrize("q_len", [1, 2, 3])
+def test_many_small_probabilities_beside_a_large_one(q_len):
+    """20000 keys of 2^-26 of the first one's weight, whose value is zero: what is left is their
+    sum.  2^-26 is 2^-19 as it is held, where f16's half step is 2^-25, 2^-6 of it; the queries and
+    the result add 2^-8 at most."""
+    L = 20000
+    b = make_batch([L], q_len, (8, 1), seed=24)
+    k, v = np.zeros((b.num_pages, 1, 64, 128)), np.full((b.num_pages, 1, 64, 128), 6.0)
+    first = int(b.page_indices[0])
+    k[first, 0, 0], v[first, 0, 0] = 6.0, 0.0
+    b.k_pool, b.v_pool = torch.from_numpy(fourbit.pack(k)), torch.from_numpy(fourbit.pack(v))
+    b.q = torch.ones_like(b.q)
+    b.k_scale[:], b.v_scale[:] = 1.0, 1.0
+    sm = 26 * np.log(2) / (128 * 6)
+    ws, out, lse = step(b, DeviceBatch(b), C=1, tile=64, sm_scale=sm)
+    torch.cuda.synchronize()
+    assert ws.status() == 0
+    small = (L - q_len + np.arange(q_len)) * 2.0 ** -26
+    want = (6 * small / (1 + small))[None, :, None, None]
+    got = out.double().cpu().numpy()
+    assert (np.abs(got / want - 1) <= 2.0 ** -5).all()
+    check = 26 * np.log(2) + np.log1p(small)
+    assert np.abs(lse.double().cpu().numpy() - check[None, :, None]).max() <= 1e-4
+
+
+def test_queries_and_scales_near_the_smallest():
+    """Scores of nothing at all: hidden keys stay hidden, the rest is a mean."""
+    b = make_batch([130, 70], 2, (16, 2), seed=25)
+    poison_hidden(b)
+    b.q = (b.q.float() * 1e-36).to(torch.bfloat16)
+    b.k_scale[:] = 1e-10
+    ws, out, lse = step(b, DeviceBatch(b))
+    torch.cuda.synchronize()
+    assert ws.status() == 0
+    check_attention(b, out, lse, bounded.attention_rows(b), "e2m1")
 
 
 @pytest.mark.parametrize("kind", ["static", "weighted"])
