@@ -8,7 +8,10 @@
 //
 // What bounds it: at 4.5 bits an element the DRAM delivers 42 elements a clock to each SM, so
 // the widening to f16 has about three instruction slots an element before it, not the memory,
-// is what the kernel waits for.  The layout keeps to about half of them:
+// is what the kernel waits for; and an MMA takes 8 of them, in which little else issues (an FFMA
+// beside it costs 1 more, a conversion half of one).  With 8 rows the memory still sets the pace
+// (5.5 TB/s over 32 x 8192 keys, starts and ends included), with 16 the slots (4.65 TB/s).  The
+// layout:
 //  * the products run as m16n8k16 MMAs with the KEYS (S = K Q^T) and the HEAD DIMS (O^T = V^T P^T)
 //    as the 16 rows and 8 query rows as the 8 columns, so an MMA takes 256 cache elements for 8
 //    query rows, where queries on the 16 rows would take 128 and leave half of the tile empty
@@ -21,9 +24,9 @@
 //  * P moves from the first product's accumulator layout to the second's operand by movmatrix;
 //  * the softmax's running maximum moves only when a score passes it by 2^8 (as in the 8-bit
 //    kernel), so a page costs one vote and no exchange of maxima;
-//  * a warp takes 32 or 64 keys of a page at a time, with one wait, vote and release.  One
-//    producer warp keeps a ring of pages in flight with bulk copies, two a page (codes and scales
-//    lie together).
+//  * a warp takes 32 keys of a page at a time, with one wait, vote and release.  One producer
+//    warp keeps a ring of pages in flight with bulk copies, two a page (codes and scales lie
+//    together).
 // Sums, softmax statistics and outputs are fp32.  Queries enter as f16, each row scaled by a power
 // of two that puts its largest element into [2^14, 2^15) (exact down to 2^-28 of it), and the
 // probabilities are rounded to f16 as the second product's operand: 2^-11 of each, and of those
@@ -44,32 +47,34 @@ namespace hpa {
 namespace {
 
 // Query rows in tiles of 8 columns, and what was measured best for each number of them, in us (32
-// x 8192 keys with 8 rows and 128 x 4096 in a window; 64 x 20000 with 16 rows and 64 x 2000 in a
-// window; 13 x 20011 with 20 rows):
-//   1 tile:  4 consumer warps in pairs that share a page, three CTAs per SM at 128 registers, 61
-//            and 113 (5 warps with a page each, two CTAs: 62 and 127; four to a page: 72 and 127);
-//   2 tiles: the same pairs, two CTAs at 168 registers, query fragments in shared memory, 343
-//            and 52 (a page each, with the keys on M: 346 to the pairs' 351, but 95 to their 57
-//            in the window: a segment's last pages, and its start, then leave warps idle for a
-//            page's time);
-//   3 tiles: 7 warps with a page each, one CTA at 255 registers: one pass for up to 24 rows, 101
-//            (two passes of 2 tiles 153, 4 warps at 168 registers with spills 184, pairs 127).
+// x 8192 keys with 8 rows and 128 x 4096 in a window of 1024 and 4 sinks; 64 x 20000 with 16 rows
+// and 64 x 8000 in a window of 2000; 13 x 20011 with 20 rows and that window with 24):
+//   1 tile:  4 consumer warps in pairs that share a page, three CTAs per SM at 128 registers, 60
+//            and 111 (5 warps with a page each, two CTAs: 62 and 127; four to a page: 72 and 127);
+//   2 tiles: the same pairs, two CTAs at 168 registers, query fragments in shared memory, 335
+//            and 48 (a page each gains 1 %, but takes 95 in the window: a segment's last pages,
+//            and its start, then leave warps idle for a page's time; 12 warps in one CTA 315
+//            and 63);
+//   3 tiles: 8 warps in pairs, one CTA, at the 232 registers that the producer's warps leave, one
+//            pass for up to 24 rows: 102 and 76 (a page each and 64 keys a step 97 and 104, two
+//            passes of 2 tiles 153, 4 warps at 168 registers with spills 184).
+// The warps of an SM come in fours: with 10 in a CTA the schedulers that have three set the pace.
 template <int NT>
 struct Cfg {
-  static constexpr int kWarps = NT == 3 ? 7 : 4;                 // consumer warps
-  static constexpr int kShare = NT == 3 ? 1 : 2;                 // warps of a team: a page's
+  static constexpr int kWarps = NT == 3 ? 8 : 4;  // consumer warps
+  static constexpr int kShare = 2;         // warps of a team, which share a page
   static constexpr int kTeams = kWarps / kShare;
   static constexpr int kBlocks = NT == 1 ? 3 : NT == 2 ? 2 : 1;  // CTAs per SM
-  static constexpr int kStages = NT == 1 ? 6 : NT == 2 ? 8 : 14;
+  static constexpr int kStages = NT == 1 ? 6 : NT == 2 ? 8 : 16;
   // A team meets the same stages again.  Copies may land out of order, so a warp that came to a
   // stage whose page before it, another team's, had not landed would take that page's phase for
   // the end of its own.
   static_assert(kWarps % kShare == 0 && kStages % kTeams == 0, "each stage belongs to one team");
-  static constexpr int kThreads = (kWarps + 1) * 32;
-  static constexpr int kMine = 4 / kShare;             // a page's groups of 16 keys for a warp
-  static constexpr int kGroups = NT == 3 ? 4 : 2;      // groups that share a softmax step
-  static constexpr int kSide = NT == 1 ? 1 : 2;        // groups whose MMA chains run side by side
-  static constexpr bool kSharedQ = NT > 1;             // query fragments in shared memory
+  static constexpr int kThreads = NT == 3 ? 384 : (kWarps + 1) * 32;  // 3: whole warpgroups
+  static constexpr int kMine = 4 / kShare;  // a page's groups of 16 keys for a warp
+  static constexpr int kGroups = 2;         // groups that share a softmax step
+  static constexpr int kSide = NT == 2 ? 2 : 1;  // groups whose MMA chains run side by side
+  static constexpr bool kSharedQ = NT > 1;       // query fragments in shared memory
   // With 16 rows they fill the MMA's 16: S = Q K^T has P in the layout that the second product
   // wants, without movmatrix, and a lane has 2 rows' statistics, not 4 (351 -> 343 us).
   static constexpr bool kRowsOnM = NT == 2;
@@ -194,7 +199,26 @@ __device__ __forceinline__ int group_rows(const AttnParams &p) {
   return min(p.group, p.rows - row_base(p));
 }
 
+// Wait for a phase; false if it took too long, or if another warp of the CTA gave up.
+__device__ bool wait_phase(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag || globaltimer_ns() - t0 > 2000000000ull) return false;
+  }
+}
+
 // ----------------------------------------------------------------------------- producer
+// One warp.  Reading a segment's row, its request's page list and its page ids are round trips to
+// L2 that follow from one another, so a lane each reads the rows of 32 segments at once, and the
+// next 32 page ids are on their way while the last are used.  A lane copies the page whose id it
+// holds, and a segment's query rows are bulk copies too, so that the warp waits for nothing but
+// stages to become free.  (With each segment's loads before its pages this warp was what the others
+// waited for: 343 us where this takes 335, 64 x 20000 keys with 16 rows, and 52 for 48 in a window
+// of 2000.)
 template <int NT, bool WIN>
 __device__ void producer(const AttnParams &p, const uint8_t *k_pool, const uint8_t *v_pool,
                          uint8_t *smem, const MapHead &head) {
@@ -204,81 +228,119 @@ __device__ void producer(const AttnParams &p, const uint8_t *k_pool, const uint8
   const uint32_t base = smem_u32(smem);
   const uint32_t full0 = base + S::kBars, empty0 = full0 + 8 * kStages;
   const uint32_t qfull0 = empty0 + 8 * kStages, qempty0 = qfull0 + 16;
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kFlag);
+  const volatile int *abort_flag = reinterpret_cast<const volatile int *>(smem + S::kFlag);
   const uint64_t pol = l2_policy_evict_first();
-  int stage = 0;
-  uint32_t phase = 0, issued = 0, parity_bits = 0;
+  const int rows = group_rows(p), rb = row_base(p);
+  // where this lane's query row lies behind its request's first
+  const int64_t q_at =
+      (static_cast<int64_t>((rb + lane) / p.G) * p.Hq + h * p.G + (rb + lane) % p.G) * HEAD_DIM;
+  int n0 = 0, nq = 0;  // pages and segments on their way
   bool ok = true;
-  for (int s = head.s_begin; s < head.s_end && ok; ++s) {
-    const Seg f = read_seg<WIN>(p, s, head.tile, lane == 0);
-    WinSpan win = {};
-    if (WIN && f.pg0 < f.pg1) win = WinSpan::make(f.L, p.q_len, head.window, head.sinks);
-    {  // the segment's place and query rows, two segments ahead of the consumers at most
-      const int k = s - head.s_begin, slot = k & 1;
-      int good = 1;
-      if (lane == 0)
-        good = !*abort_flag && mbar_wait_bounded(qempty0 + 8 * slot, ((k >> 1) & 1) ^ 1);
-      if (!__shfl_sync(kFull, good, 0)) {
-        ok = false;
-        break;
-      }
-      uint8_t *qs = smem + S::kQ + slot * S::kQSlot;
-      const int G = p.G, rb = row_base(p);
-      for (int ch = lane; ch < group_rows(p) * 16; ch += 32) {  // 16-byte chunks of 256-byte rows
-        const int row = ch >> 4, c16 = ch & 15, j = (rb + row) / G, g = (rb + row) % G;
-        const int4 v = reinterpret_cast<const int4 *>(
-            p.q + ((static_cast<int64_t>(f.r) * p.q_len + j) * p.Hq + h * G + g) * HEAD_DIM)[c16];
-        *reinterpret_cast<int4 *>(qs + row * kQRowBytes + c16 * 16) = v;
-      }
-      if (lane == 0)
-        reinterpret_cast<int4 *>(smem + S::kInfo)[slot] = make_int4(f.r, f.L, f.klo, f.khi);
-      mbar_arrive(qfull0 + 8 * slot);  // every lane publishes its own stores
+  for (int s0 = head.s_begin; s0 < head.s_end && ok; s0 += 32) {
+    Seg mine = {0, 0, 0, 0, 0, 0};
+    int list = 0, listed = 0;  // its request's page list
+    if (s0 + lane < head.s_end) {
+      mine = read_seg<WIN>(p, s0 + lane, head.tile, true);
+      list = p.page_indptr[mine.r];
+      listed = p.page_indptr[mine.r + 1] - list;
     }
-    const int pstart = p.page_indptr[f.r], pcount = p.page_indptr[f.r + 1] - pstart;
-    const int32_t *pidx = p.page_indices + pstart;
-    for (int pb = f.pg0; pb < f.pg1 && ok; pb += 32) {
-      const int cnt = min(32, f.pg1 - pb);
-      int id = 0;
-      if (lane < cnt) {
-        const int pg = WIN ? win.real_page(pb + lane) : pb + lane;
-        id = pg < pcount ? pidx[pg] : -1;
-        if (id < 0 || id >= p.num_pages) {  // bad id or too short a page list
+    struct Walk {
+      Seg f;
+      int list, listed;
+      WinSpan win;
+    };
+    auto segment = [&](int j) {
+      Walk x = {};
+      x.f.r = __shfl_sync(kFull, mine.r, j);
+      x.f.L = __shfl_sync(kFull, mine.L, j);
+      x.f.klo = __shfl_sync(kFull, mine.klo, j);
+      x.f.khi = __shfl_sync(kFull, mine.khi, j);
+      x.f.pg0 = x.f.klo / PAGE;
+      x.f.pg1 = (x.f.khi + PAGE - 1) / PAGE;
+      x.list = __shfl_sync(kFull, list, j);
+      x.listed = __shfl_sync(kFull, listed, j);
+      if (WIN && x.f.pg0 < x.f.pg1) x.win = WinSpan::make(x.f.L, p.q_len, head.window, head.sinks);
+      return x;
+    };
+    auto load_id = [&](const Walk &x, int pb) {
+      if (pb + lane >= x.f.pg1) return 0;
+      const int pg = WIN ? x.win.real_page(pb + lane) : pb + lane;
+      return pg < x.listed ? p.page_indices[x.list + pg] : -1;
+    };
+    const int n_seg = min(32, head.s_end - s0);
+    Walk cur = segment(0);
+    int next_id = load_id(cur, cur.f.pg0);
+    for (int j = 0; j < n_seg && ok; ++j) {
+      const Walk nxt = segment(j + 1 < n_seg ? j + 1 : j);
+      {  // the segment's place and query rows, two segments ahead of the consumers at most
+        const int slot = nq & 1;
+        bool good = true;
+        if (lane == 0) good = wait_phase(qempty0 + 8 * slot, ((nq >> 1) & 1) ^ 1, abort_flag);
+        if (!__shfl_sync(kFull, good, 0)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          reinterpret_cast<int4 *>(smem + S::kInfo)[slot] =
+              make_int4(cur.f.r, cur.f.L, cur.f.klo, cur.f.khi);
+          mbar_arrive_expect_tx(qfull0 + 8 * slot, rows * HEAD_DIM * 2);
+        }
+        __syncwarp();
+        if (lane < rows)
+          bulk_load(base + S::kQ + slot * S::kQSlot + lane * kQRowBytes,
+                    p.q + static_cast<int64_t>(cur.f.r) * p.q_len * p.Hq * HEAD_DIM + q_at,
+                    HEAD_DIM * 2, qfull0 + 8 * slot);
+        ++nq;
+      }
+      if (cur.f.pg0 >= cur.f.pg1) next_id = load_id(nxt, nxt.f.pg0);
+      for (int pb = cur.f.pg0; pb < cur.f.pg1 && ok; pb += 32) {
+        const int cnt = min(32, cur.f.pg1 - pb);
+        int id = next_id;
+        next_id = pb + 32 < cur.f.pg1 ? load_id(cur, pb + 32) : load_id(nxt, nxt.f.pg0);
+        if (lane < cnt && (id < 0 || id >= p.num_pages)) {  // bad id or too short a page list
           status_or(p.tm, HPA_STATUS_BAD_PAGE);
           id = 0;
         }
-      }
-      for (int i = 0; i < cnt; ++i) {
-        const int pid = __shfl_sync(kFull, id, i);
-        int good = 1;
-        if (lane == 0) {
-          if (*abort_flag || !mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1)) {
-            good = 0;
-          } else {
-            const uint32_t fb = full0 + 8 * stage, dst = base + stage * kStageBytes;
-            const int64_t at = (static_cast<int64_t>(pid) * p.Hkv + h) * kUnit;
-            mbar_arrive_expect_tx(fb, kStageBytes);
-            bulk_load_hint(dst, k_pool + at, kUnit, fb, pol);
-            bulk_load_hint(dst + kUnit, v_pool + at, kUnit, fb, pol);
-            issued |= 1u << stage;
-            parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
+        const int n = n0 + lane, stage = n % kStages;
+        const uint32_t phase = (n / kStages) & 1;
+        const uint32_t fb = full0 + 8 * stage, dst = base + stage * kStageBytes;
+        const int64_t at = (static_cast<int64_t>(id) * p.Hkv + h) * kUnit;
+        for (int i = 0; i < cnt; ++i) {
+          bool good = true;
+          if (lane == i) {
+            good = wait_phase(empty0 + 8 * stage, phase ^ 1, abort_flag);
+            if (good) {
+              mbar_arrive_expect_tx(fb, kStageBytes);
+              bulk_load_hint(dst, k_pool + at, kUnit, fb, pol);
+              bulk_load_hint(dst + kUnit, v_pool + at, kUnit, fb, pol);
+            }
+          }
+          if (!__all_sync(kFull, good)) {
+            n0 += i;
+            ok = false;
+            break;
           }
         }
-        ok = __shfl_sync(kFull, good, 0) != 0;
-        if (!ok) break;
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
+        if (ok) n0 += cnt;
       }
+      cur = nxt;
     }
   }
-  if (!ok && lane == 0) {
-    status_or(p.tm, HPA_STATUS_TIMEOUT);
-    *abort_flag = 1;
-    // never leave the CTA with copies still landing in its shared memory
-    for (int st = 0; st < kStages; ++st)
-      if (issued & (1u << st))
-        mbar_wait_bounded(full0 + 8 * st, (parity_bits >> st) & 1u, 1000000000ull);
+  if (!ok || *abort_flag) {
+    if (lane == 0) {
+      status_or(p.tm, HPA_STATUS_TIMEOUT);
+      *reinterpret_cast<volatile int *>(smem + S::kFlag) = 1;
+    }
+    // never leave the CTA with copies still landing in its shared memory: the last page of each
+    // stage, and the last query rows of each slot
+    if (lane < kStages && n0 > lane) {
+      const int last = n0 - 1 - (n0 - 1 - lane) % kStages;
+      mbar_wait_bounded_rolled(full0 + 8 * lane, (last / kStages) & 1, 1000000000ull);
+    }
+    if (lane < 2 && nq > lane) {
+      const int last = nq - 1 - (nq - 1 - lane) % 2;
+      mbar_wait_bounded_rolled(qfull0 + 8 * lane, (last >> 1) & 1, 1000000000ull);
+    }
   }
 }
 
@@ -343,7 +405,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
   const int n_items = head.s_end - head.s_begin;
   for (int k = 0; k < n_items; ++k) {
     const int s = head.s_begin + k, slot = k & 1;
-    bool ok = !*abort_flag && mbar_wait_bounded(qfull0 + 8 * slot, (k >> 1) & 1);
+    bool ok = wait_phase(qfull0 + 8 * slot, (k >> 1) & 1, abort_flag);
     ok = __all_sync(kFull, ok);
     Seg f;
     {
@@ -443,7 +505,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
     auto page = [&](int pg, int stage, uint32_t phase, auto edge_tag) {
       constexpr bool EDGE = decltype(edge_tag)::value;
       constexpr int KG = Cfg<NT>::kGroups, KP = Cfg<NT>::kSide;
-      const bool got = !(*abort_flag) && mbar_wait_bounded(full0 + 8 * stage, phase);
+      const bool got = wait_phase(full0 + 8 * stage, phase, abort_flag);
       if (!__all_sync(kFull, got)) {
         ok = false;
         return;
@@ -789,7 +851,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kBlocks)
       mbar_init(base + S::kBars + 8 * (kStages + st), Cfg<NT>::kShare);
     }
     for (int sl = 0; sl < 2; ++sl) {
-      mbar_init(base + S::kBars + 8 * (2 * kStages + sl), 32);           // qfull
+      mbar_init(base + S::kBars + 8 * (2 * kStages + sl), 1);            // qfull
       mbar_init(base + S::kBars + 8 * (2 * kStages + 2 + sl), kWarps);   // qempty
     }
     *reinterpret_cast<int *>(smem + S::kFlag) = 0;
@@ -809,8 +871,15 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kBlocks)
   pdl_launch_dependents();  // the combine kernel may be scheduled; it waits for this grid
   if (!head.go) return;     // bad map, or a partition with no tiles
   const MapHead m = head;
-  if (threadIdx.x >= kWarps * 32) producer<NT, WIN>(p, k_pool, v_pool, smem, m);
-  else consumer<NT, WIN>(p, smem, m);
+  // With 3 row tiles a thread's share of the registers at launch is 168; the consumers take more,
+  // the producer's warps (one works) keep fewer.  8 * 232 + 4 * 40 = 12 * 168.
+  if (threadIdx.x >= kWarps * 32) {
+    if (NT == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (threadIdx.x < (kWarps + 1) * 32) producer<NT, WIN>(p, k_pool, v_pool, smem, m);
+  } else {
+    if (NT == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    consumer<NT, WIN>(p, smem, m);
+  }
 }
 
 template <int NT, bool WIN>
