@@ -221,11 +221,13 @@ int hpa_plan_window(const int32_t *seq_lens_dev, int32_t B, int32_t q_len, int32
  *               [2^14, 2^15) (taken back out of the scores), so any finite bf16
  *               query converts exactly, down to 2^-28 of its row's largest.
  *               With HPA_KV_E2M1 pages (layout above, pools 16-byte aligned) a kernel of
- *               their own runs at every row count, in row groups of up to 16, with the
+ *               their own runs at every row count, in passes of up to 24 rows, with the
  *               precision of E4M3 pages here: codes times block scales and queries enter the
  *               products exactly, in f16, sums and softmax statistics are fp32 and the
- *               probabilities are rounded to f16 (2^-11).  NaN block scales of keys that a
- *               row does not see do not reach it; a row that sees one is NaN in the result.
+ *               probabilities are rounded to f16 (2^-11 of each; those below 2^-21 of the
+ *               row's largest to 2^-32 of that one).  NaN block scales of keys that a row does
+ *               not see do not reach it; a row that sees one is NaN in the result, of a value's
+ *               block in its 16 elements.
  * page_indptr_dev: int32 [B+1]; page_indices_dev: int32; key i of request r
  *               is slot i % page_size of page page_indices[page_indptr[r] + i / page_size].
  *               page_indptr has to be right when the kernel reads it: no call is told how
@@ -558,8 +560,10 @@ int hpa_evict(void *k_pool_dev, void *v_pool_dev, int32_t kv_dtype, float *acc_d
  * All arithmetic is fp32; nothing is rounded between the steps.
  * q_dev, k_dev, v_dev: bf16, token t's heads from t * stride elements on (so they may be parts
  * of one packed projection), 16-byte aligned, strides multiples of 8.  q_out_dev likewise; it may
- * be q_dev with its stride (in place).  q_dev NULL: no queries; k_dev and v_dev NULL: no cache
- * (num_pages then only bounds the slots).  positions_dev int32, slots_dev int64 [num_tokens].
+ * be q_dev with its stride (in place), and other columns of the rows that hold keys and values;
+ * otherwise what the call writes overlaps neither itself nor what it reads.  q_dev NULL: no
+ * queries; k_dev and v_dev NULL: no cache (num_pages then only bounds the slots).  positions_dev
+ * int32, slots_dev int64 [num_tokens].
  * cos_sin_dev: fp32 [max_pos][rot_dim], 16-byte aligned.
  * A token of slot -1 is passed over, its q_out row left as it was (rows of a captured batch that
  * hold no token, requests that got no pages); so is one of another slot outside the pool

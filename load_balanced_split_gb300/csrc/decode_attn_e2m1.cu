@@ -47,7 +47,7 @@ namespace hpa {
 namespace {
 
 // Query rows in tiles of 8 columns, and what was measured best for each number of them, in us (32
-// x 8192 keys with 8 rows and 128 x 4096 in a window of 1024 and 4 sinks; 64 x 20000 with 16 rows
+// x 8192 keys with 8 rows and 128 windows of 4096 with 16 sinks; 64 x 20000 with 16 rows
 // and 64 x 8000 in a window of 2000; 13 x 20011 with 20 rows and that window with 24):
 //   1 tile:  4 consumer warps in pairs that share a page, three CTAs per SM at 128 registers, 60
 //            and 111 (5 warps with a page each, two CTAs: 62 and 127; four to a page: 72 and 127);

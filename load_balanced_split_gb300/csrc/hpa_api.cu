@@ -278,8 +278,10 @@ static int decode_attn_impl(const void *q_dev, const void *k_pool_dev, const voi
   cudaError_t e =
       e2m1 ? hpa::launch_decode_attn_e2m1(p, k_pool_dev, v_pool_dev,
                                           reinterpret_cast<cudaStream_t>(stream))
-      : tc ? hpa::launch_decode_attn_tc(p, tmk, tmv, kv_dtype, reinterpret_cast<cudaStream_t>(stream))
-           : hpa::launch_decode_attn(p, tmk, tmv, kv_dtype, reinterpret_cast<cudaStream_t>(stream));
+      : tc ? hpa::launch_decode_attn_tc(p, tmk, tmv, kv_dtype,
+                                        reinterpret_cast<cudaStream_t>(stream))
+           : hpa::launch_decode_attn(p, tmk, tmv, kv_dtype,
+                                     reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? HPA_OK : cuda_fail(e);
 }
 
@@ -344,7 +346,7 @@ int hpa_decode_attn_window(const void *q_dev, const void *k_pool_dev, const void
 
 // More than 16 query rows per KV head (MTP with several draft tokens) go to the
 // tcgen05 kernel, which takes all rows in one pass over the keys.
-// (4-bit pages have one kernel, in groups of up to 16 rows.)
+// (4-bit pages have one kernel, in passes of up to 24 rows.)
 static bool routes_to_tc(int32_t Hq, int32_t Hkv, int32_t q_len, int32_t kv_dtype) {
   return kv_dtype != HPA_KV_E2M1 && Hkv >= 1 && Hq % Hkv == 0 &&
          int64_t(Hq / Hkv) * q_len > hpa::MAX_ROWS;
@@ -600,7 +602,8 @@ int hpa_store_qkv(const void *q_dev, int64_t q_stride, const void *k_dev, int64_
   if ((has_q && (q_stride < int64_t(Hq) * d || q_out_stride < int64_t(Hq) * d)) ||
       (has_kv && (k_stride < int64_t(Hkv) * d || v_stride < int64_t(Hkv) * d)))
     return HPA_ERR_INVALID;
-  if ((has_q && (q_stride % 8 || q_out_stride % 8 || !aligned(q_dev, 16) || !aligned(q_out_dev, 16))) ||
+  if ((has_q && (q_stride % 8 || q_out_stride % 8 || !aligned(q_dev, 16) ||
+                 !aligned(q_out_dev, 16))) ||
       (has_kv && (k_stride % 8 || v_stride % 8 || !aligned(k_dev, 16) || !aligned(v_dev, 16) ||
                   !aligned(k_pool_dev, 16) || !aligned(v_pool_dev, 16))) ||
       !aligned(positions_dev, 4) || !aligned(slots_dev, 8) || !aligned(cos_sin_dev, 16) ||
@@ -608,12 +611,36 @@ int hpa_store_qkv(const void *q_dev, int64_t q_stride, const void *k_dev, int64_
       !aligned(v_scale_dev, 4) || !aligned(status_dev, 4))
     return HPA_ERR_ALIGN;
   if (num_tokens == 0) return HPA_OK;
-  const auto span = [&](int64_t stride) {  // bytes from the first query to the last one's end
-    return 2ull * (stride * (num_tokens - 1) + int64_t(Hq) * d);
+  // what the call writes lies apart from what it reads, but for queries in place
+  const auto span = [&](int64_t stride, int32_t heads) {  // from the first row to the last's end
+    return 2ull * (stride * (num_tokens - 1) + int64_t(heads) * d);
   };
+  const uint64_t q_out_bytes = has_q ? span(q_out_stride, Hq) : 0;
   if (has_q && (q_dev != q_out_dev || (q_stride != q_out_stride && num_tokens > 1)) &&
-      overlap(q_dev, span(q_stride), q_out_dev, span(q_out_stride)))
+      overlap(q_dev, span(q_stride, Hq), q_out_dev, q_out_bytes))
     return HPA_ERR_INVALID;
+  const auto meets_q_out = [&](const void *x, int64_t stride) {  // keys or values
+    if (!overlap(x, span(stride, Hkv), q_out_dev, q_out_bytes)) return false;
+    if (num_tokens == 1 || stride != q_out_stride) return true;
+    const int64_t apart = (static_cast<const char *>(x) - static_cast<char *>(q_out_dev)) / 2;
+    const int64_t column = (apart % stride + stride) % stride;  // in a token's packed row
+    return column < int64_t(Hq) * d || column + int64_t(Hkv) * d > stride;
+  };
+  if (has_q && has_kv && (meets_q_out(k_dev, k_stride) || meets_q_out(v_dev, v_stride)))
+    return HPA_ERR_INVALID;
+  if (has_kv) {
+    const uint64_t unit = kv_dtype == HPA_KV_E2M1   ? hpa::E2M1_UNIT
+                          : kv_dtype == HPA_KV_E4M3 ? hpa::PAGE * hpa::HEAD_DIM
+                                                    : hpa::PAGE * hpa::HEAD_DIM * 2;
+    const uint64_t bytes = unit * num_pages * Hkv;
+    if (overlap(k_pool_dev, bytes, v_pool_dev, bytes)) return HPA_ERR_INVALID;
+    for (const void *pool : {k_pool_dev, v_pool_dev})
+      if (overlap(pool, bytes, k_dev, span(k_stride, Hkv)) ||
+          overlap(pool, bytes, v_dev, span(v_stride, Hkv)) ||
+          (has_q && (overlap(pool, bytes, q_dev, span(q_stride, Hq)) ||
+                     overlap(pool, bytes, q_out_dev, q_out_bytes))))
+        return HPA_ERR_INVALID;
+  }
   hpa::StoreQkvParams p;
   p.q = static_cast<const __nv_bfloat16 *>(q_dev);
   p.k = static_cast<const __nv_bfloat16 *>(k_dev);
@@ -673,15 +700,11 @@ int hpa_assign_pages(const int32_t *seq_lens_dev, const int32_t *new_tokens_dev,
   if (!rows_dev && B > num_rows) return HPA_ERR_INVALID;
   if (page_size != hpa::PAGE) return HPA_ERR_UNSUPPORTED;
   if (!aligned(workspace_dev, 16) || !aligned(slots_dev, 8)) return HPA_ERR_ALIGN;
-  for (const void *p : {static_cast<const void *>(seq_lens_dev), static_cast<const void *>(new_tokens_dev),
-                        static_cast<const void *>(rows_dev), static_cast<const void *>(pos_offset_dev),
-                        static_cast<const void *>(table_dev), static_cast<const void *>(held_in_dev),
-                        static_cast<const void *>(held_out_dev), static_cast<const void *>(free_pages_dev),
-                        static_cast<const void *>(free_count_in_dev),
-                        static_cast<const void *>(free_count_out_dev),
-                        static_cast<const void *>(page_indptr_dev),
-                        static_cast<const void *>(page_indices_dev),
-                        static_cast<const void *>(positions_dev), static_cast<const void *>(status_dev)})
+  const int32_t *const words[] = {
+      seq_lens_dev,      new_tokens_dev,     rows_dev,        pos_offset_dev,   table_dev,
+      held_in_dev,       held_out_dev,       free_pages_dev,  page_indices_dev, page_indptr_dev,
+      free_count_in_dev, free_count_out_dev, positions_dev,   status_dev};
+  for (const int32_t *p : words)
     if (!aligned(p, 4)) return HPA_ERR_ALIGN;
   if (workspace_bytes < hpa_assign_pages_workspace(B, num_rows)) return HPA_ERR_WORKSPACE;
   // the arrays that the call writes lie apart from each other and from what it reads; the state
@@ -710,7 +733,8 @@ int hpa_assign_pages(const int32_t *seq_lens_dev, const int32_t *new_tokens_dev,
       if (overlap(written[i].p, written[i].bytes, written[j].p, written[j].bytes))
         return HPA_ERR_INVALID;
     if (held_in_dev != held_out_dev || written[i].p != held_out_dev)
-      if (overlap(written[i].p, written[i].bytes, held_in_dev, 4ull * num_rows)) return HPA_ERR_INVALID;
+      if (overlap(written[i].p, written[i].bytes, held_in_dev, 4ull * num_rows))
+        return HPA_ERR_INVALID;
     if (free_count_in_dev != free_count_out_dev || written[i].p != free_count_out_dev)
       if (overlap(written[i].p, written[i].bytes, free_count_in_dev, 4)) return HPA_ERR_INVALID;
   }

@@ -674,11 +674,12 @@ def hpa_store_qkv(q, k, v, positions, slots, cos_sin, k_pool=None, v_pool=None, 
                 v_scale, status)
     if n == 0:                    # tensors without elements have no address to pass on
         return
+    flags = (1 if norm_after else 0) + (2 if interleaved else 0) + (4 if use_hadamard else 0)
     rc = lib().hpa_store_qkv(
         _ptr(q), sq, _ptr(k), sk, _ptr(v), sv, n, Hq, Hkv, 128, _ptr(positions), _ptr(slots),
-        _ptr(cos_sin), max_pos, rot, _ptr(q_norm), _ptr(k_norm), eps,
-        (1 if norm_after else 0) + (2 if interleaved else 0) + (4 if use_hadamard else 0), _ptr(q_out), so, kv, _ptr(k_scale),
-        _ptr(v_scale), _ptr(k_pool), _ptr(v_pool), num_pages, 64, _ptr(status), _stream(stream))
+        _ptr(cos_sin), max_pos, rot, _ptr(q_norm), _ptr(k_norm), eps, flags, _ptr(q_out), so, kv,
+        _ptr(k_scale), _ptr(v_scale), _ptr(k_pool), _ptr(v_pool), num_pages, 64, _ptr(status),
+        _stream(stream))
     if rc != 0:
         _check(rc, "hpa_store_qkv")
 
@@ -962,7 +963,8 @@ class PageTable:
     def assign(self, seq_lens, new_tokens=None, rows=None, pos_offset=None, stream=None):
         B = seq_lens.numel()
         if B + 1 > self._indptr.numel():
-            raise HpaError("a batch of %d requests, and room for %d" % (B, self._indptr.numel() - 1))
+            raise HpaError("a batch of %d requests, and room for %d"
+                           % (B, self._indptr.numel() - 1))
         self.page_indptr = self._indptr[:B + 1]
         slots, positions = (None, None) if new_tokens is None else (self.slots, self.positions)
         hpa_assign_pages(seq_lens, new_tokens, self.table, self.held, self.free_pages,
@@ -1060,7 +1062,7 @@ def decode_step(ws: Workspace, q, k_pool, v_pool, seq_lens, page_indptr, page_in
     stream = _stream(stream)
     if plan:
         if tile is None and ws.window is None and _is_e2m1(k_pool):
-            tile = 256      # 4-bit pages: as long a read as 128 keys of 8 bits (1 x 100000: 35 -> 33 us)
+            tile = 256  # as long a read as 144 keys of 8 bits (1 x 100000 keys: 35 -> 33 us)
         ws.plan(seq_lens, tile, stream)
     if fused:
         hpa_decode_attn_fused(q, k_pool, v_pool, page_indptr, page_indices, ws.taskmap,

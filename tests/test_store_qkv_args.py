@@ -41,6 +41,20 @@ def test_argument_checks():
     assert _call(n=0) == 0
 
 
+def test_what_is_written_lies_apart():
+    """Queries over keys or values still to be read, and pools over anything, are refused."""
+    far = dict(q=FAKE, k=2 * FAKE, v=3 * FAKE, qo=4 * FAKE, kp=8 * FAKE, vp=16 * FAKE)
+    for bad in (dict(qo=2 * FAKE), dict(qo=2 * FAKE + 256), dict(qo=3 * FAKE - 2048),
+                dict(qo=2 * FAKE - 256, n=1), dict(vp=8 * FAKE), dict(vp=8 * FAKE + 16384),
+                dict(kp=FAKE), dict(vp=4 * FAKE - 32768), dict(kp=2 * FAKE), dict(vp=3 * FAKE + 512),
+                # packed rows of 12 heads: queries reaching into the keys, keys before the queries
+                dict(q=FAKE, qo=FAKE, k=FAKE + 7 * 256, v=FAKE + 10 * 256, sq=1536, sk=1536,
+                     sv=1536, so=1536),
+                dict(q=FAKE, qo=FAKE, k=FAKE + 8 * 256, v=FAKE + 11 * 256, sq=1536, sk=1536,
+                     sv=1536, so=1536)):
+        assert _call(**{**far, **bad}) == -1, bad
+
+
 def test_binding_refusals():
     t = torch.zeros(4, 8, 128, dtype=torch.bfloat16)
     i = torch.zeros(4, dtype=torch.int32)
