@@ -10,17 +10,22 @@
 // 1 / rms is one factor per row and passes through the linear steps, so it is applied once, with
 // the cache's scale, where the row is written; nothing is rounded before that.
 //
-// Every row is read once and written once, so the DRAM bounds it.  A warp takes items of up to 8
-// rows (one token, heads of q, of k or of v), four rows at a time, 8 lanes to a row: lane k holds
-// dims [8k, 8k + 8) and [64 + 8k, 64 + 8k + 8), so that the pairs of a full rotation of halves and
-// of adjacent dims lie in one lane, and loads and stores are 16 bytes wide.  The next item's rows
-// are on their way to shared memory while one is worked on.
+// Every row is read once and written once.  Without the transform the DRAM bounds it: 32768 tokens
+// of 64/8 heads, normed and rotated into a bf16 cache, take 211 us, 6.4 TB/s or 0.95 of the copy
+// peak.  With it the issue slots do, two thirds of which are taken (48 shuffles and 24 additions
+// of pairs for four rows, beside some 130 others): 296 us into a 4-bit cache, 4.3 TB/s.  A small
+// batch is one launch (3.7 us for a token, 4.3 for 128).
+//
+// A warp takes items of up to 8 rows (one token, heads of q, of k or of v), four rows at a time, 8
+// lanes to a row: lane k holds dims [8k, 8k + 8) and [64 + 8k, 64 + 8k + 8), so that the pairs of a
+// full rotation of halves and of adjacent dims lie in one lane, and loads and stores are 16 bytes
+// wide.  The next item's rows are on their way to shared memory while one is worked on.
 #include "hpa_internal.cuh"
 
 namespace hpa {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 10;  // two blocks at 96 registers (8 at 108 take 311 us, 12 at 80 300)
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kLanesPerHead = 8;
 constexpr int kHeadsPerPass = 32 / kLanesPerHead;
@@ -281,7 +286,7 @@ __device__ __forceinline__ void store_row(void *pool, int kv_dtype, int64_t unit
     // codes = E2M1 of the quotients.  A quotient on the border of two codes is common (bf16
     // inputs, scales of 4 bits) and has to fall to the even one, which v * (1 / s) alone may miss
     // by its last bit: its exact remainder, times 1 / s, puts that right (Markstein, IBM J. Res.
-    // Dev. 34, 1990; a division each took 335 us where this takes 300, 32768 tokens of 64/8 heads).
+    // Dev. 34, 1990; a division each takes 30 us more, 32768 tokens of 64/8 heads).
     uint8_t *base = static_cast<uint8_t *>(pool) + unit * E2M1_UNIT;
     uint32_t codes[2], sb[2];
 #pragma unroll
@@ -321,29 +326,16 @@ __device__ __forceinline__ void store_row(void *pool, int kv_dtype, int64_t unit
   }
 }
 
-// What a lane keeps from item to item: its table entries and its norm weights.
+// One item, with the table entries that a lane keeps from one to the next of a token.  Norm weights
+// are read again for every four rows: kept too, their 16 registers cost two warps a block.
 template <int ROPE>
-struct Kept {
-  Turn<ROPE> t;
-  f32x2 w[8];
-  int w_kind;
-};
-
-template <int ROPE>
-__device__ __forceinline__ void work(const StoreQkvParams &p, const Item &x, Kept<ROPE> &kept,
+__device__ __forceinline__ void work(const StoreQkvParams &p, const Item &x, Turn<ROPE> &t,
                                      uint32_t slot, uint32_t norms, int lane) {
   const int k = lane % kLanesPerHead, hp = lane / kLanesPerHead;
   const bool key_like = x.kind != KIND_V;
   const bool has_norm = x.kind == KIND_Q ? p.q_norm != nullptr : p.k_norm != nullptr;
-  Turn<ROPE> &t = kept.t;
-  f32x2(&w)[8] = kept.w;
   if (key_like && x.fresh) load_turn<ROPE>(t, slot + kCosOff, k, p.rot_dim);
-  if (key_like && has_norm && kept.w_kind != x.kind) {
-    const uint32_t at = norms + (x.kind == KIND_K) * (HEAD_DIM * 4) + 32 * k;
-    lds_f32x8(at, reinterpret_cast<f32x2(&)[4]>(w[0]));
-    lds_f32x8(at + 256, reinterpret_cast<f32x2(&)[4]>(w[4]));
-    kept.w_kind = x.kind;
-  }
+  const uint32_t wat = norms + (x.kind == KIND_K) * (HEAD_DIM * 4) + 32 * k;
 #pragma unroll 1
   for (int ps = 0; ps * kHeadsPerPass < x.nh; ++ps) {
     const int hh = ps * kHeadsPerPass + hp, h = x.h0 + hh;
@@ -364,12 +356,18 @@ __device__ __forceinline__ void work(const StoreQkvParams &p, const Item &x, Kep
     if (key_like) {
       if (has_norm && !p.norm_after) {
         f = rsqrtf(row_sum_squares(y) / HEAD_DIM + p.eps);
+        f32x2 w[8];
+        lds_f32x8(wat, reinterpret_cast<f32x2(&)[4]>(w[0]));
+        lds_f32x8(wat + 256, reinterpret_cast<f32x2(&)[4]>(w[4]));
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = mul2(y[j], w[j]);
       }
       turn<ROPE>(y, t, k, p.rot_dim);
       if (has_norm && p.norm_after) {
         f = rsqrtf(row_sum_squares(y) / HEAD_DIM + p.eps);
+        f32x2 w[8];
+        lds_f32x8(wat, reinterpret_cast<f32x2(&)[4]>(w[0]));
+        lds_f32x8(wat + 256, reinterpret_cast<f32x2(&)[4]>(w[4]));
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = mul2(y[j], w[j]);
       }
@@ -425,8 +423,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) store_qkv_kernel(const StoreQk
   set_token(p, cur, lane == 0);
   fetch<ROPE>(p, cur, slots, lane);
   cp_async_commit();
-  Kept<ROPE> kept;
-  kept.w_kind = -1;
+  Turn<ROPE> kept;
   for (int i = 0, buf = 0; i < count; ++i, buf ^= 1) {
     Item nxt = cur;
     if (i + 1 < count) {

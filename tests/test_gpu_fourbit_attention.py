@@ -44,6 +44,16 @@ def test_partitions_and_tiles(C, tile):
     _run([1, 500, 1300, 40, 640], 1, C=C, tile=tile, seed=C)
 
 
+@pytest.mark.parametrize("window,sinks", [(None, 0), (70, 3)])
+@pytest.mark.parametrize("C,q_len", [(1, 1), (1, 3), (2, 5), (3, 2)])
+def test_partitions_of_many_requests(C, q_len, window, sinks):
+    """More segments in a partition than are read at once (32), some of them two pages short of a
+    ring's length, some with many pages."""
+    g = np.random.default_rng(50 + C)
+    lens = [int(n) for n in g.integers(q_len, 200, size=75)] + [2500, q_len, 64, 65, 2100, 70]
+    _run(lens, q_len, window, sinks, heads=(8, 1), C=C, tile=64, seed=51)
+
+
 def test_one_long_request_and_a_large_batch():
     _run([70000], 2, heads=(8, 1), seed=3)
     g = np.random.default_rng(4)
