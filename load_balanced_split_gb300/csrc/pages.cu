@@ -10,8 +10,14 @@
 // Two launches.  scan_kernel, one block, makes the sums and a record per request; fill_kernel, a
 // few blocks per request, moves page ids and writes the token slots.  A returned page that is
 // given out in the same step is read from the row that returns it, so no block of the second
-// waits for another.  Both are bound by latency: the second starts while the first still runs
-// (programmatic dependent launch) and waits for its records.
+// waits for another.  Both are bound by latency, of launches and of loads that follow from one
+// another (the largest case reads and writes 5 MB): one request takes 4.3 us, 128 that take a token
+// each 6.3, 1000 with chunks of 256 tokens 12.8, 4000 with a token each 25.6.  The second starts
+// while the first still runs (programmatic dependent launch) and waits for its records.  One block
+// for the sums because a step of 1000 requests is then one load and two scans, without a meeting of
+// blocks; its scattered accesses (a row per request) are what it spends most on, so the owners of
+// rows are in shared memory where they fit (1000 requests 17.3 -> 12.8 us with records in two
+// arrays, 4000 60 -> 25.6).
 #include <climits>
 
 #include "hpa_internal.cuh"
@@ -21,21 +27,31 @@ namespace {
 
 constexpr int kFillThreads = 256;
 
-// What fill_kernel needs of a request, two 16-byte words.
-struct Record {
-  int row;       // its row of the table, -1: none
-  int held;      // pages it holds before the step
-  int pages;     // pages it holds after the step
-  int served;    // its tokens get slots
+// What fill_kernel needs of a request, two 16-byte words in arrays of their own (a warp's then lie
+// together).
+struct __align__(16) Pages {
+  int row;     // its row of the table, -1: none
+  int held;    // pages it holds before the step
+  int pages;   // pages it holds after the step
+  int served;  // its tokens get slots
+};
+struct __align__(16) Places {
   int take_off;  // pages that requests before it take
   int back_off;  // pages that requests before it return
   int tok_off;   // tokens of the requests before it
   int len;
 };
-static_assert(sizeof(Record) == 32, "two int4");
 
-// Workspace: totals (16 words), records, the owner of each row.
+// Workspace: totals (16 words), Pages and Places of each request, the owner of each row.
 enum { WS_FREE = 0, WS_AVAIL, WS_TOKENS, WS_HEADER_WORDS = 16 };
+constexpr int kSharedRows = 8192;  // tables of up to so many rows have their owners in shared memory
+
+__device__ __forceinline__ Pages *pages_at(const AssignParams &p) {
+  return reinterpret_cast<Pages *>(p.ws + WS_HEADER_WORDS);
+}
+__device__ __forceinline__ Places *places_at(const AssignParams &p) {
+  return reinterpret_cast<Places *>(p.ws + WS_HEADER_WORDS) + p.B;
+}
 
 struct Sum2 {
   long long a, b;
@@ -76,16 +92,35 @@ __device__ __forceinline__ int clip(long long x) {
   return x > INT_MAX ? INT_MAX : static_cast<int>(x);
 }
 
+// What a request says and has, its loads started together.
+struct Request {
+  int row, L, nt, held;
+};
+__device__ __forceinline__ Request load_request(const AssignParams &p, int r) {
+  Request q;
+  q.row = p.rows ? p.rows[r] : r;
+  q.L = p.seq_lens[r];
+  q.nt = p.new_tokens ? p.new_tokens[r] : 0;
+  q.held = q.row >= 0 && q.row < p.num_rows ? p.held_in[q.row] : 0;
+  return q;
+}
+
+template <bool kOwnersShared>
 __global__ void __launch_bounds__(1024) scan_kernel(const AssignParams p) {
   pdl_launch_dependents();  // fill_kernel waits for this grid before it reads
   pdl_wait();
   __shared__ Sum2 wbuf[32];
   __shared__ int s_bad;
+  extern __shared__ int32_t s_owner[];
   const int tid = threadIdx.x, n = blockDim.x;
-  Record *rec = reinterpret_cast<Record *>(p.ws + WS_HEADER_WORDS);
-  int32_t *owner = p.ws + WS_HEADER_WORDS + 8 * static_cast<int64_t>(p.B);
+  Pages *pages_ws = pages_at(p);
+  Places *places_ws = places_at(p);
+  int32_t *owner =
+      kOwnersShared ? s_owner : p.ws + WS_HEADER_WORDS + 8 * static_cast<int64_t>(p.B);
   if (tid == 0) s_bad = 0;
   int free = *p.free_in;
+  Request req = {-1, 0, 0, 0};
+  if (tid < p.B) req = load_request(p, tid);
   __syncthreads();
   if (free < 0 || free > p.num_pages) {  // a damaged state: nothing is given out
     if (tid == 0) atomicOr(&s_bad, HPA_STATUS_BAD_MAP);
@@ -93,34 +128,37 @@ __global__ void __launch_bounds__(1024) scan_kernel(const AssignParams p) {
   }
   if (p.rows) {  // a row listed twice belongs to the first request that lists it
     for (int r = tid; r < p.B; r += n) {
-      const int row = p.rows[r];
+      const int row = r == tid ? req.row : p.rows[r];
       if (row >= 0 && row < p.num_rows) owner[row] = INT_MAX;
     }
     __syncthreads();
     for (int r = tid; r < p.B; r += n) {
-      const int row = p.rows[r];
+      const int row = r == tid ? req.row : p.rows[r];
       if (row >= 0 && row < p.num_rows) atomicMin(owner + row, r);
     }
-    __threadfence_block();
+    if (!kOwnersShared) __threadfence_block();
     __syncthreads();
   }
   // returned and wanted pages
   Sum2 carry = {0, 0}, total;
-  Record mine = {};
+  Pages mine = {-1, 0, 0, 0};
+  Places mine_at = {0, 0, 0, 0};
   for (int base = 0; base < p.B; base += n) {
     const int r = base + tid;
-    Record x = {-1, 0, 0, 0, 0, 0, 0, 0};
+    Pages x = {-1, 0, 0, 0};
+    Places at = {0, 0, 0, 0};
     long long back = 0, take = 0;
     if (r < p.B) {
-      int row = p.rows ? p.rows[r] : r;
-      const int L = p.seq_lens[r], nt = p.new_tokens ? p.new_tokens[r] : 0;
+      if (base > 0) req = load_request(p, r);
+      int row = req.row, held = req.held;
+      const int L = req.L, nt = req.nt;
       int bad = 0;
       if (row < 0 || row >= p.num_rows ||
           (p.rows && *reinterpret_cast<volatile int32_t *>(owner + row) != r)) {
         bad = HPA_STATUS_BAD_MAP;
         row = -1;
+        held = 0;
       }
-      int held = row < 0 ? 0 : p.held_in[row];
       if (held < 0 || held > p.stride) {
         bad |= HPA_STATUS_BAD_MAP;
         row = -1;
@@ -134,16 +172,21 @@ __global__ void __launch_bounds__(1024) scan_kernel(const AssignParams p) {
       x.held = held;
       x.pages = bad ? held : need;
       x.served = !bad;
-      x.len = L;
+      at.len = L;
       back = max(held - x.pages, 0);
       take = max(x.pages - held, 0);
     }
     const Sum2 s = block_scan2({back, take}, wbuf, total);
     if (r < p.B) {
-      x.back_off = clip(carry.a + s.a - back);
-      x.take_off = clip(carry.b + s.b - take);
-      if (p.B <= n) mine = x;  // one round: the records stay in registers
-      else rec[r] = x;
+      at.back_off = clip(carry.a + s.a - back);
+      at.take_off = clip(carry.b + s.b - take);
+      if (p.B <= n) {  // one round: they stay in registers
+        mine = x;
+        mine_at = at;
+      } else {
+        pages_ws[r] = x;
+        places_ws[r] = at;
+      }
     }
     carry.a += total.a;
     carry.b += total.b;
@@ -155,24 +198,31 @@ __global__ void __launch_bounds__(1024) scan_kernel(const AssignParams p) {
   for (int base = 0; base < p.B; base += n) {
     const int r = base + tid;
     long long pages = 0, tokens = 0;
-    Record x = {-1, 0, 0, 0, 0, 0, 0, 0};
+    Pages x = mine;
+    Places at = mine_at;
+    int nt = req.nt;
     if (r < p.B) {
-      x = p.B <= n ? mine : rec[r];
+      if (p.B > n) {
+        x = pages_ws[r];
+        at = places_ws[r];
+        nt = p.new_tokens ? p.new_tokens[r] : 0;
+      }
       const int take = x.pages - x.held;
-      if (take > 0 && static_cast<long long>(x.take_off) + take > avail) {
+      if (take > 0 && static_cast<long long>(at.take_off) + take > avail) {
         x.pages = x.held;
         x.served = 0;
         atomicOr(&s_bad, HPA_STATUS_NO_PAGES);
       }
-      if (take > 0 && x.served) given = max(given, static_cast<long long>(x.take_off) + take);
+      if (take > 0 && x.served) given = max(given, static_cast<long long>(at.take_off) + take);
       pages = x.pages;
-      tokens = p.new_tokens ? max(p.new_tokens[r], 0) : 0;
+      tokens = max(nt, 0);
       if (x.row >= 0) p.held_out[x.row] = x.pages;
     }
     const Sum2 s = block_scan2({pages, tokens}, wbuf, total);
     if (r < p.B) {
-      x.tok_off = clip(done.b + s.b - tokens);
-      rec[r] = x;
+      at.tok_off = clip(done.b + s.b - tokens);
+      pages_ws[r] = x;
+      places_ws[r] = at;
       // what passes the list's end is cut, for the attention calls trust these offsets
       const long long end = done.a + s.a;
       p.page_indptr[r + 1] = static_cast<int32_t>(end < p.indices_cap ? end : p.indices_cap);
@@ -199,60 +249,61 @@ __global__ void __launch_bounds__(1024) scan_kernel(const AssignParams p) {
 }
 
 // Page i of a request after the step: from its own row, or from the stack.
-__device__ __forceinline__ int page_of(const AssignParams &p, const Record *rec, const Record &x,
+__device__ __forceinline__ int page_of(const AssignParams &p, const Pages &x, const Places &at,
                                        int i, int free, int avail) {
   if (i < x.held) return p.table[static_cast<int64_t>(x.row) * p.stride + i];
-  const int v = avail - 1 - (x.take_off + i - x.held);
+  const int v = avail - 1 - (at.take_off + i - x.held);
   if (v < free) return p.free_pages[v];
   // returned in this step: the last request with back_off <= v - free that returns any
   const int want = v - free;
   int lo = 0, hi = p.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (rec[mid].back_off <= want) lo = mid;
+    if (places_at(p)[mid].back_off <= want) lo = mid;
     else hi = mid - 1;
   }
-  const Record q = rec[lo];
-  return p.table[static_cast<int64_t>(q.row) * p.stride + q.pages + want - q.back_off];
+  const Pages q = pages_at(p)[lo];
+  return p.table[static_cast<int64_t>(q.row) * p.stride + q.pages + want -
+                 places_at(p)[lo].back_off];
 }
 
 __global__ void __launch_bounds__(kFillThreads) fill_kernel(const AssignParams p) {
   pdl_wait();
-  const Record *rec = reinterpret_cast<const Record *>(p.ws + WS_HEADER_WORDS);
   const int r = blockIdx.x, first = blockIdx.y * kFillThreads + threadIdx.x;
   const int step = gridDim.y * kFillThreads;
   const int free = p.ws[WS_FREE], avail = p.ws[WS_AVAIL];
-  const Record x = rec[r];
+  const Pages x = pages_at(p)[r];
+  const Places at = places_at(p)[r];
   int bad = 0;
   // the request's page list, and its new pages into the table
   const int begin = p.page_indptr[r], room = p.page_indptr[r + 1] - begin;
   int32_t *row = p.table + static_cast<int64_t>(x.row < 0 ? 0 : x.row) * p.stride;
   for (int i = first; i < x.pages; i += step) {
-    const int id = page_of(p, rec, x, i, free, avail);
+    const int id = page_of(p, x, at, i, free, avail);
     if (id < 0 || id >= p.num_pages) bad = HPA_STATUS_BAD_PAGE;
     if (i >= x.held) row[i] = id;
     if (i < room) p.page_indices[begin + i] = id;
   }
   // the pages it returns
   for (int i = x.pages + first; i < x.held; i += step) {
-    const long long to = static_cast<long long>(free) + x.back_off + i - x.pages;
+    const long long to = static_cast<long long>(free) + at.back_off + i - x.pages;
     if (to < p.num_pages) p.free_pages[to] = row[i];
     else bad |= HPA_STATUS_BAD_MAP;  // more pages than there are: a damaged state
   }
   if (p.new_tokens) {
     const int nt = p.new_tokens[r], offset = p.pos_offset ? p.pos_offset[r] : 0;
-    const int end = min(max(nt, 0), max(p.max_tokens - x.tok_off, 0));
+    const int end = min(max(nt, 0), max(p.max_tokens - at.tok_off, 0));
     for (int t = first; t < end; t += step) {
-      const int pos = max(x.len - nt + t, 0);
+      const int pos = max(at.len - nt + t, 0);
       long long slot = -1;
       if (x.served) {
-        const int id = page_of(p, rec, x, pos / PAGE, free, avail);
+        const int id = page_of(p, x, at, pos / PAGE, free, avail);
         if (id >= 0 && id < p.num_pages) slot = static_cast<long long>(id) * PAGE + pos % PAGE;
       }
-      p.slots[x.tok_off + t] = slot;
-      const long long at = static_cast<long long>(pos) + offset;
-      p.positions[x.tok_off + t] =
-          static_cast<int32_t>(at > INT_MAX ? INT_MAX : at < INT_MIN ? INT_MIN : at);
+      p.slots[at.tok_off + t] = slot;
+      const long long text = static_cast<long long>(pos) + offset;
+      p.positions[at.tok_off + t] =
+          static_cast<int32_t>(text > INT_MAX ? INT_MAX : text < INT_MIN ? INT_MIN : text);
     }
     // places behind the last token
     const int total = p.ws[WS_TOKENS];
@@ -281,8 +332,12 @@ cudaError_t launch_assign_pages(const AssignParams &p, cudaStream_t s) {
   cfg.stream = s;
   cfg.gridDim = dim3(1);
   cfg.blockDim = dim3(p.B >= 1024 ? 1024 : (p.B + 31) / 32 * 32);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, scan_kernel, p);
+  const bool shared = p.rows && p.num_rows <= kSharedRows;
+  cfg.dynamicSmemBytes = shared ? 4 * p.num_rows : 0;
+  cudaError_t e = shared ? cudaLaunchKernelEx(&cfg, scan_kernel<true>, p)
+                         : cudaLaunchKernelEx(&cfg, scan_kernel<false>, p);
   if (e != cudaSuccess) return e;
+  cfg.dynamicSmemBytes = 0;
   const int y = (p.stride + 4 * kFillThreads - 1) / (4 * kFillThreads);
   cfg.gridDim = dim3(p.B, y < 64 ? y : 64);
   cfg.blockDim = dim3(kFillThreads);

@@ -94,6 +94,17 @@ def test_lengths_and_counts_out_of_range():
     assert both.step([70, 70], [1, 1], [4, 5]) == paging.BAD_MAP
 
 
+@pytest.mark.parametrize("rows", [8192, 8193])
+def test_rows_listed_twice_in_large_tables(rows):
+    """Tables on both sides of the size up to which shared memory tells who owns a row."""
+    rng = random.Random(rows)
+    both = Both(6000, rows, 3, 1300, 2000)
+    for B in (1300, 900, 1024):
+        which = [rng.choice([rng.randrange(rows), rng.randrange(40), -1, rows]) for _ in range(B)]
+        lens = [rng.randint(0, 192) for _ in range(B)]
+        assert both.step(lens, [min(x, 1) for x in lens], which) == paging.BAD_MAP
+
+
 def test_damaged_stack_is_reported_and_nothing_is_written_past_it():
     pt = hpa.PageTable(8, 2, 8, max_tokens=70)
     pt.assign(_i32([64 * 3, 64]), _i32([1, 1]))
