@@ -7,17 +7,17 @@
 //   and its i-th new page is the stack's entry free + sum back - 1 - (sum_{q < r} take_q + i).
 // All of it follows from running sums over the requests, so the result is the same on every run.
 //
-// Two launches.  scan_kernel, one block, makes the sums and a record per request; fill_kernel, a
-// few blocks per request, moves page ids and writes the token slots.  A returned page that is
-// given out in the same step is read from the row that returns it, so no block of the second
-// waits for another.  Both are bound by latency, of launches and of loads that follow from one
-// another (the largest case reads and writes 5 MB): one request takes 4.3 us, 128 that take a token
-// each 6.3, 1000 with chunks of 256 tokens 12.8, 4000 with a token each 25.6.  The second starts
-// while the first still runs (programmatic dependent launch) and waits for its records.  One block
-// for the sums because a step of 1000 requests is then one load and two scans, without a meeting of
-// blocks; its scattered accesses (a row per request) are what it spends most on, so the owners of
-// rows are in shared memory where they fit (1000 requests 17.3 -> 12.8 us with records in two
-// arrays, 4000 60 -> 25.6).
+// Two launches (one for a few short requests).  scan_kernel, one block, makes the sums and a record
+// per request; fill_kernel, a few blocks per request, moves page ids and writes the token slots.  A
+// returned page that is given out in the same step is read from the row that returns it, so no
+// block of the second waits for another.  Both are bound by latency, of launches and of loads that
+// follow from one another (the largest case reads and writes 5 MB): one request takes 3.9 us, 128
+// that take a token each 6.3 to 7.2, 1000 with chunks of 256 tokens 13, 4000 with a token each 26.
+// The second starts while the first still runs (programmatic dependent launch) and waits for its
+// records.  One block for the sums because a step of 1000 requests is then one load and two scans,
+// without a meeting of blocks; its scattered accesses (a row per request) are what it spends most
+// on, so the owners of rows are in shared memory where they fit (1000 requests 17 -> 13 us with
+// records in two arrays, 4000 60 -> 26).
 #include <climits>
 
 #include "hpa_internal.cuh"
@@ -44,7 +44,7 @@ struct __align__(16) Places {
 
 // Workspace: totals (16 words), Pages and Places of each request, the owner of each row.
 enum { WS_FREE = 0, WS_AVAIL, WS_TOKENS, WS_HEADER_WORDS = 16 };
-constexpr int kSharedRows = 8192;  // tables of up to so many rows have their owners in shared memory
+constexpr int kSharedRows = 8192;  // up to so many rows have their owners in shared memory
 
 __device__ __forceinline__ Pages *pages_at(const AssignParams &p) {
   return reinterpret_cast<Pages *>(p.ws + WS_HEADER_WORDS);
@@ -92,6 +92,82 @@ __device__ __forceinline__ int clip(long long x) {
   return x > INT_MAX ? INT_MAX : static_cast<int>(x);
 }
 
+// Page i of a request after the step: from its own row, or from the stack.
+__device__ __forceinline__ int page_of(const AssignParams &p, const Pages &x, const Places &at,
+                                       int i, int free, int avail) {
+  if (i < x.held) return p.table[static_cast<int64_t>(x.row) * p.stride + i];
+  const int v = avail - 1 - (at.take_off + i - x.held);
+  if (v < free) return p.free_pages[v];
+  // returned in this step: the last request with back_off <= v - free that returns any
+  const int want = v - free;
+  int lo = 0, hi = p.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (places_at(p)[mid].back_off <= want) lo = mid;
+    else hi = mid - 1;
+  }
+  const Pages q = pages_at(p)[lo];
+  return p.table[static_cast<int64_t>(q.row) * p.stride + q.pages + want -
+                 places_at(p)[lo].back_off];
+}
+
+// What follows from the sums for one request, by `step` threads of which this is number `first`.
+__device__ __forceinline__ void fill_request(const AssignParams &p, int r, int first, int step) {
+  const int free = p.ws[WS_FREE], avail = p.ws[WS_AVAIL];
+  const Pages x = pages_at(p)[r];
+  const Places at = places_at(p)[r];
+  int bad = 0;
+  // the request's page list, and its new pages into the table
+  const int begin = p.page_indptr[r], room = p.page_indptr[r + 1] - begin;
+  int32_t *row = p.table + static_cast<int64_t>(x.row < 0 ? 0 : x.row) * p.stride;
+  for (int i = first; i < x.pages; i += step) {
+    const int id = page_of(p, x, at, i, free, avail);
+    if (id < 0 || id >= p.num_pages) bad = HPA_STATUS_BAD_PAGE;
+    if (i >= x.held) row[i] = id;
+    if (i < room) p.page_indices[begin + i] = id;
+  }
+  // the pages it returns
+  for (int i = x.pages + first; i < x.held; i += step) {
+    const long long to = static_cast<long long>(free) + at.back_off + i - x.pages;
+    if (to < p.num_pages) p.free_pages[to] = row[i];
+    else bad |= HPA_STATUS_BAD_MAP;  // more pages than there are: a damaged state
+  }
+  if (p.new_tokens) {
+    const int nt = p.new_tokens[r], offset = p.pos_offset ? p.pos_offset[r] : 0;
+    const int end = min(max(nt, 0), max(p.max_tokens - at.tok_off, 0));
+    for (int t = first; t < end; t += step) {
+      const int pos = max(at.len - nt + t, 0);
+      long long slot = -1;
+      if (x.served) {
+        const int id = page_of(p, x, at, pos / PAGE, free, avail);
+        if (id >= 0 && id < p.num_pages) slot = static_cast<long long>(id) * PAGE + pos % PAGE;
+      }
+      p.slots[at.tok_off + t] = slot;
+      const long long text = static_cast<long long>(pos) + offset;
+      p.positions[at.tok_off + t] =
+          static_cast<int32_t>(text > INT_MAX ? INT_MAX : text < INT_MIN ? INT_MIN : text);
+    }
+  }
+  if (bad && p.status) atomicOr(reinterpret_cast<int *>(p.status), bad);
+}
+
+// The places behind the last token.
+__device__ __forceinline__ void fill_rest(const AssignParams &p, long long first, long long step) {
+  if (!p.new_tokens) return;
+  for (long long t = p.ws[WS_TOKENS] + first; t < p.max_tokens; t += step) {
+    p.slots[t] = -1;
+    p.positions[t] = 0;
+  }
+}
+
+__global__ void __launch_bounds__(kFillThreads) fill_kernel(const AssignParams p) {
+  pdl_wait();
+  const int first = blockIdx.y * kFillThreads + threadIdx.x, step = gridDim.y * kFillThreads;
+  fill_request(p, blockIdx.x, first, step);
+  fill_rest(p, static_cast<long long>(blockIdx.x) * step + first,
+            static_cast<long long>(gridDim.x) * step);
+}
+
 // What a request says and has, its loads started together.
 struct Request {
   int row, L, nt, held;
@@ -105,9 +181,10 @@ __device__ __forceinline__ Request load_request(const AssignParams &p, int r) {
   return q;
 }
 
+// spread: threads a request for the whole step in this one block; 0: fill_kernel follows.
 template <bool kOwnersShared>
-__global__ void __launch_bounds__(1024) scan_kernel(const AssignParams p) {
-  pdl_launch_dependents();  // fill_kernel waits for this grid before it reads
+__global__ void __launch_bounds__(1024) scan_kernel(const AssignParams p, int spread) {
+  if (spread == 0) pdl_launch_dependents();  // fill_kernel waits for this grid before it reads
   pdl_wait();
   __shared__ Sum2 wbuf[32];
   __shared__ int s_bad;
@@ -246,74 +323,11 @@ __global__ void __launch_bounds__(1024) scan_kernel(const AssignParams p) {
     p.ws[WS_TOKENS] = clip(done.b);
     if (p.status && s_bad) atomicOr(reinterpret_cast<int *>(p.status), s_bad);
   }
-}
-
-// Page i of a request after the step: from its own row, or from the stack.
-__device__ __forceinline__ int page_of(const AssignParams &p, const Pages &x, const Places &at,
-                                       int i, int free, int avail) {
-  if (i < x.held) return p.table[static_cast<int64_t>(x.row) * p.stride + i];
-  const int v = avail - 1 - (at.take_off + i - x.held);
-  if (v < free) return p.free_pages[v];
-  // returned in this step: the last request with back_off <= v - free that returns any
-  const int want = v - free;
-  int lo = 0, hi = p.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (places_at(p)[mid].back_off <= want) lo = mid;
-    else hi = mid - 1;
+  if (spread > 0) {
+    __syncthreads();
+    if (tid / spread < p.B) fill_request(p, tid / spread, tid % spread, spread);
+    fill_rest(p, tid, n);
   }
-  const Pages q = pages_at(p)[lo];
-  return p.table[static_cast<int64_t>(q.row) * p.stride + q.pages + want -
-                 places_at(p)[lo].back_off];
-}
-
-__global__ void __launch_bounds__(kFillThreads) fill_kernel(const AssignParams p) {
-  pdl_wait();
-  const int r = blockIdx.x, first = blockIdx.y * kFillThreads + threadIdx.x;
-  const int step = gridDim.y * kFillThreads;
-  const int free = p.ws[WS_FREE], avail = p.ws[WS_AVAIL];
-  const Pages x = pages_at(p)[r];
-  const Places at = places_at(p)[r];
-  int bad = 0;
-  // the request's page list, and its new pages into the table
-  const int begin = p.page_indptr[r], room = p.page_indptr[r + 1] - begin;
-  int32_t *row = p.table + static_cast<int64_t>(x.row < 0 ? 0 : x.row) * p.stride;
-  for (int i = first; i < x.pages; i += step) {
-    const int id = page_of(p, x, at, i, free, avail);
-    if (id < 0 || id >= p.num_pages) bad = HPA_STATUS_BAD_PAGE;
-    if (i >= x.held) row[i] = id;
-    if (i < room) p.page_indices[begin + i] = id;
-  }
-  // the pages it returns
-  for (int i = x.pages + first; i < x.held; i += step) {
-    const long long to = static_cast<long long>(free) + at.back_off + i - x.pages;
-    if (to < p.num_pages) p.free_pages[to] = row[i];
-    else bad |= HPA_STATUS_BAD_MAP;  // more pages than there are: a damaged state
-  }
-  if (p.new_tokens) {
-    const int nt = p.new_tokens[r], offset = p.pos_offset ? p.pos_offset[r] : 0;
-    const int end = min(max(nt, 0), max(p.max_tokens - at.tok_off, 0));
-    for (int t = first; t < end; t += step) {
-      const int pos = max(at.len - nt + t, 0);
-      long long slot = -1;
-      if (x.served) {
-        const int id = page_of(p, x, at, pos / PAGE, free, avail);
-        if (id >= 0 && id < p.num_pages) slot = static_cast<long long>(id) * PAGE + pos % PAGE;
-      }
-      p.slots[at.tok_off + t] = slot;
-      const long long text = static_cast<long long>(pos) + offset;
-      p.positions[at.tok_off + t] =
-          static_cast<int32_t>(text > INT_MAX ? INT_MAX : text < INT_MIN ? INT_MIN : text);
-    }
-    // places behind the last token
-    const int total = p.ws[WS_TOKENS];
-    for (long long t = total + static_cast<long long>(r) * step + first; t < p.max_tokens;
-         t += static_cast<long long>(gridDim.x) * step) {
-      p.slots[t] = -1;
-      p.positions[t] = 0;
-    }
-  }
-  if (bad && p.status) atomicOr(reinterpret_cast<int *>(p.status), bad);
 }
 
 }  // namespace
@@ -331,12 +345,23 @@ cudaError_t launch_assign_pages(const AssignParams &p, cudaStream_t s) {
   cfg.numAttrs = 1;
   cfg.stream = s;
   cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(p.B >= 1024 ? 1024 : (p.B + 31) / 32 * 32);
+  // A few requests of short lists are done in the first launch, whose one block then has no more
+  // than 4 places a thread to fill: one of 900 tokens 4.3 -> 3.8 us, and 2 of the 12 that the host
+  // takes.  (With 8 to 12 a thread, 8 requests of 8192 tokens 4.2 -> 4.9 and 32 4.9 -> 8.1; with
+  // 32 requests and 3 a thread 5.4 -> 6.0.)
+  int slots = 1;
+  while (slots < p.B) slots *= 2;
+  const int threads = slots <= 8 ? 256 : 32 * slots;
+  const int spread = slots <= 16 && p.stride <= 4 * (threads / slots) &&
+                             p.max_tokens <= 4 * (threads / slots)
+                         ? threads / slots
+                         : 0;
+  cfg.blockDim = dim3(spread ? threads : p.B >= 1024 ? 1024 : (p.B + 31) / 32 * 32);
   const bool shared = p.rows && p.num_rows <= kSharedRows;
   cfg.dynamicSmemBytes = shared ? 4 * p.num_rows : 0;
-  cudaError_t e = shared ? cudaLaunchKernelEx(&cfg, scan_kernel<true>, p)
-                         : cudaLaunchKernelEx(&cfg, scan_kernel<false>, p);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = shared ? cudaLaunchKernelEx(&cfg, scan_kernel<true>, p, spread)
+                         : cudaLaunchKernelEx(&cfg, scan_kernel<false>, p, spread);
+  if (e != cudaSuccess || spread) return e;
   cfg.dynamicSmemBytes = 0;
   const int y = (p.stride + 4 * kFillThreads - 1) / (4 * kFillThreads);
   cfg.gridDim = dim3(p.B, y < 64 ? y : 64);
