@@ -220,8 +220,8 @@ int hpa_plan_window(const int32_t *seq_lens_dev, int32_t B, int32_t q_len, int32
  *               scaled by a power of two that puts its largest |element| in
  *               [2^14, 2^15) (taken back out of the scores), so any finite bf16
  *               query converts exactly, down to 2^-28 of its row's largest.
- *               With HPA_KV_E2M1 pages (layout above, pools 16-byte aligned) a kernel of
- *               their own runs at every row count, in passes of up to 24 rows, with the
+ *               With HPA_KV_E2M1 pages (layout above, pools 16-byte aligned) kernels of
+ *               their own run at every row count, in passes of up to 32 rows, with the
  *               precision of E4M3 pages here: codes times block scales and queries enter the
  *               products exactly, in f16, sums and softmax statistics are fp32 and the
  *               probabilities are rounded to f16 (2^-11 of each; those below 2^-21 of the

@@ -41,52 +41,45 @@
 
 #include <type_traits>
 
-#include "hpa_internal.cuh"
+#include "e2m1.cuh"
 
 namespace hpa {
 namespace {
 
-// Query rows in tiles of 8 columns, and what was measured best for each number of them, in us (32
-// x 8192 keys with 8 rows and 128 windows of 4096 with 16 sinks; 64 x 20000 with 16 rows
-// and 64 x 8000 in a window of 2000; 13 x 20011 with 20 rows and that window with 24):
+// Query rows in tiles of 8 columns (1 or 2), and what was measured best for each number of them, in
+// us (32 x 8192 keys with 8 rows and 128 windows of 4096 with 16 sinks; 64 x 20000 with 16 rows and
+// 64 x 8000 in a window of 2000):
 //   1 tile:  4 consumer warps in pairs that share a page, three CTAs per SM at 128 registers, 60
 //            and 111 (5 warps with a page each, two CTAs: 62 and 127; four to a page: 72 and 127);
 //   2 tiles: the same pairs, two CTAs at 168 registers, query fragments in shared memory, 335
 //            and 48 (a page each gains 1 %, but takes 95 in the window: a segment's last pages,
 //            and its start, then leave warps idle for a page's time; 12 warps in one CTA 315
-//            and 63);
-//   3 tiles: 8 warps in pairs, one CTA, at the 232 registers that the producer's warps leave, one
-//            pass for up to 24 rows: 102 and 76 (a page each and 64 keys a step 97 and 104, two
-//            passes of 2 tiles 153, 4 warps at 168 registers with spills 184).
+//            and 63).
 // The warps of an SM come in fours: with 10 in a CTA the schedulers that have three set the pace.
+// More rows go to decode_attn_e2m1_tc.cu (as 3 tiles here, 8 warps at 232 registers, 13 x 20011
+// keys with 20 rows took 102 where it takes 94).
 template <int NT>
 struct Cfg {
-  static constexpr int kWarps = NT == 3 ? 8 : 4;  // consumer warps
-  static constexpr int kShare = 2;         // warps of a team, which share a page
+  static constexpr int kWarps = 4;                   // consumer warps
+  static constexpr int kShare = 2;                   // warps of a team, which share a page
   static constexpr int kTeams = kWarps / kShare;
-  static constexpr int kBlocks = NT == 1 ? 3 : NT == 2 ? 2 : 1;  // CTAs per SM
-  static constexpr int kStages = NT == 1 ? 6 : NT == 2 ? 8 : 16;
+  static constexpr int kBlocks = NT == 1 ? 3 : 2;    // CTAs per SM
+  static constexpr int kStages = NT == 1 ? 6 : 8;
   // A team meets the same stages again.  Copies may land out of order, so a warp that came to a
   // stage whose page before it, another team's, had not landed would take that page's phase for
   // the end of its own.
   static_assert(kWarps % kShare == 0 && kStages % kTeams == 0, "each stage belongs to one team");
-  static constexpr int kThreads = NT == 3 ? 384 : (kWarps + 1) * 32;  // 3: whole warpgroups
-  static constexpr int kMine = 4 / kShare;  // a page's groups of 16 keys for a warp
-  static constexpr int kGroups = 2;         // groups that share a softmax step
-  static constexpr int kSide = NT == 2 ? 2 : 1;  // groups whose MMA chains run side by side
-  static constexpr bool kSharedQ = NT > 1;       // query fragments in shared memory
+  static constexpr int kThreads = (kWarps + 1) * 32;
+  static constexpr int kMine = 4 / kShare;           // a page's groups of 16 keys for a warp
+  static constexpr int kGroups = 2;                  // groups that share a softmax step
+  static constexpr int kSide = NT == 1 ? 1 : 2;      // groups whose MMA chains run side by side
   // With 16 rows they fill the MMA's 16: S = Q K^T has P in the layout that the second product
-  // wants, without movmatrix, and a lane has 2 rows' statistics, not 4 (351 -> 343 us).
+  // wants, without movmatrix, and a lane has 2 rows' statistics, not 4 (351 -> 343 us).  The query
+  // fragments lie in shared memory then.
   static constexpr bool kRowsOnM = NT == 2;
   static constexpr int kStats = kRowsOnM ? 2 : 2 * NT;
 };
-constexpr int kUnit = E2M1_UNIT;  // bytes of one page and KV head of K or V
 constexpr int kStageBytes = 2 * kUnit;
-constexpr float kRescaleSlack = 8.f;
-// Probabilities are held times 2^7: with the slack up to 2^15 in f16, whose smallest step is then
-// 2^-31 of the row's largest, so that a million small ones beside it are not lost to rounding.
-constexpr float kLift = 7.f;
-constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kQRowBytes = 272;  // 256 of a query row, padded against bank conflicts
 constexpr int kMergeStride = HEAD_DIM + 4;
 
@@ -102,7 +95,7 @@ struct Smem {
   static constexpr int kInfo = kQ + 2 * kQSlot;                      // int4[2]
   static constexpr int kFrag = kInfo + 2 * 16;                       // query fragments, factors
   // full[stages], empty[stages], qfull[2], qempty[2]
-  static constexpr int kBars = kFrag + (Cfg<NT>::kSharedQ ? NT * 8 * 256 + kRows * 4 : 0);
+  static constexpr int kBars = kFrag + (Cfg<NT>::kRowsOnM ? NT * 8 * 256 + kRows * 4 : 0);
   static constexpr int kFlag = kBars + (2 * kStages + 4) * 8;
   static constexpr int kAlloc = kFlag + 16;
 };
@@ -111,44 +104,6 @@ struct Smem {
 // four lanes of a quad read together for V (k = 0, 2, 4, 6 and 1, 3, 5, 7) then lie in both
 // halves of the 128 bytes that shared memory serves at once.
 __device__ __forceinline__ constexpr int key_at(int k) { return k ^ ((k >> 1) & 1); }
-
-// The four bytes of w, two E2M1 codes each, as f16 pairs (low nibble in the low half; exact).
-__device__ __forceinline__ void widen8(uint32_t w, uint32_t (&r)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-      : "r"(w));
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// One half of an f16 pair in both halves (written so that a multiplication can take it in place).
-template <int HI>
-__device__ __forceinline__ uint32_t both_halves(uint32_t a) {
-  uint32_t d;
-  if (HI)
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}"
-        : "=r"(d) : "r"(a));
-  else
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}"
-        : "=r"(d) : "r"(a));
-  return d;
-}
-
-__device__ __forceinline__ void lds64(uint32_t addr, uint32_t &a, uint32_t &b) {
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
-}
-__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
-  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
-}
 
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t a) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
@@ -161,15 +116,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   return d;
 }
 
-__device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void *src, uint32_t bytes,
-                                               uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-      "[%0], [%1], %2, [%3], %4;" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
-      : "memory");
-}
-
 __device__ __forceinline__ float absmax8_bf16(uint4 v) {
   float m = 0.f;
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -178,37 +124,6 @@ __device__ __forceinline__ float absmax8_bf16(uint4 v) {
     m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[i] << 16)),
                        fabsf(__uint_as_float(w[i] & 0xffff0000u))));
   return m;
-}
-
-__device__ __forceinline__ bool e4m3_nan(uint32_t byte) { return (byte & 0x7fu) == 0x7fu; }
-
-struct Seg {
-  int r, L, klo, khi, pg0, pg1;
-};
-
-template <bool WIN>
-__device__ __forceinline__ Seg read_seg(const AttnParams &p, int s, int tile, bool report) {
-  const SegRow sr = read_seg_row<WIN>(p.tm, p.lay, p.B, s, blockIdx.x, tile, report);
-  return Seg{sr.r, sr.L, sr.klo, sr.khi, sr.klo / PAGE, (sr.khi + PAGE - 1) / PAGE};
-}
-
-__device__ __forceinline__ int row_base(const AttnParams &p) {
-  return p.group * static_cast<int>(blockIdx.z);
-}
-__device__ __forceinline__ int group_rows(const AttnParams &p) {
-  return min(p.group, p.rows - row_base(p));
-}
-
-// Wait for a phase; false if it took too long, or if another warp of the CTA gave up.
-__device__ bool wait_phase(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag || globaltimer_ns() - t0 > 2000000000ull) return false;
-  }
 }
 
 // ----------------------------------------------------------------------------- producer
@@ -433,15 +348,14 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
     // Query rows as the B operand: lane (g, c) holds dims [32 c, 32 c + 32) of rows 8 nt + g,
     // scaled by 2^e of the row; sl holds what takes the scores of its columns to log2 units.
     // From 9 rows on the fragments lie in shared memory, one warp's work for all.
-    constexpr bool QS = Cfg<NT>::kSharedQ;
-    uint32_t qf[QS ? 1 : NT][8][2];
-    const uint32_t frag = base + S::kFrag + lane * (RM ? 16 : 8);
+    uint32_t qf[RM ? 1 : NT][8][2];
+    const uint32_t frag = base + S::kFrag + lane * 16;
     float *factor = reinterpret_cast<float *>(smem + S::kFrag + NT * 8 * 256);
     float sl[NS];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if (QS && w != nt) continue;
-      const int row = 8 * nt + g, at = QS ? 0 : nt;
+      if (RM && w != nt) continue;
+      const int row = 8 * nt + g, at = RM ? 0 : nt;
       const uint32_t qa = base + S::kQ + slot * S::kQSlot + row * kQRowBytes + c * 64;
       uint4 raw[4];
       float am = 0.f;
@@ -467,15 +381,11 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
       // never zero, which would make NaN of a hidden key's -inf; at 2^-126 all scores are nothing
       float down = sl2 == 0.f ? 1.f : fabsf(sl2) * exp2i(-e);
       if (down < exp2i(-126)) down = exp2i(-126);
-      if (QS) {
+      if (RM) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          if (RM) {  // registers nt and nt + 2 of the A operand
-            sts32(frag + ks * 512 + 4 * nt, qf[0][ks][0]);
-            sts32(frag + ks * 512 + 8 + 4 * nt, qf[0][ks][1]);
-          } else {
-            sts64(frag + (nt * 8 + ks) * 256, qf[0][ks][0], qf[0][ks][1]);
-          }
+        for (int ks = 0; ks < 8; ++ks) {  // registers nt and nt + 2 of the A operand
+          sts32(frag + ks * 512 + 4 * nt, qf[0][ks][0]);
+          sts32(frag + ks * 512 + 8 + 4 * nt, qf[0][ks][1]);
         }
         if (c == 0) factor[row] = down;
       } else {
@@ -483,7 +393,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
         sl[(2 * nt + 1) % NS] = __shfl_sync(kFull, down, 8 * c + 4);
       }
     }
-    if (QS) {
+    if (RM) {
       named_barrier(1, kWarps * 32);
 #pragma unroll
       for (int i = 0; i < NS; ++i) sl[i] = factor[stat_row(i)];
@@ -549,8 +459,8 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
               } else {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  if (QS) lds64(frag + (nt * 8 + 2 * i + st) * 256, qb[st][nt][0], qb[st][nt][1]);
-                  else qb[st][nt][0] = qf[nt][2 * i + st][0], qb[st][nt][1] = qf[nt][2 * i + st][1];
+                  qb[st][nt][0] = qf[nt][2 * i + st][0];
+                  qb[st][nt][1] = qf[nt][2 * i + st][1];
                 }
               }
             }
@@ -871,15 +781,8 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kBlocks)
   pdl_launch_dependents();  // the combine kernel may be scheduled; it waits for this grid
   if (!head.go) return;     // bad map, or a partition with no tiles
   const MapHead m = head;
-  // With 3 row tiles a thread's share of the registers at launch is 168; the consumers take more,
-  // the producer's warps (one works) keep fewer.  8 * 232 + 4 * 40 = 12 * 168.
-  if (threadIdx.x >= kWarps * 32) {
-    if (NT == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (threadIdx.x < (kWarps + 1) * 32) producer<NT, WIN>(p, k_pool, v_pool, smem, m);
-  } else {
-    if (NT == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-    consumer<NT, WIN>(p, smem, m);
-  }
+  if (threadIdx.x >= kWarps * 32) producer<NT, WIN>(p, k_pool, v_pool, smem, m);
+  else consumer<NT, WIN>(p, smem, m);
 }
 
 template <int NT, bool WIN>
@@ -924,24 +827,28 @@ int occupancy(int *ctas) {
 
 }  // namespace
 
-// Query rows of a KV head in groups of equal size, up to 24: CTAs that share pages keep pace and
+// Query rows of a KV head in groups of equal size, up to 32: CTAs that share pages keep pace and
 // find them in L2.
 int attn_e2m1_group(int rows) {
-  const int groups = (rows + 23) / 24;
+  const int groups = (rows + 31) / 32;
   return (rows + groups - 1) / groups;
 }
 
 cudaError_t launch_decode_attn_e2m1(const AttnParams &p, const void *k_pool, const void *v_pool,
                                     cudaStream_t s) {
-  const auto run = p.group <= 8    ? (p.window ? launch<1, true> : launch<1, false>)
-                   : p.group <= 16 ? (p.window ? launch<2, true> : launch<2, false>)
-                                   : (p.window ? launch<3, true> : launch<3, false>);
+  if (p.group > 16) return launch_decode_attn_e2m1_tc(p, k_pool, v_pool, s);
+  const auto run = p.group <= 8 ? (p.window ? launch<1, true> : launch<1, false>)
+                                : (p.window ? launch<2, true> : launch<2, false>);
   return run(p, k_pool, v_pool, s);
 }
 
 int attn_e2m1_ctas_per_sm(int rows, int *ctas) {
   const int group = attn_e2m1_group(rows);
-  return group <= 8 ? occupancy<1>(ctas) : group <= 16 ? occupancy<2>(ctas) : occupancy<3>(ctas);
+  if (group > 16) {  // a CTA takes an SM's tensor memory
+    *ctas = 1;
+    return 0;
+  }
+  return group <= 8 ? occupancy<1>(ctas) : occupancy<2>(ctas);
 }
 
 }  // namespace hpa

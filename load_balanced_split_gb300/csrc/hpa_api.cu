@@ -346,7 +346,7 @@ int hpa_decode_attn_window(const void *q_dev, const void *k_pool_dev, const void
 
 // More than 16 query rows per KV head (MTP with several draft tokens) go to the
 // tcgen05 kernel, which takes all rows in one pass over the keys.
-// (4-bit pages have one kernel, in passes of up to 24 rows.)
+// (4-bit pages choose by rows in their own launch.)
 static bool routes_to_tc(int32_t Hq, int32_t Hkv, int32_t q_len, int32_t kv_dtype) {
   return kv_dtype != HPA_KV_E2M1 && Hkv >= 1 && Hq % Hkv == 0 &&
          int64_t(Hq / Hkv) * q_len > hpa::MAX_ROWS;

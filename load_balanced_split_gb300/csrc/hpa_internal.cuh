@@ -114,6 +114,8 @@ cudaError_t launch_decode_attn_tc(const AttnParams &p, const CUtensorMap &tmk,
 int attn_tc_ctas_per_sm(int kv_dtype, int rows, int *ctas);  // occupancy query (host)
 cudaError_t launch_decode_attn_e2m1(const AttnParams &p, const void *k_pool, const void *v_pool,
                                     cudaStream_t s);
+cudaError_t launch_decode_attn_e2m1_tc(const AttnParams &p, const void *k_pool, const void *v_pool,
+                                       cudaStream_t s);
 int attn_e2m1_group(int rows);                         // query rows per CTA
 int attn_e2m1_ctas_per_sm(int rows, int *ctas);        // occupancy query (host)
 cudaError_t launch_selftest_wait(int32_t *status, long long limit_ns, cudaStream_t s);

@@ -157,6 +157,93 @@ def test_many_small_probabilities_beside_a_large_one(q_len):
     assert np.abs(lse.double().cpu().numpy() - check[None, :, None]).max() <= 1e-4
 
 
+@pytest.mark.parametrize("heads,q_len", [((8, 1), 4), ((25, 1), 1), ((17, 1), 1), ((8, 1), 8),
+                                         ((50, 2), 2), ((33, 1), 1), ((32, 1), 1)])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (100, 20), (1, 0)])
+def test_more_than_16_rows(heads, q_len, window, sinks):
+    """Every count of pages around a tile's two and the teams' six, in partitions of one to many
+    segments."""
+    lens = [q_len, 63, 64, 65, 127, 128, 129, 200, 330, 385, 450, 700, 1100, 1500]
+    _run(lens, q_len, window, sinks, heads, C=3, tile=128, seed=60)
+    _run([q_len, 2000, 130, 900], q_len, window, sinks, heads, seed=61)
+
+
+@pytest.mark.parametrize("case", ["large", "tiny", "mixed_rows", "negative", "zero"])
+def test_query_scales_of_many_rows(case):
+    b = make_batch([500, 64, 130], 4, (16, 2), seed=62)
+    sm, q = 1 / np.sqrt(128), b.q.float()
+    if case == "large":
+        q, sm = q * 1e5, sm / 1e5
+    elif case == "tiny":
+        q, sm = q * 1e-6, sm * 1e6
+    elif case == "mixed_rows":
+        q[:, :, ::3] *= 1e5
+        q[:, :, 1::3] *= 1e-6
+    else:
+        sm = -sm if case == "negative" else 0.0
+    b.q = q.to(torch.bfloat16)
+    ws, out, lse = step(b, DeviceBatch(b), sm_scale=sm)
+    torch.cuda.synchronize()
+    check_attention(b, out, lse, bounded.attention_rows(b, sm_scale=sm), "e2m1")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_query_row_stays_alone_among_many(bad):
+    b = make_batch([300, 70], 4, (16, 2), seed=63)
+    ref = bounded.attention_rows(b)
+    b.q[0, 1, 3, 77] = bad
+    b.q[1, 0, 12, 0] = bad
+    ws, out, lse = step(b, DeviceBatch(b))
+    got = out.float().cpu().numpy()
+    hit = np.zeros(got.shape[:3], bool)
+    hit[0, 1, 3] = hit[1, 0, 12] = True
+    assert np.isnan(got[hit]).all()
+    bound = out_bound(ref[0], ref[2], ref[3], "e2m1")
+    assert (np.abs(got - ref[0])[~hit] <= bound[~hit]).all()
+
+
+def test_rising_scores_of_many_rows():
+    """The maximum moves with nearly every tile, each row's at its own keys."""
+    b = make_batch([3000, 1300], 3, (16, 2), seed=64)
+    _, scales = rows_of(b.k_pool)
+    for r, L in enumerate([3000, 1300]):
+        ids = b.page_indices[int(b.page_indptr[r]):int(b.page_indptr[r + 1])]
+        for n, page in enumerate(ids):   # scales of a page, 2^(n / 4) times as large in all
+            scales[page] = (scales[page].to(torch.int32) // 4 + 2 * min(n, 40)).to(torch.uint8)
+    ws, out, lse = step(b, DeviceBatch(b))
+    torch.cuda.synchronize()
+    assert ws.status() == 0
+    check_attention(b, out, lse, bounded.attention_rows(b), "e2m1")
+
+
+@pytest.mark.parametrize("q_len", [3, 4])
+def test_many_rows_captured_twice_and_on_two_streams(q_len):
+    b = make_batch([900, 64, 2000, 130], q_len, (16, 2), seed=65)
+    poison_hidden(b)
+    db = DeviceBatch(b)
+    want = step(b, db)
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    torch.cuda.synchronize()
+    for s in streams:
+        got.append(step(b, db, stream=s))
+    torch.cuda.synchronize()
+    for ws, out, lse in got:
+        assert ws.status() == 0
+        assert torch.equal(out, want[1]) and torch.equal(lse, want[2])
+    ws, out, lse = want
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(2):
+            hpa.decode_step(ws, db.q, db.k, db.v, db.lens, db.indptr, db.indices, out, lse, db.ks,
+                            db.vs)
+    first = out.clone()
+    out.zero_()
+    g.replay()
+    g.replay()
+    torch.cuda.synchronize()
+    assert ws.status() == 0 and torch.equal(out, first)
+
+
 def test_queries_and_scales_near_the_smallest():
     """Scores of nothing at all: hidden keys stay hidden, the rest is a mean."""
     b = make_batch([130, 70], 2, (16, 2), seed=25)
@@ -298,6 +385,37 @@ def test_guard_bands():
     assert (po[:256] == 3.25).all() and (po[-256:] == 3.25).all()
     assert (pl[:256] == 3.25).all() and (pl[-256:] == 3.25).all()
     rows = b.q_len * b.Hq
+    assert (po[256 + S * rows * 128:] == 3.25).all() and (pl[256 + S * rows:] == 3.25).all()
+    assert not (pl[256:256 + S * rows] == 3.25).any()
+
+
+def test_errors_and_guard_bands_of_many_rows():
+    b = make_batch([800, 90, 300, 4], 4, (16, 2), seed=33)
+    ix = torch.from_numpy(b.page_indices).cuda()
+    for at, bad in ((1, b.num_pages), (2, -1), (14, 2 ** 31 - 1)):
+        db = DeviceBatch(b)
+        db.indices = ix.clone()
+        db.indices[at] = bad
+        ws, out, lse = step(b, db, C=5)
+        torch.cuda.synchronize()
+        assert ws.status() == 4 and torch.isnan(out).all()
+    short = make_batch([300, 70], 4, (16, 2), seed=33)
+    short.seq_lens[1] = 3                          # fewer keys than new tokens
+    ws, out, lse = step(short, DeviceBatch(short), C=5)
+    torch.cuda.synchronize()
+    assert ws.status() == 1 and torch.isnan(out).all()
+    db, C = DeviceBatch(b), 11
+    ws = hpa.Workspace(b.B, b.q_len, b.Hq, 128, num_ctas=C, Hkv=b.Hkv)
+    n = ws.partial_lse.numel()
+    po = torch.full((n * 128 + 512,), 3.25, device="cuda")
+    pl = torch.full((n + 512,), 3.25, device="cuda")
+    ws.plan(db.lens)
+    hpa.hpa_decode_attn(db.q, db.k, db.v, db.indptr, db.indices, ws.taskmap, C, po[256:-256],
+                        pl[256:-256], db.ks, db.vs)
+    torch.cuda.synchronize()
+    assert ws.status() == 0
+    S, rows = int(ws.taskmap[5]), b.q_len * b.Hq
+    assert (po[:256] == 3.25).all() and (pl[:256] == 3.25).all()
     assert (po[256 + S * rows * 128:] == 3.25).all() and (pl[256 + S * rows:] == 3.25).all()
     assert not (pl[256:256 + S * rows] == 3.25).any()
 
