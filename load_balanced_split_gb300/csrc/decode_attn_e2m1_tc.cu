@@ -14,8 +14,8 @@
 // whatever its width (16 a tile: 1400), but three threads' overlap.
 //
 // What bounds it: a tile takes 1450 cycles of an SM (64 x 20000 keys with 24 rows: 390 us, 3.8
-// TB/s), where the DRAM would allow 790.  Shared memory's banks are taken for some 1150 of them (V
-// as f16 goes through it twice, 512; then P, codes and queries), the issue slots for 800.  Against
+// TB/s), where the DRAM would allow 790.  Shared memory's banks are taken for some 1100 of them (V
+// as f16 goes through it twice, 512; then P, codes and queries), the issue slots for 780.  Against
 // passes of up to 24 rows in the other kernel, in us: 64 x 8000 keys with 32 rows 190 (260), with
 // 64 rows 384 (564), 13 x 20011 with 20 rows 94 (102); but a segment costs more here (Q, the first
 // product and the teams' merge follow one another, 8 us for four tiles): 64 x 500 with 24 rows 38
