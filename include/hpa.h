@@ -124,8 +124,9 @@ size_t hpa_static_taskmap_bytes(int32_t B, int32_t splits);
 
 /* Partitions per KV head that fill the current device once with the kernel
  * hpa_decode_attn picks for this shape: hpa_default_num_ctas_mma up to 16
- * query rows per KV head (G * q_len), hpa_default_num_ctas_tc above.  Returns
- * <= 0 on a CUDA error or unsupported arguments. */
+ * query rows per KV head (G * q_len), hpa_default_num_ctas_tc above; for 4-bit
+ * pages that of their kernels.  Returns <= 0 on a CUDA error or unsupported
+ * arguments. */
 int32_t hpa_default_num_ctas(int32_t Hq, int32_t Hkv, int32_t q_len, int32_t kv_dtype);
 
 /* Partitions per KV head for hpa_decode_attn_mma: SMs x resident CTAs per SM /
@@ -215,7 +216,7 @@ int hpa_plan_window(const int32_t *seq_lens_dev, int32_t B, int32_t q_len, int32
  * q_dev:        bf16 [B][q_len][Hq][d], 16-byte aligned.
  * k_pool_dev, v_pool_dev: [num_pages][Hkv][page_size][d] of bf16 or E4M3
  *               bytes, 16-byte aligned (read with TMA tensor copies).
- * k_scale_dev, v_scale_dev: fp32 [Hkv] for HPA_KV_E4M3, ignored for bf16.
+ * k_scale_dev, v_scale_dev: fp32 [Hkv] for HPA_KV_E4M3 and HPA_KV_E2M1, ignored for bf16.
  *               With E4M3 pages the products run in f16: each query row is
  *               scaled by a power of two that puts its largest |element| in
  *               [2^14, 2^15) (taken back out of the scores), so any finite bf16
