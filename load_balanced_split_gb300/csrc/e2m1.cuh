@@ -72,14 +72,26 @@ __device__ __forceinline__ int group_rows(const AttnParams &p) {
   return min(p.group, p.rows - row_base(p));
 }
 
+// mbarrier.try_wait that may sleep for up to 20 us before it answers no.
+__device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait for a phase; false if it took too long, or if another warp of the CTA gave up.
-__device__ bool wait_phase(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity,
+                                           const volatile int *abort_flag) {
+  if (try_wait_long(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+    if (try_wait_long(bar, parity)) return true;
     if (*abort_flag || globaltimer_ns() - t0 > 2000000000ull) return false;
   }
 }
