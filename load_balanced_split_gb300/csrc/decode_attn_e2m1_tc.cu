@@ -9,17 +9,19 @@
 //   widen V, a key a thread, into shared memory (f16, 128-byte swizzle), operand A (MN-major) of
 //   O^T[128 dims][rows] += V^T P^T, which stays in tensor memory for the segment.
 // Three teams of four warps take tiles in turn, each with its own S, O, running maxima and V
-// buffer; K of a team's next tile is widened before V of this one, so that the first product runs
-// under that.  One thread per team issues both products: an MMA costs its thread some 87 cycles
-// whatever its width (16 a tile: 1400), but three threads' overlap.
+// buffer; K of a team's next tile is widened while the votes on the maximum come in, so that the
+// first product runs under the softmax and V.  One thread per team issues both products: an MMA
+// costs its thread some 87 cycles whatever its width (16 a tile: 1400), but three threads' overlap.
 //
-// What bounds it: a tile takes 1450 cycles of an SM (64 x 20000 keys with 24 rows: 390 us, 3.8
-// TB/s), where the DRAM would allow 790.  Shared memory's banks are taken for some 1100 of them (V
-// as f16 goes through it twice, 512; then P, codes and queries), the issue slots for 780.  Against
-// passes of up to 24 rows in the other kernel, in us: 64 x 8000 keys with 32 rows 190 (260), with
-// 64 rows 384 (564), 13 x 20011 with 20 rows 94 (102); but a segment costs more here (Q, the first
-// product and the teams' merge follow one another, 8 us for four tiles): 64 x 500 with 24 rows 38
-// (33), 64 x 8000 in a window of 2000 80 (76).  With 16 rows that kernel is ahead at every length.
+// What bounds it: a tile takes 1380 cycles of an SM (64 x 20000 keys with 24 rows: 372 us, 4.0
+// TB/s), where the DRAM would allow 790 and shared memory's banks are taken for some 1100 (V as f16
+// goes through it twice, 512; then P, codes and queries).  Neither less arithmetic (-6 % without
+// any) nor fewer MMAs (0 %) change that much; the steps' meetings do: the fence between the stores
+// and the second product is 10 %, a barrier for the votes was as much.  Against passes of up to 24
+// rows in the other kernel, in us: 64 x 8000 keys with 32 rows 185 (260), with 64 rows 374 (564),
+// 13 x 20011 with 20 rows 92 (102), in a window of 2000 with 24 rows 75 (76); but a short segment
+// costs more here (Q, the first product and the teams' merge follow one another): 64 x 500 with 24
+// rows 39 (33).  With 16 rows that kernel is ahead at every length.
 //
 // Tensor memory of a team, in columns: K 64, S 2 x 32, O 32.
 #include <math_constants.h>
@@ -37,15 +39,16 @@ constexpr int kProducerWarp = kConsumers / 32;
 constexpr int kIssuerWarp = kProducerWarp + 1;  // one for each team
 constexpr int kThreads = (kIssuerWarp + kTeams) * 32;
 // Rings of tiles.  K of a tile is widened while the team is at the tile before, and its place then
-// holds P until the second product is done; V is needed an iteration later and free as soon as it
-// is widened.  So three places a team for K and one for V: with two for both together the copies
-// of a tile began when it was nearly needed (461 us where this takes 390).
+// holds P until the second product is done: three places a team.  V is needed an iteration later
+// and free as soon as it is widened: one place a team, which the team's issuer fills (from L2,
+// where the producer has asked for it with K).  With two places a team for K and V together the
+// copies of a tile began when it was nearly needed (64 x 20000 with 24 rows 461 us, then 385; the
+// issuers' copies gained most in windows, 80 to 75).
 constexpr int kStages = 9, kVStages = 3;
 // Copies may land out of order: a team that came to a stage whose tile before, another team's,
 // had not landed would take that tile's phase for the end of its own.
 static_assert(kStages % kTeams == 0 && kVStages % kTeams == 0, "each stage belongs to one team");
 constexpr int kStageBytes = 2 * kUnit;  // two pages of K or of V
-constexpr int kLead = 6;                // tiles by which copies of K are ahead of those of V
 constexpr int kTileKeys = 2 * PAGE;
 static_assert(kThreads == 512, "128 registers a thread");
 constexpr float kNoMax = 1e30f;  // in the place of lift - m before a row's first key: all pass it
@@ -73,11 +76,12 @@ struct Tc {
   static constexpr int kTok = kFactor + 32 * 4;                  // int[32]: token of each row
   static constexpr int kNan = kTok + 32 * 4;                     // uint32[2][32]: NaN blocks
   static constexpr int kIds = kNan + 2 * 32 * 4;                   // int2[16]: pages of tiles
-  static constexpr int kInfo = kIds + 16 * 8;                    // int4
+  static constexpr int kVotes = kIds + 16 * 8;                   // int4[teams][2]
+  static constexpr int kInfo = kVotes + kTeams * 2 * 16;         // int4
   static constexpr int kBars = kInfo + 16;
-  // full[9] empty[9] vfull[3] vempty[3] qfull qempty drain, and for each team: K ready, S ready, P
-  // ready, PV done
-  static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 3 + 4 * kTeams;
+  // full[9] empty[9] vfull[3] qfull qempty drain, and for each team: K ready, S ready, P
+  // ready, PV done, votes
+  static constexpr int kNumBars = 2 * kStages + kVStages + 3 + 5 * kTeams;
   static constexpr int kTmem = kBars + 8 * kNumBars;
   static constexpr int kFlag = kTmem + 4;
   static constexpr int kBytes = kFlag + 4;
@@ -88,13 +92,12 @@ enum {
   B_FULL = 0,
   B_EMPTY = kStages,
   B_VFULL = 2 * kStages,
-  B_VEMPTY = B_VFULL + kVStages,
-  B_QFULL = B_VEMPTY + kVStages,
+  B_QFULL = B_VFULL + kVStages,
   B_QEMPTY,
   B_DRAIN,
   B_TEAM
 };
-enum { T_K = 0, T_S, T_P, T_PV };
+enum { T_K = 0, T_S, T_P, T_PV, T_VOTE };
 
 __device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                            uint32_t acc) {
@@ -182,30 +185,8 @@ __device__ void producer(const AttnParams &p, const uint8_t *k_pool, const uint8
   const int64_t q_at =
       (static_cast<int64_t>((rb + lane) / p.G) * p.Hq + h * p.G + (rb + lane) % p.G) * HEAD_DIM;
   int2 *ids = reinterpret_cast<int2 *>(smem + S::kIds);
-  int n0 = 0, nv = 0, nq = 0;  // tiles whose K and V, and segments, are on their way
+  int n0 = 0, nq = 0;  // tiles whose K, and segments, are on their way
   bool ok = true;
-  int before = 0;              // tiles before the segment that came last
-  auto send_v = [&]() {  // V of tile nv
-    bool good = true;
-    __syncwarp();
-    if (lane == 0) {
-      const int st = nv % kVStages;
-      good = wait_phase(bars + 8 * (B_VEMPTY + st), ((nv / kVStages) & 1) ^ 1, abort_flag);
-      if (good) {
-        const int2 id = ids[nv & 15];
-        const uint32_t fb = bars + 8 * (B_VFULL + st), dst = base + S::kPacked + st * kStageBytes;
-        mbar_arrive_expect_tx(fb, (id.y < 0 ? 1 : 2) * kUnit);
-        bulk_load_hint(dst, v_pool + (static_cast<int64_t>(id.x) * p.Hkv + h) * kUnit, kUnit, fb,
-                       pol);
-        if (id.y >= 0)
-          bulk_load_hint(dst + kUnit, v_pool + (static_cast<int64_t>(id.y) * p.Hkv + h) * kUnit,
-                         kUnit, fb, pol);
-      }
-    }
-    good = __shfl_sync(kFull, good, 0);
-    if (good) ++nv;
-    return good;
-  };
   for (int s0 = head.s_begin; s0 < head.s_end && ok; s0 += 32) {
     Seg mine = {0, 0, 0, 0, 0, 0};
     int list = 0, listed = 0;  // its request's page list
@@ -242,15 +223,8 @@ __device__ void producer(const AttnParams &p, const uint8_t *k_pool, const uint8
     int next_id = load_id(cur, cur.f.pg0);
     for (int j = 0; j < n_seg && ok; ++j) {
       const Walk nxt = segment(j + 1 < n_seg ? j + 1 : j);
-      {  // The segment's place and query rows, once the last ones have been taken up: which waits
-         // for the end of the segment before those, and so for its V.
+      {  // the segment's place and query rows, once the last ones have been taken up
         bool good = true;
-        while (good && nv < before) good = send_v();
-        if (!good) {
-          ok = false;
-          break;
-        }
-        before = n0;
         if (lane == 0) good = wait_phase(bars + 8 * B_QEMPTY, (nq & 1) ^ 1, abort_flag);
         if (!__shfl_sync(kFull, good, 0)) {
           ok = false;
@@ -282,11 +256,10 @@ __device__ void producer(const AttnParams &p, const uint8_t *k_pool, const uint8
         const uint32_t fb = bars + 8 * (B_FULL + stage);
         const uint32_t dst = base + stage * kStageBytes + (lane & 1) * kUnit;
         const int64_t at = (static_cast<int64_t>(id) * p.Hkv + h) * kUnit;
-        const int tiles = (cnt + 1) / 2;
+        const int tiles = (cnt + 1) / 2, second = __shfl_down_sync(kFull, id, 1);
         for (int i = 0; i < tiles; ++i) {
-          bool good = n0 + i < nv + kLead || send_v();
-          const int second = __shfl_down_sync(kFull, id, 1);
-          if (lane == 2 * i && good) {
+          bool good = true;
+          if (lane == 2 * i) {
             good = wait_phase(bars + 8 * (B_EMPTY + stage), phase ^ 1, abort_flag);
             if (good) {
               ids[n & 15] = make_int2(id, lane + 1 < cnt ? second : -1);
@@ -298,15 +271,17 @@ __device__ void producer(const AttnParams &p, const uint8_t *k_pool, const uint8
             ok = false;
             break;
           }
-          if (lane / 2 == i && lane < cnt) bulk_load_hint(dst, k_pool + at, kUnit, fb, pol);
+          if (lane / 2 == i && lane < cnt) {
+            bulk_load_hint(dst, k_pool + at, kUnit, fb, pol);
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(v_pool + at), "r"(kUnit)
+                         : "memory");
+          }
         }
         if (ok) n0 += tiles;
       }
       cur = nxt;
     }
   }
-  __syncwarp();
-  while (ok && nv < n0) ok = send_v();
   if (!ok || *abort_flag) {
     if (lane == 0) {
       status_or(p.tm, HPA_STATUS_TIMEOUT);
@@ -317,30 +292,42 @@ __device__ void producer(const AttnParams &p, const uint8_t *k_pool, const uint8
       const int last = n0 - 1 - (n0 - 1 - lane) % kStages;
       mbar_wait_bounded_rolled(bars + 8 * (B_FULL + lane), (last / kStages) & 1, 1000000000ull);
     }
-    if (lane < kVStages && nv > lane) {
-      const int last = nv - 1 - (nv - 1 - lane) % kVStages;
-      mbar_wait_bounded_rolled(bars + 8 * (B_VFULL + lane), (last / kVStages) & 1, 1000000000ull);
-    }
     if (lane == 0 && nq > 0)
       mbar_wait_bounded_rolled(bars + 8 * B_QFULL, (nq - 1) & 1, 1000000000ull);
   }
 }
 
 // ----------------------------------------------------------------------------- MMA issue
-// One thread for each team: S = K Q^T of its next tile, then O += V P of this one.
+// One thread for each team: S = K Q^T of its next tile, then O += V P of this one; and the copies
+// of V, whose place is free when P of the tile before is there.
 template <int NG>
-__device__ void issuer(const AttnParams &p, uint8_t *smem, const MapHead &head, uint32_t tmem,
-                       int team) {
+__device__ void issuer(const AttnParams &p, const uint8_t *v_pool, uint8_t *smem,
+                       const MapHead &head, uint32_t tmem, int team) {
   using S = Tc<NG>;
   constexpr int N = S::N;
   const uint32_t base = smem_u32(smem), bars = base + S::kBars;
-  const uint32_t mine = bars + 8 * (B_TEAM + 4 * team);
+  const uint32_t mine = bars + 8 * (B_TEAM + 5 * team);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kFlag);
   const uint32_t t0 = tmem + team * S::kTeamCols, o_t = t0 + 64 + 2 * N;
   const uint32_t vb = base + S::kV + team * S::kVBytes, qb = base + S::kQ;
   const uint32_t id_qk = tc_idesc(0, N, 0, 0), id_pv = tc_idesc(0, N, 1, 1);
-  int count = 0, nk = 0, np = 0;  // tiles of the CTA; products of this team
+  const int2 *ids = reinterpret_cast<const int2 *>(smem + S::kIds);
+  const uint64_t pol = l2_policy_evict_first();
+  const uint32_t vfull = bars + 8 * (B_VFULL + team);
+  int count = 0, nk = 0, np = 0, nv = 0;  // tiles of the CTA; products and copies of this team
   bool ok = true;
+  auto copy_v = [&](int n) {  // its K has come, so its pages are known
+    const int2 id = ids[n & 15];
+    const uint32_t dst = base + S::kPacked + team * kStageBytes;
+    const int64_t h = blockIdx.y;
+    mbar_arrive_expect_tx(vfull, (id.y < 0 ? 1 : 2) * kUnit);
+    bulk_load_hint(dst, v_pool + (static_cast<int64_t>(id.x) * p.Hkv + h) * kUnit, kUnit, vfull,
+                   pol);
+    if (id.y >= 0)
+      bulk_load_hint(dst + kUnit, v_pool + (static_cast<int64_t>(id.y) * p.Hkv + h) * kUnit, kUnit,
+                     vfull, pol);
+    ++nv;
+  };
   auto qk = [&]() {
     if (!wait_phase(mine + 8 * T_K, nk & 1, abort_flag)) return false;
     tc_fence_after();
@@ -362,7 +349,10 @@ __device__ void issuer(const AttnParams &p, uint8_t *smem, const MapHead &head, 
     mbar_arrive(bars + 8 * B_QEMPTY);
     const int pg0 = inf.z / PAGE, pg1 = (inf.w + PAGE - 1) / PAGE, tiles = (pg1 - pg0 + 1) / 2;
     const int first = first_of_team(team, count);
-    if (first < tiles) ok = qk();
+    if (first < tiles) {
+      ok = qk();
+      if (ok) copy_v(count + first);
+    }
     for (int i = first; i < tiles && ok; i += kTeams) {
       if (i + kTeams < tiles && !qk()) {
         ok = false;
@@ -373,6 +363,7 @@ __device__ void issuer(const AttnParams &p, uint8_t *smem, const MapHead &head, 
         break;
       }
       tc_fence_after();
+      if (i + kTeams < tiles) copy_v(count + i + kTeams);
       const int stage = (count + i) % kStages;
       const uint32_t pb = base + stage * kStageBytes;
 #pragma unroll
@@ -390,6 +381,8 @@ __device__ void issuer(const AttnParams &p, uint8_t *smem, const MapHead &head, 
     status_or(p.tm, HPA_STATUS_TIMEOUT);
     *abort_flag = 1;
   }
+  // never leave the CTA with copies still landing in its shared memory
+  if ((!ok || *abort_flag) && nv > 0) mbar_wait_bounded_rolled(vfull, (nv - 1) & 1, 1000000000ull);
   tc_commit(bars + 8 * B_DRAIN);  // everything issued is done before the CTA frees its memory
 }
 
@@ -401,7 +394,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, h = blockIdx.y;
   const int team = w >> 2, quarter = w & 3, kt = tid & 127;  // this thread's key of a tile
   const uint32_t base = smem_u32(smem), bars = base + S::kBars;
-  const uint32_t mine = bars + 8 * (B_TEAM + 4 * team);
+  const uint32_t mine = bars + 8 * (B_TEAM + 5 * team);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kFlag);
   // A wait that gives up raises the flag, so that no other lasts; the thread still takes part in
   // everything that follows, barriers among them.
@@ -419,6 +412,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
   float *max_f = reinterpret_cast<float *>(smem + S::kMax);
   float *top_f = reinterpret_cast<float *>(smem + S::kTop) + team * 128;
   float *fac_f = reinterpret_cast<float *>(smem + S::kFac) + team * 32;
+  int4 *votes = reinterpret_cast<int4 *>(smem + S::kVotes) + 2 * team;
   const float *factor = reinterpret_cast<const float *>(smem + S::kFactor);
   const int *tok = reinterpret_cast<const int *>(smem + S::kTok);
   const int G = p.G, q_len = p.q_len, rows = group_rows(p), rb = row_base(p);
@@ -557,8 +551,18 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
         x[r + 1] = fmaf(x[r + 1], __uint_as_float(c), __uint_as_float(d));
         most = fmaxf(most, fmaxf(x[r], x[r + 1]));
       }
-      const bool over = most > kRescaleSlack + kLift;
-      if (team_any(team, over)) {
+      // The warps' votes; while they come in, K of the next tile.  Every warp of the team gets here
+      // within its waits' limits, so this wait always ends, and all read the same votes.
+      const bool over = __any_sync(kFull, most > kRescaleSlack + kLift);
+      if (lane == 0) {
+        reinterpret_cast<int *>(votes + (n_s & 1))[quarter] = over;
+        mbar_arrive(mine + 8 * T_VOTE);
+      }
+      if (i + kTeams < tiles) widen_k(i + kTeams);
+      mbar_wait_bounded_rolled(mine + 8 * T_VOTE, n_s & 1, 60000000000ull);
+      __syncwarp();
+      const int4 vote = votes[n_s & 1];
+      if (vote.x | vote.y | vote.z | vote.w) {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {  // the scores themselves again
           float v[8];
@@ -612,7 +616,6 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
         l[r + 1] += b;
         pk2[r / 2] = pack_f16(a, b);
       }
-      if (i + kTeams < tiles) widen_k(i + kTeams);
       // The tile's K is read, and the products of the tile before are done with V: P over the one,
       // V over the other.
       if (i > first) ok = wait(mine + 8 * T_PV, (n_s - 1) & 1) && ok;
@@ -670,8 +673,6 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (B_VEMPTY + n % kVStages));
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(mine + 8 * T_P);
@@ -770,18 +771,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bars + 8 * (B_FULL + st), 1);
       mbar_init(bars + 8 * (B_EMPTY + st), 1);
     }
-    for (int st = 0; st < kVStages; ++st) {
-      mbar_init(bars + 8 * (B_VFULL + st), 1);
-      mbar_init(bars + 8 * (B_VEMPTY + st), 4);
-    }
+    for (int st = 0; st < kVStages; ++st) mbar_init(bars + 8 * (B_VFULL + st), 1);
     mbar_init(bars + 8 * B_QFULL, 1);
     mbar_init(bars + 8 * B_QEMPTY, kConsumers / 32 + kTeams);
     mbar_init(bars + 8 * B_DRAIN, kTeams);
     for (int t = 0; t < kTeams; ++t) {
-      mbar_init(bars + 8 * (B_TEAM + 4 * t + T_K), kTeamThreads);
-      mbar_init(bars + 8 * (B_TEAM + 4 * t + T_S), 1);
-      mbar_init(bars + 8 * (B_TEAM + 4 * t + T_P), kTeamThreads);
-      mbar_init(bars + 8 * (B_TEAM + 4 * t + T_PV), 1);
+      mbar_init(bars + 8 * (B_TEAM + 5 * t + T_K), kTeamThreads);
+      mbar_init(bars + 8 * (B_TEAM + 5 * t + T_S), 1);
+      mbar_init(bars + 8 * (B_TEAM + 5 * t + T_P), kTeamThreads);
+      mbar_init(bars + 8 * (B_TEAM + 5 * t + T_PV), 1);
+      mbar_init(bars + 8 * (B_TEAM + 5 * t + T_VOTE), 4);
     }
     *reinterpret_cast<int *>(smem + S::kFlag) = 0;
     fence_barrier_init();
@@ -815,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (w == kProducerWarp) {
     producer<NG, WIN>(p, k_pool, v_pool, smem, m);
   } else {
-    if ((threadIdx.x & 31) == 0) issuer<NG>(p, smem, m, tmem, w - kIssuerWarp);
+    if ((threadIdx.x & 31) == 0) issuer<NG>(p, v_pool, smem, m, tmem, w - kIssuerWarp);
     __syncwarp();
   }
   tc_fence_before();
