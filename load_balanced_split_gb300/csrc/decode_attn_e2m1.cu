@@ -80,7 +80,6 @@ struct Cfg {
   static constexpr int kStats = kRowsOnM ? 2 : 2 * NT;
 };
 constexpr int kStageBytes = 2 * kUnit;
-constexpr float kFar = 1048576.f;  // 2^20: there a product is off by its rounding, 2^-4, at most
 constexpr int kQRowBytes = 272;  // 256 of a query row, padded against bank conflicts
 constexpr int kMergeStride = HEAD_DIM + 4;
 
@@ -405,7 +404,6 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
     float m[NS], l[NS], o[NT][8][4];
 #pragma unroll
     for (int i = 0; i < NS; ++i) m[i] = -CUDART_INF_F, l[i] = 0.f;
-    bool far = false;  // a maximum beyond kFar
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -502,7 +500,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
                   x[kg][nt][e] = -CUDART_INF_F;
               }
         }
-        // running maximum: moves when a score passes it by more than the slack
+        // running maximum, of the plain sums: moves when a score passes it by more than the slack
         bool over = false;
         float top[NS];
 #pragma unroll
@@ -517,10 +515,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
               top[i] = fresh ? fmaxf(a, b) : fmaxf(top[i], fmaxf(a, b));
             }
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          top[i] = __fmul_rn(top[i], sl[i]);
-          over |= top[i] - m[i] > kRescaleSlack;
-        }
+        for (int i = 0; i < NS; ++i) over |= (top[i] - m[i]) * sl[i] > kRescaleSlack;
         if (__any_sync(kFull, over)) {
           float a[NS];
 #pragma unroll
@@ -528,15 +523,11 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
 #pragma unroll
             for (int d = RM ? 1 : 4; d < (RM ? 4 : 32); d <<= 1)
               top[i] = fmaxf(top[i], __shfl_xor_sync(kFull, top[i], d));
-            const float mn = top[i] - m[i] > kRescaleSlack ? top[i] : m[i];
-            a[i] = mn == -CUDART_INF_F ? 1.f : exp2f(m[i] - mn);
+            const float mn = (top[i] - m[i]) * sl[i] > kRescaleSlack ? top[i] : m[i];
+            a[i] = mn == -CUDART_INF_F ? 1.f : exp2f((m[i] - mn) * sl[i]);
             m[i] = mn;
             l[i] *= a[i];
           }
-          far = false;
-#pragma unroll
-          for (int i = 0; i < NS; ++i) far |= fabsf(m[i]) > kFar && m[i] != -CUDART_INF_F;
-          far = __any_sync(kFull, far);
 #pragma unroll
           for (int i = 0; i < 2 * NT; ++i) {  // the columns of o
             const float f = RM ? __shfl_sync(kFull, a[(i >> 1) % NS], 8 * c + 4 * (i & 1))
@@ -548,45 +539,28 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
             }
           }
         }
-        // Their exponents: the exact product less the maximum, which is a rounded one.  Where a step
-        // of fp32 at the maximum is no longer small, that difference would take the largest score's
-        // own weight to zero or beyond f16, so the product is rounded first there.
-        if (far) {
-          float less[NS];
-#pragma unroll
-          for (int i = 0; i < NS; ++i) less[i] = m[i] == -CUDART_INF_F ? 0.f : m[i];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int kg = 0; kg < KG; ++kg)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int i = stat_of(nt, e);
-                x[kg][nt][e] = __fsub_rn(__fmul_rn(x[kg][nt][e], sl[i]), less[i]) + kLift;
-              }
-        } else {
-          float less[NS];
-#pragma unroll
-          for (int i = 0; i < NS; ++i) less[i] = m[i] == -CUDART_INF_F ? 0.f : kLift - m[i];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int kg = 0; kg < KG; ++kg)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int i = stat_of(nt, e);
-                x[kg][nt][e] = fmaf(x[kg][nt][e], sl[i], less[i]);
-              }
-        }
-        // probabilities; their sums in fp32 before the rounding to f16
+        // Probabilities; their sums in fp32 before the rounding to f16.  The exponent is the plain
+        // sum less the maximum's, then the factor: however large the scores, the largest one's own
+        // is the lift and none passes it by more than the slack.  (The product less a rounded
+        // maximum, one instruction less, is off by half a step of fp32 at that maximum: from 2^26 on
+        // the weight of the largest score itself went to zero or beyond f16.)
         uint32_t pb[KG][NT][2];
+        float less[NS];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) less[i] = m[i] == -CUDART_INF_F ? 0.f : -m[i];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int kg = 0; kg < KG; ++kg) {
             float pr[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) pr[e] = exp2f(x[kg][nt][e]);
+            for (int u = 0; u < 2; ++u) {
+              const int i = stat_of(nt, 2 * u), j = stat_of(nt, 2 * u + 1);
+              const f32x2 d = add2(pk(x[kg][nt][2 * u], x[kg][nt][2 * u + 1]), pk(less[i], less[j]));
+              upk(fma2(d, pk(sl[i], sl[j]), pk(kLift, kLift)), pr[2 * u], pr[2 * u + 1]);
+              pr[2 * u] = exp2f(pr[2 * u]);
+              pr[2 * u + 1] = exp2f(pr[2 * u + 1]);
+            }
 #pragma unroll
             for (int u = 0; u < 2; ++u)
               l[stat_of(nt, RM ? 2 * u : u)] += pr[RM ? 2 * u : u] + pr[RM ? 2 * u + 1 : u + 2];
@@ -695,7 +669,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
 #pragma unroll
       for (int d = RM ? 1 : 4; d < (RM ? 4 : 32); d <<= 1) l[i] += __shfl_xor_sync(kFull, l[i], d);
       if (RM ? c == 0 : g == 0) {
-        sm_m[w * S::kRows + stat_row(i)] = m[i];
+        sm_m[w * S::kRows + stat_row(i)] = m[i] * sl[i];
         sm_l[w * S::kRows + stat_row(i)] = l[i];
       }
     }
