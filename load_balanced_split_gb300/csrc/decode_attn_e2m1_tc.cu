@@ -51,7 +51,6 @@ static_assert(kStages % kTeams == 0 && kVStages % kTeams == 0, "each stage belon
 constexpr int kStageBytes = 2 * kUnit;  // two pages of K or of V
 constexpr int kTileKeys = 2 * PAGE;
 static_assert(kThreads == 512, "128 registers a thread");
-constexpr float kNoMax = 1e30f;  // in the place of lift - m before a row's first key: all pass it
 
 // NG: groups of 8 query rows that hold one (3 or 4 of the MMAs' 4)
 template <int NG>
@@ -472,7 +471,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
     };
     if (kt < 32) {
       pair_f[2 * kt] = kt < R8 ? factor[kt] : 1.f;
-      pair_f[2 * kt + 1] = kNoMax;
+      pair_f[2 * kt + 1] = 0.f;
       max_f[team * 32 + kt] = -CUDART_INF_F;
     }
     float l[R8];
@@ -521,7 +520,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
     };
 
     if (first < tiles) widen_k(first);
-    bool started = false;
+    bool unset = true;  // a row of the team has met no key yet: it has no maximum to compare with
     for (int i = first; i < tiles; i += kTeams) {
       ok = wait(mine + 8 * T_S, n_s & 1) && ok;
       tc_fence_after();
@@ -553,7 +552,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
       }
       // The warps' votes; while they come in, K of the next tile.  Every warp of the team gets here
       // within its waits' limits, so this wait always ends, and all read the same votes.
-      const bool over = __any_sync(kFull, most > kRescaleSlack + kLift);
+      const bool over = unset || __any_sync(kFull, most > kRescaleSlack + kLift);
       if (lane == 0) {
         reinterpret_cast<int *>(votes + (n_s & 1))[quarter] = over;
         mbar_arrive(mine + 8 * T_VOTE);
@@ -577,6 +576,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
           }
         }
         team_any(team, false);
+        bool none = false;
         if (kt < R8) {
           const float m = max_f[team * 32 + kt];
           const float t = fmaxf(fmaxf(top_f[kt], top_f[32 + kt]),
@@ -584,10 +584,11 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
           const float mn = t > m + kRescaleSlack ? t : m;
           fac_f[kt] = mn == -CUDART_INF_F ? 1.f : exp2f(m - mn);
           max_f[team * 32 + kt] = mn;
-          pair_f[2 * kt + 1] = mn == -CUDART_INF_F ? kNoMax : kLift - mn;
+          none = mn == -CUDART_INF_F;
+          pair_f[2 * kt + 1] = none ? 0.f : kLift - mn;
         }
-        team_any(team, false);
-        if (started) {  // O of the tiles before is at rest once their products are done
+        unset = team_any(team, none);
+        if (i > first) {  // O of the tiles before is at rest once their products are done
           ok = wait(mine + 8 * T_PV, (n_s - 1) & 1) && ok;
           tc_fence_after();
 #pragma unroll
@@ -676,10 +677,10 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(mine + 8 * T_P);
-      started = true;
       ++n_s;
     }
     count += tiles;
+    const bool started = first < tiles;
 
     // ---- segment end: the teams' (m, l, O) together, and the partial
     if (started) {

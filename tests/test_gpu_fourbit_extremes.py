@@ -123,3 +123,14 @@ def one_step_apart(heads, q_len, window=None, C=1):
 def test_two_keys_one_step_apart(heads, q_len, C):
     one_step_apart(heads, q_len, None, C)
     one_step_apart(heads, q_len, 650, C)
+
+
+@pytest.mark.parametrize("window,sinks", [(None, 0), (70, 3)])
+@pytest.mark.parametrize("heads,q_len", ROWS)
+def test_a_first_maximum_below_any_constant(heads, q_len, window, sinks):
+    """Every score of every row is near -1e33 (keys without a negative element, queries without a
+    positive one), in tiles without a row of padding too."""
+    b = make_batch([300, 70, 500, q_len], q_len, heads, seed=100 + q_len)
+    b.k_pool[..., :fourbit.CODES] &= 0x77
+    b.q = (-b.q.float().abs() * 1e33).to(torch.bfloat16)
+    check(b, window, sinks)
