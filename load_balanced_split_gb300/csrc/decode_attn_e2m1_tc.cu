@@ -570,7 +570,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int r = 8 * g + e;
-            x[r] = x[r] == -CUDART_INF_F ? x[r] : v[e] * pair_f[2 * r];
+            x[r] = x[r] == -CUDART_INF_F ? x[r] : __fmul_rn(v[e], pair_f[2 * r]);
             const float t = warp_max(x[r]);
             if (lane == 0) top_f[quarter * 32 + r] = t;
           }
@@ -581,11 +581,13 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
           const float m = max_f[team * 32 + kt];
           const float t = fmaxf(fmaxf(top_f[kt], top_f[32 + kt]),
                                 fmaxf(top_f[64 + kt], top_f[96 + kt]));
-          const float mn = t > m + kRescaleSlack ? t : m;
+          const float mn = t - m > kRescaleSlack ? t : m;
           fac_f[kt] = mn == -CUDART_INF_F ? 1.f : exp2f(m - mn);
           max_f[team * 32 + kt] = mn;
           none = mn == -CUDART_INF_F;
-          pair_f[2 * kt + 1] = none ? 0.f : kLift - mn;
+          // rounded down: with the slack it must not pass what f16 holds where a step of fp32 at the
+          // maximum is as large as the lift (the scores are rounded products here)
+          pair_f[2 * kt + 1] = none ? 0.f : __fsub_rd(kLift, mn);
         }
         unset = team_any(team, none);
         if (i > first) {  // O of the tiles before is at rest once their products are done

@@ -119,7 +119,8 @@ def one_step_apart(heads, q_len, window=None, C=1):
 
 
 @pytest.mark.parametrize("C", [1, 7])
-@pytest.mark.parametrize("heads,q_len", [((8, 1), 1), ((5, 1), 1), ((16, 2), 2), ((9, 1), 1)])
+@pytest.mark.parametrize("heads,q_len", [((8, 1), 1), ((5, 1), 1), ((16, 2), 2), ((9, 1), 1),
+                                         ((17, 1), 1), ((24, 1), 1), ((8, 1), 4), ((40, 1), 1)])
 def test_two_keys_one_step_apart(heads, q_len, C):
     one_step_apart(heads, q_len, None, C)
     one_step_apart(heads, q_len, 650, C)
