@@ -228,7 +228,9 @@ int hpa_plan_window(const int32_t *seq_lens_dev, int32_t B, int32_t q_len, int32
  *               probabilities are rounded to f16 (2^-11 of each; those below 2^-21 of the
  *               row's largest to 2^-32 of that one).  NaN block scales of keys that a row does
  *               not see do not reach it; a row that sees one is NaN in the result, of a value's
- *               block in its 16 elements.
+ *               block in its 16 elements, of a key's in all of them and in the lse, as is a row
+ *               with a score of NaN or +inf (its partial lse is +inf); scores of -inf are
+ *               those of keys that are not seen.
  * page_indptr_dev: int32 [B+1]; page_indices_dev: int32; key i of request r
  *               is slot i % page_size of page page_indices[page_indptr[r] + i / page_size].
  *               page_indptr has to be right when the kernel reads it: no call is told how

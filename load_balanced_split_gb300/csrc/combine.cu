@@ -14,6 +14,8 @@
 //   partitions): one 128-thread block per item; the four warps take every fourth
 //   segment with several loads in flight, so a request split over many partitions
 //   costs a few round trips, not one per segment.
+// A partial of lse +inf (a 4-bit row that sees a NaN) makes W, and so output and lse, NaN; an lse of
+// -inf says that no key was seen.
 // A task map whose status word is non-zero makes every output NaN, and so does a
 // request whose segment range in the map is out of bounds (reported as
 // HPA_STATUS_BAD_MAP).
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(kItemsPerBlock * 32)
   pk.x = *reinterpret_cast<const uint32_t *>(&lo);
   pk.y = *reinterpret_cast<const uint32_t *>(&hi);
   reinterpret_cast<uint2 *>(out + item * HEAD_DIM)[lane] = pk;
-  if (out_lse != nullptr && lane == 0) out_lse[item] = W > 0.f ? M + logf(W) : -CUDART_INF_F;
+  if (out_lse != nullptr && lane == 0) out_lse[item] = W == 0.f ? -CUDART_INF_F : M + logf(W);
 }
 
 __global__ void __launch_bounds__(kBlockWarps * 32)
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32)
   pk.x = *reinterpret_cast<const uint32_t *>(&lo);
   pk.y = *reinterpret_cast<const uint32_t *>(&hi);
   reinterpret_cast<uint2 *>(out + item * HEAD_DIM)[lane] = pk;
-  if (out_lse != nullptr && lane == 0) out_lse[item] = Wt > 0.f ? Mb + logf(Wt) : -CUDART_INF_F;
+  if (out_lse != nullptr && lane == 0) out_lse[item] = Wt == 0.f ? -CUDART_INF_F : Mb + logf(Wt);
 }
 
 }  // namespace
