@@ -13,7 +13,7 @@
 // Every row is read once and written once.  Without the transform the DRAM bounds it: 32768 tokens
 // of 64/8 heads, normed and rotated into a bf16 cache, take 211 us, 6.4 TB/s or 0.95 of the copy
 // peak.  With it the issue slots do, two thirds of which are taken (48 shuffles and 24 additions
-// of pairs for four rows, beside some 130 others): 296 us into a 4-bit cache, 4.3 TB/s.  A small
+// of pairs for four rows, beside some 130 others): 297 us into a 4-bit cache, 4.3 TB/s.  A small
 // batch is one launch (3.7 us for a token, 4.3 for 128).
 //
 // A warp takes items of up to 8 rows (one token, heads of q, of k or of v), four rows at a time, 8
@@ -286,7 +286,8 @@ __device__ __forceinline__ void store_row(void *pool, int kv_dtype, int64_t unit
     // codes = E2M1 of the quotients.  A quotient on the border of two codes is common (bf16
     // inputs, scales of 4 bits) and has to fall to the even one, which v * (1 / s) alone may miss
     // by its last bit: its exact remainder, times 1 / s, puts that right (Markstein, IBM J. Res.
-    // Dev. 34, 1990; a division each takes 30 us more, 32768 tokens of 64/8 heads).
+    // Dev. 34, 1990; a division each takes 30 us more, 32768 tokens of 64/8 heads).  The remainder
+    // is taken negative, so that a quotient of zero keeps its sign.
     uint8_t *base = static_cast<uint8_t *>(pool) + unit * E2M1_UNIT;
     uint32_t codes[2], sb[2];
 #pragma unroll
@@ -303,13 +304,13 @@ __device__ __forceinline__ void store_row(void *pool, int kv_dtype, int64_t unit
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float q = v[8 * hf + i] * r;
-        z[i] = fmaf(fmaf(-q, s, v[8 * hf + i]), r, q);
+        z[i] = fmaf(fmaf(q, s, -v[8 * hf + i]), -r, q);
       }
       if (am > 3e38f) {  // an infinity has no remainder
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] = v[8 * hf + i] * r;
       }
-      codes[hf] = pack_e2m1(z);
+      codes[hf] = s == 0.f ? 0u : pack_e2m1(z);
       // the row's four scales of this half, gathered into a word
       sb[hf] = (k & 1) ? 0u : sb[hf] << (4 * k);
       sb[hf] |= __shfl_xor_sync(kFull, sb[hf], 2);
