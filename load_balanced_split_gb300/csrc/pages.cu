@@ -135,8 +135,9 @@ __device__ __forceinline__ void fill_request(const AssignParams &p, int r, int f
   if (p.new_tokens) {
     const int nt = p.new_tokens[r], offset = p.pos_offset ? p.pos_offset[r] : 0;
     const int end = min(max(nt, 0), max(p.max_tokens - at.tok_off, 0));
+    const long long before = static_cast<long long>(at.len) - nt;  // of a bad request below 0
     for (int t = first; t < end; t += step) {
-      const int pos = max(at.len - nt + t, 0);
+      const int pos = static_cast<int>(max(before + t, 0ll));
       long long slot = -1;
       if (x.served) {
         const int id = page_of(p, x, at, pos / PAGE, free, avail);
