@@ -974,6 +974,12 @@ class PageTable:
 
 
 # ----------------------------------------------------------------------------- workspace helper
+def _default_tile(window, e2m1):
+    """Keys per tile of a plan: a 4-bit tile of 256 gives short batches more to share out (one
+    request of 100000 keys 35 -> 33 us) and long ones lose nothing by it."""
+    return 64 if window is not None else 256 if e2m1 else 512
+
+
 class Workspace:
     """Device buffers for one decode step: task map and split partials.
 
@@ -985,11 +991,13 @@ class Workspace:
     hpa_default_num_ctas_mma / _tc size for a forced kernel.  Either kernel
     accepts any partition count.  With `window` (keys) and `sinks` the steps run
     sliding-window attention: hpa_plan_window and hpa_decode_attn_window, sized by
-    hpa_default_num_ctas_window.
+    hpa_default_num_ctas_window.  kv_dtype: the cache's type, where it is KV_E2M1; plan then
+    takes as many keys a tile as decode_step does for 4-bit pages, so that a map planned once
+    for many layers is the one that each of them would plan.
     """
 
     def __init__(self, B, q_len, Hq, d, num_ctas=None, splits=None, device="cuda", Hkv=8,
-                 weighted=False, window=None, sinks=0):
+                 weighted=False, window=None, sinks=0, kv_dtype=None):
         if window is not None and (splits is not None or weighted):
             raise HpaError("a window has the dynamic plan alone")
         if window is None and sinks:
@@ -1005,6 +1013,7 @@ class Workspace:
             raise HpaError("workspace size query failed")
         self.splits = splits
         self.weighted = weighted
+        self.kv_dtype = kv_dtype
         self.window, self.sinks, self.q_len = window, sinks, q_len
         self.capacity = cap
         self.taskmap = torch.zeros((nbytes + 3) // 4, dtype=torch.int32, device=device)
@@ -1014,9 +1023,10 @@ class Workspace:
                                     device=device)  # fused combine
 
     def plan(self, seq_lens, tile=None, stream=None):
-        """tile: keys per tile, by default 512, or one page of 64 with a window."""
+        """tile: keys per tile, by default 512 (256 of 4-bit pages), or one page of 64 with a
+        window."""
         if tile is None:
-            tile = 512 if self.window is None else 64
+            tile = _default_tile(self.window, self.kv_dtype == KV_E2M1)
         if self.window is not None:
             hpa_plan_window(seq_lens, self.q_len, self.window, self.sinks, tile, self.num_ctas,
                             self.taskmap, stream)
@@ -1061,8 +1071,8 @@ def decode_step(ws: Workspace, q, k_pool, v_pool, seq_lens, page_indptr, page_in
         raise HpaError("hpa_key_weights has no 4-bit form")
     stream = _stream(stream)
     if plan:
-        if tile is None and ws.window is None and _is_e2m1(k_pool):
-            tile = 256  # as long a read as 144 keys of 8 bits (1 x 100000 keys: 35 -> 33 us)
+        if tile is None:
+            tile = _default_tile(ws.window, ws.kv_dtype == KV_E2M1 or _is_e2m1(k_pool))
         ws.plan(seq_lens, tile, stream)
     if fused:
         hpa_decode_attn_fused(q, k_pool, v_pool, page_indptr, page_indices, ws.taskmap,
