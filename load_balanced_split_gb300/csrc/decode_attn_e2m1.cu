@@ -831,10 +831,10 @@ int occupancy(int *ctas) {
 
 }  // namespace
 
-// Query rows of a KV head in groups of equal size, up to 32: CTAs that share pages keep pace and
-// find them in L2.
+// Query rows of a KV head in groups of equal size: CTAs that share pages keep pace and find them in
+// L2.
 int attn_e2m1_group(int rows) {
-  const int groups = (rows + 31) / 32;
+  const int groups = (rows + E2M1_MAX_ROWS - 1) / E2M1_MAX_ROWS;
   return (rows + groups - 1) / groups;
 }
 

@@ -57,6 +57,7 @@ template <int NG>
 struct Tc {
   static constexpr int N = 32;        // columns of an MMA
   static constexpr int kRows = 8 * NG;
+  static_assert(kRows <= N && N == E2M1_MAX_ROWS, "a group's rows, and the buffers of N rows");
   static constexpr int kPRow = 2 * N;  // bytes of P of one key
   static constexpr int kPSwz = 4;      // descriptor mode of a 64-byte swizzle
   static_assert(kTileKeys * kPRow <= 2 * kUnit, "P lies over the tile's K");

@@ -38,13 +38,14 @@ struct TaskMapLayout {
 
 constexpr int PAGE = 64;       // tokens per KV page
 constexpr int HEAD_DIM = 128;  // d
-constexpr int MAX_ROWS = 16;   // query rows per CTA (one m16 MMA tile)
+constexpr int MAX_ROWS = 16;   // query rows per CTA (one m16 MMA tile) of 16- and 8-bit pages
+constexpr int E2M1_MAX_ROWS = 32;  // query rows per CTA of 4-bit pages: a lane of a warp for each
 // One page and KV head of a 4-bit pool: 64 rows of 64 bytes of E2M1 codes, then 64 x 8 E4M3
 // scales, one for each 16 elements.
 constexpr int E2M1_BLOCK = 16;
 constexpr int E2M1_UNIT = PAGE * HEAD_DIM / 2 + PAGE * HEAD_DIM / E2M1_BLOCK;
 static_assert(E2M1_UNIT == HPA_E2M1_PAGE_BYTES, "as the header states");
-constexpr int MAX_ROWS_TOTAL = 64;  // G * q_len rows per KV head, in groups of up to 16
+constexpr int MAX_ROWS_TOTAL = 64;  // G * q_len rows per KV head, in groups of up to the above
 
 // The pages of one request that a sliding window of `window` keys with `sinks` first
 // keys reaches, as a shorter "compact" sequence of pages: the pages holding sinks, then
@@ -85,7 +86,8 @@ struct AttnParams {
   int64_t num_pages;
   TaskMapLayout lay;
   int B, C, q_len, Hq, Hkv, G, rows;
-  int group;          // query rows per CTA of the mma.sync kernel, at most MAX_ROWS
+  int group;          // query rows per CTA: of the mma.sync kernel at most MAX_ROWS, of the kernels
+                      // of 4-bit pages at most E2M1_MAX_ROWS
   int heads_per_cta;  // KV heads one CTA walks per segment: 1 (grid over heads) or Hkv
   bool window;        // the map is one of hpa_plan_window
   float scale_log2;   // sm_scale * log2(e)
