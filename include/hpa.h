@@ -222,7 +222,9 @@ int hpa_plan_window(const int32_t *seq_lens_dev, int32_t B, int32_t q_len, int32
  *               [2^14, 2^15) (taken back out of the scores), so any finite bf16
  *               query converts exactly, down to 2^-28 of its row's largest.
  *               With HPA_KV_E2M1 pages (layout above, pools 16-byte aligned) kernels of
- *               their own run at every row count, in passes of up to 32 rows, with the
+ *               their own run at every row count, in passes of up to 32 rows (up to 32 rows
+ *               per KV head 4-bit pages are faster than E4M3 ones, or level; above, the second
+ *               pass over a long cache takes up to 1.6 times E4M3's time), with the
  *               precision of E4M3 pages here: codes times block scales and queries enter the
  *               products exactly, in f16, sums and softmax statistics are fp32 and the
  *               probabilities are rounded to f16 (2^-11 of each; those below 2^-21 of the

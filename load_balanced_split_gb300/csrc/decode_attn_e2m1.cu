@@ -10,7 +10,7 @@
 // the widening to f16 has about three instruction slots an element before it, not the memory,
 // is what the kernel waits for; and an MMA takes 8 of them, in which little else issues (an FFMA
 // beside it costs 1 more, a conversion half of one).  With 8 rows the memory still sets the pace
-// (5.5 TB/s over 32 x 8192 keys, starts and ends included), with 16 the slots (4.65 TB/s).  The
+// (5.6 TB/s over 32 x 8192 keys, starts and ends included), with 16 the slots (4.7 TB/s).  The
 // layout:
 //  * the products run as m16n8k16 MMAs with the KEYS (S = K Q^T) and the HEAD DIMS (O^T = V^T P^T)
 //    as the 16 rows and 8 query rows as the 8 columns, so an MMA takes 256 cache elements for 8
@@ -49,12 +49,12 @@ namespace {
 // Query rows in tiles of 8 columns (1 or 2), and what was measured best for each number of them, in
 // us (32 x 8192 keys with 8 rows and 128 windows of 4096 with 16 sinks; 64 x 20000 with 16 rows and
 // 64 x 8000 in a window of 2000):
-//   1 tile:  4 consumer warps in pairs that share a page, three CTAs per SM at 128 registers, 58
-//            and 110 (5 warps with a page each, two CTAs: 62 and 127; four to a page: 72 and 127);
-//   2 tiles: the same pairs, two CTAs at 168 registers, query fragments in shared memory, 333
-//            and 47 (a page each gains 1 %, but takes 95 in the window: a segment's last pages,
+//   1 tile:  4 consumer warps in pairs that share a page, three CTAs per SM at 128 registers, 59
+//            and 111 (5 warps with a page each, two CTAs: 62 and 127; four to a page: 72 and 127);
+//   2 tiles: the same pairs, two CTAs at 168 registers, query fragments in shared memory, 332
+//            and 48 (a page each gains 1 %, but takes 95 in the window: a segment's last pages,
 //            and its start, then leave warps idle for a page's time; 12 warps in one CTA 315
-//            and 63).
+//            for 317 on 64 requests of equal length, and 63 for 48 in the window).
 // The warps of an SM come in fours: with 10 in a CTA the schedulers that have three set the pace.
 // More rows go to decode_attn_e2m1_tc.cu (as 3 tiles here, 8 warps at 232 registers, 13 x 20011
 // keys with 20 rows took 102 where it takes 92).

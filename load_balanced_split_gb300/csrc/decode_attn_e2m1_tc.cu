@@ -13,13 +13,13 @@
 // first product runs under the softmax and V.  One thread per team issues both products: an MMA
 // costs its thread some 87 cycles whatever its width (16 a tile: 1400), but three threads' overlap.
 //
-// What bounds it: a tile takes 1380 cycles of an SM (64 x 20000 keys with 24 rows: 372 us, 4.0
+// What bounds it: a tile takes 1370 cycles of an SM (64 x 20000 keys with 24 rows: 369 us, 4.0
 // TB/s), where the DRAM would allow 790 and shared memory's banks are taken for some 1100 (V as f16
 // goes through it twice, 512; then P, codes and queries).  Neither less arithmetic (-6 % without
 // any) nor fewer MMAs (0 %) change that much; the steps' meetings do: the fence between the stores
 // and the second product is 10 %, a barrier for the votes was as much.  Against passes of up to 24
-// rows in the other kernel, in us: 64 x 8000 keys with 32 rows 185 (260), with 64 rows 374 (564),
-// 13 x 20011 with 20 rows 92 (102), in a window of 2000 with 24 rows 75 (76); but a short segment
+// rows in the other kernel, in us: 64 x 8000 keys with 32 rows 184 (260), with 64 rows 372 (564),
+// 13 x 20011 with 20 rows 92 (102), in a window of 2000 with 24 rows 77 (76); but a short segment
 // costs more here (Q, the first product and the teams' merge follow one another): 64 x 500 with 24
 // rows 39 (33).  With 16 rows that kernel is ahead at every length.
 //

@@ -975,8 +975,8 @@ class PageTable:
 
 # ----------------------------------------------------------------------------- workspace helper
 def _default_tile(window, e2m1):
-    """Keys per tile of a plan: a 4-bit tile of 256 gives short batches more to share out (one
-    request of 100000 keys 35 -> 33 us) and long ones lose nothing by it."""
+    """Keys per tile of a plan: 256 of 4-bit pages give small batches more to share out (one
+    request of 900 keys 12.8 -> 11.6 us, of 100000 33.9 -> 32.5) and change large ones little."""
     return 64 if window is not None else 256 if e2m1 else 512
 
 
