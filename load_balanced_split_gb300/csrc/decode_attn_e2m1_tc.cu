@@ -126,6 +126,17 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&r)[16])
       : "memory");
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // Barrier of a team, with the OR of its threads' predicates.
 __device__ __forceinline__ bool team_any(int team, bool x) {
   uint32_t r;
@@ -572,7 +583,7 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
           for (int e = 0; e < 8; ++e) {
             const int r = 8 * g + e;
             x[r] = x[r] == -CUDART_INF_F ? x[r] : __fmul_rn(v[e], pair_f[2 * r]);
-            const float t = warp_max(x[r]);
+            const float t = warp_max_nan(x[r]);
             if (lane == 0) top_f[quarter * 32 + r] = t;
           }
         }
@@ -580,9 +591,10 @@ __device__ void consumer(const AttnParams &p, uint8_t *smem, const MapHead &head
         bool none = false;
         if (kt < R8) {
           const float m = max_f[team * 32 + kt];
-          const float t = fmaxf(fmaxf(top_f[kt], top_f[32 + kt]),
-                                fmaxf(top_f[64 + kt], top_f[96 + kt]));
-          const float mn = t - m > kRescaleSlack ? t : m;
+          const float t = max_nan(max_nan(top_f[kt], top_f[32 + kt]),
+                                  max_nan(top_f[64 + kt], top_f[96 + kt]));
+          // (a NaN becomes the maximum: its row is NaN whatever that is, and not without one)
+          const float mn = t - m <= kRescaleSlack ? m : t;
           fac_f[kt] = mn == -CUDART_INF_F ? 1.f : exp2f(m - mn);
           max_f[team * 32 + kt] = mn;
           none = mn == -CUDART_INF_F;

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from bounded_helpers import lse_bound
+from bounded_helpers import lse_bound, out_bound
 from fourbit_helpers import make_batch, poison_hidden, rows_of, step
 from gpu_helpers import DeviceBatch
 from oracle import bounded
@@ -68,3 +68,28 @@ def test_a_nan_value_leaves_the_lse(heads, q_len):
     torch.cuda.synchronize()
     assert np.isnan(out.float().cpu().numpy()[0, ..., 32:48]).all()
     assert (np.abs(lse.double().cpu().numpy() - ref[1]) <= lse_bound(ref[1], ref[3])).all()
+
+
+@pytest.mark.parametrize("at", [5, 700, 1999])
+@pytest.mark.parametrize("heads,q_len", ROWS)
+def test_a_nan_key_among_rising_scores(heads, q_len, at):
+    """The maximum moves with nearly every tile, before and after the NaN."""
+    b = make_batch([2000, 1300], q_len, heads, seed=113)
+    _, scales = rows_of(b.k_pool)
+    for r in range(2):
+        ids = b.page_indices[int(b.page_indptr[r]):int(b.page_indptr[r + 1])]
+        for n, page in enumerate(ids):   # scales of a page, 2^(n / 4) times as large in all
+            scales[page] = (scales[page].to(torch.int32) // 4 + 2 * min(n, 40)).to(torch.uint8)
+    ref = bounded.attention_rows(b)
+    scales[int(b.page_indices[at // 64]), 0, at % 64, 3] = 0x7F
+    hit = np.zeros(ref[1].shape, bool)
+    sees = [j for j in range(q_len) if at <= 2000 - q_len + j]
+    hit[0, sees, :b.Hq // b.Hkv] = True
+    ws, out, lse = step(b, DeviceBatch(b), C=2, tile=512)
+    torch.cuda.synchronize()
+    assert ws.status() == 0
+    got, l = out.float().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.isnan(got[hit]).all() and np.isnan(l[hit]).all()
+    bound = out_bound(ref[0], ref[2], ref[3], "e2m1")
+    assert (np.abs(got - ref[0])[~hit] <= bound[~hit]).all()
+    assert (np.abs(l - ref[1])[~hit] <= lse_bound(ref[1], ref[3])[~hit]).all()
